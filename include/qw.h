@@ -275,6 +275,187 @@ qw_status qw_op_gemm_swiglu_f16(int32_t M, int32_t N, int32_t K, const void *A,
                                  const void *Wg, const void *Wu, void *act, int32_t *err_dev,
                                  void *cuda_stream);
 
+/* ---- a paged key-value cache and the operators around it ----
+ *
+ * One serving step of many sequences: qw_op_page_plan hands out pages and says where each new
+ * token goes, qw_op_rope_append rotates the queries and keys and writes keys and values
+ * there, qw_op_paged_attention reads the pages back for one new token per sequence, and
+ * qw_op_token_logprobs turns the step's logits into log probabilities.
+ * qw_op_page_release returns the pages of finished sequences.
+ *
+ * Conventions of these calls:
+ *   - All pointers are device pointers on the current device unless marked host; a pointer to
+ *     host memory or to another device's is refused (QW_ERR_INVALID_ARG). The stream belongs
+ *     to the current device. Nothing is allocated and nothing synchronises; every call may be
+ *     captured into a CUDA graph, which then reads the lengths, tables and counts that the
+ *     device memory holds at each replay.
+ *   - What only the device can see (lengths, page ids, slots, token ids) is checked there:
+ *     a bad value is never used as an address, and its QW_DEV_* bit is OR-ed into err_dev
+ *     (device int32, required, never cleared by the library).
+ *   - Zero sequences, tokens or rows are allowed and do nothing, unless stated otherwise.
+ *   - Tensors of one call must not overlap, unless stated otherwise. */
+
+/* Bits of a device error word (err_dev). */
+enum {
+  QW_DEV_TOKEN = 1,      /* a token id outside [0, vocab) */
+  QW_DEV_NONFINITE = 2,  /* a row of logits without a distribution */
+  QW_DEV_TIMEOUT = 4,    /* a bounded wait gave up */
+  QW_DEV_RANGE = 8,      /* a value outside the fp16 range (stored as an infinity), or not finite */
+  QW_DEV_LAYOUT = 16,    /* shared memory found misaligned; the work was skipped */
+  QW_DEV_PAGE = 32,      /* a page id, slot or length outside the cache */
+  QW_DEV_CAPACITY = 64   /* a page plan that does not fit; nothing was handed out */
+};
+
+/* One layer's cache: n_pages pages of page_size positions. Element (page p, KV head h, position
+ * i of the page, dimension d) of the keys lies at k[p * page_stride + h * head_stride +
+ * i * pos_stride + d], of the values at the same place of v; strides are in elements of dtype
+ * (QW_F32, QW_F16 or QW_BF16). Either [page][head][position] or [page][position][head] order,
+ * with gaps allowed between rows, heads and pages; a stride along an extent of 1 is not
+ * looked at. k and v are 16-byte aligned, the strides multiples of 16 bytes. head_dim is a
+ * multiple of 8, at most 256. Slot s of the cache is position s % page_size of page
+ * s / page_size. The struct itself is host memory and is read during the call only. */
+typedef struct {
+  void *k, *v;
+  int32_t dtype, n_pages, page_size, n_kv_heads, head_dim;
+  int64_t page_stride, head_stride, pos_stride;
+} qw_paged_kv;
+
+/* Page plan of one step: takes pages for the new tokens of every sequence from a list of free
+ * pages and says where each token goes. Sequence b holds lens[b] positions in the pages
+ * block_table[b][0 .. ceil(lens[b] / page_size) - 1] and gets n_new[b] >= 0 more (n_new NULL: one
+ * each). Its further pages are taken from the end of free_pages[0 .. n_free[0] - 1]: the i-th page
+ * taken, counted over sequences in order and over a sequence's pages in order, is
+ * free_pages[n_free[0] - 1 - i].
+ *   block_table  [n_seqs][max_blocks], in and out: the new pages' entries are written
+ *   lens_out     [n_seqs]: lens + n_new; may be lens
+ *   n_free_out   [1]: what is left of free_pages, which is not written; may be n_free
+ *   cu_tokens    [n_seqs + 1]: token t of the step belongs to the sequence b with
+ *                cu_tokens[b] <= t < cu_tokens[b + 1]
+ *   positions    [max_tokens]: lens[b] + t - cu_tokens[b]; 0 behind the last token
+ *   slots        [max_tokens]: the token's slot in the cache; -1 behind the last token
+ * If the step does not fit (too few free pages, more than max_tokens tokens or max_blocks pages
+ * of a sequence, a negative length or count, n_free outside [0, n_pages]) QW_DEV_CAPACITY is
+ * set and the step is empty: lens_out = lens, n_free_out = n_free, cu_tokens 0, positions 0,
+ * slots -1. A page id outside [0, n_pages) gives slot -1 and sets QW_DEV_PAGE. n_seqs <= 16384.
+ * With n_seqs = 0 the outputs are those of an empty step. max_tokens = 0 is allowed. */
+qw_status qw_op_page_plan(int32_t n_seqs, int32_t page_size, int32_t n_pages, int32_t max_blocks, int32_t max_tokens,
+                          const int32_t *lens, const int32_t *n_new, const int32_t *free_pages,
+                          const int32_t *n_free, int32_t *block_table, int32_t *lens_out,
+                          int32_t *n_free_out, int32_t *cu_tokens, int32_t *positions, int64_t *slots,
+                          int32_t *err_dev, void *cuda_stream);
+
+/* Gives the pages of finished sequences back: for every b with done[b] != 0, in order, its pages
+ * block_table[b][0 .. ceil(lens[b] / page_size) - 1] are appended to free_pages (device
+ * [n_pages]) behind its first n_free[0] entries. lens_out[b] is 0 for those sequences and
+ * lens[b] for the others (lens_out may be lens); n_free_out is the new count (may be n_free).
+ * The table is not written. If the list would exceed n_pages, a length is negative or beyond
+ * max_blocks pages, or n_free is outside [0, n_pages], QW_DEV_CAPACITY is set, lens_out = lens
+ * and n_free_out = n_free, and no page moves. A page id outside [0, n_pages) moves as it is and
+ * sets QW_DEV_PAGE. n_seqs <= 16384. */
+qw_status qw_op_page_release(int32_t n_seqs, int32_t page_size, int32_t n_pages, int32_t max_blocks,
+                             const int32_t *lens, const int32_t *done, const int32_t *block_table,
+                             int32_t *free_pages, const int32_t *n_free, int32_t *lens_out,
+                             int32_t *n_free_out, int32_t *err_dev, void *cuda_stream);
+
+/* How rotary frequencies are stretched for contexts longer than the trained one. With r the
+ * rotated dimensions, w_i = theta^(-2i/r), i < r/2, and L = orig_len:
+ *   QW_ROPE_NONE    w_i
+ *   QW_ROPE_LINEAR  w_i / factor
+ *   QW_ROPE_NTK     theta replaced by theta * factor^(r / (r - 2))
+ *   QW_ROPE_YARN    (1 - c_i) w_i + c_i w_i / factor, c_i rising linearly from 0 to 1 between
+ *                   the indices (rounded outwards, inside [0, r - 1]) whose frequency turns
+ *                   `high` and `low` times over L positions; cos and sin times
+ *                   0.1 ln(factor) + 1
+ *   QW_ROPE_BANDS   w_i / factor where L w_i / 2 pi <= low, w_i where it is >= high, and a
+ *                   linear blend in L w_i / 2 pi between them */
+typedef enum { QW_ROPE_NONE = 0, QW_ROPE_LINEAR = 1, QW_ROPE_NTK = 2, QW_ROPE_YARN = 3, QW_ROPE_BANDS = 4 } qw_rope_scaling;
+
+/* The rotary frequencies of qw_op_rope_append, on the host (no GPU needed): turns[i] (host
+ * [rot_dim / 2]) is w_i / 2 pi as a fraction of a turn in units of 2^-64, rounded; *mscale (host)
+ * the factor of cos and sin. rot_dim even and positive, theta > 1, factor >= 1, orig_len > 0 and
+ * 0 < low < high where the scaling uses them; else QW_ERR_INVALID_ARG. The fraction of a turn at
+ * position p is then the low 64 bits of p * turns[i]: exact for every position. */
+qw_status qw_rope_turns(int32_t rot_dim, double theta, int32_t scaling, double factor, double orig_len, double low,
+                        double high, uint64_t *turns, float *mscale);
+
+/* Rotary positions of the queries and keys of n_tokens tokens, and the append of the keys and
+ * values to a paged cache [LSA RoPE; KV cache]. Token t stands at positions[t] (any int32). The
+ * first rot_dim dimensions of every query and key head are rotated in pairs (a, b), pair i by
+ * the angle positions[t] * w_i: a' = mscale (a cos - b sin), b' = mscale (a sin + b cos); the
+ * pair is dimensions (i, i + rot_dim / 2), or (2i, 2i + 1) when adjacent is 1. The remaining
+ * dimensions pass unchanged. q_out receives the queries, slot slots[t] of the cache the
+ * rotated key and the value; slot -1 writes no key and value, a slot outside
+ * [0, n_pages * page_size) neither, and sets QW_DEV_PAGE. Two tokens of a call must not have
+ * the same slot (either's values may end up there).
+ *   q [n_tokens][n_heads][head_dim], k, v [n_tokens][n_kv_heads][head_dim], all of io_dtype, heads
+ *   contiguous, one token's row q_stride (k_stride, v_stride) elements after the last one's;
+ *   q_out like q with q_out_stride. q_out may be q (with the same stride). All 16-byte aligned,
+ *   strides multiples of 16 bytes; q, k and v may lie in one fused row.
+ *   turns (device [rot_dim / 2]) and mscale as from qw_rope_turns; rot_dim even, 2 .. head_dim.
+ * io_dtype QW_F32 with any cache type, or the cache's own type. Angles are reduced in 64-bit
+ * fixed point, all else is fp32, rounded once. An fp16 result out of range, or not finite,
+ * sets QW_DEV_RANGE. */
+qw_status qw_op_rope_append(const qw_paged_kv *cache, int32_t n_tokens, int32_t n_heads, int32_t io_dtype,
+                            const int32_t *positions, const int64_t *slots, const uint64_t *turns, int32_t rot_dim,
+                            int32_t adjacent, float mscale, const void *q, int64_t q_stride, const void *k,
+                            int64_t k_stride, const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride,
+                            int32_t *err_dev, void *cuda_stream);
+
+/* GQA decode attention over a paged cache, one query token per sequence [LSA Attention, GQA]: for
+ * sequence b and query head h, scores s_j = scale * q_h . K_j over the positions j = 0 ..
+ * lens[b] - 1 of KV head h / (n_heads / n_kv_heads), out_h = sum_j softmax(s)_j V_j and
+ * lse_h = ln sum_j exp(s_j). Position j lies in page block_table[b][j / page_size]; what the last
+ * page holds behind it is not read. A sequence of length 0 gives out 0 and lse -inf.
+ * A NaN among the keys, values or queries makes every output that it reaches NaN, an infinity
+ * makes it infinite or NaN; other heads and sequences are not touched. A length that is negative or
+ * beyond max_blocks pages is cut to that range, the positions of a page outside [0, n_pages)
+ * are left out, and both set QW_DEV_PAGE.
+ *   block_table [n_seqs][max_blocks]; lens [n_seqs]
+ *   q   [n_seqs][n_heads][head_dim] of io_dtype, heads contiguous, q_stride elements between
+ *       sequences; out the same with out_stride; both 16-byte aligned, strides multiples of
+ *       16 bytes. out may be q (with the same stride).
+ *   lse fp32 [n_seqs][n_heads], or NULL
+ *   workspace at least qw_op_paged_attention_workspace() bytes, 16-byte aligned, zeroed once
+ *       before its first use (cudaMemset); every call leaves it ready for the next. Calls
+ *       that may run at the same time need workspaces of their own.
+ * io_dtype QW_F32 with any cache type, or the cache's own type; sums are fp32. Any n_heads that is
+ * a multiple of the cache's n_kv_heads. The result does not depend on the run: equal inputs give
+ * equal bits on equal devices. */
+size_t qw_op_paged_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+qw_status qw_op_paged_attention(const qw_paged_kv *cache, int32_t n_seqs, int32_t n_heads, const int32_t *block_table,
+                                int32_t max_blocks, const int32_t *lens, int32_t io_dtype, const void *q,
+                                int64_t q_stride, float scale, void *out, int64_t out_stride, float *lse,
+                                void *workspace, size_t workspace_bytes, int32_t *err_dev, void *cuda_stream);
+
+/* Log probabilities of given tokens, with their ranks, the entropy and the likeliest tokens, of
+ * n_rows rows of logits [LSA Decoding: softmax of the logits]. For a row z:
+ *   logprobs[i] = z_t - ln sum_j exp(z_j) for t = ids[i], i < n_ids
+ *   ranks[i]    = 1 + the tokens with a larger logit, or the same and a lower id
+ *   entropy     = - sum_j p_j ln p_j in nats (p = softmax(z); 0 where p_j is 0)
+ *   top_ids, top_logprobs: the top_k tokens in that order, and their log probabilities
+ * A logit of -inf is a token of probability 0. A row that holds a NaN or +inf, or nothing but
+ * -inf, has no distribution: QW_DEV_NONFINITE is set, logprobs, entropy and top_logprobs are NaN,
+ * ranks 0 and top_ids -1. An id of -1 marks no token (logprob 0, rank 0); any other id outside
+ * [0, vocab) gives NaN and rank 0 and sets QW_DEV_TOKEN.
+ *   logits [n_rows][row_stride >= vocab] of logits_dtype, aligned to its own size
+ *   ids, logprobs, ranks [n_rows][n_ids], n_ids 0 .. 8 (0: all three may be NULL); ranks may be NULL
+ *   entropy [n_rows] or NULL
+ *   top_ids, top_logprobs [n_rows][top_k], top_k 0 .. min(32, vocab) (0: both may be NULL)
+ *   workspace as for qw_op_paged_attention, of qw_op_token_logprobs_workspace() bytes. */
+size_t qw_op_token_logprobs_workspace(int32_t n_rows, int32_t vocab, int32_t top_k);
+qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t vocab, const void *logits,
+                               int64_t row_stride, const int32_t *ids, int32_t n_ids, float *logprobs, int32_t *ranks,
+                               float *entropy, int32_t top_k, int32_t *top_ids, float *top_logprobs, void *workspace,
+                               size_t workspace_bytes, int32_t *err_dev, void *cuda_stream);
+
+/* The same for the logits of sequence seq's last step, into host memory (all pointers host, sizes
+ * and NULL rules as above, one row; entropy one float). The scratch is allocated by the first
+ * call and released by qw_destroy. Synchronises. Errors: QW_ERR_INVALID_ARG for a sequence that
+ * is not active, QW_ERR_TOKEN_RANGE for an id outside [0, vocab), QW_ERR_NUMERIC for
+ * non-finite logits. */
+qw_status qw_read_logprobs(qw_model *m, int32_t seq, const int32_t *ids, int32_t n_ids, float *logprobs,
+                           int32_t *ranks, float *entropy, int32_t top_k, int32_t *top_ids, float *top_logprobs);
+
 #ifdef __cplusplus
 }
 #endif

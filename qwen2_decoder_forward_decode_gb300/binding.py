@@ -49,6 +49,19 @@ class QwWeights(ctypes.Structure):
                 ("lm_head", ctypes.c_void_p), ("layers", ctypes.POINTER(QwLayerWeights))]
 
 
+class PagedKV(ctypes.Structure):
+    """One layer's paged cache (qw_paged_kv): device addresses of the keys and values, the element
+    type (F32, BF16 or F16), the extents, and the strides in elements of a page, a KV head and a
+    position within its page (head dimensions are contiguous)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (n, ctypes.c_int32) for n in ("dtype", "n_pages", "page_size", "n_kv_heads", "head_dim")] + [
+        (n, ctypes.c_int64) for n in ("page_stride", "head_stride", "pos_stride")]
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+# bits of a device error word (err_ptr of the operators)
+DEV_TOKEN, DEV_NONFINITE, DEV_TIMEOUT, DEV_RANGE, DEV_LAYOUT, DEV_PAGE, DEV_CAPACITY = (1 << i for i in range(7))
+
 _lib = None
 
 
@@ -61,7 +74,8 @@ def lib():
         raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
     L = ctypes.CDLL(LIB_PATH)
     P, I32, VP, SZ = ctypes.POINTER, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
-    pi = P(I32)
+    I64, F32C, F64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
+    pi, pf = P(I32), P(F32C)
     sig = {
         "qw_create": ([P(QwConfig), P(QwWeights), VP, P(VP)], I32),
         "qw_destroy": ([VP], None),
@@ -86,6 +100,15 @@ def lib():
         "qw_op_decode_attention_noalloc_limit": ([], SZ),
         "qw_op_gemm_f16": ([I32, I32, I32, VP, VP, VP, VP, I32, VP, VP], I32),
         "qw_op_gemm_swiglu_f16": ([I32, I32, I32, VP, VP, VP, VP, VP, VP], I32),
+        "qw_op_page_plan": ([I32] * 5 + [VP] * 12, I32),
+        "qw_op_page_release": ([I32] * 4 + [VP] * 9, I32),
+        "qw_rope_turns": ([I32, F64, I32, F64, F64, F64, F64, P(ctypes.c_uint64), pf], I32),
+        "qw_op_rope_append": ([P(PagedKV), I32, I32, I32, VP, VP, VP, I32, I32, F32C] + [VP, I64] * 4 + [VP, VP], I32),
+        "qw_op_paged_attention_workspace": ([I32, I32, I32], SZ),
+        "qw_op_paged_attention": ([P(PagedKV), I32, I32, VP, I32, VP, I32, VP, I64, F32C, VP, I64, VP, VP, SZ, VP, VP], I32),
+        "qw_op_token_logprobs_workspace": ([I32, I32, I32], SZ),
+        "qw_op_token_logprobs": ([I32, I32, I32, VP, I64, VP, I32, VP, VP, VP, I32, VP, VP, VP, SZ, VP, VP], I32),
+        "qw_read_logprobs": ([VP, I32, pi, I32, pf, pi, pf, I32, pi, pf], I32),
         "qw_op_decode_attention_workspace": ([I32, I32, I32, I32], SZ),
         "qw_op_decode_attention": ([I32, I32, I32, I32, I32, I32, VP, VP, VP, VP, VP, SZ, VP], I32),
     }
@@ -105,7 +128,9 @@ def exported_symbols():
             "qw_set_timeline", "qw_read_timeline",
             "qw_op_decode_attention_workspace", "qw_op_decode_attention",
             "qw_op_decode_attention_noalloc", "qw_op_decode_attention_noalloc_limit", "qw_op_gemm_f16",
-            "qw_op_gemm_swiglu_f16"]
+            "qw_op_gemm_swiglu_f16", "qw_op_page_plan", "qw_op_page_release", "qw_rope_turns",
+            "qw_op_rope_append", "qw_op_paged_attention_workspace", "qw_op_paged_attention",
+            "qw_op_token_logprobs_workspace", "qw_op_token_logprobs", "qw_read_logprobs"]
 
 
 def check(status):
@@ -115,6 +140,10 @@ def check(status):
 
 def _iptr(a):
     return a.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+
+
+def _fptr(a):
+    return a.ctypes.data_as(ctypes.POINTER(ctypes.c_float))
 
 
 class DeviceWeights:
@@ -235,6 +264,18 @@ class Model:
         check(lib().qw_read_logits(self.h, seq, z.ctypes.data_as(ctypes.POINTER(ctypes.c_float))))
         return z
 
+    def logprobs(self, ids=(), top_k=0, seq=0):
+        """Log probabilities of the tokens ids after sequence seq's last step (at most 8), their
+        ranks, the entropy in nats, and the top_k likeliest tokens (at most 32) with theirs:
+        (logprobs, ranks, entropy, top_ids, top_logprobs) as numpy arrays and a float."""
+        ids = np.ascontiguousarray(ids, dtype=np.int32)
+        lp, ranks = np.empty(len(ids), dtype=np.float32), np.empty(len(ids), dtype=np.int32)
+        top_ids, top_lp = np.empty(max(top_k, 0), dtype=np.int32), np.empty(max(top_k, 0), dtype=np.float32)
+        ent = np.empty(1, dtype=np.float32)
+        check(lib().qw_read_logprobs(self.h, seq, _iptr(ids), len(ids), _fptr(lp), _iptr(ranks), _fptr(ent), top_k,
+                                     _iptr(top_ids), _fptr(top_lp)))
+        return lp, ranks, float(ent[0]), top_ids, top_lp
+
     def logits_ptr(self):
         return lib().qw_logits(self.h)
 
@@ -303,3 +344,66 @@ def gemm_f16(M, N, K, a_ptr, b_ptr, bias_ptr, c_ptr, accumulate, err_ptr, stream
 
 def gemm_swiglu_f16(M, N, K, a_ptr, wg_ptr, wu_ptr, act_ptr, err_ptr, stream=None):
     check(lib().qw_op_gemm_swiglu_f16(M, N, K, a_ptr, wg_ptr, wu_ptr, act_ptr, err_ptr, stream))
+
+
+# ---- a paged key-value cache (qw.h gives each operator's formulas, layouts and errors) ----
+
+def page_plan(n_seqs, page_size, n_pages, max_blocks, max_tokens, lens_ptr, n_new_ptr, free_ptr, n_free_ptr,
+              table_ptr, lens_out_ptr, n_free_out_ptr, cu_ptr, positions_ptr, slots_ptr, err_ptr, stream=None):
+    """Takes free pages for every sequence's new tokens and maps each token to its position and slot."""
+    check(lib().qw_op_page_plan(n_seqs, page_size, n_pages, max_blocks, max_tokens, lens_ptr, n_new_ptr, free_ptr,
+                                n_free_ptr, table_ptr, lens_out_ptr, n_free_out_ptr, cu_ptr, positions_ptr, slots_ptr,
+                                err_ptr, stream))
+
+
+def page_release(n_seqs, page_size, n_pages, max_blocks, lens_ptr, done_ptr, table_ptr, free_ptr, n_free_ptr,
+                 lens_out_ptr, n_free_out_ptr, err_ptr, stream=None):
+    """Gives the pages of finished sequences back to the free list."""
+    check(lib().qw_op_page_release(n_seqs, page_size, n_pages, max_blocks, lens_ptr, done_ptr, table_ptr, free_ptr,
+                                   n_free_ptr, lens_out_ptr, n_free_out_ptr, err_ptr, stream))
+
+
+def rope_turns(rot_dim, theta, scaling="none", factor=1.0, orig_len=0.0, low=1.0, high=None):
+    """Rotary frequencies as 64-bit fractions of a turn (uint64 [rot_dim / 2]) and the factor of cos and
+    sin, for rope_append. scaling is a key of ROPE_SCALING; high defaults to 32 turns ("yarn") or 4
+    ("bands") over orig_len."""
+    if scaling not in ROPE_SCALING:
+        raise QwError(1, f"unknown rope scaling {scaling!r}")
+    turns = np.empty(max(rot_dim // 2, 1), dtype=np.uint64)
+    mscale = ctypes.c_float()
+    check(lib().qw_rope_turns(rot_dim, theta, ROPE_SCALING[scaling], factor, orig_len, low,
+                              (32.0 if scaling == "yarn" else 4.0) if high is None else high,
+                              turns.ctypes.data_as(ctypes.POINTER(ctypes.c_uint64)), ctypes.byref(mscale)))
+    return turns, float(mscale.value)
+
+
+def rope_append(cache, n_tokens, n_heads, io_dtype, positions_ptr, slots_ptr, turns_ptr, rot_dim, adjacent, mscale,
+                q_ptr, q_stride, k_ptr, k_stride, v_ptr, v_stride, q_out_ptr, q_out_stride, err_ptr, stream=None):
+    """Rotates queries and keys by their positions and appends keys and values to the paged cache."""
+    check(lib().qw_op_rope_append(ctypes.byref(cache), n_tokens, n_heads, io_dtype, positions_ptr, slots_ptr, turns_ptr,
+                                  rot_dim, int(adjacent), mscale, q_ptr, q_stride, k_ptr, k_stride, v_ptr, v_stride,
+                                  q_out_ptr, q_out_stride, err_ptr, stream))
+
+
+def paged_attention_workspace(n_heads, n_kv_heads, head_dim):
+    return int(lib().qw_op_paged_attention_workspace(n_heads, n_kv_heads, head_dim))
+
+
+def paged_attention(cache, n_seqs, n_heads, table_ptr, max_blocks, lens_ptr, io_dtype, q_ptr, q_stride, scale,
+                    out_ptr, out_stride, lse_ptr, ws_ptr, ws_bytes, err_ptr, stream=None):
+    """Attention of one new token per sequence over the pages of its block table."""
+    check(lib().qw_op_paged_attention(ctypes.byref(cache), n_seqs, n_heads, table_ptr, max_blocks, lens_ptr, io_dtype,
+                                      q_ptr, q_stride, scale, out_ptr, out_stride, lse_ptr, ws_ptr, ws_bytes, err_ptr,
+                                      stream))
+
+
+def token_logprobs_workspace(n_rows, vocab, top_k):
+    return int(lib().qw_op_token_logprobs_workspace(n_rows, vocab, top_k))
+
+
+def token_logprobs(logits_dtype, n_rows, vocab, logits_ptr, row_stride, ids_ptr, n_ids, logprobs_ptr, ranks_ptr,
+                   entropy_ptr, top_k, top_ids_ptr, top_logprobs_ptr, ws_ptr, ws_bytes, err_ptr, stream=None):
+    """Log probabilities, ranks, entropy and top tokens of rows of logits."""
+    check(lib().qw_op_token_logprobs(logits_dtype, n_rows, vocab, logits_ptr, row_stride, ids_ptr, n_ids, logprobs_ptr,
+                                     ranks_ptr, entropy_ptr, top_k, top_ids_ptr, top_logprobs_ptr, ws_ptr, ws_bytes,
+                                     err_ptr, stream))

@@ -48,6 +48,7 @@ constexpr int ATTN_CHUNK_MIN = 32;
 }  // namespace
 
 void qw::set_error_message(const char* msg) { g_err = msg; }
+void qw::set_error_message(const char* where, const char* what) { g_err = std::string(where) + ": " + what; }
 
 struct qw_model {
   Dims d;
@@ -104,6 +105,7 @@ struct qw_model {
   int* bactive = nullptr;          // device copy of the active flags
   bool bactive_dirty = true;
   cudaGraphExec_t bgraph = nullptr;
+  void* lp_block = nullptr;  // qw_read_logprobs: ids and results of one row, then its workspace
   unsigned long long* tl_buf = nullptr;  // device timeline of one decode step (or null)
   int tl_n = 0;                          // launches per decode step
   std::vector<unsigned long long> tl_init;
@@ -408,7 +410,7 @@ struct qw_model {
     if (battn_ws) cudaFree(battn_ws);
     void* bufs[] = {kv, x, q, attn, act, logits, rope, attn_ws, keys, lm_counter, pos, tok,
                     hist, hist_n, err, ids, pf_block, pf_ws, w16, tl_buf, mega_layers, mega_part,
-                    mega_bar, mega_abort};
+                    mega_bar, mega_abort, lp_block};
     for (void* b : bufs)
       if (b) cudaFree(b);
     if (pinned) cudaFreeHost(pinned);
@@ -975,6 +977,54 @@ qw_status qw_read_logits(qw_model* m, int32_t seq, float* host_out) {
   QW_CUDA(cudaMemcpyAsync(host_out, m->logits + (size_t)seq * m->d.V, sizeof(float) * m->d.V,
                           cudaMemcpyDeviceToHost, m->stream));
   return m->check_device_errors();
+}
+
+qw_status qw_read_logprobs(qw_model* m, int32_t seq, const int32_t* ids, int32_t n_ids, float* logprobs,
+                           int32_t* ranks, float* entropy, int32_t top_k, int32_t* top_ids, float* top_logprobs) {
+  g_err.clear();
+  if (!m) return fail(QW_ERR_INVALID_ARG, "null model");
+  if (seq < 0 || seq >= m->d.max_seqs) return fail(QW_ERR_INVALID_ARG, "sequence index out of range");
+  if (!m->active[seq]) return fail(QW_ERR_INVALID_ARG, "sequence holds no tokens");
+  if (n_ids < 0 || n_ids > 8) return fail(QW_ERR_INVALID_ARG, "n_ids must be 0 .. 8");
+  if (top_k < 0 || top_k > 32 || top_k > m->d.V) return fail(QW_ERR_INVALID_ARG, "top_k must be 0 .. min(32, vocab)");
+  if ((n_ids && (!ids || !logprobs)) || (top_k && (!top_ids || !top_logprobs)))
+    return fail(QW_ERR_INVALID_ARG, "null pointer");
+  for (int i = 0; i < n_ids; ++i)
+    if (ids[i] < 0 || ids[i] >= m->d.V) return fail(QW_ERR_TOKEN_RANGE, "token id outside [0, vocab)");
+  // one row: ids [8] | logprobs [8] | ranks [8] | entropy | top ids [32] | top logprobs [32]
+  struct Row {
+    int32_t ids[8];
+    float logprobs[8];
+    int32_t ranks[8];
+    float entropy;
+    int32_t top_ids[32];
+    float top_logprobs[32];
+  };
+  constexpr size_t ws_at = (sizeof(Row) + 255) / 256 * 256;
+  const size_t ws_bytes = qw_op_token_logprobs_workspace(1, m->d.V, 32);
+  if (!m->lp_block) {
+    QW_CUDA(cudaMalloc(&m->lp_block, ws_at + ws_bytes));
+    const cudaError_t e = cudaMemset(m->lp_block, 0, ws_at + ws_bytes);
+    if (e) return cuda_fail(e, "cudaMemset");
+  }
+  Row* r = (Row*)m->lp_block;
+  Row h{};
+  if (n_ids) std::memcpy(h.ids, ids, sizeof(int32_t) * n_ids);
+  QW_CUDA(cudaMemcpyAsync(r->ids, h.ids, sizeof h.ids, cudaMemcpyHostToDevice, m->stream));
+  qw_status st = qw_op_token_logprobs(QW_F32, 1, m->d.V, m->logits + (size_t)seq * m->d.V, m->d.V, r->ids, n_ids,
+                                      r->logprobs, r->ranks, &r->entropy, top_k, r->top_ids, r->top_logprobs,
+                                      (char*)m->lp_block + ws_at, ws_bytes, m->err, m->stream);
+  if (st) return st;
+  QW_CUDA(cudaMemcpyAsync(&h, r, sizeof h, cudaMemcpyDeviceToHost, m->stream));
+  if ((st = m->check_device_errors())) return st;
+  if (n_ids) std::memcpy(logprobs, h.logprobs, sizeof(float) * n_ids);
+  if (n_ids && ranks) std::memcpy(ranks, h.ranks, sizeof(int32_t) * n_ids);
+  if (entropy) *entropy = h.entropy;
+  if (top_k) {
+    std::memcpy(top_ids, h.top_ids, sizeof(int32_t) * top_k);
+    std::memcpy(top_logprobs, h.top_logprobs, sizeof(float) * top_k);
+  }
+  return QW_OK;
 }
 
 const int32_t* qw_tokens_device(const qw_model* m) { return m ? m->tok : nullptr; }

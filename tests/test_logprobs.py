@@ -1,0 +1,234 @@
+"""Token log probabilities, ranks, entropy and top tokens against 64-bit numpy."""
+import math
+
+import numpy as np
+import pytest
+
+import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+class Call:
+    def __init__(self, z, dtype, ids, top_k, gap=0, offset=0):
+        """z [rows][vocab] numpy; ids [rows][n_ids]; offset: elements before the first row."""
+        from qwen2_decoder_forward_decode_gb300 import binding
+        t = torch.from_numpy(np.asarray(z, dtype=np.float64)).to(ref.torch_dtype(dtype))
+        self.z = t.double().numpy()
+        self.rows, self.vocab = t.shape
+        self.dtype, self.k, self.stride, self.offset = dtype, top_k, self.vocab + gap, offset
+        buf = torch.full((offset + self.rows * self.stride,), float("inf"), dtype=t.dtype)  # gaps that must not count
+        buf[offset:].view(self.rows, self.stride)[:, :self.vocab] = t
+        self.buf = buf.cuda()
+        self.ids = np.asarray(ids, dtype=np.int32).reshape(self.rows, -1)
+        self.n_ids = self.ids.shape[1]
+        self.tids = torch.from_numpy(self.ids).cuda()
+        full = lambda *s, d=torch.float32: torch.full(s, 55, dtype=d, device="cuda")  # noqa: E731
+        self.lp, self.ranks, self.ent = full(self.rows + 1, max(self.n_ids, 1)), full(self.rows + 1, max(self.n_ids, 1), d=torch.int32), full(self.rows + 1)
+        self.top_ids, self.top_lp = full(self.rows + 1, max(top_k, 1), d=torch.int32), full(self.rows + 1, max(top_k, 1))
+        self.ws = torch.zeros(binding.token_logprobs_workspace(self.rows, self.vocab, top_k), dtype=torch.uint8, device="cuda")
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run(self, ranks=True, entropy=True):
+        from qwen2_decoder_forward_decode_gb300 import binding
+        p = lambda t, on=True: t.data_ptr() if on else None  # noqa: E731
+        binding.token_logprobs(ref.CODE[self.dtype], self.rows, self.vocab, self.buf.data_ptr() + self.offset * self.buf.element_size(), self.stride, p(self.tids, self.n_ids), self.n_ids,
+                               p(self.lp, self.n_ids), p(self.ranks, self.n_ids and ranks), p(self.ent, entropy), self.k, p(self.top_ids, self.k), p(self.top_lp, self.k), self.ws.data_ptr(),
+                               self.ws.numel(), self.err.data_ptr(), torch.cuda.current_stream().cuda_stream)
+
+    def check(self, err=0, ranks=True, entropy=True):
+        torch.cuda.synchronize()
+        assert int(self.err) == err
+        n = self.rows
+        lp, rk, ent, ti, tl = (t.cpu().numpy() for t in (self.lp, self.ranks, self.ent, self.top_ids, self.top_lp))
+        for t in (lp, rk, ent, ti, tl):
+            assert (t[n:] == 55).all(), "written behind the last row"
+        assert ranks or (rk == 55).all()
+        assert entropy or (ent == 55).all()
+        for r in range(n):
+            z = self.z[r]
+            ids = self.ids[r]
+            in_range = (ids >= 0) & (ids < self.vocab)
+            if np.isnan(z).any() or (z == np.inf).any() or (z == -np.inf).all():
+                for i, t in enumerate(ids):
+                    assert (lp[r, i] == 0 if t == -1 else np.isnan(lp[r, i])) and (not ranks or rk[r, i] == 0)
+                assert not entropy or np.isnan(ent[r])
+                if self.k:
+                    assert (ti[r] == -1).all() and np.isnan(tl[r]).all()
+                continue
+            m = z.max()
+            e = np.exp(z - m)
+            S = e.sum()
+            lse = m + math.log(S)
+            p = e / S
+            H = -np.sum(np.where(p > 0, p * (np.maximum(z, -1e30) - lse), 0.0))
+            # S: positive terms summed in at most 400 steps on one path, at 8 standard deviations of half a
+            # step, and exponentials good to 2^-22: 8 * 20 * 2^-24 + 2^-22 = 9.8e-6; z - m, ln S and their
+            # difference: a step each
+            tol = lambda v: 1e-5 + ref.U * (abs(v - m) + abs(math.log(S)))  # noqa: E731
+            order = np.lexsort((np.arange(self.vocab), -(z + 0.0)))
+            place = np.empty(self.vocab, dtype=np.int64)
+            place[order] = np.arange(1, self.vocab + 1)
+            for i, t in enumerate(ids):
+                if not in_range[i]:
+                    assert (lp[r, i] == 0 if t == -1 else np.isnan(lp[r, i])) and (not ranks or rk[r, i] == 0)
+                    continue
+                assert lp[r, i] == z[t] if z[t] == -np.inf else abs(lp[r, i] - (z[t] - lse)) <= tol(z[t]), (r, i)
+                assert not ranks or rk[r, i] == place[t], (r, i)
+            # W / S has the relative errors of both sums, and W / S = ln S - H
+            assert not entropy or abs(ent[r] - H) <= 1e-5 * (2 + 2 * abs(H) + abs(math.log(S))), r
+            if self.k:
+                np.testing.assert_array_equal(ti[r], order[:self.k], err_msg=f"row {r}")
+                for i in range(self.k):
+                    v = z[order[i]]
+                    assert tl[r, i] == v if v == -np.inf else abs(tl[r, i] - (v - lse)) <= tol(v), (r, i)
+
+
+def logits(rng, rows, vocab, hot=6):
+    z = 2 * rng.standard_normal((rows, vocab))
+    for r in range(rows):
+        z[r, rng.integers(0, vocab, min(hot, vocab))] += 6
+    return z
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,vocab,n_ids,top_k", [
+    (1, 151936, 1, 5), (1, 151936, 8, 32), (3, 152064, 2, 20), (1, 1, 1, 1), (2, 2, 1, 2), (5, 32, 3, 32), (7, 33, 0, 32), (40, 1000, 1, 0), (33, 3001, 1, 1), (300, 257, 2, 10),
+    (2, 16384, 1, 20), (2, 16385, 1, 20), (6, 32000, 1, 20), (400, 5000, 1, 20), (1, 300001, 2, 32), (170, 32767, 5, 32),
+])
+def test_rows_match_the_definition(dtype, rows, vocab, n_ids, top_k):
+    rng = np.random.default_rng(rows + vocab)
+    z = logits(rng, rows, vocab)
+    c = Call(z, dtype, rng.integers(0, vocab, (rows, n_ids)), top_k)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("gap,offset", [(1, 0), (7, 3), (8, 8), (64, 1)])
+def test_strided_and_misaligned_rows(dtype, gap, offset):
+    rng = np.random.default_rng(gap)
+    c = Call(logits(rng, 9, 4099), dtype, rng.integers(0, 4099, (9, 2)), 12, gap, offset)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [100, 5000, 152064])
+@pytest.mark.parametrize("kind", ["equal", "two values", "ascending", "descending", "one finite", "zeros", "masked", "blocks", "late"])
+def test_ties_and_orders(dtype, vocab, kind):
+    """Rows on which a threshold for the top tokens holds badly: ties, sorted logits, mostly -inf."""
+    rng = np.random.default_rng(4)
+    j = np.arange(vocab)
+    z = {"equal": np.full(vocab, -3.25), "two values": (j % 7 == 5) * 1.0, "ascending": j / vocab * 8, "descending": -(j / vocab) * 8, "one finite": np.where(j == vocab - 2, 1.5, -np.inf),
+         "zeros": np.where(j % 2 == 0, -0.0, 0.0), "masked": np.where(j % 50 == 3, rng.standard_normal(vocab), -np.inf), "blocks": (j // 64 % 5) * 0.5,
+         "late": np.where(j >= vocab - 40, 5.0 + (j - vocab) / 64, rng.standard_normal(vocab) * 0.1)}[kind]
+    c = Call(np.stack([z, z[::-1]]), dtype, [[0, vocab - 2, vocab // 2], [vocab - 1, 1, 1]], 32)
+    c.run()
+    c.check()
+
+
+def test_rows_without_a_distribution():
+    from qwen2_decoder_forward_decode_gb300 import binding
+    rng = np.random.default_rng(0)
+    for vocab in (50, 40000):
+        z = logits(rng, 6, vocab)
+        z[1, 7] = np.nan
+        z[2, vocab - 1] = np.inf
+        z[3, :] = -np.inf
+        z[4, 5] = -np.inf
+        c = Call(z, "f32", [[3, -1]] * 6, 4)
+        c.run()
+        c.check(err=binding.DEV_NONFINITE)
+
+
+def test_ids_outside_the_vocabulary():
+    from qwen2_decoder_forward_decode_gb300 import binding
+    rng = np.random.default_rng(0)
+    c = Call(logits(rng, 3, 500), "f32", [[3, -1, 3], [-1, -1, 499], [0, 1, 2]], 4)
+    c.run()
+    c.check()
+    for bad in (500, -2, 2 ** 31 - 1, -2 ** 31):
+        c = Call(logits(rng, 2, 500), "f32", [[3, bad], [1, 2]], 4)
+        c.run()
+        c.check(err=binding.DEV_TOKEN)
+
+
+def test_optional_outputs():
+    rng = np.random.default_rng(0)
+    for n_ids, k, ranks, entropy in ((0, 0, False, True), (1, 0, False, False), (0, 3, False, False), (2, 3, True, False)):
+        c = Call(logits(rng, 4, 20000), "f32", rng.integers(0, 20000, (4, n_ids)), k)
+        c.run(ranks, entropy)
+        c.check(0, ranks and n_ids > 0, entropy)
+
+
+def test_large_values():
+    rng = np.random.default_rng(0)
+    for shift, scale in ((1e4, 1.0), (-3e4, 1.0), (0.0, 300.0)):
+        c = Call(shift + scale * rng.standard_normal((3, 30000)), "f32", rng.integers(0, 30000, (3, 1)), 20)
+        c.run()
+        c.check()
+
+
+def test_repeats_bit_by_bit_captured_and_on_another_stream():
+    rng = np.random.default_rng(1)
+    z = logits(rng, 5, 151936)
+    c = Call(z, "f32", rng.integers(0, 151936, (5, 2)), 20)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c.run()
+    c.check()
+    first = [t.clone() for t in (c.lp, c.ent, c.top_lp)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run()
+    for _ in range(3):
+        for t in (c.lp, c.ent, c.top_lp, c.ranks, c.top_ids):
+            t.fill_(55)
+        g.replay()
+        c.check()
+        assert all(torch.equal(a, b) for a, b in zip(first, (c.lp, c.ent, c.top_lp)))
+    # other logits in the same buffers: nothing is kept
+    z2 = logits(rng, 5, 151936)
+    c.buf.copy_(torch.from_numpy(z2.astype(np.float32)).reshape(-1))
+    c.z = z2.astype(np.float32).astype(np.float64)
+    g.replay()
+    c.check()
+
+
+def test_a_model_reads_the_log_probabilities_of_its_last_step():
+    from qwen2_decoder_forward_decode_gb300 import DeviceWeights, Model, QwError
+    from synth import SHAPES, make_prompt, make_weights
+    for name, dt in (("tiny", 0), ("small_bf16", 1)):
+        s = SHAPES[name]
+        m = Model(s, DeviceWeights(make_weights(s), dt), 32, max_seqs=2)
+        try:
+            with pytest.raises(QwError):
+                m.logprobs([1])  # nothing prefilled
+            t = m.prefill(make_prompt(s, 9), seq=1)
+            for _ in range(2):
+                z = m.logits(seq=1).astype(np.float64)
+                lse = z.max() + math.log(np.exp(z - z.max()).sum())
+                lp, ranks, ent, top_ids, top_lp = m.logprobs([t, 3], top_k=7, seq=1)
+                order = np.lexsort((np.arange(len(z)), -z))
+                assert top_ids.tolist() == order[:7].tolist() and top_ids[0] == t and ranks[0] == 1
+                np.testing.assert_allclose(lp, z[[t, 3]] - lse, rtol=0, atol=2e-5)
+                np.testing.assert_allclose(top_lp, z[order[:7]] - lse, rtol=0, atol=2e-5)
+                assert ranks[1] == 1 + int(np.where(order == 3)[0][0])
+                p = np.exp(z - lse)
+                assert abs(ent + (p * (z - lse)).sum()) < 1e-4
+                t = int(m.decode_step()[1])
+            for ids, k in (([s.vocab], 0), ([-1], 0), ([0] * 9, 0), ([], 33)):
+                with pytest.raises(QwError):
+                    m.logprobs(ids, top_k=k, seq=1)
+            assert m.position(1) == 11
+        finally:
+            m.close()
