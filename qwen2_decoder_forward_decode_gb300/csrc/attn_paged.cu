@@ -369,7 +369,7 @@ struct Finish {
   // the CTA's end: an announcement takes a memory fence and an atomic's round trip, about 1 us, the merge
   // of a level 2 us.
   template <int V>
-  static __device__ __noinline__ void join(const PagedAttnArgs& a, const Range& r, const Place* pend, int n, int n_hb, float* buf) {
+  static __device__ __forceinline__ void join(const PagedAttnArgs& a, const Range& r, const Place* pend, int n, int n_hb, float* buf) {
     constexpr int S4 = HB * CS / 4;
     // what is merged next: states of CTAs from, from + step, ...; the unit's first slot; its CTAs and groups
     __shared__ int s_from[2], s_step[2], s_count[2], s_first[2], s_c0[2], s_groups[2], s_last[2];
