@@ -1,136 +1,603 @@
 // Log probabilities of given tokens, with ranks, entropy and the likeliest tokens ("LLM Speedrun:
 // Architecture", Decoding: the softmax of the logits).
 //
-// With m = max z, S = sum exp(z - m) and W = sum (z - m) exp(z - m): ln p_t = z_t - m - ln S and the
-// entropy is ln S - W / S. Tokens are ordered by (logit, lower id first) as one 64-bit key.
+// Mathematics: with m = max z, S = sum exp(z - m) and W = sum (z - m) exp(z - m), ln p_t = z_t - m - ln S and the
+// entropy is ln S - W / S. A larger maximum m' turns S into S e^(m - m') and W into (W + (m - m') S) e^(m - m'),
+// so one pass with running values does. Tokens are ordered by (logit, lower id first) as one 64-bit key.
+//
+// What bounds it: each logit is read once and costs about ten instructions (one exponential among them), so HBM
+// for fp32 logits and nearly so for 16-bit ones.
+//   - All rows' batches (NT threads x 8 vectors of 16 bytes) form one list, cut into equal consecutive ranges,
+//     one per CTA, four CTAs an SM: their loads overlap each other's arithmetic. A row that a cut divides
+//     is joined by the last of its CTAs to arrive; every sum's order is fixed, results repeat bit by bit.
+//   - A batch stays in registers for all passes: vector maxima, exponentials, counts for the ranks, top tokens.
+//   - Top tokens: a shared-memory list of the best so far gives a threshold T; only logits above it are pushed, of
+//     a later batch nearly none. The first batch bounds T from below by thread maxima: if every one of the 8
+//     warps has r of them at or above a value, 8 r >= top_k logits are. Ties beyond the buffer fall back to
+//     taking the batch's largest keys one by one.
 #include "common.cuh"
 #include "op_util.h"
 
 #include <math.h>
 
+#include <algorithm>
+
 namespace qw {
 namespace {
 
-constexpr int LP_THREADS = 512;
+constexpr int LP_NT = 256, LP_NW = LP_NT / 32, LP_VPT = 8;  // threads, warps, 16-byte vectors a thread
 constexpr int LP_MAX_IDS = 8, LP_MAX_TOP = 32;
+constexpr int LP_CTAS_PER_SM = 4, LP_MAX_CTAS = 640;
+constexpr int LP_CAP = 1024;      // keys in the list and the pushed ones
+constexpr int LP_COMPACT = 64;    // pushed keys that are worth a new threshold
+constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
+typedef unsigned long long u64;
+
+struct LogprobPart {  // of a row that several CTAs share
+  float m, s, w;
+  int nan;
+  int above[LP_MAX_IDS];
+  int n, pad[3];
+  u64 key[LP_MAX_TOP];
+};
 
 struct LogprobArgs {
   const void* logits;
   long long row_stride;
-  int n_rows, vocab, n_ids, top_k;
+  int n_rows, vocab, n_ids, top_k, batches;  // batches of a row
   const int* ids;
   float* logprobs;
   int* ranks;
   float* entropy;
   int* top_ids;
   float* top_logprobs;
+  unsigned int* counters;  // [2 * LP_MAX_CTAS], zero between calls
+  LogprobPart* parts;      // [2 * LP_MAX_CTAS]
   int* err;
 };
 
 // (logit, lower id first) as an integer; -0 counts as 0
-__device__ __forceinline__ unsigned long long order_key(float z, int j) { return argmax_key(z + 0.f, j); }
-__device__ __forceinline__ float order_key_value(unsigned long long k) {
-  const uint32_t u = (uint32_t)(k >> 32);
-  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+__device__ __forceinline__ uint32_t order_bits(float z) {
+  const uint32_t u = __float_as_uint(z + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
+__device__ __forceinline__ u64 order_key(float z, int j) { return (u64)order_bits(z) << 32 | (0xffffffffu - (uint32_t)j); }
+__device__ __forceinline__ float key_value(u64 k) { return order_value((uint32_t)(k >> 32)); }
+
+__device__ __forceinline__ float lp_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// ---- 16 bytes of logits ------------------------------------------------------------------------------------
+template <typename T> struct Logits;
+template <> struct Logits<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ uint32_t minus_inf() { return 0xff800000u; }
+  static __device__ __forceinline__ void unpack(const uint4& r, float* f) {
+    f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y); f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
+  }
+  static __device__ __forceinline__ float top(const uint4& r) {
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
+  // logits at or above thr
+  static __device__ __forceinline__ int at_least(const uint4& r, float thr) {
+    return (__uint_as_float(r.x) >= thr) + (__uint_as_float(r.y) >= thr) + (__uint_as_float(r.z) >= thr) + (__uint_as_float(r.w) >= thr);
+  }
+
+};
+template <typename T2>
+__device__ __forceinline__ T2 as_pair(uint32_t u) { return *reinterpret_cast<const T2*>(&u); }
+template <typename T, typename T2>
+struct Logits16 {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ T2 max4(const uint4& r) {
+    return __hmax2(__hmax2(as_pair<T2>(r.x), as_pair<T2>(r.y)), __hmax2(as_pair<T2>(r.z), as_pair<T2>(r.w)));
+  }
+};
+template <> struct Logits<bf16> : Logits16<bf16, __nv_bfloat162> {
+  static __device__ __forceinline__ uint32_t minus_inf() { return 0xff80ff80u; }
+  static __device__ __forceinline__ void unpack(const uint4& r, float* f) {
+    f[0] = bf_lo(r.x); f[1] = bf_hi(r.x); f[2] = bf_lo(r.y); f[3] = bf_hi(r.y);
+    f[4] = bf_lo(r.z); f[5] = bf_hi(r.z); f[6] = bf_lo(r.w); f[7] = bf_hi(r.w);
+  }
+  static __device__ __forceinline__ float top(const uint4& r) {
+    const __nv_bfloat162 m = max4(r);
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ int at_least(const uint4& r, float thr) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = reinterpret_cast<const uint32_t*>(&r)[i];
+      n += (bf_lo(u) >= thr) + (bf_hi(u) >= thr);
+    }
+    return n;
+  }
+};
+template <> struct Logits<f16> : Logits16<f16, __half2> {
+  static __device__ __forceinline__ uint32_t minus_inf() { return 0xfc00fc00u; }
+  static __device__ __forceinline__ void unpack(const uint4& r, float* f) {
+    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = __half22float2(as_pair<__half2>(u[i]));
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    }
+  }
+  static __device__ __forceinline__ float top(const uint4& r) {
+    const __half2 m = max4(r);
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ int at_least(const uint4& r, float thr) {
+    float f[8];
+    unpack(r, f);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n += f[i] >= thr;
+    return n;
+  }
+};
+
+struct Shared {
+  u64 buf[2][LP_CAP];
+  int n, side;                 // keys in buf[side]: the list, then what was pushed since
+  float t;                     // a key whose logit is not above t cannot enter the list
+  uint32_t warp_bound[LP_NW];
+  u64 warp_key[LP_NW];
+  float red[3][LP_NW];
+  int id[LP_MAX_IDS], above[LP_MAX_IDS], nan;
+  float given[LP_MAX_IDS];
+  bool last;
+};
+
+// Keeps the top_k largest of the n keys in buf[side], sorted, and their threshold. All threads; a barrier before.
+__device__ __noinline__ void compact(Shared& sh, int top_k) {
+  const int n = sh.n, side = sh.side, kept = min(n, top_k);
+  const u64* from = sh.buf[side];
+  u64* to = sh.buf[side ^ 1];
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n; i += LP_NT) {
+    const u64 key = from[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int x = 0; x < n; ++x) rank += from[x] > key;
+    if (rank < top_k) to[rank] = key;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sh.n = kept;
+    sh.side = side ^ 1;
+    sh.t = kept == top_k ? key_value(to[top_k - 1]) : -INFINITY;
+  }
+  __syncthreads();
+}
+
+// One batch of a row in registers: vector i of the thread is vector batch * LP_NT * LP_VPT + i * LP_NT + tid of
+// the row, counted from the 16-byte boundary at or before its first logit.
+template <typename T>
+struct Batch {
+  using Lg = Logits<T>;
+  static constexpr int N = Lg::N;
+  uint4 r[LP_VPT];
+  float vm[LP_VPT];  // their maxima
+  int j0;            // id of vector 0's first logit (negative where the row begins inside a vector)
+  __device__ __forceinline__ int id(int i) const { return j0 + i * LP_NT * N; }
+
+  // vector i, i known at run time only
+  __device__ __forceinline__ uint4 pick(int i) const {
+    uint4 v = r[0];
+#pragma unroll
+    for (int k = 1; k < LP_VPT; ++k)
+      if (i == k) v = r[k];
+    return v;
+  }
+
+  __device__ __forceinline__ void load(const LogprobArgs& a, int row, int batch) {
+    const T* z = (const T*)a.logits + (long long)row * a.row_stride;
+    const int shift = (int)((uintptr_t)z % 16) / (int)sizeof(T);
+    j0 = (batch * LP_NT * LP_VPT + (int)threadIdx.x) * N - shift;
+    const uint32_t none = Lg::minus_inf();
+    int ragged = 0;  // vectors that a row's ends cut
+#pragma unroll
+    for (int i = 0; i < LP_VPT; ++i) {
+      const int j = id(i);
+      r[i] = make_uint4(none, none, none, none);
+      if (j >= 0 && j + N <= a.vocab) r[i] = ld_stream(z + j);
+      else if (j > -N && j < a.vocab) ragged |= 1 << i;
+    }
+#pragma unroll 1
+    for (; ragged; ragged &= ragged - 1) {
+      const int i = __ffs(ragged) - 1, j = id(i);
+      uint32_t u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = none;
+#pragma unroll 1
+      for (int e = max(0, -j); e < min(N, a.vocab - j); ++e) {
+        const int k = sizeof(T) == 4 ? e : e / 2;
+        uint32_t x = k == 0 ? u[0] : k == 1 ? u[1] : k == 2 ? u[2] : u[3];
+        if (sizeof(T) == 4) x = reinterpret_cast<const uint32_t*>(z)[j + e];
+        else x = (x & (e & 1 ? 0x0000ffffu : 0xffff0000u)) | (uint32_t) reinterpret_cast<const uint16_t*>(z)[j + e] << (e & 1 ? 16 : 0);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (n == k) u[n] = x;
+      }
+#pragma unroll
+      for (int k = 0; k < LP_VPT; ++k)
+        if (k == i) r[k] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  }
+};
+
+// f(logit, id) for each logit of a vector
+template <typename T, typename F>
+__device__ __forceinline__ void each_logit(uint4 v, int id, F f) {
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      f(__uint_as_float(v.x), id + k);
+    } else {
+      float x[8];
+      Logits<T>::unpack(v, x);
+      f(x[0], id + 2 * k);
+      f(x[1], id + 2 * k + 1);
+    }
+    v = make_uint4(v.y, v.z, v.w, v.x);
+  }
+}
+
+// The batch's keys above the list's threshold go to the list, which holds n0 keys (the same for all threads, who
+// all call this; top_k > 0).
+template <typename T>
+__device__ __forceinline__ void push_batch(Shared& sh, const Batch<T>& b, float tmax, int top_k, int& n0) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float t = sh.t;  // (changes in compact() only)
+#pragma unroll 1
+  for (int attempt = t == -INFINITY; attempt < 2; ++attempt) {
+    if (attempt == 1) {  // a bound from the thread maxima: the r-th largest of every warp
+      uint32_t key = order_bits(tmax), bound = 0;
+#pragma unroll 1
+      for (int r = (top_k + LP_NW - 1) / LP_NW; r; --r) {
+        bound = __reduce_max_sync(0xffffffffu, key);
+        if (lane == __ffs(__ballot_sync(0xffffffffu, key == bound)) - 1) key = 0;
+      }
+      if (lane == 0) sh.warp_bound[warp] = bound;
+      __syncthreads();
+      bound = sh.warp_bound[0];
+#pragma unroll
+      for (int w = 1; w < LP_NW; ++w) bound = min(bound, sh.warp_bound[w]);
+      // the value below the bound, so that "above t" takes the bound in (-inf where the bound is -inf)
+      const float below = order_value(bound) > -INFINITY ? order_value(bound == 0x80000000u ? 0x7ffffffeu : bound - 1) : -INFINITY;
+      t = fmaxf(t, below);
+    }
+    int hits = 0;  // vectors with a logit above t
+#pragma unroll
+    for (int i = 0; i < LP_VPT; ++i) hits |= (b.vm[i] > t) << i;
+#pragma unroll 1
+    for (; hits; hits &= hits - 1) {
+      const int i = __ffs(hits) - 1;
+      each_logit<T>(b.pick(i), b.id(i), [&](float x, int j) {
+        if (x > t) {
+          const int at = atomicAdd(&sh.n, 1);
+          if (at < LP_CAP) sh.buf[sh.side][at] = order_key(x, j);
+        }
+      });
+    }
+    __syncthreads();
+    const int n = sh.n;
+    __syncthreads();  // (the next batch's first pushes wait for everyone's look at n)
+    if (n <= LP_CAP) {
+      const bool shrink = n > top_k && (n0 == 0 || n >= n0 + LP_COMPACT || n > LP_CAP / 2);
+      if (shrink) compact(sh, top_k);
+      n0 = shrink ? top_k : n;
+      return;
+    }
+    if (threadIdx.x == 0) sh.n = n0;  // too many: forget them
+    __syncthreads();
+  }
+  // ties, mostly: the batch's top_k largest keys above t, one by one
+  u64 last = ~0ull;
+#pragma unroll 1
+  for (int k = 0; k < top_k; ++k) {
+    u64 best = 0;
+#pragma unroll 1
+    for (int i = 0; i < LP_VPT; ++i)
+      each_logit<T>(b.pick(i), b.id(i), [&](float x, int j) {
+        const u64 key = order_key(x, j);
+        if (x > t && key < last && key > best) best = key;
+      });
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const u64 other = __shfl_xor_sync(0xffffffffu, best, o);
+      best = other > best ? other : best;
+    }
+    if (lane == 0) sh.warp_key[warp] = best;
+    __syncthreads();
+    best = sh.warp_key[0];
+#pragma unroll
+    for (int w = 1; w < LP_NW; ++w) best = sh.warp_key[w] > best ? sh.warp_key[w] : best;
+    if (best && threadIdx.x == 0 && sh.n < LP_CAP) sh.buf[sh.side][sh.n++] = best;
+    last = best;
+    __syncthreads();
+    if (!best) break;
+  }
+  const int n = sh.n;
+  __syncthreads();
+  if (n > top_k) compact(sh, top_k);
+  n0 = min(n, top_k);
+}
+
+// Writes a row's results from its state (the list sorted in sh). All threads.
+template <typename T>
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, Shared& sh, int row, float m, float s, float w, bool nan) {
+  const int tid = threadIdx.x;
+  const bool odd = nan || s != s || !(m < INFINITY) || m == -INFINITY;  // no distribution
+  const float ln_s = odd ? NAN : logf(s);
+  if (tid == 0) {
+    if (odd) atomicOr(a.err, ERR_NONFINITE);
+    if (a.entropy) a.entropy[row] = odd ? NAN : ln_s - w * LP_LN2 / s;
+  }
+  if (tid < a.n_ids) {
+    const int t = sh.id[tid];
+    const bool in = t >= 0 && t < a.vocab;
+    if (!in && t != -1) atomicOr(a.err, ERR_TOKEN);
+    a.logprobs[(size_t)row * a.n_ids + tid] = t == -1 ? 0.f : odd || !in ? NAN : sh.given[tid] - m - ln_s;
+    if (a.ranks) a.ranks[(size_t)row * a.n_ids + tid] = odd || !in ? 0 : 1 + sh.above[tid];
+  }
+  if (tid < a.top_k && (odd || tid < sh.n)) {
+    const u64 key = odd ? 0 : sh.buf[sh.side][tid];
+    a.top_ids[(size_t)row * a.top_k + tid] = odd ? -1 : argmax_key_index(key);
+    a.top_logprobs[(size_t)row * a.top_k + tid] = odd ? NAN : key_value(key) - m - ln_s;
+  }
+  if (!odd && sh.n < a.top_k && tid == 0) {  // fewer finite logits: the lowest ids of probability 0
+    const T* z = (const T*)a.logits + (long long)row * a.row_stride;
+    int k = sh.n;
+#pragma unroll 1
+    for (int j = 0; j < a.vocab && k < a.top_k; ++j) {
+      if (to_f32(z[j]) == -INFINITY) {
+        a.top_ids[(size_t)row * a.top_k + k] = j;
+        a.top_logprobs[(size_t)row * a.top_k + k] = -INFINITY;
+        ++k;
+      }
+    }
+  }
+}
+
+// One CTA's range of the list of batches.
+template <typename T>
+__global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const LogprobArgs a) {
+  constexpr int N = Batch<T>::N;
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int total = a.n_rows * a.batches, each = total / (int)gridDim.x, rest = total - each * (int)gridDim.x;
+  auto cut = [&](int c) { return each * c + min(c, rest); };
+  int at = cut(blockIdx.x);
+  const int end = cut(blockIdx.x + 1);
+#pragma unroll 1
+  while (at < end) {
+    const int row = at / a.batches, b0 = at - row * a.batches, b1 = min(a.batches, b0 + end - at);
+    Batch<T> b;
+    b.load(a, row, b0);
+    if (tid < a.n_ids) {
+      const int t = a.ids[(size_t)row * a.n_ids + tid];
+      const T* z = (const T*)a.logits + (long long)row * a.row_stride;
+      float given = NAN;
+      int equal = 0;  // before t in its vector
+      if (t >= 0 && t < a.vocab) {
+        given = to_f32(z[t]);
+        const int shift = (int)((uintptr_t)z % 16) / (int)sizeof(T), vec = (t + shift) / N, batch = vec / (LP_NT * LP_VPT);
+        if (batch >= b0 && batch < b1)
+#pragma unroll 1
+          for (int j = max(0, vec * N - shift); j < t; ++j) equal += to_f32(z[j]) == given;
+        if (given == -INFINITY && b0 == 0 && vec > 0) equal -= shift;  // what fills the first vector is counted too
+      }
+      sh.id[tid] = t;
+      sh.above[tid] = equal;
+      sh.given[tid] = given;
+    }
+    if (tid == 0) {
+      sh.n = 0;
+      sh.side = 0;
+      sh.t = -INFINITY;
+      sh.nan = 0;
+    }
+    __syncthreads();
+    float m = -INFINITY, s = 0.f, w = 0.f;  // this thread's, w in base 2
+    bool nan = false;
+    int listed = 0;  // keys in the list
+#pragma unroll 1
+    for (int batch = b0; batch < b1; ++batch) {
+      if (batch > b0) b.load(a, row, batch);
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < LP_VPT; ++i) {
+        b.vm[i] = Batch<T>::Lg::top(b.r[i]);
+        top = fmaxf(top, b.vm[i]);
+      }
+      if (top > m) {
+        const float d = (m - top) * LP_LOG2E, f = lp_ex2(d);
+        w = m == -INFINITY ? 0.f : fmaf(d, s, w) * f;
+        s = m == -INFINITY ? 0.f : s * f;
+        m = top;
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      float s1 = 0.f, w1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < LP_VPT; ++i) {
+        float x[N];
+        Batch<T>::Lg::unpack(b.r[i], x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float d = max_nan((x[e] - ref) * LP_LOG2E, -126.f);  // (-inf: 2^-126, nothing next to the maximum's 1)
+          const float p = lp_ex2(d);
+          if (e & 1) {
+            s1 += p;
+            w1 = fmaf(d, p, w1);
+          } else {
+            s += p;
+            w = fmaf(d, p, w);
+          }
+        }
+      }
+      s += s1;
+      w += w1;
+      nan |= s != s;
+      if (a.ranks) {
+#pragma unroll 1
+        for (int q = 0; q < a.n_ids; ++q) {
+          const int t = sh.id[q];
+          const float z = sh.given[q];
+          // whole vectors before t count from z on, the others from the next larger value on; equal logits
+          // before t in its own vector were counted when the row began
+          const uint32_t bits = order_bits(z);
+          const float next = order_value(bits == 0x80000000u ? 0x80000001u : bits + 1);
+          int above = 0;
+#pragma unroll
+          for (int i = 0; i < LP_VPT; ++i) above += Batch<T>::Lg::at_least(b.r[i], b.id(i) + N <= t ? z : next);
+          above = __reduce_add_sync(0xffffffffu, above);
+          if (lane == 0 && above) atomicAdd(&sh.above[q], above);
+        }
+      }
+      if (a.top_k) push_batch(sh, b, top, a.top_k, listed);
+    }
+    // the CTA's state of the row
+    __syncthreads();
+    if (a.top_k && sh.n) compact(sh, a.top_k);
+    float mm = warp_max(m);
+    if (lane == 0) sh.red[0][warp] = mm;
+    if (nan) sh.nan = 1;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < LP_NW; ++i) mm = fmaxf(mm, sh.red[0][i]);
+    {
+      const float d = m == -INFINITY ? 0.f : (m - mm) * LP_LOG2E, f = m == -INFINITY ? 0.f : lp_ex2(d);
+      w = warp_sum(fmaf(d, s, w) * f);
+      s = warp_sum(s * f);
+    }
+    if (lane == 0) {
+      sh.red[1][warp] = s;
+      sh.red[2][warp] = w;
+    }
+    __syncthreads();
+    s = w = 0.f;
+#pragma unroll
+    for (int i = 0; i < LP_NW; ++i) {
+      s += sh.red[1][i];
+      w += sh.red[2][i];
+    }
+    nan = sh.nan;
+    bool write = b1 - b0 == a.batches;
+    if (!write) {
+      // part slots as the list is cut: 2 c for the row a CTA begins with, 2 c + 1 for one that it begins itself
+      const int r0 = row * a.batches;
+      auto cta_of = [&](int x) {
+        const int big = rest * (each + 1);
+        return x < big ? x / (each + 1) : rest + (x - big) / each;
+      };
+      const int c0 = cta_of(r0), c1 = cta_of(r0 + a.batches - 1), first = 2 * c0 + (cut(c0) < r0 ? 1 : 0);
+      auto slot_of = [&](int c) { return a.parts + (c == c0 ? first : 2 * c); };
+      LogprobPart* mine = slot_of(blockIdx.x);
+      if (tid == 0) {
+        mine->m = mm;
+        mine->s = s;
+        mine->w = w;
+        mine->nan = nan;
+        mine->n = sh.n;
+      }
+      if (tid < a.n_ids) mine->above[tid] = sh.above[tid];
+      if (tid < sh.n) mine->key[tid] = sh.buf[sh.side][tid];
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        sh.last = atomicAdd(a.counters + first, 1u) == (unsigned)(c1 - c0);
+        if (sh.last) a.counters[first] = 0u;
+        __threadfence();
+        sh.n = 0;
+        sh.nan = 0;
+      }
+      if (tid < a.n_ids) sh.above[tid] = 0;
+      __syncthreads();
+      write = sh.last;
+      if (write) {
+        // every thread takes the parts c0 + tid, + LP_NT, ...: the same order of sums at every run
+        mm = -INFINITY;
+#pragma unroll 1
+        for (int c = c0 + tid; c <= c1; c += LP_NT) mm = fmaxf(mm, __ldcg(&slot_of(c)->m));
+        mm = warp_max(mm);
+        if (lane == 0) sh.red[0][warp] = mm;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < LP_NW; ++i) mm = fmaxf(mm, sh.red[0][i]);
+        s = w = 0.f;
+#pragma unroll 1
+        for (int c = c0 + tid; c <= c1; c += LP_NT) {
+          const LogprobPart* p = slot_of(c);
+          const float pm = __ldcg(&p->m), ps = __ldcg(&p->s), pw = __ldcg(&p->w);
+          if (__ldcg(&p->nan)) sh.nan = 1;
+          if (pm > -INFINITY) {
+            const float d = (pm - mm) * LP_LOG2E, f = lp_ex2(d);
+            w = fmaf(fmaf(d, ps, pw), f, w);
+            s = fmaf(ps, f, s);
+          }
+#pragma unroll 1
+          for (int q = 0; q < a.n_ids; ++q) {
+            const int n = __ldcg(&p->above[q]);
+            if (n) atomicAdd(&sh.above[q], n);
+          }
+        }
+        s = warp_sum(s);
+        w = warp_sum(w);
+        if (lane == 0) {
+          sh.red[1][warp] = s;
+          sh.red[2][warp] = w;
+        }
+        __syncthreads();
+        s = w = 0.f;
+#pragma unroll
+        for (int i = 0; i < LP_NW; ++i) {
+          s += sh.red[1][i];
+          w += sh.red[2][i];
+        }
+        nan = sh.nan;
+        // the parts' lists, so many at a time that they fit next to the best ones
+        const int step = (LP_CAP - LP_MAX_TOP) / LP_MAX_TOP;
+#pragma unroll 1
+        for (int c = c0; a.top_k && c <= c1; c += step) {
+          const int n = min(step, c1 - c + 1);
+#pragma unroll 1
+          for (int i = tid; i < n * LP_MAX_TOP; i += LP_NT) {
+            const LogprobPart* p = slot_of(c + i / LP_MAX_TOP);
+            if (i % LP_MAX_TOP < __ldcg(&p->n)) sh.buf[sh.side][atomicAdd(&sh.n, 1)] = __ldcg(&p->key[i % LP_MAX_TOP]);
+          }
+          __syncthreads();
+          compact(sh, a.top_k);
+        }
+      }
+    }
+    if (write) finish_row<T>(a, sh, row, mm, s, w, nan);
+    __syncthreads();
+    at += b1 - b0;
+  }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(LP_THREADS) logprob_kernel(const LogprobArgs a) {
-  __shared__ float red[32];
-  __shared__ unsigned long long kred[32];
-  __shared__ int ired[32];
-  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = LP_THREADS / 32;
-  const T* z = (const T*)a.logits + (size_t)row * a.row_stride;
-  float m = -INFINITY;
-  int odd = 0;  // a NaN or +inf in the row
-  for (int j = tid; j < a.vocab; j += LP_THREADS) {
-    const float x = to_f32(z[j]);
-    if (!(x < INFINITY)) odd = 1;
-    m = fmaxf(m, x);
-  }
-  m = warp_max(m);
-  odd = __syncthreads_or(odd);
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-  for (int w = 0; w < nw; ++w) m = fmaxf(m, red[w]);
-  if (odd || m == -INFINITY) {  // no distribution
-    if (tid == 0) atomicOr(a.err, ERR_NONFINITE);
-    for (int i = tid; i < a.n_ids; i += LP_THREADS) {
-      const int t = a.ids[(size_t)row * a.n_ids + i];
-      a.logprobs[(size_t)row * a.n_ids + i] = t == -1 ? 0.f : NAN;
-      if (a.ranks) a.ranks[(size_t)row * a.n_ids + i] = 0;
-      if (t < -1 || t >= a.vocab) atomicOr(a.err, ERR_TOKEN);
-    }
-    if (tid == 0 && a.entropy) a.entropy[row] = NAN;
-    for (int i = tid; i < a.top_k; i += LP_THREADS) {
-      a.top_ids[(size_t)row * a.top_k + i] = -1;
-      a.top_logprobs[(size_t)row * a.top_k + i] = NAN;
-    }
-    return;
-  }
-  float S = 0.f, W = 0.f;
-  for (int j = tid; j < a.vocab; j += LP_THREADS) {
-    const float d = to_f32(z[j]) - m;
-    const float e = expf(d);
-    S += e;
-    if (e > 0.f) W = fmaf(d, e, W);
-  }
-  S = block_sum(S, red);
-  W = block_sum(W, red);
-  const float ln_s = logf(S);
-  if (tid == 0 && a.entropy) a.entropy[row] = ln_s - W / S;
-  for (int i = 0; i < a.n_ids; ++i) {
-    const int t = a.ids[(size_t)row * a.n_ids + i];
-    if (t < 0 || t >= a.vocab) {
-      if (tid == 0) {
-        if (t != -1) atomicOr(a.err, ERR_TOKEN);
-        a.logprobs[(size_t)row * a.n_ids + i] = t == -1 ? 0.f : NAN;
-        if (a.ranks) a.ranks[(size_t)row * a.n_ids + i] = 0;
-      }
-      continue;
-    }
-    const float zt = to_f32(z[t]);
-    if (tid == 0) a.logprobs[(size_t)row * a.n_ids + i] = zt - m - ln_s;
-    if (!a.ranks) continue;
-    int above = 0;
-    for (int j = tid; j < a.vocab; j += LP_THREADS) {
-      const float x = to_f32(z[j]);
-      above += x > zt || (x == zt && j < t);
-    }
-    above = __reduce_add_sync(0xffffffffu, above);
-    __syncthreads();
-    if (lane == 0) ired[warp] = above;
-    __syncthreads();
-    if (tid == 0) {
-      int r = 1;
-      for (int w = 0; w < nw; ++w) r += ired[w];
-      a.ranks[(size_t)row * a.n_ids + i] = r;
-    }
-  }
-  unsigned long long last = ~0ull;  // the key taken before: the next is the largest below it
-  for (int k = 0; k < a.top_k; ++k) {
-    unsigned long long best = 0;
-    for (int j = tid; j < a.vocab; j += LP_THREADS) {
-      const unsigned long long key = order_key(to_f32(z[j]), j);
-      if (key < last && key > best) best = key;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
-      best = other > best ? other : best;
-    }
-    __syncthreads();
-    if (lane == 0) kred[warp] = best;
-    __syncthreads();
-    best = kred[0];
-    for (int w = 1; w < nw; ++w) best = kred[w] > best ? kred[w] : best;
-    last = best;
-    if (tid == 0) {
-      a.top_ids[(size_t)row * a.top_k + k] = argmax_key_index(best);
-      a.top_logprobs[(size_t)row * a.top_k + k] = order_key_value(best) - m - ln_s;
-    }
-  }
+cudaError_t launch_logprobs(LogprobArgs a, int nsm, cudaStream_t s) {
+  constexpr int N = Logits<T>::N;
+  // the first vector may begin before the row, by up to N - 1 logits
+  a.batches = (int)(((long long)a.vocab + N - 1 + LP_NT * LP_VPT * N - 1) / (LP_NT * LP_VPT * N));
+  const long long total = (long long)a.n_rows * a.batches;
+  const int grid = (int)std::min<long long>(total, std::min(nsm * LP_CTAS_PER_SM, LP_MAX_CTAS));
+  return launch_k(logprob_kernel<T>, dim3(grid), dim3(LP_NT), 0, s, false, a);
 }
+constexpr size_t LP_COUNTER_BYTES = 2 * LP_MAX_CTAS * sizeof(unsigned int);
 
 }  // namespace
 }  // namespace qw
@@ -141,7 +608,7 @@ extern "C" {
 
 size_t qw_op_token_logprobs_workspace(int32_t n_rows, int32_t vocab, int32_t top_k) {
   if (n_rows < 0 || vocab < 1 || top_k < 0 || top_k > LP_MAX_TOP) return 0;
-  return 256;
+  return LP_COUNTER_BYTES + 2 * LP_MAX_CTAS * sizeof(LogprobPart);
 }
 
 qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t vocab, const void* logits,
@@ -155,6 +622,9 @@ qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t voc
   if (top_k < 0 || top_k > LP_MAX_TOP || top_k > vocab)
     return op_fail(QW_ERR_INVALID_ARG, "top_k must be 0 .. min(32, vocab)");
   if (row_stride < vocab || row_stride > (int64_t)1 << 40) return op_fail(QW_ERR_INVALID_ARG, "row_stride smaller than a row");
+  // the list of batches (of at least 8192 logits) has 31-bit numbers, and so have ids with a batch's overhang
+  if ((int64_t)n_rows * (vocab / 8192 + 2) > 0x7fffffffll || vocab > 0x7fff0000)
+    return op_fail(QW_ERR_UNSUPPORTED, "n_rows * vocab too large");
   if (n_rows == 0) return QW_OK;
   if (!logits || !err_dev || !workspace || (n_ids && (!ids || !logprobs)) || (top_k && (!top_ids || !top_logprobs)))
     return op_fail(QW_ERR_INVALID_ARG, "null pointer");
@@ -166,13 +636,15 @@ qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t voc
                                   entropy, top_k ? top_ids : nullptr, top_k ? top_logprobs : nullptr, workspace,
                                   err_dev});
   if (st) return st;
-  LogprobArgs a{logits, row_stride, n_rows, vocab, n_ids, top_k, ids, logprobs, ranks, entropy, top_ids,
-                top_logprobs, err_dev};
+  int dev = 0, nsm = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) || (e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)))
+    return op_cuda_fail(e, "device query");
+  const LogprobArgs a{logits, row_stride, n_rows, vocab, n_ids, top_k, 0, ids, logprobs, ranks, entropy, top_ids,
+                      top_logprobs, (unsigned int*)workspace, (LogprobPart*)((char*)workspace + LP_COUNTER_BYTES), err_dev};
   cudaStream_t s = (cudaStream_t)cuda_stream;
-  const dim3 grid(n_rows), block(LP_THREADS);
-  const cudaError_t e = logits_dtype == QW_F32   ? launch_k(logprob_kernel<float>, grid, block, 0, s, false, a)
-                        : logits_dtype == QW_F16 ? launch_k(logprob_kernel<f16>, grid, block, 0, s, false, a)
-                                                 : launch_k(logprob_kernel<bf16>, grid, block, 0, s, false, a);
+  e = logits_dtype == QW_F32   ? launch_logprobs<float>(a, nsm, s)
+      : logits_dtype == QW_F16 ? launch_logprobs<f16>(a, nsm, s) : launch_logprobs<bf16>(a, nsm, s);
   if (e) return op_cuda_fail(e, "token logprobs launch");
   return QW_OK;
 }
