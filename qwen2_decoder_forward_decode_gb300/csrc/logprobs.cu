@@ -65,11 +65,6 @@ __device__ __forceinline__ float order_value(uint32_t u) { return __uint_as_floa
 __device__ __forceinline__ u64 order_key(float z, int j) { return (u64)order_bits(z) << 32 | (0xffffffffu - (uint32_t)j); }
 __device__ __forceinline__ float key_value(u64 k) { return order_value((uint32_t)(k >> 32)); }
 
-__device__ __forceinline__ float lp_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
@@ -77,73 +72,83 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
 }
 
 // ---- 16 bytes of logits ------------------------------------------------------------------------------------
+//
+// pair(u): the logits of word u (two for 16-bit types) as packed fp32, with -inf raised to a finite value whose
+// exponential is 0 (so that d * exp(d) is 0 as well); a NaN stays.
+constexpr float LP_FLOOR = -1e38f;  // (finite after the product with log2 e)
 template <typename T> struct Logits;
 template <> struct Logits<float> {
   static constexpr int N = 4;
   static __device__ __forceinline__ uint32_t minus_inf() { return 0xff800000u; }
-  static __device__ __forceinline__ void unpack(const uint4& r, float* f) {
-    f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y); f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
-  }
   static __device__ __forceinline__ float top(const uint4& r) {
     return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
   }
-  // logits at or above thr
-  static __device__ __forceinline__ int at_least(const uint4& r, float thr) {
-    return (__uint_as_float(r.x) >= thr) + (__uint_as_float(r.y) >= thr) + (__uint_as_float(r.z) >= thr) + (__uint_as_float(r.w) >= thr);
+  static __device__ __forceinline__ void pairs(const uint4& r, f32x2* p) {
+    p[0] = pack2(max_nan(__uint_as_float(r.x), LP_FLOOR), max_nan(__uint_as_float(r.y), LP_FLOOR));
+    p[1] = pack2(max_nan(__uint_as_float(r.z), LP_FLOOR), max_nan(__uint_as_float(r.w), LP_FLOOR));
   }
-
+  // counts of logits at or above a threshold, a vector at a time
+  struct Count {
+    int n = 0;
+    __device__ __forceinline__ void add(const uint4& r, float thr) {
+      n += (__uint_as_float(r.x) >= thr) + (__uint_as_float(r.y) >= thr) + (__uint_as_float(r.z) >= thr) + (__uint_as_float(r.w) >= thr);
+    }
+    __device__ __forceinline__ int total() const { return n; }
+  };
+  typedef float Thr;
+  static __device__ __forceinline__ Thr thr(float z) { return z; }
+  static __device__ __forceinline__ Thr thr_above(float z) {  // the next larger value
+    const uint32_t bits = order_bits(z);
+    return order_value(bits == 0x80000000u ? 0x80000001u : bits + 1);
+  }
 };
 template <typename T2>
 __device__ __forceinline__ T2 as_pair(uint32_t u) { return *reinterpret_cast<const T2*>(&u); }
+// the next larger value of a 16-bit float's bits (0 and -0: the smallest positive one)
+__device__ __forceinline__ uint32_t next16(uint32_t b) { return (b & 0x7fff) == 0 ? 1u : b & 0x8000 ? b - 1 : b + 1; }
 template <typename T, typename T2>
 struct Logits16 {
   static constexpr int N = 8;
-  static __device__ __forceinline__ T2 max4(const uint4& r) {
-    return __hmax2(__hmax2(as_pair<T2>(r.x), as_pair<T2>(r.y)), __hmax2(as_pair<T2>(r.z), as_pair<T2>(r.w)));
+  static __device__ __forceinline__ float top(const uint4& r) {
+    const T2 m = __hmax2(__hmax2(as_pair<T2>(r.x), as_pair<T2>(r.y)), __hmax2(as_pair<T2>(r.z), as_pair<T2>(r.w)));
+    return fmaxf(__low2float(m), __high2float(m));
   }
+  // packed counts: exact, a thread's are at most 4 LP_VPT a lane
+  struct Count {
+    T2 n = as_pair<T2>(0u);
+    __device__ __forceinline__ void add(const uint4& r, T2 thr) {
+      n = __hadd2(n, __hadd2(__hadd2(__hge2(as_pair<T2>(r.x), thr), __hge2(as_pair<T2>(r.y), thr)),
+                             __hadd2(__hge2(as_pair<T2>(r.z), thr), __hge2(as_pair<T2>(r.w), thr))));
+    }
+    __device__ __forceinline__ int total() const { return (int)(__low2float(n) + __high2float(n)); }
+  };
+  typedef T2 Thr;
+  static __device__ __forceinline__ uint32_t bits(float z) {
+    const T h = from_f32<T>(z);
+    return *reinterpret_cast<const uint16_t*>(&h);
+  }
+  static __device__ __forceinline__ T2 thr(float z) { return as_pair<T2>(bits(z) * 0x10001u); }
+  static __device__ __forceinline__ T2 thr_above(float z) { return as_pair<T2>(next16(bits(z)) * 0x10001u); }
 };
 template <> struct Logits<bf16> : Logits16<bf16, __nv_bfloat162> {
   static __device__ __forceinline__ uint32_t minus_inf() { return 0xff80ff80u; }
-  static __device__ __forceinline__ void unpack(const uint4& r, float* f) {
-    f[0] = bf_lo(r.x); f[1] = bf_hi(r.x); f[2] = bf_lo(r.y); f[3] = bf_hi(r.y);
-    f[4] = bf_lo(r.z); f[5] = bf_hi(r.z); f[6] = bf_lo(r.w); f[7] = bf_hi(r.w);
+  static __device__ __forceinline__ f32x2 pair(uint32_t u) {
+    const __nv_bfloat162 h = __hmax2_nan(as_pair<__nv_bfloat162>(u), __float2bfloat162_rn(LP_FLOOR));
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(&h);
+    return pack2(bf_lo(v), bf_hi(v));
   }
-  static __device__ __forceinline__ float top(const uint4& r) {
-    const __nv_bfloat162 m = max4(r);
-    return fmaxf(__low2float(m), __high2float(m));
-  }
-  static __device__ __forceinline__ int at_least(const uint4& r, float thr) {
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t u = reinterpret_cast<const uint32_t*>(&r)[i];
-      n += (bf_lo(u) >= thr) + (bf_hi(u) >= thr);
-    }
-    return n;
+  static __device__ __forceinline__ void pairs(const uint4& r, f32x2* p) {
+    p[0] = pair(r.x); p[1] = pair(r.y); p[2] = pair(r.z); p[3] = pair(r.w);
   }
 };
 template <> struct Logits<f16> : Logits16<f16, __half2> {
   static __device__ __forceinline__ uint32_t minus_inf() { return 0xfc00fc00u; }
-  static __device__ __forceinline__ void unpack(const uint4& r, float* f) {
-    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = __half22float2(as_pair<__half2>(u[i]));
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
-    }
+  static __device__ __forceinline__ f32x2 pair(uint32_t u) {
+    const float2 t = __half22float2(__hmax2_nan(as_pair<__half2>(u), __float2half2_rn(-65504.f)));
+    return pack2(t.x, t.y);
   }
-  static __device__ __forceinline__ float top(const uint4& r) {
-    const __half2 m = max4(r);
-    return fmaxf(__low2float(m), __high2float(m));
-  }
-  static __device__ __forceinline__ int at_least(const uint4& r, float thr) {
-    float f[8];
-    unpack(r, f);
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) n += f[i] >= thr;
-    return n;
+  static __device__ __forceinline__ void pairs(const uint4& r, f32x2* p) {
+    p[0] = pair(r.x); p[1] = pair(r.y); p[2] = pair(r.z); p[3] = pair(r.w);
   }
 };
 
@@ -151,7 +156,6 @@ struct Shared {
   u64 buf[2][LP_CAP];
   int n, side;                 // keys in buf[side]: the list, then what was pushed since
   float t;                     // a key whose logit is not above t cannot enter the list
-  uint32_t warp_bound[LP_NW];
   u64 warp_key[LP_NW];
   float red[3][LP_NW];
   int id[LP_MAX_IDS], above[LP_MAX_IDS], nan;
@@ -243,12 +247,12 @@ __device__ __forceinline__ void each_logit(uint4 v, int id, F f) {
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
     if constexpr (sizeof(T) == 4) {
-      f(__uint_as_float(v.x), id + k);
+      f(__uint_as_float(v.x), id++);
     } else {
-      float x[8];
-      Logits<T>::unpack(v, x);
-      f(x[0], id + 2 * k);
-      f(x[1], id + 2 * k + 1);
+      const uint32_t lo = v.x & 0xffffu, hi = v.x >> 16;
+      const uint16_t l16 = (uint16_t)lo, h16 = (uint16_t)hi;
+      f(to_f32(*reinterpret_cast<const T*>(&l16)), id++);
+      f(to_f32(*reinterpret_cast<const T*>(&h16)), id++);
     }
     v = make_uint4(v.y, v.z, v.w, v.x);
   }
@@ -262,21 +266,18 @@ __device__ __forceinline__ void push_batch(Shared& sh, const Batch<T>& b, float 
   float t = sh.t;  // (changes in compact() only)
 #pragma unroll 1
   for (int attempt = t == -INFINITY; attempt < 2; ++attempt) {
-    if (attempt == 1) {  // a bound from the thread maxima: the r-th largest of every warp
-      uint32_t key = order_bits(tmax), bound = 0;
+    if (attempt == 1) {
+      // a bound from the thread maxima, in steps of their upper 16 bits: the largest that top_k threads reach
+      const uint32_t key = order_bits(tmax) >> 16;
+      uint32_t bound = 0;
 #pragma unroll 1
-      for (int r = (top_k + LP_NW - 1) / LP_NW; r; --r) {
-        bound = __reduce_max_sync(0xffffffffu, key);
-        if (lane == __ffs(__ballot_sync(0xffffffffu, key == bound)) - 1) key = 0;
+      for (uint32_t bit = 0x8000u; bit; bit >>= 1)
+        if (__syncthreads_count(key >= (bound | bit)) >= top_k) bound |= bit;
+      if (bound > 0x7fu) {  // (else -inf is: fewer threads have a finite one)
+        bound <<= 16;
+        // the value below it, so that "above t" takes the bound in
+        t = fmaxf(t, order_value(bound == 0x80000000u ? 0x7ffffffeu : bound - 1));
       }
-      if (lane == 0) sh.warp_bound[warp] = bound;
-      __syncthreads();
-      bound = sh.warp_bound[0];
-#pragma unroll
-      for (int w = 1; w < LP_NW; ++w) bound = min(bound, sh.warp_bound[w]);
-      // the value below the bound, so that "above t" takes the bound in (-inf where the bound is -inf)
-      const float below = order_value(bound) > -INFINITY ? order_value(bound == 0x80000000u ? 0x7ffffffeu : bound - 1) : -INFINITY;
-      t = fmaxf(t, below);
     }
     int hits = 0;  // vectors with a logit above t
 #pragma unroll
@@ -295,7 +296,7 @@ __device__ __forceinline__ void push_batch(Shared& sh, const Batch<T>& b, float 
     const int n = sh.n;
     __syncthreads();  // (the next batch's first pushes wait for everyone's look at n)
     if (n <= LP_CAP) {
-      const bool shrink = n > top_k && (n0 == 0 || n >= n0 + LP_COMPACT || n > LP_CAP / 2);
+      const bool shrink = n >= top_k && (sh.t == -INFINITY || n >= n0 + LP_COMPACT || n > LP_CAP / 2);
       if (shrink) compact(sh, top_k);
       n0 = shrink ? top_k : n;
       return;
@@ -331,7 +332,7 @@ __device__ __forceinline__ void push_batch(Shared& sh, const Batch<T>& b, float 
   }
   const int n = sh.n;
   __syncthreads();
-  if (n > top_k) compact(sh, top_k);
+  if (n >= top_k) compact(sh, top_k);
   n0 = min(n, top_k);
 }
 
@@ -423,32 +424,29 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const Lo
         top = fmaxf(top, b.vm[i]);
       }
       if (top > m) {
-        const float d = (m - top) * LP_LOG2E, f = lp_ex2(d);
+        const float d = (m - top) * LP_LOG2E, f = ex2(d);
         w = m == -INFINITY ? 0.f : fmaf(d, s, w) * f;
         s = m == -INFINITY ? 0.f : s * f;
         m = top;
       }
-      const float ref = m == -INFINITY ? 0.f : m;
-      float s1 = 0.f, w1 = 0.f;
+      const f32x2 ref = pack2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m), l2e = pack2(LP_LOG2E, LP_LOG2E);
+      f32x2 s2 = pack2(s, 0.f), w2 = pack2(w, 0.f);
 #pragma unroll
       for (int i = 0; i < LP_VPT; ++i) {
-        float x[N];
-        Batch<T>::Lg::unpack(b.r[i], x);
+        f32x2 x[N / 2];
+        Batch<T>::Lg::pairs(b.r[i], x);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float d = max_nan((x[e] - ref) * LP_LOG2E, -126.f);  // (-inf: 2^-126, nothing next to the maximum's 1)
-          const float p = lp_ex2(d);
-          if (e & 1) {
-            s1 += p;
-            w1 = fmaf(d, p, w1);
-          } else {
-            s += p;
-            w = fmaf(d, p, w);
-          }
+        for (int e = 0; e < N / 2; ++e) {
+          f32x2 d = add2(x[e], ref);
+          mul2(d, l2e);
+          const float2 v = unpack2(d);
+          const f32x2 p = pack2(ex2(v.x), ex2(v.y));
+          s2 = add2(s2, p);
+          fma2(w2, d, p);
         }
       }
-      s += s1;
-      w += w1;
+      s = unpack2(s2).x + unpack2(s2).y;
+      w = unpack2(w2).x + unpack2(w2).y;
       nan |= s != s;
       if (a.ranks) {
 #pragma unroll 1
@@ -457,11 +455,11 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const Lo
           const float z = sh.given[q];
           // whole vectors before t count from z on, the others from the next larger value on; equal logits
           // before t in its own vector were counted when the row began
-          const uint32_t bits = order_bits(z);
-          const float next = order_value(bits == 0x80000000u ? 0x80000001u : bits + 1);
-          int above = 0;
+          const typename Batch<T>::Lg::Thr here = Batch<T>::Lg::thr(z), next = Batch<T>::Lg::thr_above(z);
+          typename Batch<T>::Lg::Count count;
 #pragma unroll
-          for (int i = 0; i < LP_VPT; ++i) above += Batch<T>::Lg::at_least(b.r[i], b.id(i) + N <= t ? z : next);
+          for (int i = 0; i < LP_VPT; ++i) count.add(b.r[i], b.id(i) + N <= t ? here : next);
+          int above = count.total();
           above = __reduce_add_sync(0xffffffffu, above);
           if (lane == 0 && above) atomicAdd(&sh.above[q], above);
         }
@@ -478,7 +476,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const Lo
 #pragma unroll
     for (int i = 0; i < LP_NW; ++i) mm = fmaxf(mm, sh.red[0][i]);
     {
-      const float d = m == -INFINITY ? 0.f : (m - mm) * LP_LOG2E, f = m == -INFINITY ? 0.f : lp_ex2(d);
+      const float d = m == -INFINITY ? 0.f : (m - mm) * LP_LOG2E, f = m == -INFINITY ? 0.f : ex2(d);
       w = warp_sum(fmaf(d, s, w) * f);
       s = warp_sum(s * f);
     }
@@ -543,7 +541,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const Lo
           const float pm = __ldcg(&p->m), ps = __ldcg(&p->s), pw = __ldcg(&p->w);
           if (__ldcg(&p->nan)) sh.nan = 1;
           if (pm > -INFINITY) {
-            const float d = (pm - mm) * LP_LOG2E, f = lp_ex2(d);
+            const float d = (pm - mm) * LP_LOG2E, f = ex2(d);
             w = fmaf(fmaf(d, ps, pw), f, w);
             s = fmaf(ps, f, s);
           }
