@@ -7,14 +7,16 @@
 //
 // What bounds it: each logit is read once and costs about ten instructions (one exponential among them), so HBM
 // for fp32 logits and nearly so for 16-bit ones.
-//   - All rows' batches (NT threads x 8 vectors of 16 bytes) form one list, cut into equal consecutive ranges,
-//     one per CTA, four CTAs an SM: their loads overlap each other's arithmetic. A row that a cut divides
-//     is joined by the last of its CTAs to arrive; every sum's order is fixed, results repeat bit by bit.
-//   - A batch stays in registers for all passes: vector maxima, exponentials, counts for the ranks, top tokens.
-//   - Top tokens: a shared-memory list of the best so far gives a threshold T; only logits above it are pushed, of
-//     a later batch nearly none. The first batch bounds T from below by thread maxima: if every one of the 8
-//     warps has r of them at or above a value, 8 r >= top_k logits are. Ties beyond the buffer fall back to
-//     taking the batch's largest keys one by one.
+//   - All rows' batches (256 threads x 4 vectors of 16 bytes) form one list, cut into equal consecutive ranges,
+//     one per CTA, four CTAs an SM. A row that a cut divides is joined by the last of its CTAs to arrive;
+//     every sum's order is fixed, results repeat bit by bit.
+//   - Each thread copies its own vectors (cp.async) into a ring of three batches and reads them back itself: no
+//     barrier, and up to 128 KB in flight an SM. A batch is then in registers for all passes: vector maxima,
+//     exponentials, counts for the ranks, top tokens.
+//   - Top tokens: a shared-memory list of the best so far gives a threshold T; only logits above it are pushed,
+//     without a barrier either. The warps meet (to keep the best and raise T) after a row's first batch,
+//     when the list has filled, and at the row's end. The first batch bounds T from below by the top_k-th
+//     thread maximum. A warp that finds the list full waits for a meeting and goes on where it stopped.
 #include "common.cuh"
 #include "op_util.h"
 
@@ -25,11 +27,10 @@
 namespace qw {
 namespace {
 
-constexpr int LP_NT = 256, LP_NW = LP_NT / 32, LP_VPT = 8;  // threads, warps, 16-byte vectors a thread
+constexpr int LP_NT = 256, LP_NW = LP_NT / 32, LP_VPT = 8, LP_NS = 3;  // threads, warps, a batch's 16-byte vectors a thread, ring
 constexpr int LP_MAX_IDS = 8, LP_MAX_TOP = 32;
-constexpr int LP_CTAS_PER_SM = 4, LP_MAX_CTAS = 640;
-constexpr int LP_CAP = 1024;      // keys in the list and the pushed ones
-constexpr int LP_COMPACT = 64;    // pushed keys that are worth a new threshold
+constexpr int LP_CTAS_PER_SM = 2, LP_MAX_CTAS = 640;
+constexpr int LP_CAP = 384;       // keys in the list and the pushed ones
 constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
 typedef unsigned long long u64;
 
@@ -70,6 +71,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
+
+constexpr u64 LP_NO_BAR = 0x007fffffffffffffull;  // the key of (-inf, id 0): every finite logit's is above
 
 // ---- 16 bytes of logits ------------------------------------------------------------------------------------
 //
@@ -155,46 +158,61 @@ template <> struct Logits<f16> : Logits16<f16, __half2> {
 struct Shared {
   u64 buf[2][LP_CAP];
   int n, side;                 // keys in buf[side]: the list, then what was pushed since
-  float t;                     // a key whose logit is not above t cannot enter the list
-  u64 warp_key[LP_NW];
+  int done;                    // warps that have no batch of the row left
+  u64 bar;                     // a key that is not above it cannot enter the list
   float red[3][LP_NW];
-  int id[LP_MAX_IDS], above[LP_MAX_IDS], nan;
-  float given[LP_MAX_IDS];
+  int above[LP_MAX_IDS], nan;
+  int id[2][LP_MAX_IDS], equal[2][LP_MAX_IDS];  // of the row and the next, by turns; equal: see fetch_ids
+  float given[2][LP_MAX_IDS];
   bool last;
 };
 
 // Keeps the top_k largest of the n keys in buf[side], sorted, and their threshold. All threads; a barrier before.
-__device__ __noinline__ void compact(Shared& sh, int top_k) {
-  const int n = sh.n, side = sh.side, kept = min(n, top_k);
+__device__ __forceinline__ void compact(Shared& sh, int top_k) {
+  const int n = min(sh.n, LP_CAP), side = sh.side, kept = min(n, top_k);
   const u64* from = sh.buf[side];
   u64* to = sh.buf[side ^ 1];
+  // so many lanes count the keys above one
+  const int log_lanes = n <= LP_NT / 8 ? 3 : n <= LP_NT / 4 ? 2 : n <= LP_NT / 2 ? 1 : 0, lanes = 1 << log_lanes;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < n; i += LP_NT) {
-    const u64 key = from[i];
+  for (int i = threadIdx.x >> log_lanes; i < (n + 31 & ~31); i += LP_NT >> log_lanes) {  // (whole warps)
+    const u64 key = i < n ? from[i] : ~0ull;
     int rank = 0;
 #pragma unroll 4
-    for (int x = 0; x < n; ++x) rank += from[x] > key;
-    if (rank < top_k) to[rank] = key;
+    for (int x = threadIdx.x & (lanes - 1); x < n; x += lanes) rank += from[x] > key;
+#pragma unroll 1
+    for (int o = 1; o < lanes; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (i < n && rank < top_k) to[rank] = key;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
     sh.n = kept;
     sh.side = side ^ 1;
-    sh.t = kept == top_k ? key_value(to[top_k - 1]) : -INFINITY;
+    sh.bar = kept == top_k ? to[top_k - 1] : LP_NO_BAR;
   }
   __syncthreads();
 }
 
-// One batch of a row in registers: vector i of the thread is vector batch * LP_NT * LP_VPT + i * LP_NT + tid of
-// the row, counted from the 16-byte boundary at or before its first logit.
+// All warps meet, each from wherever it stands, and keep the best of the list; true when none has a batch left.
+__device__ __noinline__ bool meet(Shared& sh, int top_k) {
+  __syncthreads();
+  const bool done = sh.done == LP_NW;
+  compact(sh, top_k);
+  return done;
+}
+
+// One batch of a row in registers: vector i of the thread is vector (batch * LP_VPT + i) * LP_NT + tid of the
+// row, counted from the 16-byte boundary at or before its first logit.
 template <typename T>
 struct Batch {
   using Lg = Logits<T>;
   static constexpr int N = Lg::N;
   uint4 r[LP_VPT];
-  float vm[LP_VPT];  // their maxima
   int j0;            // id of vector 0's first logit (negative where the row begins inside a vector)
   __device__ __forceinline__ int id(int i) const { return j0 + i * LP_NT * N; }
+  static __device__ __forceinline__ int first_id(const T* z, int batch) {
+    return (batch * LP_NT * LP_VPT + (int)threadIdx.x) * N - (int)((uintptr_t)z % 16) / (int)sizeof(T);
+  }
 
   // vector i, i known at run time only
   __device__ __forceinline__ uint4 pick(int i) const {
@@ -205,140 +223,111 @@ struct Batch {
     return v;
   }
 
-  __device__ __forceinline__ void load(const LogprobArgs& a, int row, int batch) {
+  // requests the thread's vectors of a batch into its places of a stage (place i: 16 bytes at i * LP_NT * 16)
+  static __device__ __forceinline__ void request(const LogprobArgs& a, int row, int batch, unsigned char* stage) {
     const T* z = (const T*)a.logits + (long long)row * a.row_stride;
-    const int shift = (int)((uintptr_t)z % 16) / (int)sizeof(T);
-    j0 = (batch * LP_NT * LP_VPT + (int)threadIdx.x) * N - shift;
+    const int j0 = first_id(z, batch);
+    if (j0 >= 0 && j0 + (LP_VPT - 1) * LP_NT * N + N <= a.vocab) {
+#pragma unroll
+      for (int i = 0; i < LP_VPT; ++i) cp_async16(stage + i * LP_NT * 16, z + j0 + i * LP_NT * N);
+      return;
+    }
     const uint32_t none = Lg::minus_inf();
-    int ragged = 0;  // vectors that a row's ends cut
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < LP_VPT; ++i) {
-      const int j = id(i);
-      r[i] = make_uint4(none, none, none, none);
-      if (j >= 0 && j + N <= a.vocab) r[i] = ld_stream(z + j);
-      else if (j > -N && j < a.vocab) ragged |= 1 << i;
-    }
+      const int j = j0 + i * LP_NT * N;
+      unsigned char* to = stage + i * LP_NT * 16;
+      if (j >= 0 && j + N <= a.vocab) {
+        cp_async16(to, z + j);
+      } else {  // behind the row, or cut by one of its ends
+        *reinterpret_cast<uint4*>(to) = make_uint4(none, none, none, none);
 #pragma unroll 1
-    for (; ragged; ragged &= ragged - 1) {
-      const int i = __ffs(ragged) - 1, j = id(i);
-      uint32_t u[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) u[k] = none;
-#pragma unroll 1
-      for (int e = max(0, -j); e < min(N, a.vocab - j); ++e) {
-        const int k = sizeof(T) == 4 ? e : e / 2;
-        uint32_t x = k == 0 ? u[0] : k == 1 ? u[1] : k == 2 ? u[2] : u[3];
-        if (sizeof(T) == 4) x = reinterpret_cast<const uint32_t*>(z)[j + e];
-        else x = (x & (e & 1 ? 0x0000ffffu : 0xffff0000u)) | (uint32_t) reinterpret_cast<const uint16_t*>(z)[j + e] << (e & 1 ? 16 : 0);
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-          if (n == k) u[n] = x;
+        for (int e = max(0, -j); e < min(N, a.vocab - j); ++e) reinterpret_cast<T*>(to)[e] = z[j + e];
       }
-#pragma unroll
-      for (int k = 0; k < LP_VPT; ++k)
-        if (k == i) r[k] = make_uint4(u[0], u[1], u[2], u[3]);
     }
+  }
+  __device__ __forceinline__ void take(const LogprobArgs& a, int row, int batch, const unsigned char* stage) {
+    j0 = first_id((const T*)a.logits + (long long)row * a.row_stride, batch);
+#pragma unroll
+    for (int i = 0; i < LP_VPT; ++i) r[i] = *reinterpret_cast<const uint4*>(stage + i * LP_NT * 16);
   }
 };
 
-// f(logit, id) for each logit of a vector
-template <typename T, typename F>
-__device__ __forceinline__ void each_logit(uint4 v, int id, F f) {
-#pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
-    if constexpr (sizeof(T) == 4) {
-      f(__uint_as_float(v.x), id++);
-    } else {
-      const uint32_t lo = v.x & 0xffffu, hi = v.x >> 16;
-      const uint16_t l16 = (uint16_t)lo, h16 = (uint16_t)hi;
-      f(to_f32(*reinterpret_cast<const T*>(&l16)), id++);
-      f(to_f32(*reinterpret_cast<const T*>(&h16)), id++);
-    }
-    v = make_uint4(v.y, v.z, v.w, v.x);
+// the logits of a vector
+__device__ __forceinline__ void unpack(const uint4& r, float* x, float) {
+  x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y); x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void unpack(const uint4& r, float* x, bf16) {
+  x[0] = bf_lo(r.x); x[1] = bf_hi(r.x); x[2] = bf_lo(r.y); x[3] = bf_hi(r.y);
+  x[4] = bf_lo(r.z); x[5] = bf_hi(r.z); x[6] = bf_lo(r.w); x[7] = bf_hi(r.w);
+}
+__device__ __forceinline__ void unpack(const uint4& r, float* x, f16) {
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = __half22float2(as_pair<__half2>(u[i]));
+    x[2 * i] = t.x;
+    x[2 * i + 1] = t.y;
   }
 }
 
-// The batch's keys above the list's threshold go to the list, which holds n0 keys (the same for all threads, who
-// all call this; top_k > 0).
+// A bar for a row's first batch, from the thread maxima in steps of their upper 16 bits: the largest value that
+// top_k threads reach, so top_k keys at least are above it. All threads.
+__device__ __forceinline__ u64 first_bar(float tmax, int top_k) {
+  const uint32_t key = order_bits(tmax) >> 16;
+  uint32_t bound = 0;
+#pragma unroll 1
+  for (uint32_t bit = 0x8000u; bit; bit >>= 1)
+    if (__syncthreads_count(key >= (bound | bit)) >= top_k) bound |= bit;
+  return bound < 0x80u ? LP_NO_BAR : ((u64)bound << 48) - 1;  // (below 0x80: fewer threads have a finite one)
+}
+
+// The batch's keys above bar, and above the list's, go to the list. Warps come here on their own, so equal
+// logits come in any order: keys are compared, not logits.
 template <typename T>
-__device__ __forceinline__ void push_batch(Shared& sh, const Batch<T>& b, float tmax, int top_k, int& n0) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float t = sh.t;  // (changes in compact() only)
-#pragma unroll 1
-  for (int attempt = t == -INFINITY; attempt < 2; ++attempt) {
-    if (attempt == 1) {
-      // a bound from the thread maxima, in steps of their upper 16 bits: the largest that top_k threads reach
-      const uint32_t key = order_bits(tmax) >> 16;
-      uint32_t bound = 0;
-#pragma unroll 1
-      for (uint32_t bit = 0x8000u; bit; bit >>= 1)
-        if (__syncthreads_count(key >= (bound | bit)) >= top_k) bound |= bit;
-      if (bound > 0x7fu) {  // (else -inf is: fewer threads have a finite one)
-        bound <<= 16;
-        // the value below it, so that "above t" takes the bound in
-        t = fmaxf(t, order_value(bound == 0x80000000u ? 0x7ffffffeu : bound - 1));
-      }
-    }
-    int hits = 0;  // vectors with a logit above t
+__device__ __forceinline__ void push_batch(Shared& sh, const Batch<T>& b, float tmax, u64 bar, int top_k) {
+  auto raise = [&]() { bar = sh.bar > bar ? sh.bar : bar; };
+  raise();
+  const float least = order_value((uint32_t)(bar >> 32) + ((uint32_t)bar == 0xffffffffu ? 1u : 0u));
+  if (!__any_sync(0xffffffffu, tmax >= least)) return;
+  int hits = 0;  // vectors that may have a key above bar
 #pragma unroll
-    for (int i = 0; i < LP_VPT; ++i) hits |= (b.vm[i] > t) << i;
+  for (int i = 0; i < LP_VPT; ++i) hits |= (Batch<T>::Lg::top(b.r[i]) >= least) << i;
+  constexpr int N = Batch<T>::N;
+  uint32_t pending = ~0u;  // logits of the lane's current vector that are not dealt with
 #pragma unroll 1
-    for (; hits; hits &= hits - 1) {
-      const int i = __ffs(hits) - 1;
-      each_logit<T>(b.pick(i), b.id(i), [&](float x, int j) {
-        if (x > t) {
-          const int at = atomicAdd(&sh.n, 1);
-          if (at < LP_CAP) sh.buf[sh.side][at] = order_key(x, j);
+  while (__any_sync(0xffffffffu, hits)) {
+    uint32_t left = 0;  // keys that found the list full
+    if (hits) {
+      const int i = __ffs(hits) - 1, j = b.id(i);
+      float x[N];
+      unpack(b.pick(i), x, T());
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e) m |= (order_key(x[e], j + e) > bar && x[e] == x[e] ? 1u : 0u) << e;
+      m &= pending;
+      int at = m ? atomicAdd(&sh.n, __popc(m)) : 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if (m >> e & 1) {
+          if (at < LP_CAP) sh.buf[sh.side][at] = order_key(x[e], j + e);
+          else left |= 1u << e;
+          ++at;
         }
-      });
+      }
+      pending = left ? left : ~0u;
+      if (!left) hits &= hits - 1;
     }
-    __syncthreads();
-    const int n = sh.n;
-    __syncthreads();  // (the next batch's first pushes wait for everyone's look at n)
-    if (n <= LP_CAP) {
-      const bool shrink = n >= top_k && (sh.t == -INFINITY || n >= n0 + LP_COMPACT || n > LP_CAP / 2);
-      if (shrink) compact(sh, top_k);
-      n0 = shrink ? top_k : n;
-      return;
+    if (__any_sync(0xffffffffu, left)) {
+      meet(sh, top_k);
+      raise();
     }
-    if (threadIdx.x == 0) sh.n = n0;  // too many: forget them
-    __syncthreads();
   }
-  // ties, mostly: the batch's top_k largest keys above t, one by one
-  u64 last = ~0ull;
-#pragma unroll 1
-  for (int k = 0; k < top_k; ++k) {
-    u64 best = 0;
-#pragma unroll 1
-    for (int i = 0; i < LP_VPT; ++i)
-      each_logit<T>(b.pick(i), b.id(i), [&](float x, int j) {
-        const u64 key = order_key(x, j);
-        if (x > t && key < last && key > best) best = key;
-      });
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const u64 other = __shfl_xor_sync(0xffffffffu, best, o);
-      best = other > best ? other : best;
-    }
-    if (lane == 0) sh.warp_key[warp] = best;
-    __syncthreads();
-    best = sh.warp_key[0];
-#pragma unroll
-    for (int w = 1; w < LP_NW; ++w) best = sh.warp_key[w] > best ? sh.warp_key[w] : best;
-    if (best && threadIdx.x == 0 && sh.n < LP_CAP) sh.buf[sh.side][sh.n++] = best;
-    last = best;
-    __syncthreads();
-    if (!best) break;
-  }
-  const int n = sh.n;
-  __syncthreads();
-  if (n >= top_k) compact(sh, top_k);
-  n0 = min(n, top_k);
 }
 
 // Writes a row's results from its state (the list sorted in sh). All threads.
 template <typename T>
-__device__ __forceinline__ void finish_row(const LogprobArgs& a, Shared& sh, int row, float m, float s, float w, bool nan) {
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, Shared& sh, int row, float m, float s, float w, bool nan, int turn) {
   const int tid = threadIdx.x;
   const bool odd = nan || s != s || !(m < INFINITY) || m == -INFINITY;  // no distribution
   const float ln_s = odd ? NAN : logf(s);
@@ -347,10 +336,10 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& a, Shared& sh, int
     if (a.entropy) a.entropy[row] = odd ? NAN : ln_s - w * LP_LN2 / s;
   }
   if (tid < a.n_ids) {
-    const int t = sh.id[tid];
+    const int t = sh.id[turn][tid];
     const bool in = t >= 0 && t < a.vocab;
     if (!in && t != -1) atomicOr(a.err, ERR_TOKEN);
-    a.logprobs[(size_t)row * a.n_ids + tid] = t == -1 ? 0.f : odd || !in ? NAN : sh.given[tid] - m - ln_s;
+    a.logprobs[(size_t)row * a.n_ids + tid] = t == -1 ? 0.f : odd || !in ? NAN : sh.given[turn][tid] - m - ln_s;
     if (a.ranks) a.ranks[(size_t)row * a.n_ids + tid] = odd || !in ? 0 : 1 + sh.above[tid];
   }
   if (tid < a.top_k && (odd || tid < sh.n)) {
@@ -372,56 +361,88 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& a, Shared& sh, int
   }
 }
 
+// Reads one id of a row (this thread's), its logit, and how many equal logits stand before it in its vector (if that
+// is in batches b0 .. b1 - 1: the passes count whole vectors), into place `turn`. Three loads that depend on one
+// another: done a row ahead.
+template <typename T>
+__device__ __noinline__ void fetch_ids(const LogprobArgs& a, Shared& sh, int row, int b0, int b1, int turn) {
+  constexpr int N = Logits<T>::N;
+  const int t = a.ids[(size_t)row * a.n_ids + threadIdx.x];
+  const T* z = (const T*)a.logits + (long long)row * a.row_stride;
+  float given = NAN;
+  int equal = 0;
+  if (t >= 0 && t < a.vocab) {
+    given = to_f32(z[t]);
+    const int shift = (int)((uintptr_t)z % 16) / (int)sizeof(T), vec = (t + shift) / N, batch = vec / (LP_NT * LP_VPT);
+    if (batch >= b0 && batch < b1)
+#pragma unroll 1
+      for (int j = max(0, vec * N - shift); j < t; ++j) equal += to_f32(z[j]) == given;
+    if (given == -INFINITY && b0 == 0 && vec > 0) equal -= shift;  // what fills the first vector is counted too
+  }
+  sh.id[turn][threadIdx.x] = t;
+  sh.equal[turn][threadIdx.x] = equal;
+  sh.given[turn][threadIdx.x] = given;
+}
+
 // One CTA's range of the list of batches.
 template <typename T>
-__global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __grid_constant__ LogprobArgs a) {
   constexpr int N = Batch<T>::N;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ __align__(16) unsigned char lp_ring[];
   const int total = a.n_rows * a.batches, each = total / (int)gridDim.x, rest = total - each * (int)gridDim.x;
   auto cut = [&](int c) { return each * c + min(c, rest); };
   int at = cut(blockIdx.x);
   const int end = cut(blockIdx.x + 1);
+  int ld_row = at / a.batches, ld_batch = at - ld_row * a.batches, to_load = end - at, ld_stage = 0, stage = 0;
+  auto stage_ptr = [&](int i) { return lp_ring + (i * LP_NT * LP_VPT + tid) * 16; };
+  auto load_next = [&]() {
+    if (to_load > 0) {
+      --to_load;
+      Batch<T>::request(a, ld_row, ld_batch, stage_ptr(ld_stage));
+      if (++ld_batch == a.batches) {
+        ld_batch = 0;
+        ++ld_row;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++ld_stage == LP_NS) ld_stage = 0;
+  };
+  int turn = 0;           // which of the two places has the row's ids
+  int ahead = LP_NS - 1;  // batches still to be requested before the first is used
 #pragma unroll 1
   while (at < end) {
     const int row = at / a.batches, b0 = at - row * a.batches, b1 = min(a.batches, b0 + end - at);
-    Batch<T> b;
-    b.load(a, row, b0);
     if (tid < a.n_ids) {
-      const int t = a.ids[(size_t)row * a.n_ids + tid];
-      const T* z = (const T*)a.logits + (long long)row * a.row_stride;
-      float given = NAN;
-      int equal = 0;  // before t in its vector
-      if (t >= 0 && t < a.vocab) {
-        given = to_f32(z[t]);
-        const int shift = (int)((uintptr_t)z % 16) / (int)sizeof(T), vec = (t + shift) / N, batch = vec / (LP_NT * LP_VPT);
-        if (batch >= b0 && batch < b1)
-#pragma unroll 1
-          for (int j = max(0, vec * N - shift); j < t; ++j) equal += to_f32(z[j]) == given;
-        if (given == -INFINITY && b0 == 0 && vec > 0) equal -= shift;  // what fills the first vector is counted too
-      }
-      sh.id[tid] = t;
-      sh.above[tid] = equal;
-      sh.given[tid] = given;
+      if (at == cut(blockIdx.x)) fetch_ids<T>(a, sh, row, b0, b1, 0);
+      sh.above[tid] = sh.equal[turn][tid];
     }
     if (tid == 0) {
       sh.n = 0;
       sh.side = 0;
-      sh.t = -INFINITY;
+      sh.done = 0;
+      sh.bar = LP_NO_BAR;
       sh.nan = 0;
     }
     __syncthreads();
     float m = -INFINITY, s = 0.f, w = 0.f;  // this thread's, w in base 2
     bool nan = false;
-    int listed = 0;  // keys in the list
+    Batch<T> b;
 #pragma unroll 1
-    for (int batch = b0; batch < b1; ++batch) {
-      if (batch > b0) b.load(a, row, batch);
+    for (int batch = b0; batch < b1;) {
+      load_next();  // into the stage that the last batch used
+      if (ahead) {
+        --ahead;
+        continue;
+      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(LP_NS - 1) : "memory");
+      b.take(a, row, batch, stage_ptr(stage));
+      if (++stage == LP_NS) stage = 0;
       float top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < LP_VPT; ++i) {
-        b.vm[i] = Batch<T>::Lg::top(b.r[i]);
-        top = fmaxf(top, b.vm[i]);
+        top = fmaxf(top, Batch<T>::Lg::top(b.r[i]));
       }
       if (top > m) {
         const float d = (m - top) * LP_LOG2E, f = ex2(d);
@@ -451,8 +472,9 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const Lo
       if (a.ranks) {
 #pragma unroll 1
         for (int q = 0; q < a.n_ids; ++q) {
-          const int t = sh.id[q];
-          const float z = sh.given[q];
+          const int t = sh.id[turn][q];
+          const float z = sh.given[turn][q];
+          if (!__any_sync(0xffffffffu, top >= z)) continue;  // (none above a likely token in most batches)
           // whole vectors before t count from z on, the others from the next larger value on; equal logits
           // before t in its own vector were counted when the row began
           const typename Batch<T>::Lg::Thr here = Batch<T>::Lg::thr(z), next = Batch<T>::Lg::thr_above(z);
@@ -464,11 +486,26 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const Lo
           if (lane == 0 && above) atomicAdd(&sh.above[q], above);
         }
       }
-      if (a.top_k) push_batch(sh, b, top, a.top_k, listed);
+      if (a.top_k) {
+        const bool first = batch == b0;
+        push_batch(sh, b, top, first ? first_bar(top, a.top_k) : LP_NO_BAR, a.top_k);
+        __syncwarp();
+        // one lane looks, for the whole warp (a look that a later push makes stale only delays the meeting)
+        int listed = 0;
+        if (lane == 0) listed = *(volatile int*)&sh.n;
+        listed = __shfl_sync(0xffffffffu, listed, 0);
+        if (first || listed >= 2 * a.top_k + 8) meet(sh, a.top_k);
+      }
+      // the next row's ids, by the first warp, while the others go on
+      if (batch++ == b0 && tid < a.n_ids && at + b1 - b0 < end) fetch_ids<T>(a, sh, row + 1, 0, min(a.batches, end - at - (b1 - b0)), turn ^ 1);
     }
     // the CTA's state of the row
-    __syncthreads();
-    if (a.top_k && sh.n) compact(sh, a.top_k);
+    if (a.top_k) {
+      __syncwarp();
+      if (lane == 0) atomicAdd(&sh.done, 1);
+      while (!meet(sh, a.top_k)) {
+      }
+    }
     float mm = warp_max(m);
     if (lane == 0) sh.red[0][warp] = mm;
     if (nan) sh.nan = 1;
@@ -565,25 +602,40 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const Lo
           w += sh.red[2][i];
         }
         nan = sh.nan;
-        // the parts' lists, so many at a time that they fit next to the best ones
-        const int step = (LP_CAP - LP_MAX_TOP) / LP_MAX_TOP;
-#pragma unroll 1
-        for (int c = c0; a.top_k && c <= c1; c += step) {
-          const int n = min(step, c1 - c + 1);
-#pragma unroll 1
-          for (int i = tid; i < n * LP_MAX_TOP; i += LP_NT) {
-            const LogprobPart* p = slot_of(c + i / LP_MAX_TOP);
-            if (i % LP_MAX_TOP < __ldcg(&p->n)) sh.buf[sh.side][atomicAdd(&sh.n, 1)] = __ldcg(&p->key[i % LP_MAX_TOP]);
+        // the parts' lists: at least top_k keys are not below the largest of the full lists' last keys
+        if (a.top_k) {
+          if (tid == 0) sh.bar = 0;
+          __syncthreads();
+          for (int c = c0 + tid; c <= c1; c += LP_NT) {
+            const LogprobPart* p = slot_of(c);
+            if (__ldcg(&p->n) == a.top_k) atomicMax(&sh.bar, __ldcg(&p->key[a.top_k - 1]));
           }
           __syncthreads();
-          compact(sh, a.top_k);
+          const u64 bar = sh.bar;
+          // so many parts at a time that they fit next to the best ones even if all their keys are taken
+          constexpr int step = (LP_CAP - LP_MAX_TOP) / LP_MAX_TOP;
+          for (int c = c0; c <= c1; c += step) {
+            const int n = min(step, c1 - c + 1);
+#pragma unroll 1
+            for (int i = tid; i < n * LP_MAX_TOP; i += LP_NT) {
+              const LogprobPart* p = slot_of(c + i / LP_MAX_TOP);
+              const u64 key = i % LP_MAX_TOP < a.top_k ? __ldcg(&p->key[i % LP_MAX_TOP]) : 0;
+              if (i % LP_MAX_TOP < __ldcg(&p->n) && key >= bar) sh.buf[sh.side][atomicAdd(&sh.n, 1)] = key;
+            }
+            __syncthreads();
+            const int listed = sh.n;
+            __syncthreads();
+            if (c + step > c1 || listed > LP_MAX_TOP) compact(sh, a.top_k);
+          }
         }
       }
     }
-    if (write) finish_row<T>(a, sh, row, mm, s, w, nan);
+    if (write) finish_row<T>(a, sh, row, mm, s, w, nan, turn);
     __syncthreads();
     at += b1 - b0;
+    turn ^= 1;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <typename T>
@@ -593,7 +645,9 @@ cudaError_t launch_logprobs(LogprobArgs a, int nsm, cudaStream_t s) {
   a.batches = (int)(((long long)a.vocab + N - 1 + LP_NT * LP_VPT * N - 1) / (LP_NT * LP_VPT * N));
   const long long total = (long long)a.n_rows * a.batches;
   const int grid = (int)std::min<long long>(total, std::min(nsm * LP_CTAS_PER_SM, LP_MAX_CTAS));
-  return launch_k(logprob_kernel<T>, dim3(grid), dim3(LP_NT), 0, s, false, a);
+  constexpr int ring = LP_NS * LP_NT * LP_VPT * 16;
+  const cudaError_t e = cudaFuncSetAttribute(logprob_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+  return e ? e : launch_k(logprob_kernel<T>, dim3(grid), dim3(LP_NT), ring, s, false, a);
 }
 constexpr size_t LP_COUNTER_BYTES = 2 * LP_MAX_CTAS * sizeof(unsigned int);
 
@@ -620,8 +674,8 @@ qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t voc
   if (top_k < 0 || top_k > LP_MAX_TOP || top_k > vocab)
     return op_fail(QW_ERR_INVALID_ARG, "top_k must be 0 .. min(32, vocab)");
   if (row_stride < vocab || row_stride > (int64_t)1 << 40) return op_fail(QW_ERR_INVALID_ARG, "row_stride smaller than a row");
-  // the list of batches (of at least 8192 logits) has 31-bit numbers, and so have ids with a batch's overhang
-  if ((int64_t)n_rows * (vocab / 8192 + 2) > 0x7fffffffll || vocab > 0x7fff0000)
+  // the list of batches (of at least 4096 logits) has 31-bit numbers, and so have ids with a batch's overhang
+  if ((int64_t)n_rows * (vocab / 4096 + 2) > 0x7fffffffll || vocab > 0x7fff0000)
     return op_fail(QW_ERR_UNSUPPORTED, "n_rows * vocab too large");
   if (n_rows == 0) return QW_OK;
   if (!logits || !err_dev || !workspace || (n_ids && (!ids || !logprobs)) || (top_k && (!top_ids || !top_logprobs)))
