@@ -7,16 +7,17 @@
 //
 // What bounds it: each logit is read once and costs about ten instructions (one exponential among them), so HBM
 // for fp32 logits and nearly so for 16-bit ones.
-//   - All rows' batches (256 threads x 4 vectors of 16 bytes) form one list, cut into equal consecutive ranges,
-//     one per CTA, four CTAs an SM. A row that a cut divides is joined by the last of its CTAs to arrive;
+//   - All rows' batches (256 threads x 8 vectors of 16 bytes) form one list, cut into equal consecutive ranges,
+//     one per CTA, two CTAs an SM. A row that a cut divides is joined by the last of its CTAs to arrive;
 //     every sum's order is fixed, results repeat bit by bit.
 //   - Each thread copies its own vectors (cp.async) into a ring of three batches and reads them back itself: no
-//     barrier, and up to 128 KB in flight an SM. A batch is then in registers for all passes: vector maxima,
-//     exponentials, counts for the ranks, top tokens.
-//   - Top tokens: a shared-memory list of the best so far gives a threshold T; only logits above it are pushed,
-//     without a barrier either. The warps meet (to keep the best and raise T) after a row's first batch,
-//     when the list has filled, and at the row's end. The first batch bounds T from below by the top_k-th
-//     thread maximum. A warp that finds the list full waits for a meeting and goes on where it stopped.
+//     barrier, and up to 128 KB in flight an SM. A batch is then in registers for its passes: maxima,
+//     exponentials, counts for the ranks.
+//   - Top tokens cost nothing while the row streams by but one stored maximum per thread and group of batches. At
+//     the row's end the top_k-th largest thread maximum bounds the top_k-th logit from below; the groups whose
+//     maximum reaches it, hardly more than top_k of them, are read again and their logits at or above the
+//     bound sorted. (Lists that were kept while streaming, with a rising threshold, cost 50 us of 134 for
+//     1024 rows of 152064: the warps met to raise it.)
 #include "common.cuh"
 #include "op_util.h"
 
@@ -155,11 +156,16 @@ template <> struct Logits<f16> : Logits16<f16, __half2> {
   }
 };
 
+constexpr int LP_GROUPS = 16;  // groups of a row's batches, of which each thread keeps a maximum
+constexpr int LP_WORK = 128;   // groups that are read again at a time
+
 struct Shared {
   u64 buf[2][LP_CAP];
-  int n, side;                 // keys in buf[side]: the list, then what was pushed since
-  int done;                    // warps that have no batch of the row left
-  u64 bar;                     // a key that is not above it cannot enter the list
+  int n, side;                   // keys in buf[side]: the list, then what was pushed since
+  u64 bar;                       // a key that is not above it cannot enter the list
+  uint16_t top[LP_GROUPS][LP_NT];  // upper 16 bits of the ordered maxima
+  uint16_t work[LP_WORK];        // group * LP_NT + thread
+  int n_work;
   float red[3][LP_NW];
   int above[LP_MAX_IDS], nan;
   int id[2][LP_MAX_IDS], equal[2][LP_MAX_IDS];  // of the row and the next, by turns; equal: see fetch_ids
@@ -193,14 +199,6 @@ __device__ __forceinline__ void compact(Shared& sh, int top_k) {
   __syncthreads();
 }
 
-// All warps meet, each from wherever it stands, and keep the best of the list; true when none has a batch left.
-__device__ __noinline__ bool meet(Shared& sh, int top_k) {
-  __syncthreads();
-  const bool done = sh.done == LP_NW;
-  compact(sh, top_k);
-  return done;
-}
-
 // One batch of a row in registers: vector i of the thread is vector (batch * LP_VPT + i) * LP_NT + tid of the
 // row, counted from the 16-byte boundary at or before its first logit.
 template <typename T>
@@ -212,15 +210,6 @@ struct Batch {
   __device__ __forceinline__ int id(int i) const { return j0 + i * LP_NT * N; }
   static __device__ __forceinline__ int first_id(const T* z, int batch) {
     return (batch * LP_NT * LP_VPT + (int)threadIdx.x) * N - (int)((uintptr_t)z % 16) / (int)sizeof(T);
-  }
-
-  // vector i, i known at run time only
-  __device__ __forceinline__ uint4 pick(int i) const {
-    uint4 v = r[0];
-#pragma unroll
-    for (int k = 1; k < LP_VPT; ++k)
-      if (i == k) v = r[k];
-    return v;
   }
 
   // requests the thread's vectors of a batch into its places of a stage (place i: 16 bytes at i * LP_NT * 16)
@@ -271,58 +260,91 @@ __device__ __forceinline__ void unpack(const uint4& r, float* x, f16) {
   }
 }
 
-// A bar for a row's first batch, from the thread maxima in steps of their upper 16 bits: the largest value that
-// top_k threads reach, so top_k keys at least are above it. All threads.
-__device__ __forceinline__ u64 first_bar(float tmax, int top_k) {
+// A bound on the top_k-th largest logit from the thread maxima, in steps of their upper 16 bits: the largest that
+// top_k threads reach. 0x7f (-inf's) or less where fewer have a finite maximum. All threads.
+__device__ __forceinline__ uint32_t top_bound(float tmax, int top_k) {
   const uint32_t key = order_bits(tmax) >> 16;
   uint32_t bound = 0;
 #pragma unroll 1
   for (uint32_t bit = 0x8000u; bit; bit >>= 1)
     if (__syncthreads_count(key >= (bound | bit)) >= top_k) bound |= bit;
-  return bound < 0x80u ? LP_NO_BAR : ((u64)bound << 48) - 1;  // (below 0x80: fewer threads have a finite one)
+  return bound;
 }
 
-// The batch's keys above bar, and above the list's, go to the list. Warps come here on their own, so equal
-// logits come in any order: keys are compared, not logits.
+// The sorted top_k (or fewer, of finite logits) of batches b0 .. b1 - 1 of a row, into the empty list. tmax: the
+// thread's maximum of them; sh.top: its groups' (group: (batch - b0) / per). All threads.
 template <typename T>
-__device__ __forceinline__ void push_batch(Shared& sh, const Batch<T>& b, float tmax, u64 bar, int top_k) {
-  auto raise = [&]() { bar = sh.bar > bar ? sh.bar : bar; };
-  raise();
-  const float least = order_value((uint32_t)(bar >> 32) + ((uint32_t)bar == 0xffffffffu ? 1u : 0u));
-  if (!__any_sync(0xffffffffu, tmax >= least)) return;
-  int hits = 0;  // vectors that may have a key above bar
-#pragma unroll
-  for (int i = 0; i < LP_VPT; ++i) hits |= (Batch<T>::Lg::top(b.r[i]) >= least) << i;
-  constexpr int N = Batch<T>::N;
-  uint32_t pending = ~0u;  // logits of the lane's current vector that are not dealt with
+__device__ __forceinline__ void select_top(const LogprobArgs& a, Shared& sh, int row, int b0, int b1, int per, float tmax) {
+  constexpr int N = Logits<T>::N;
+  const int tid = threadIdx.x, top_k = a.top_k;
+  const uint32_t bound = max(top_bound(tmax, top_k), 0x80u);  // (finite logits only)
+  const T* z = (const T*)a.logits + (long long)row * a.row_stride;
+  const int shift = (int)((uintptr_t)z % 16) / (int)sizeof(T);
+  int hits = 0;  // the thread's groups that reach the bound
+  for (int g = 0; g * per < b1 - b0; ++g) hits |= (sh.top[g][tid] >= bound) << g;
+  u64 bar = ((u64)bound << 48) - 1;
 #pragma unroll 1
-  while (__any_sync(0xffffffffu, hits)) {
-    uint32_t left = 0;  // keys that found the list full
-    if (hits) {
-      const int i = __ffs(hits) - 1, j = b.id(i);
+  for (bool more = true; more;) {
+    if (tid == 0) sh.n_work = 0;
+    __syncthreads();
+    while (hits) {
+      const int at = atomicAdd(&sh.n_work, 1);
+      if (at >= LP_WORK) break;
+      sh.work[at] = (uint16_t)((__ffs(hits) - 1) * LP_NT + tid);
+      hits &= hits - 1;
+    }
+    more = __syncthreads_or(hits);
+    const int items = min(sh.n_work, LP_WORK) * per * LP_VPT;  // vectors
+#pragma unroll 1
+    for (int i0 = 0; i0 < items; i0 += LP_NT) {
       float x[N];
-      unpack(b.pick(i), x, T());
-      uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < N; ++e) m |= (order_key(x[e], j + e) > bar && x[e] == x[e] ? 1u : 0u) << e;
-      m &= pending;
-      int at = m ? atomicAdd(&sh.n, __popc(m)) : 0;
+      for (int e = 0; e < N; ++e) x[e] = -INFINITY;
+      int j = 0;
+      if (i0 + tid < items) {
+        const int w = (i0 + tid) / (per * LP_VPT), v = (i0 + tid) - w * per * LP_VPT, g = sh.work[w] / LP_NT, th = sh.work[w] % LP_NT;
+        const int batch = b0 + g * per + v / LP_VPT;
+        j = ((batch * LP_VPT + v % LP_VPT) * LP_NT + th) * N - shift;
+        if (batch < b1) {
+          if (j >= 0 && j + N <= a.vocab) {
+            unpack(ld_stream(z + j), x, T());
+          } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        if (m >> e & 1) {
-          if (at < LP_CAP) sh.buf[sh.side][at] = order_key(x[e], j + e);
-          else left |= 1u << e;
-          ++at;
+            for (int e = 0; e < N; ++e)
+              if (j + e >= 0 && j + e < a.vocab) x[e] = to_f32(z[j + e]);
+          }
         }
       }
-      pending = left ? left : ~0u;
-      if (!left) hits &= hits - 1;
-    }
-    if (__any_sync(0xffffffffu, left)) {
-      meet(sh, top_k);
-      raise();
+      uint32_t m = 0, left;
+#pragma unroll
+      for (int e = 0; e < N; ++e) m |= (x[e] == x[e] ? 1u : 0u) << e;
+#pragma unroll 1
+      do {  // (once, unless ties fill the list)
+        uint32_t take = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) take |= (order_key(x[e], j + e) > bar ? 1u : 0u) << e;
+        take &= m;
+        int at = take ? atomicAdd(&sh.n, __popc(take)) : 0;
+        left = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          if (take >> e & 1) {
+            if (at < LP_CAP) sh.buf[sh.side][at] = order_key(x[e], j + e);
+            else left |= 1u << e;
+            ++at;
+          }
+        }
+        m = left;
+        left = __syncthreads_or(left);
+        if (left) {
+          compact(sh, top_k);
+          bar = sh.bar > bar ? sh.bar : bar;
+        }
+      } while (left);
     }
   }
+  __syncthreads();
+  compact(sh, top_k);
 }
 
 // Writes a row's results from its state (the list sorted in sh). All threads.
@@ -421,13 +443,13 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
     if (tid == 0) {
       sh.n = 0;
       sh.side = 0;
-      sh.done = 0;
       sh.bar = LP_NO_BAR;
       sh.nan = 0;
     }
     __syncthreads();
     float m = -INFINITY, s = 0.f, w = 0.f;  // this thread's, w in base 2
     bool nan = false;
+    const int per = (b1 - b0 + LP_GROUPS - 1) / LP_GROUPS;  // batches of a group
     Batch<T> b;
 #pragma unroll 1
     for (int batch = b0; batch < b1;) {
@@ -487,25 +509,15 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
         }
       }
       if (a.top_k) {
-        const bool first = batch == b0;
-        push_batch(sh, b, top, first ? first_bar(top, a.top_k) : LP_NO_BAR, a.top_k);
-        __syncwarp();
-        // one lane looks, for the whole warp (a look that a later push makes stale only delays the meeting)
-        int listed = 0;
-        if (lane == 0) listed = *(volatile int*)&sh.n;
-        listed = __shfl_sync(0xffffffffu, listed, 0);
-        if (first || listed >= 2 * a.top_k + 8) meet(sh, a.top_k);
+        const int g = (batch - b0) / per;
+        const uint32_t key = order_bits(top) >> 16;
+        sh.top[g][tid] = (uint16_t)((batch - b0) % per ? max(key, (uint32_t)sh.top[g][tid]) : key);
       }
       // the next row's ids, by the first warp, while the others go on
       if (batch++ == b0 && tid < a.n_ids && at + b1 - b0 < end) fetch_ids<T>(a, sh, row + 1, 0, min(a.batches, end - at - (b1 - b0)), turn ^ 1);
     }
     // the CTA's state of the row
-    if (a.top_k) {
-      __syncwarp();
-      if (lane == 0) atomicAdd(&sh.done, 1);
-      while (!meet(sh, a.top_k)) {
-      }
-    }
+    if (a.top_k) select_top<T>(a, sh, row, b0, b1, per, m);
     float mm = warp_max(m);
     if (lane == 0) sh.red[0][warp] = mm;
     if (nan) sh.nan = 1;
