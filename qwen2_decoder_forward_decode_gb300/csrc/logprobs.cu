@@ -79,7 +79,7 @@ constexpr u64 LP_NO_BAR = 0x007fffffffffffffull;  // the key of (-inf, id 0): ev
 //
 // pair(u): the logits of word u (two for 16-bit types) as packed fp32, with -inf raised to a finite value whose
 // exponential is 0 (so that d * exp(d) is 0 as well); a NaN stays.
-constexpr float LP_FLOOR = -1e38f;  // (finite after the product with log2 e)
+constexpr float LP_FLOOR = -1e38f;  // (finite after the product with log2 e and the difference)
 template <typename T> struct Logits;
 template <> struct Logits<float> {
   static constexpr int N = 4;
@@ -117,14 +117,18 @@ struct Logits16 {
     const T2 m = __hmax2(__hmax2(as_pair<T2>(r.x), as_pair<T2>(r.y)), __hmax2(as_pair<T2>(r.z), as_pair<T2>(r.w)));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  // packed counts: exact, a thread's are at most 4 LP_VPT a lane
+  // Counts of both halves in one sum of masks: a true half adds 0xffff, so the sum of lo low and hi high ones is
+  // (lo - hi) 2^16 - lo.
   struct Count {
-    T2 n = as_pair<T2>(0u);
+    uint32_t n = 0;
     __device__ __forceinline__ void add(const uint4& r, T2 thr) {
-      n = __hadd2(n, __hadd2(__hadd2(__hge2(as_pair<T2>(r.x), thr), __hge2(as_pair<T2>(r.y), thr)),
-                             __hadd2(__hge2(as_pair<T2>(r.z), thr), __hge2(as_pair<T2>(r.w), thr))));
+      n += __hge2_mask(as_pair<T2>(r.x), thr) + __hge2_mask(as_pair<T2>(r.y), thr);
+      n += __hge2_mask(as_pair<T2>(r.z), thr) + __hge2_mask(as_pair<T2>(r.w), thr);
     }
-    __device__ __forceinline__ int total() const { return (int)(__low2float(n) + __high2float(n)); }
+    __device__ __forceinline__ int total() const {
+      const uint32_t lo = -n & 0xffffu;
+      return (int)(2 * lo) - (int16_t)((n + lo) >> 16);
+    }
   };
   typedef T2 Thr;
   static __device__ __forceinline__ uint32_t bits(float z) {
@@ -352,22 +356,24 @@ template <typename T>
 __device__ __forceinline__ void finish_row(const LogprobArgs& a, Shared& sh, int row, float m, float s, float w, bool nan, int turn) {
   const int tid = threadIdx.x;
   const bool odd = nan || s != s || !(m < INFINITY) || m == -INFINITY;  // no distribution
-  const float ln_s = odd ? NAN : logf(s);
+  // ln p = (log2(e) z - m - log2 S) ln 2: the product and the difference are one rounding
+  const float log2_s = odd ? NAN : log2f(s);
+  auto logprob = [&](float z) { return (fmaf(z, LP_LOG2E, -m) - log2_s) * LP_LN2; };
   if (tid == 0) {
     if (odd) atomicOr(a.err, ERR_NONFINITE);
-    if (a.entropy) a.entropy[row] = odd ? NAN : ln_s - w * LP_LN2 / s;
+    if (a.entropy) a.entropy[row] = odd ? NAN : (log2_s - w / s) * LP_LN2;
   }
   if (tid < a.n_ids) {
     const int t = sh.id[turn][tid];
     const bool in = t >= 0 && t < a.vocab;
     if (!in && t != -1) atomicOr(a.err, ERR_TOKEN);
-    a.logprobs[(size_t)row * a.n_ids + tid] = t == -1 ? 0.f : odd || !in ? NAN : sh.given[turn][tid] - m - ln_s;
+    a.logprobs[(size_t)row * a.n_ids + tid] = t == -1 ? 0.f : odd || !in ? NAN : logprob(sh.given[turn][tid]);
     if (a.ranks) a.ranks[(size_t)row * a.n_ids + tid] = odd || !in ? 0 : 1 + sh.above[tid];
   }
   if (tid < a.top_k && (odd || tid < sh.n)) {
     const u64 key = odd ? 0 : sh.buf[sh.side][tid];
     a.top_ids[(size_t)row * a.top_k + tid] = odd ? -1 : argmax_key_index(key);
-    a.top_logprobs[(size_t)row * a.top_k + tid] = odd ? NAN : key_value(key) - m - ln_s;
+    a.top_logprobs[(size_t)row * a.top_k + tid] = odd ? NAN : logprob(key_value(key));
   }
   if (!odd && sh.n < a.top_k && tid == 0) {  // fewer finite logits: the lowest ids of probability 0
     const T* z = (const T*)a.logits + (long long)row * a.row_stride;
@@ -447,7 +453,9 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
       sh.nan = 0;
     }
     __syncthreads();
-    float m = -INFINITY, s = 0.f, w = 0.f;  // this thread's, w in base 2
+    // this thread's sums, in base 2 all: s = sum 2^(log2(e) z - m), w = sum (log2(e) z - m) 2^(..). m is the
+    // maximum's product with log2(e) as it was rounded, so that its rounding is in no result.
+    float m = -INFINITY, s = 0.f, w = 0.f, most = -INFINITY;
     bool nan = false;
     const int per = (b1 - b0 + LP_GROUPS - 1) / LP_GROUPS;  // batches of a group
     Batch<T> b;
@@ -466,13 +474,18 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
       for (int i = 0; i < LP_VPT; ++i) {
         top = fmaxf(top, Batch<T>::Lg::top(b.r[i]));
       }
-      if (top > m) {
-        const float d = (m - top) * LP_LOG2E, f = ex2(d);
-        w = m == -INFINITY ? 0.f : fmaf(d, s, w) * f;
-        s = m == -INFINITY ? 0.f : s * f;
-        m = top;
+      most = fmaxf(most, top);
+      if (top * LP_LOG2E > m) {
+        const float to = top * LP_LOG2E, d = m - to, f = ex2(d);
+        if (m == -INFINITY) s = w = 0.f;
+        else {
+          w = fmaf(d, s, w) * f;
+          s *= f;
+        }
+        m = to;
       }
-      const f32x2 ref = pack2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m), l2e = pack2(LP_LOG2E, LP_LOG2E);
+      const float minus = m == -INFINITY ? 0.f : -m;
+      const f32x2 ref = pack2(minus, minus), l2e = pack2(LP_LOG2E, LP_LOG2E);
       f32x2 s2 = pack2(s, 0.f), w2 = pack2(w, 0.f);
 #pragma unroll
       for (int i = 0; i < LP_VPT; ++i) {
@@ -480,8 +493,8 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
         Batch<T>::Lg::pairs(b.r[i], x);
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) {
-          f32x2 d = add2(x[e], ref);
-          mul2(d, l2e);
+          f32x2 d = ref;
+          fma2(d, x[e], l2e);
           const float2 v = unpack2(d);
           const f32x2 p = pack2(ex2(v.x), ex2(v.y));
           s2 = add2(s2, p);
@@ -517,7 +530,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
       if (batch++ == b0 && tid < a.n_ids && at + b1 - b0 < end) fetch_ids<T>(a, sh, row + 1, 0, min(a.batches, end - at - (b1 - b0)), turn ^ 1);
     }
     // the CTA's state of the row
-    if (a.top_k) select_top<T>(a, sh, row, b0, b1, per, m);
+    if (a.top_k) select_top<T>(a, sh, row, b0, b1, per, most);
     float mm = warp_max(m);
     if (lane == 0) sh.red[0][warp] = mm;
     if (nan) sh.nan = 1;
@@ -525,7 +538,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
 #pragma unroll
     for (int i = 0; i < LP_NW; ++i) mm = fmaxf(mm, sh.red[0][i]);
     {
-      const float d = m == -INFINITY ? 0.f : (m - mm) * LP_LOG2E, f = m == -INFINITY ? 0.f : ex2(d);
+      const float d = m == -INFINITY ? 0.f : m - mm, f = m == -INFINITY ? 0.f : ex2(d);
       w = warp_sum(fmaf(d, s, w) * f);
       s = warp_sum(s * f);
     }
@@ -590,7 +603,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
           const float pm = __ldcg(&p->m), ps = __ldcg(&p->s), pw = __ldcg(&p->w);
           if (__ldcg(&p->nan)) sh.nan = 1;
           if (pm > -INFINITY) {
-            const float d = (pm - mm) * LP_LOG2E, f = ex2(d);
+            const float d = pm - mm, f = ex2(d);
             w = fmaf(fmaf(d, ps, pw), f, w);
             s = fmaf(ps, f, s);
           }
