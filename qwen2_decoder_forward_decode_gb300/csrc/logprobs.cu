@@ -31,6 +31,7 @@ namespace {
 constexpr int LP_NT = 256, LP_NW = LP_NT / 32, LP_VPT = 8, LP_NS = 3;  // threads, warps, a batch's 16-byte vectors a thread, ring
 constexpr int LP_MAX_IDS = 8, LP_MAX_TOP = 32;
 constexpr int LP_CTAS_PER_SM = 2, LP_MAX_CTAS = 640;
+constexpr int LP_END = 5;         // what a row's end costs, in batches
 constexpr int LP_CAP = 384;       // keys in the list and the pushed ones
 constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
 typedef unsigned long long u64;
@@ -47,6 +48,7 @@ struct LogprobArgs {
   const void* logits;
   long long row_stride;
   int n_rows, vocab, n_ids, top_k, batches;  // batches of a row
+  int pieces;  // > 0: rows are cut into so many pieces of their own and CTAs take whole pieces; 0: see Cuts
   const int* ids;
   float* logprobs;
   int* ranks;
@@ -412,6 +414,26 @@ __device__ __noinline__ void fetch_ids(const LogprobArgs& a, Shared& sh, int row
   sh.given[turn][threadIdx.x] = given;
 }
 
+// The list of all rows' batches, cut for the CTAs: into equal ranges (a range may end inside a row and go on with the
+// next), or into ranges of whole row pieces.
+struct Cuts {
+  int batches, pieces, ctas, each, rest, items;
+  __device__ __forceinline__ explicit Cuts(const LogprobArgs& a) : batches(a.batches), pieces(a.pieces), ctas(gridDim.x) {
+    items = pieces ? a.n_rows * pieces : a.n_rows * batches;
+    each = items / ctas;
+    rest = items - each * ctas;
+  }
+  __device__ __forceinline__ int begin(int c) const {
+    const int i = each * c + min(c, rest);
+    return pieces ? i / pieces * batches + i % pieces * batches / pieces : i;
+  }
+  // the CTA that has batch x, the first or the last of a row
+  __device__ __forceinline__ int cta_of(int x) const {
+    const int i = pieces ? x / batches * pieces + (x % batches ? pieces - 1 : 0) : x, big = rest * (each + 1);
+    return i < big ? i / (each + 1) : rest + (i - big) / each;
+  }
+};
+
 // One CTA's range of the list of batches.
 template <typename T>
 __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __grid_constant__ LogprobArgs a) {
@@ -419,10 +441,9 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   extern __shared__ __align__(16) unsigned char lp_ring[];
-  const int total = a.n_rows * a.batches, each = total / (int)gridDim.x, rest = total - each * (int)gridDim.x;
-  auto cut = [&](int c) { return each * c + min(c, rest); };
-  int at = cut(blockIdx.x);
-  const int end = cut(blockIdx.x + 1);
+  const Cuts cuts(a);
+  const int mine = cuts.begin(blockIdx.x), end = cuts.begin(blockIdx.x + 1);
+  int at = mine;
   int ld_row = at / a.batches, ld_batch = at - ld_row * a.batches, to_load = end - at, ld_stage = 0, stage = 0;
   auto stage_ptr = [&](int i) { return lp_ring + (i * LP_NT * LP_VPT + tid) * 16; };
   auto load_next = [&]() {
@@ -443,7 +464,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
   while (at < end) {
     const int row = at / a.batches, b0 = at - row * a.batches, b1 = min(a.batches, b0 + end - at);
     if (tid < a.n_ids) {
-      if (at == cut(blockIdx.x)) fetch_ids<T>(a, sh, row, b0, b1, 0);
+      if (at == mine) fetch_ids<T>(a, sh, row, b0, b1, 0);
       sh.above[tid] = sh.equal[turn][tid];
     }
     if (tid == 0) {
@@ -558,11 +579,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
     if (!write) {
       // part slots as the list is cut: 2 c for the row a CTA begins with, 2 c + 1 for one that it begins itself
       const int r0 = row * a.batches;
-      auto cta_of = [&](int x) {
-        const int big = rest * (each + 1);
-        return x < big ? x / (each + 1) : rest + (x - big) / each;
-      };
-      const int c0 = cta_of(r0), c1 = cta_of(r0 + a.batches - 1), first = 2 * c0 + (cut(c0) < r0 ? 1 : 0);
+      const int c0 = cuts.cta_of(r0), c1 = cuts.cta_of(r0 + a.batches - 1), first = 2 * c0 + (cuts.begin(c0) < r0 ? 1 : 0);
       auto slot_of = [&](int c) { return a.parts + (c == c0 ? first : 2 * c); };
       LogprobPart* mine = slot_of(blockIdx.x);
       if (tid == 0) {
@@ -669,7 +686,14 @@ cudaError_t launch_logprobs(LogprobArgs a, int nsm, cudaStream_t s) {
   // the first vector may begin before the row, by up to N - 1 logits
   a.batches = (int)(((long long)a.vocab + N - 1 + LP_NT * LP_VPT * N - 1) / (LP_NT * LP_VPT * N));
   const long long total = (long long)a.n_rows * a.batches;
-  const int grid = (int)std::min<long long>(total, std::min(nsm * LP_CTAS_PER_SM, LP_MAX_CTAS));
+  const int ctas = std::min(nsm * LP_CTAS_PER_SM, LP_MAX_CTAS);
+  // The last CTA's time, in batches: equal ranges pay for one row end more than they have rows (about LP_END batches:
+  // 8 us of latency against 1.5 us a batch), whole pieces for what the largest range has over the mean.
+  const double equal = (double)total / ctas + LP_END * ((double)a.n_rows / ctas + 1);
+  const int split = a.n_rows >= ctas ? 1 : std::min(ctas / a.n_rows, a.batches);
+  const double whole = (double)(((long long)a.n_rows * split + ctas - 1) / ctas) * ((a.batches + split - 1) / split + LP_END);
+  a.pieces = whole <= equal ? split : 0;
+  const int grid = (int)std::min<long long>(a.pieces ? (long long)a.n_rows * a.pieces : total, ctas);
   constexpr int ring = LP_NS * LP_NT * LP_VPT * 16;
   const cudaError_t e = cudaFuncSetAttribute(logprob_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
   return e ? e : launch_k(logprob_kernel<T>, dim3(grid), dim3(LP_NT), ring, s, false, a);
@@ -717,7 +741,7 @@ qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t voc
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) || (e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)))
     return op_cuda_fail(e, "device query");
-  const LogprobArgs a{logits, row_stride, n_rows, vocab, n_ids, top_k, 0, ids, logprobs, ranks, entropy, top_ids,
+  const LogprobArgs a{logits, row_stride, n_rows, vocab, n_ids, top_k, 0, 0, ids, logprobs, ranks, entropy, top_ids,
                       top_logprobs, (unsigned int*)workspace, (LogprobPart*)((char*)workspace + LP_COUNTER_BYTES), err_dev};
   cudaStream_t s = (cudaStream_t)cuda_stream;
   e = logits_dtype == QW_F32   ? launch_logprobs<float>(a, nsm, s)
