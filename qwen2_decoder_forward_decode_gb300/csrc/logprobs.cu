@@ -8,10 +8,10 @@
 // What bounds it: each logit is read once and costs about ten instructions (one exponential among them), so HBM
 // for fp32 logits and nearly so for 16-bit ones.
 //   - All rows' batches (256 threads x 8 vectors of 16 bytes) form one list, cut into equal consecutive ranges,
-//     one per CTA, two CTAs an SM. A row that a cut divides is joined by the last of its CTAs to arrive;
+//     one per CTA, three CTAs an SM. A row that a cut divides is joined by the last of its CTAs to arrive;
 //     every sum's order is fixed, results repeat bit by bit.
-//   - Each thread copies its own vectors (cp.async) into a ring of three batches and reads them back itself: no
-//     barrier, and up to 128 KB in flight an SM. A batch is then in registers for its passes: maxima,
+//   - Each thread copies its own vectors (cp.async) into a ring of two batches and reads them back itself: no
+//     barrier, and up to 96 KB in flight an SM. A batch is then in registers for its passes: maxima,
 //     exponentials, counts for the ranks.
 //   - Top tokens cost nothing while the row streams by but one stored maximum per thread and group of batches. At
 //     the row's end the top_k-th largest thread maximum bounds the top_k-th logit from below; the groups whose
@@ -28,9 +28,9 @@
 namespace qw {
 namespace {
 
-constexpr int LP_NT = 256, LP_NW = LP_NT / 32, LP_VPT = 8, LP_NS = 3;  // threads, warps, a batch's 16-byte vectors a thread, ring
+constexpr int LP_NT = 256, LP_NW = LP_NT / 32, LP_VPT = 8, LP_NS = 2;  // threads, warps, a batch's 16-byte vectors a thread, ring
 constexpr int LP_MAX_IDS = 8, LP_MAX_TOP = 32;
-constexpr int LP_CTAS_PER_SM = 2, LP_MAX_CTAS = 640;
+constexpr int LP_CTAS_PER_SM = 3, LP_MAX_CTAS = 640;
 constexpr int LP_END = 5;         // what a row's end costs, in batches
 constexpr int LP_CAP = 384;       // keys in the list and the pushed ones
 constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
@@ -162,7 +162,7 @@ template <> struct Logits<f16> : Logits16<f16, __half2> {
   }
 };
 
-constexpr int LP_GROUPS = 16;  // groups of a row's batches, of which each thread keeps a maximum
+constexpr int LP_GROUPS = 8;  // groups of a row's batches, of which each thread keeps a maximum
 constexpr int LP_WORK = 128;   // groups that are read again at a time
 
 struct Shared {

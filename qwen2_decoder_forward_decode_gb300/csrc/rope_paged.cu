@@ -38,69 +38,160 @@ __device__ __forceinline__ void turn_sincos(unsigned long long turns, int pos, f
   if (quadrant >= 2) s = -s;
 }
 
-template <typename T> __device__ __forceinline__ T store_io(float v, int* err);
-template <> __device__ __forceinline__ float store_io<float>(float v, int*) { return v; }
-template <> __device__ __forceinline__ bf16 store_io<bf16>(float v, int*) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ f16 store_io<f16>(float v, int* err) { return to_half_checked(v, err); }
-
-// One thread per (token, pair or value): heads q, then k, then v.
-template <typename IO, typename KV>
-__global__ void rope_append_kernel(const RopeArgs a) {
-  const int half = a.rot / 2;
-  const int per_head = half + (a.hd - a.rot);  // rotated pairs, then single dimensions
-  const int items = (a.nq + a.nkv) * per_head + a.nkv * a.hd;
-  const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const int t = (int)(idx / items);
-  if (t >= a.n_tokens) return;
-  const int it = (int)(idx - (long long)t * items);
-  const long long slot = a.slots[t];
-  const bool open = slot >= 0 && slot < (long long)a.n_pages * a.page;
-  if (!open && slot != -1 && it == 0) atomicOr(a.err, ERR_PAGE);
-  const long long page = open ? slot / a.page : 0;
-  const long long row = page * a.page_stride + (open ? slot - page * a.page : 0) * a.pos_stride;
-  if (it >= (a.nq + a.nkv) * per_head) {  // a value
-    if (!open) return;
-    const int e = it - (a.nq + a.nkv) * per_head, h = e / a.hd;
-    const float x = to_f32(((const IO*)a.v)[t * a.v_stride + e]);
-    ((KV*)a.vc)[row + h * a.head_stride + (e - h * a.hd)] = store_io<KV>(x, a.err);
-    return;
-  }
-  const int h = it / per_head, i = it - h * per_head;
-  const bool is_q = h < a.nq;
-  if (!is_q && !open) return;
-  const IO* src = is_q ? (const IO*)a.q + t * a.q_stride + h * a.hd : (const IO*)a.k + t * a.k_stride + (h - a.nq) * a.hd;
-  int d0, d1 = -1;
-  float y0, y1 = 0.f;
-  if (i < half) {
-    d0 = a.adjacent ? 2 * i : i;
-    d1 = a.adjacent ? 2 * i + 1 : i + half;
-    float c, s;
-    turn_sincos(a.turns[i], a.positions[t], c, s);
-    c *= a.mscale;
-    s *= a.mscale;
-    const float x0 = to_f32(src[d0]), x1 = to_f32(src[d1]);
-    y0 = x0 * c - x1 * s;
-    y1 = x0 * s + x1 * c;
+// W elements as fp32
+template <int W>
+__device__ __forceinline__ void load_w(const float* p, float* x) {
+  if constexpr (W == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
   } else {
-    d0 = a.rot + (i - half);
-    y0 = to_f32(src[d0]);
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = p[i];
   }
-  if (is_q) {
-    IO* dst = (IO*)a.q_out + t * a.qo_stride + h * a.hd;
-    dst[d0] = store_io<IO>(y0, a.err);
-    if (d1 >= 0) dst[d1] = store_io<IO>(y1, a.err);
+}
+template <int W, typename T>
+__device__ __forceinline__ void load_w(const T* p, float* x) {
+  if constexpr (W == 8 || W == 4) {
+    uint32_t u[W / 2];
+    if constexpr (W == 8) *reinterpret_cast<uint4*>(u) = *reinterpret_cast<const uint4*>(p);
+    else *reinterpret_cast<uint2*>(u) = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = to_f32(reinterpret_cast<const T*>(u)[i]);
   } else {
-    KV* dst = (KV*)a.kc + row + (h - a.nq) * a.head_stride;
-    dst[d0] = store_io<KV>(y0, a.err);
-    if (d1 >= 0) dst[d1] = store_io<KV>(y1, a.err);
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = to_f32(p[i]);
+  }
+}
+// fp16 values that overflow, or are not finite, set bad
+__device__ __forceinline__ float cast_io(float v, bool&, float) { return v; }
+__device__ __forceinline__ bf16 cast_io(float v, bool&, bf16) { return __float2bfloat16_rn(v); }
+__device__ __forceinline__ f16 cast_io(float v, bool& bad, f16) {
+  bad |= !(fabsf(v) < 65520.f);
+  return __float2half_rn(v);
+}
+template <int W, typename T>
+__device__ __forceinline__ void store_w(T* p, const float* x, bool& bad) {
+  constexpr int BYTES = W * (int)sizeof(T);
+  if constexpr (BYTES == 16 || BYTES == 8) {
+    alignas(16) T y[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) y[i] = cast_io(x[i], bad, T());
+    if constexpr (BYTES == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(y);
+    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) p[i] = cast_io(x[i], bad, T());
   }
 }
 
+// One CTA per token. Its rot / 2 (cos, sin) pairs are computed once, for all heads, while the token's rows are
+// already on their way: an item is W elements of a head, with their partners rot / 2 further where the pairs are
+// halves, and a thread requests ROPE_ITEMS items before it waits for the angles.
+// What bounds it: every element is read and written once, HBM for long prefills and latency for decode steps.
+constexpr int ROPE_THREADS = 256, ROPE_ITEMS = 3;
+
+template <typename IO, typename KV, int W, bool ADJACENT>
+__global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopeArgs a) {
+  __shared__ float2 cs[128];
+  __shared__ long long s_row;  // the token's row in the caches, -1: none
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const int rotated = ADJACENT ? a.rot / W : a.rot / 2 / W, per_head = rotated + (a.hd - a.rot) / W;
+  const int qk = (a.nq + a.nkv) * per_head, items = qk + a.nkv * (a.hd / W);
+  if (tid < a.rot / 2) {
+    float c, s;
+    turn_sincos(a.turns[tid], a.positions[t], c, s);
+    cs[tid] = make_float2(c * a.mscale, s * a.mscale);
+  }
+  if (tid == ROPE_THREADS - 1) {
+    const long long slot = a.slots[t];
+    long long row = -1;
+    if (slot >= 0 && slot < (long long)a.n_pages * a.page) {
+      const long long page = slot >> 32 ? slot / a.page : (long long)((uint32_t)slot / (uint32_t)a.page);
+      row = page * a.page_stride + (slot - page * a.page) * a.pos_stride;
+    } else if (slot != -1) {
+      atomicOr(a.err, ERR_PAGE);
+    }
+    s_row = row;
+  }
+  bool bad = false;
+#pragma unroll 1
+  for (int first = 0; first < items; first += ROPE_THREADS * ROPE_ITEMS) {
+    const int base = first + tid;
+    float x[ROPE_ITEMS][2][W];
+#pragma unroll
+    for (int k = 0; k < ROPE_ITEMS; ++k) {
+      const int it = base + k * ROPE_THREADS;
+      if (it >= items) continue;
+      if (it < qk) {
+        const int h = it / per_head, i = it - h * per_head;
+        const IO* src = h < a.nq ? (const IO*)a.q + t * a.q_stride + h * a.hd : (const IO*)a.k + t * a.k_stride + (h - a.nq) * a.hd;
+        const int d = i < rotated ? i * W : a.rot + (i - rotated) * W;
+        load_w<W>(src + d, x[k][0]);
+        if (!ADJACENT && i < rotated) load_w<W>(src + d + a.rot / 2, x[k][1]);
+      } else {
+        load_w<W>((const IO*)a.v + t * a.v_stride + (it - qk) * W, x[k][0]);
+      }
+    }
+    if (first == 0) __syncthreads();  // the angles
+    const long long row = s_row;
+#pragma unroll
+    for (int k = 0; k < ROPE_ITEMS; ++k) {
+      const int it = base + k * ROPE_THREADS;
+      if (it >= items) continue;
+      if (it < qk) {
+        const int h = it / per_head, i = it - h * per_head, d = i < rotated ? i * W : a.rot + (i - rotated) * W;
+        if (i < rotated) {
+          if constexpr (ADJACENT) {
+#pragma unroll
+            for (int e = 0; e + 1 < W; e += 2) {
+              const float2 c = cs[(d + e) / 2];
+              const float u = x[k][0][e], v = x[k][0][e + 1];
+              x[k][0][e] = u * c.x - v * c.y;
+              x[k][0][e + 1] = u * c.y + v * c.x;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+              const float2 c = cs[d + e];
+              const float u = x[k][0][e], v = x[k][1][e];
+              x[k][0][e] = u * c.x - v * c.y;
+              x[k][1][e] = u * c.y + v * c.x;
+            }
+          }
+        }
+        if (h < a.nq) {
+          IO* dst = (IO*)a.q_out + t * a.qo_stride + h * a.hd + d;
+          store_w<W>(dst, x[k][0], bad);
+          if (!ADJACENT && i < rotated) store_w<W>(dst + a.rot / 2, x[k][1], bad);
+        } else if (row >= 0) {
+          KV* dst = (KV*)a.kc + row + (h - a.nq) * a.head_stride + d;
+          store_w<W>(dst, x[k][0], bad);
+          if (!ADJACENT && i < rotated) store_w<W>(dst + a.rot / 2, x[k][1], bad);
+        }
+      } else if (row >= 0) {
+        const int e = (it - qk) * W, h = e / a.hd;
+        store_w<W>((KV*)a.vc + row + h * a.head_stride + (e - h * a.hd), x[k][0], bad);
+      }
+    }
+  }
+  if (bad) atomicOr(a.err, ERR_RANGE);
+}
+
+template <typename IO, typename KV, int W>
+cudaError_t launch_rope_w(const RopeArgs& a, cudaStream_t s) {
+  return a.adjacent ? launch_k(rope_append_kernel<IO, KV, W, true>, dim3(a.n_tokens), dim3(ROPE_THREADS), 0, s, false, a)
+                    : launch_k(rope_append_kernel<IO, KV, W, false>, dim3(a.n_tokens), dim3(ROPE_THREADS), 0, s, false, a);
+}
+// W: 16 bytes of io where the rotated halves (or pairs) and the rest divide into such vectors, half of that (16-bit
+// types) or single pairs else.
 template <typename IO, typename KV>
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
-  const long long items = (long long)(a.nq + a.nkv) * (a.rot / 2 + a.hd - a.rot) + (long long)a.nkv * a.hd;
-  const long long blocks = (a.n_tokens * items + 255) / 256;
-  return launch_k(rope_append_kernel<IO, KV>, dim3((unsigned)blocks), dim3(256), 0, s, false, a);
+  const int unit = a.adjacent ? a.rot : a.rot / 2;
+  auto fits = [&](int w) { return unit % w == 0 && (a.hd - a.rot) % w == 0; };
+  if constexpr (sizeof(IO) == 2)
+    if (fits(8)) return launch_rope_w<IO, KV, 8>(a, s);
+  if (fits(4)) return launch_rope_w<IO, KV, 4>(a, s);
+  return a.adjacent ? launch_rope_w<IO, KV, 2>(a, s) : launch_rope_w<IO, KV, 1>(a, s);
 }
 
 }  // namespace
