@@ -336,7 +336,8 @@ typedef struct {
  * If the step does not fit (too few free pages, more than max_tokens tokens or max_blocks pages
  * of a sequence, a negative length or count, n_free outside [0, n_pages]) QW_DEV_CAPACITY is
  * set and the step is empty: lens_out = lens, n_free_out = n_free, cu_tokens 0, positions 0,
- * slots -1. A page id outside [0, n_pages) gives slot -1 and sets QW_DEV_PAGE. n_seqs <= 16384.
+ * slots -1. A page id outside [0, n_pages) gives slot -1 and sets QW_DEV_PAGE. n_seqs <= 16384,
+ * n_pages and max_tokens <= 2^30.
  * With n_seqs = 0 the outputs are those of an empty step. max_tokens = 0 is allowed. */
 qw_status qw_op_page_plan(int32_t n_seqs, int32_t page_size, int32_t n_pages, int32_t max_blocks, int32_t max_tokens,
                           const int32_t *lens, const int32_t *n_new, const int32_t *free_pages,
@@ -351,7 +352,7 @@ qw_status qw_op_page_plan(int32_t n_seqs, int32_t page_size, int32_t n_pages, in
  * The table is not written. If the list would exceed n_pages, a length is negative or beyond
  * max_blocks pages, or n_free is outside [0, n_pages], QW_DEV_CAPACITY is set, lens_out = lens
  * and n_free_out = n_free, and no page moves. A page id outside [0, n_pages) moves as it is and
- * sets QW_DEV_PAGE. n_seqs <= 16384. */
+ * sets QW_DEV_PAGE. n_seqs <= 16384, n_pages <= 2^30. */
 qw_status qw_op_page_release(int32_t n_seqs, int32_t page_size, int32_t n_pages, int32_t max_blocks,
                              const int32_t *lens, const int32_t *done, const int32_t *block_table,
                              int32_t *free_pages, const int32_t *n_free, int32_t *lens_out,

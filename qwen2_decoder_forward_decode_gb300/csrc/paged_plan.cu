@@ -4,8 +4,13 @@
 // With have_b = ceil(len_b / page) and need_b = ceil((len_b + new_b) / page), sequence b takes
 // need_b - have_b pages. Two exclusive prefix sums over the sequences (tokens and pages) place every
 // token and every page: token t belongs to the last b with cu[b] <= t, page i of the step to the last
-// b with pg[b] <= i, and that page is free[n_free - 1 - i]. The sums live in shared memory; tokens and
-// pages are then independent (a binary search each).
+// b with pg[b] <= i, and that page is free[n_free - 1 - i]. Every CTA computes the sums into its shared
+// memory (at most 16384 sequences); tokens, up to four to a thread, and pages are then independent, with
+// a binary search each.
+// What bounds it: latency (two dependent loads, a scan, a search, one more load). A step of at most
+// PLAN_SMALL tokens, or a release of as many table entries, takes one CTA; more are spread over the SMs.
+// Outputs that alias inputs (lengths and the free count) are then written by a second, small kernel, since
+// a CTA may still be reading when another writes.
 #include "common.cuh"
 #include "op_util.h"
 
@@ -13,7 +18,8 @@ namespace qw {
 namespace {
 
 constexpr int PLAN_MAX_SEQS = 16384;
-constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_SMALL = 8192;
 
 struct PlanArgs {
   int n, page, n_pages, max_blocks, max_tokens;
@@ -21,63 +27,70 @@ struct PlanArgs {
   int *table, *lens_out, *n_free_out, *cu, *positions;
   long long* slots;
   int* err;
+  bool items, counts;  // what this launch writes: tokens and pages; the lengths and the free count
 };
 struct ReleaseArgs {
   int n, page, n_pages, max_blocks;
   const int *lens, *done, *table, *n_free;
   int *free_pages, *lens_out, *n_free_out, *err;
+  bool items, counts;
 };
 
-__device__ __forceinline__ long long warp_incl_scan(long long v) {
+constexpr uint32_t PLAN_CAP = 0x7fffffffu;
+__device__ __forceinline__ uint32_t cap_add(uint32_t a, uint32_t b) { return min(a + b, PLAN_CAP); }  // a, b <= PLAN_CAP
+__device__ __forceinline__ uint32_t warp_incl_scan(uint32_t v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v = cap_add(v, u);
   }
   return v;
 }
 
-// Exclusive prefix sums over n items of two non-negative counts (item(i, a, b) gives them) into
-// sa[0 .. n] and sb[0 .. n]. Sums above 2^31 - 1 are cut there and returned as they are in tot.
+// Exclusive prefix sums over n items of two counts (item(i, a, b) gives them) into sa[0 .. n] and sb[0 .. n]. A sum
+// that reaches 2^31 - 1 stays there.
 template <typename Item>
-__device__ void block_scan2(int n, int* sa, int* sb, long long* tot, Item item) {
-  __shared__ long long wa[PLAN_THREADS / 32], wb[PLAN_THREADS / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  const long long cap = 0x7fffffffll;
-  long long ca = 0, cb = 0;  // sums of the items before this chunk
-  for (int base = 0; base < n; base += blockDim.x) {
-    const int i = base + tid;
-    long long a = 0, b = 0;
-    if (i < n) item(i, a, b);
-    const long long ia = warp_incl_scan(a), ib = warp_incl_scan(b);
-    if (lane == 31) {
-      wa[warp] = ia;
-      wb[warp] = ib;
-    }
-    __syncthreads();
-    long long oa = ca, ob = cb;
-    for (int w = 0; w < nw; ++w) {
-      if (w < warp) {
-        oa += wa[w];
-        ob += wb[w];
-      }
-      ca += wa[w];
-      cb += wb[w];
-    }
-    if (i < n) {
-      const long long xa = oa + ia - a, xb = ob + ib - b;
-      sa[i] = (int)(xa < cap ? xa : cap);
-      sb[i] = (int)(xb < cap ? xb : cap);
-    }
-    __syncthreads();
+__device__ __forceinline__ void block_scan2(int n, int* sa, int* sb, Item item) {
+  __shared__ uint32_t wa[32], wb[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (n + PLAN_THREADS - 1) / PLAN_THREADS, i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  uint32_t a = 0, b = 0;  // of the thread's consecutive items
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) {
+    uint32_t x = 0, y = 0;
+    item(i, x, y);
+    a = cap_add(a, x);
+    b = cap_add(b, y);
   }
-  if (tid == 0) {
-    sa[n] = (int)(ca < cap ? ca : cap);
-    sb[n] = (int)(cb < cap ? cb : cap);
+  const uint32_t ia = warp_incl_scan(a), ib = warp_incl_scan(b);
+  if (warp == 0) wa[lane] = wb[lane] = 0;
+  __syncthreads();
+  if (lane == 31) {
+    wa[warp] = ia;
+    wb[warp] = ib;
   }
-  tot[0] = ca;
-  tot[1] = cb;
+  __syncthreads();
+  const uint32_t ta = warp_incl_scan(wa[lane]), tb = warp_incl_scan(wb[lane]);  // every warp scans the warps' sums
+  uint32_t oa = warp ? __shfl_sync(0xffffffffu, ta, warp - 1) : 0, ob = warp ? __shfl_sync(0xffffffffu, tb, warp - 1) : 0;
+  const uint32_t pa = __shfl_up_sync(0xffffffffu, ia, 1), pb = __shfl_up_sync(0xffffffffu, ib, 1);
+  if (lane) {
+    oa = cap_add(oa, pa);
+    ob = cap_add(ob, pb);
+  }
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) {
+    uint32_t x = 0, y = 0;
+    item(i, x, y);
+    sa[i] = (int)oa;
+    sb[i] = (int)ob;
+    oa = cap_add(oa, x);
+    ob = cap_add(ob, y);
+  }
+  if (tid == PLAN_THREADS - 1) {
+    sa[n] = (int)ta;
+    sb[n] = (int)tb;
+  }
   __syncthreads();
 }
 
@@ -92,56 +105,81 @@ __device__ __forceinline__ int find_seq(const int* s, int n, int x) {
   return lo;
 }
 
+__device__ __forceinline__ int pages_of(long long positions, int page) {
+  return (int)(positions >> 31 ? (positions + page - 1) / page : ((uint32_t)positions + (uint32_t)page - 1u) / (uint32_t)page);
+}
+
 __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(const PlanArgs a) {
   extern __shared__ int plan_sm[];
   int* cu = plan_sm;           // [n + 1] tokens before a sequence
   int* pg = plan_sm + a.n + 1;  // [n + 1] pages taken before it
   __shared__ int s_bad;
   const int tid = threadIdx.x;
+  if (!a.items) pdl_wait();  // (the launch that reads what this one overwrites)
   if (tid == 0) s_bad = 0;
-  __syncthreads();
   const int n_free = *a.n_free;
   const long long room = (long long)a.max_blocks * a.page;
-  long long tot[2];
-  block_scan2(a.n, cu, pg, tot, [&](int i, long long& t, long long& p) {
+  __syncthreads();
+  block_scan2(a.n, cu, pg, [&](int i, uint32_t& t, uint32_t& p) {
     const int len = a.lens[i], add = a.n_new ? a.n_new[i] : 1;
     if (len < 0 || add < 0 || (long long)len + add > room) {
       s_bad = 1;
       return;
     }
-    t = add;
-    p = ((long long)len + add + a.page - 1) / a.page - (len + (long long)a.page - 1) / a.page;
+    t = (uint32_t)add;
+    p = (uint32_t)(pages_of((long long)len + add, a.page) - pages_of(len, a.page));
   });
-  const bool bad = s_bad || n_free < 0 || n_free > a.n_pages || tot[0] > a.max_tokens || tot[1] > n_free;
-  if (bad && tid == 0) atomicOr(a.err, ERR_CAPACITY);
-  const int n_tok = bad ? 0 : (int)tot[0], n_take = bad ? 0 : (int)tot[1];
-  for (int i = tid; i < n_take; i += blockDim.x) {
-    const int b = find_seq(pg, a.n, i);
-    const int have = (int)((a.lens[b] + (long long)a.page - 1) / a.page);
-    a.table[(size_t)b * a.max_blocks + have + (i - pg[b])] = a.free_pages[n_free - 1 - i];
-  }
-  for (int t = tid; t < a.max_tokens; t += blockDim.x) {
-    int pos = 0;
-    long long slot = -1;
-    if (t < n_tok) {
-      const int b = find_seq(cu, a.n, t);
-      const int len = a.lens[b];
-      pos = len + (t - cu[b]);
-      const int have = (int)((len + (long long)a.page - 1) / a.page);
-      const int j = pos / a.page;
-      const int id = j < have ? a.table[(size_t)b * a.max_blocks + j] : a.free_pages[n_free - 1 - (pg[b] + j - have)];
-      if (id >= 0 && id < a.n_pages) slot = (long long)id * a.page + (pos - j * a.page);
-      else atomicOr(a.err, ERR_PAGE);
+  // (a capped sum is 2^31 - 1; so many pages are never free, and a step of so many tokens is refused too)
+  const bool bad = s_bad || n_free < 0 || n_free > a.n_pages || cu[a.n] > a.max_tokens || (uint32_t)cu[a.n] == PLAN_CAP || pg[a.n] > n_free;
+  if (bad && tid == 0 && blockIdx.x == 0) atomicOr(a.err, ERR_CAPACITY);
+  const int n_tok = bad ? 0 : cu[a.n], n_take = bad ? 0 : pg[a.n];
+  const int first = blockIdx.x * PLAN_THREADS + tid, step = gridDim.x * PLAN_THREADS;
+  const int run = a.max_tokens > step ? 4 : 1;  // tokens a thread maps in a row: one search, mostly one page
+  if (a.items) {
+#pragma unroll 1
+    for (int i = first; i < n_take; i += step) {
+      const int b = find_seq(pg, a.n, i);
+      a.table[(size_t)b * a.max_blocks + pages_of(a.lens[b], a.page) + (i - pg[b])] = a.free_pages[n_free - 1 - i];
     }
-    a.positions[t] = pos;
-    a.slots[t] = slot;
+#pragma unroll 1
+    for (int t0 = run * first; t0 < a.max_tokens; t0 += run * step) {
+      int b = t0 < n_tok ? find_seq(cu, a.n, t0) : 0, in = -1, id = 0, len = 0, have = 0;  // in: page of the sequence that id is
+      if (t0 < n_tok) {
+        len = a.lens[b];
+        have = pages_of(len, a.page);
+      }
+#pragma unroll 1
+      for (int t = t0; t < min(t0 + run, a.max_tokens); ++t) {
+        int pos = 0;
+        long long slot = -1;
+        if (t < n_tok) {
+          while (t >= cu[b + 1]) {
+            ++b;
+            in = -1;
+            len = a.lens[b];
+            have = pages_of(len, a.page);
+          }
+          pos = len + (t - cu[b]);
+          const int j = (int)((uint32_t)pos / (uint32_t)a.page);
+          if (j != in) {
+            in = j;
+            id = j < have ? a.table[(size_t)b * a.max_blocks + j] : a.free_pages[n_free - 1 - (pg[b] + j - have)];
+          }
+          if (id >= 0 && id < a.n_pages) slot = (long long)id * a.page + (pos - j * a.page);
+          else atomicOr(a.err, ERR_PAGE);
+        }
+        a.positions[t] = pos;
+        a.slots[t] = slot;
+      }
+    }
+    if (blockIdx.x == 0)
+      for (int i = tid; i <= a.n; i += PLAN_THREADS) a.cu[i] = bad ? 0 : cu[i];
   }
-  __syncthreads();  // lens_out may be lens
-  for (int i = tid; i <= a.n; i += blockDim.x) {
-    a.cu[i] = bad ? 0 : cu[i];
-    if (i < a.n) a.lens_out[i] = a.lens[i] + (bad ? 0 : cu[i + 1] - cu[i]);
+  if (a.counts && blockIdx.x == 0) {
+    __syncthreads();  // lens_out may be lens
+    for (int i = tid; i < a.n; i += PLAN_THREADS) a.lens_out[i] = a.lens[i] + (bad ? 0 : cu[i + 1] - cu[i]);
+    if (tid == 0) *a.n_free_out = n_free - n_take;
   }
-  if (tid == 0) *a.n_free_out = n_free - n_take;
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS) page_release_kernel(const ReleaseArgs a) {
@@ -150,46 +188,65 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_release_kernel(const Releas
   int* gone = plan_sm + a.n + 1;   // [n + 1] sequences finished before it
   __shared__ int s_bad;
   const int tid = threadIdx.x;
+  if (!a.items) pdl_wait();
   if (tid == 0) s_bad = 0;
-  __syncthreads();
   const int n_free = *a.n_free;
   const long long room = (long long)a.max_blocks * a.page;
-  long long tot[2];
-  block_scan2(a.n, pg, gone, tot, [&](int i, long long& p, long long& g) {
+  __syncthreads();
+  block_scan2(a.n, pg, gone, [&](int i, uint32_t& p, uint32_t& g) {
     const int len = a.lens[i];
     if (len < 0 || len > room) {
       s_bad = 1;
       return;
     }
     if (!a.done[i]) return;
-    p = (len + (long long)a.page - 1) / a.page;
+    p = (uint32_t)pages_of(len, a.page);
     g = 1;
   });
-  const bool bad = s_bad || n_free < 0 || n_free > a.n_pages || tot[0] > a.n_pages - n_free;
-  if (bad && tid == 0) atomicOr(a.err, ERR_CAPACITY);
-  const int n_give = bad ? 0 : (int)tot[0];
-  for (int i = tid; i < n_give; i += blockDim.x) {
-    const int b = find_seq(pg, a.n, i);
-    const int id = a.table[(size_t)b * a.max_blocks + (i - pg[b])];
-    if (id < 0 || id >= a.n_pages) atomicOr(a.err, ERR_PAGE);
-    a.free_pages[n_free + i] = id;
+  const bool bad = s_bad || n_free < 0 || n_free > a.n_pages || pg[a.n] > a.n_pages - n_free;
+  if (bad && tid == 0 && blockIdx.x == 0) atomicOr(a.err, ERR_CAPACITY);
+  const int n_give = bad ? 0 : pg[a.n];
+  if (a.items) {
+#pragma unroll 1
+    for (int i = blockIdx.x * PLAN_THREADS + tid; i < n_give; i += gridDim.x * PLAN_THREADS) {
+      const int b = find_seq(pg, a.n, i);
+      const int id = a.table[(size_t)b * a.max_blocks + (i - pg[b])];
+      if (id < 0 || id >= a.n_pages) atomicOr(a.err, ERR_PAGE);
+      a.free_pages[n_free + i] = id;
+    }
   }
-  __syncthreads();  // lens_out may be lens
-  for (int i = tid; i < a.n; i += blockDim.x) a.lens_out[i] = !bad && gone[i + 1] > gone[i] ? 0 : a.lens[i];
-  if (tid == 0) *a.n_free_out = n_free + n_give;
+  if (a.counts && blockIdx.x == 0) {
+    __syncthreads();  // lens_out may be lens
+    for (int i = tid; i < a.n; i += PLAN_THREADS) a.lens_out[i] = !bad && gone[i + 1] > gone[i] ? 0 : a.lens[i];
+    if (tid == 0) *a.n_free_out = n_free + n_give;
+  }
 }
 
-template <typename K>
-cudaError_t plan_smem(K kernel, int n, size_t* bytes) {
-  *bytes = (size_t)2 * (n + 1) * sizeof(int);
-  return *bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*bytes)
-                            : cudaSuccess;
+// One launch, or, where several CTAs read what the call overwrites, a second one for the counts.
+template <typename K, typename Args>
+cudaError_t launch_plan(K kernel, Args a, int64_t items, bool aliased, cudaStream_t s) {
+  const size_t smem = (size_t)2 * (a.n + 1) * sizeof(int);
+  cudaError_t e = cudaSuccess;
+  int dev = 0, nsm = 0, ctas = 1;
+  if (smem > 40 * 1024 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) return e;
+  if (items > PLAN_SMALL) {
+    if ((e = cudaGetDevice(&dev)) || (e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev))) return e;
+    const int64_t want = (items + 4 * PLAN_THREADS - 1) / (4 * PLAN_THREADS);
+    ctas = want < nsm ? (int)want : nsm;
+  }
+  a.items = true;
+  a.counts = ctas == 1 || !aliased;
+  if ((e = launch_k(kernel, dim3(ctas), dim3(PLAN_THREADS), smem, s, false, a)) || a.counts) return e;
+  a.items = false;
+  a.counts = true;
+  return launch_k(kernel, dim3(1), dim3(PLAN_THREADS), smem, s, true, a);
 }
 
 qw_status plan_dims(int32_t n_seqs, int32_t page_size, int32_t n_pages, int32_t max_blocks) {
   if (n_seqs < 0 || page_size < 1 || n_pages < 1 || max_blocks < 1)
     return op_fail(QW_ERR_INVALID_ARG, "bad page plan dimension");
   if (n_seqs > PLAN_MAX_SEQS) return op_fail(QW_ERR_UNSUPPORTED, "more than 16384 sequences");
+  if (n_pages > 1 << 30) return op_fail(QW_ERR_UNSUPPORTED, "more than 2^30 pages");
   return QW_OK;
 }
 
@@ -209,6 +266,7 @@ qw_status qw_op_page_plan(int32_t n_seqs, int32_t page_size, int32_t n_pages, in
   qw_status st = plan_dims(n_seqs, page_size, n_pages, max_blocks);
   if (st) return st;
   if (max_tokens < 0) return op_fail(QW_ERR_INVALID_ARG, "negative max_tokens");
+  if (max_tokens > 1 << 30) return op_fail(QW_ERR_UNSUPPORTED, "more than 2^30 tokens");
   if (!free_pages || !n_free || !n_free_out || !cu_tokens || !err_dev) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
   if (n_seqs > 0 && (!lens || !block_table || !lens_out)) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
   if (max_tokens > 0 && (!positions || !slots)) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
@@ -216,12 +274,11 @@ qw_status qw_op_page_plan(int32_t n_seqs, int32_t page_size, int32_t n_pages, in
   if ((st = op_check_device({lens, n_new, free_pages, n_free, block_table, lens_out, n_free_out, cu_tokens, positions,
                              slots, err_dev})))
     return st;
-  PlanArgs a{n_seqs, page_size, n_pages, max_blocks, max_tokens, lens, n_new, free_pages, n_free, block_table,
-             lens_out, n_free_out, cu_tokens, positions, (long long*)slots, err_dev};
-  size_t smem;
-  cudaError_t e = plan_smem(page_plan_kernel, n_seqs, &smem);
-  if (e) return op_cuda_fail(e, "page plan attributes");
-  if ((e = launch_k(page_plan_kernel, dim3(1), dim3(PLAN_THREADS), smem, (cudaStream_t)cuda_stream, false, a)))
+  const PlanArgs a{n_seqs, page_size, n_pages, max_blocks, max_tokens, lens, n_new, free_pages, n_free, block_table,
+                   lens_out, n_free_out, cu_tokens, positions, (long long*)slots, err_dev, true, true};
+  const cudaError_t e =
+      launch_plan(page_plan_kernel, a, max_tokens, lens_out == lens || n_free_out == n_free, (cudaStream_t)cuda_stream);
+  if (e)
     return op_cuda_fail(e, "page plan launch");
   return QW_OK;
 }
@@ -236,12 +293,12 @@ qw_status qw_op_page_release(int32_t n_seqs, int32_t page_size, int32_t n_pages,
   if (!free_pages || !n_free || !n_free_out || !err_dev) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
   if (n_seqs > 0 && (!lens || !done || !block_table || !lens_out)) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
   if ((st = op_check_device({lens, done, block_table, free_pages, n_free, lens_out, n_free_out, err_dev}))) return st;
-  ReleaseArgs a{n_seqs, page_size, n_pages, max_blocks, lens, done, block_table, n_free, free_pages, lens_out,
-                n_free_out, err_dev};
-  size_t smem;
-  cudaError_t e = plan_smem(page_release_kernel, n_seqs, &smem);
-  if (e) return op_cuda_fail(e, "page release attributes");
-  if ((e = launch_k(page_release_kernel, dim3(1), dim3(PLAN_THREADS), smem, (cudaStream_t)cuda_stream, false, a)))
+  const ReleaseArgs a{n_seqs, page_size, n_pages, max_blocks, lens, done, block_table, n_free, free_pages, lens_out,
+                      n_free_out, err_dev, true, true};
+  const int64_t entries = (int64_t)n_seqs * max_blocks;
+  const cudaError_t e = launch_plan(page_release_kernel, a, entries < n_pages ? entries : n_pages,
+                                    lens_out == lens || n_free_out == n_free, (cudaStream_t)cuda_stream);
+  if (e)
     return op_cuda_fail(e, "page release launch");
   return QW_OK;
 }

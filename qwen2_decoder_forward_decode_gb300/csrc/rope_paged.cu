@@ -38,30 +38,12 @@ __device__ __forceinline__ void turn_sincos(unsigned long long turns, int pos, f
   if (quadrant >= 2) s = -s;
 }
 
-// W elements as fp32
-template <int W>
-__device__ __forceinline__ void load_w(const float* p, float* x) {
-  if constexpr (W == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = p[i];
-  }
-}
-template <int W, typename T>
-__device__ __forceinline__ void load_w(const T* p, float* x) {
-  if constexpr (W == 8 || W == 4) {
-    uint32_t u[W / 2];
-    if constexpr (W == 8) *reinterpret_cast<uint4*>(u) = *reinterpret_cast<const uint4*>(p);
-    else *reinterpret_cast<uint2*>(u) = *reinterpret_cast<const uint2*>(p);
-#pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = to_f32(reinterpret_cast<const T*>(u)[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = to_f32(p[i]);
-  }
-}
+// W elements as they lie in memory
+template <typename T, int W>
+struct alignas(W * sizeof(T) >= 16 ? 16 : W * sizeof(T)) Raw {
+  T x[W];
+};
+
 // fp16 values that overflow, or are not finite, set bad
 __device__ __forceinline__ float cast_io(float v, bool&, float) { return v; }
 __device__ __forceinline__ bf16 cast_io(float v, bool&, bf16) { return __float2bfloat16_rn(v); }
@@ -71,116 +53,202 @@ __device__ __forceinline__ f16 cast_io(float v, bool& bad, f16) {
 }
 template <int W, typename T>
 __device__ __forceinline__ void store_w(T* p, const float* x, bool& bad) {
-  constexpr int BYTES = W * (int)sizeof(T);
-  if constexpr (BYTES == 16 || BYTES == 8) {
-    alignas(16) T y[W];
+  Raw<T, W> y;
 #pragma unroll
-    for (int i = 0; i < W; ++i) y[i] = cast_io(x[i], bad, T());
-    if constexpr (BYTES == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(y);
-    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(y);
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) p[i] = cast_io(x[i], bad, T());
-  }
+  for (int i = 0; i < W; ++i) y.x[i] = cast_io(x[i], bad, T());
+  *reinterpret_cast<Raw<T, W>*>(p) = y;
 }
 
-// One CTA per token. Its rot / 2 (cos, sin) pairs are computed once, for all heads, while the token's rows are
-// already on their way: an item is W elements of a head, with their partners rot / 2 further where the pairs are
-// halves, and a thread requests ROPE_ITEMS items before it waits for the angles.
+// A CTA takes every gridDim-th token. An item is W elements of a head, with their partners rot / 2 further where the
+// pairs are halves; a thread has the same items of every token, so their places are worked out once. It copies
+// them itself (cp.async) into its places of a ring, ROPE_STAGES - 1 tokens ahead, and reads them back itself. The
+// rot / 2 (cos, sin) pairs, which all heads share, are computed a token ahead.
 // What bounds it: every element is read and written once, HBM for long prefills and latency for decode steps.
-constexpr int ROPE_THREADS = 256, ROPE_ITEMS = 3;
+// 8191 tokens of 36 bf16 heads of 128: 25.5 us, 5.9 TB/s. A CTA a token, with the same angles and vectors, took
+// 46 us (the chain position - angle - barrier - store, 4 us, is not hidden); tokens ahead in registers
+// instead of the ring 35 us (spills); three stages with three CTAs an SM 26.5 us.
+constexpr int ROPE_THREADS = 256, ROPE_ITEMS = 3, ROPE_STAGES = 2, ROPE_CTAS_PER_SM = 4;
 
 template <typename IO, typename KV, int W, bool ADJACENT>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopeArgs a) {
-  __shared__ float2 cs[128];
-  __shared__ long long s_row;  // the token's row in the caches, -1: none
-  const int t = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS_PER_SM) rope_append_kernel(const RopeArgs a) {
+  extern __shared__ __align__(16) unsigned char rope_ring[];  // [stage][item][half][thread] of 16 bytes
+  __shared__ float2 s_cs[2][128];
+  __shared__ long long s_row[2];  // the token's row in the caches, -1: none
+  const int tid = threadIdx.x;
   const int rotated = ADJACENT ? a.rot / W : a.rot / 2 / W, per_head = rotated + (a.hd - a.rot) / W;
   const int qk = (a.nq + a.nkv) * per_head, items = qk + a.nkv * (a.hd / W);
-  if (tid < a.rot / 2) {
-    float c, s;
-    turn_sincos(a.turns[tid], a.positions[t], c, s);
-    cs[tid] = make_float2(c * a.mscale, s * a.mscale);
-  }
-  if (tid == ROPE_THREADS - 1) {
-    const long long slot = a.slots[t];
-    long long row = -1;
-    if (slot >= 0 && slot < (long long)a.n_pages * a.page) {
-      const long long page = slot >> 32 ? slot / a.page : (long long)((uint32_t)slot / (uint32_t)a.page);
-      row = page * a.page_stride + (slot - page * a.page) * a.pos_stride;
-    } else if (slot != -1) {
-      atomicOr(a.err, ERR_PAGE);
-    }
-    s_row = row;
-  }
   bool bad = false;
-#pragma unroll 1
-  for (int first = 0; first < items; first += ROPE_THREADS * ROPE_ITEMS) {
-    const int base = first + tid;
-    float x[ROPE_ITEMS][2][W];
-#pragma unroll
-    for (int k = 0; k < ROPE_ITEMS; ++k) {
-      const int it = base + k * ROPE_THREADS;
-      if (it >= items) continue;
-      if (it < qk) {
-        const int h = it / per_head, i = it - h * per_head;
-        const IO* src = h < a.nq ? (const IO*)a.q + t * a.q_stride + h * a.hd : (const IO*)a.k + t * a.k_stride + (h - a.nq) * a.hd;
-        const int d = i < rotated ? i * W : a.rot + (i - rotated) * W;
-        load_w<W>(src + d, x[k][0]);
-        if (!ADJACENT && i < rotated) load_w<W>(src + d + a.rot / 2, x[k][1]);
+
+  struct Item {
+    const IO* src;       // token 0's
+    long long stride;    // from token to token
+    void* dst;           // q_out's token 0, or the caches' row 0
+    int d;               // dimension; -1: not rotated, -2: no item
+    bool is_q;
+  };
+  auto item = [&](int it) {
+    Item m{nullptr, 0, nullptr, -2, false};
+    if (it < qk) {
+      const int h = it / per_head, i = it - h * per_head, d = i < rotated ? i * W : a.rot + (i - rotated) * W;
+      m.d = i < rotated ? d : -1;
+      m.is_q = h < a.nq;
+      if (m.is_q) {
+        m.src = (const IO*)a.q + h * a.hd + d;
+        m.stride = a.q_stride;
+        m.dst = (IO*)a.q_out + h * a.hd + d;
       } else {
-        load_w<W>((const IO*)a.v + t * a.v_stride + (it - qk) * W, x[k][0]);
+        m.src = (const IO*)a.k + (h - a.nq) * a.hd + d;
+        m.stride = a.k_stride;
+        m.dst = (KV*)a.kc + (h - a.nq) * a.head_stride + d;
+      }
+    } else if (it < items) {
+      const int e = (it - qk) * W, h = e / a.hd;
+      m.src = (const IO*)a.v + e;
+      m.stride = a.v_stride;
+      m.dst = (KV*)a.vc + h * a.head_stride + (e - h * a.hd);
+      m.d = -1;
+    }
+    return m;
+  };
+  typedef Raw<IO, W> R;
+  auto place = [&](int stage, int k, int half) {
+    return reinterpret_cast<R*>(rope_ring + (((stage * ROPE_ITEMS + k) * 2 + half) * ROPE_THREADS + tid) * 16);
+  };
+  auto copy = [&](R* to, const IO* from) {
+    if constexpr (sizeof(R) == 2) *to = *reinterpret_cast<const R*>(from);
+    else if constexpr (sizeof(R) == 16) cp_async16(to, from);
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(to)), "l"(from), "n"(sizeof(R)) : "memory");
+  };
+  auto write = [&](const Item& m, int t, const R* r, const float2* cs, long long row) {
+    if (m.d == -2 || (!m.is_q && row < 0)) return;
+    float x[2][W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      x[0][e] = to_f32(r[0].x[e]);
+      if (!ADJACENT) x[1][e] = to_f32(r[1].x[e]);
+    }
+    if (m.d >= 0) {
+      if constexpr (ADJACENT) {
+#pragma unroll
+        for (int e = 0; e + 1 < W; e += 2) {
+          const float2 c = cs[(m.d + e) / 2];
+          const float u = x[0][e], v = x[0][e + 1];
+          x[0][e] = u * c.x - v * c.y;
+          x[0][e + 1] = u * c.y + v * c.x;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const float2 c = cs[m.d + e];
+          const float u = x[0][e], v = x[1][e];
+          x[0][e] = u * c.x - v * c.y;
+          x[1][e] = u * c.y + v * c.x;
+        }
       }
     }
-    if (first == 0) __syncthreads();  // the angles
-    const long long row = s_row;
+    if (m.is_q) {
+      IO* dst = (IO*)m.dst + t * a.qo_stride;
+      store_w<W>(dst, x[0], bad);
+      if (!ADJACENT && m.d >= 0) store_w<W>(dst + a.rot / 2, x[1], bad);
+    } else {
+      KV* dst = (KV*)m.dst + row;
+      store_w<W>(dst, x[0], bad);
+      if (!ADJACENT && m.d >= 0) store_w<W>(dst + a.rot / 2, x[1], bad);
+    }
+  };
+  // positions and slots are read a token before they are used
+  const bool turns = tid < a.rot / 2, slots = tid == ROPE_THREADS - 1;
+  const unsigned long long my_turns = turns ? a.turns[tid] : 0;
+  int pos = 0;
+  long long slot = -1;
+  auto look = [&](int t) {
+    if (turns && t < a.n_tokens) pos = a.positions[t];
+    if (slots && t < a.n_tokens) slot = a.slots[t];
+  };
+  auto angles = [&](int side) {  // the pairs and the cache row of the token looked at last
+    if (turns) {
+      float c, s;
+      turn_sincos(my_turns, pos, c, s);
+      s_cs[side][tid] = make_float2(c * a.mscale, s * a.mscale);
+    }
+    if (slots) {
+      long long row = -1;
+      if (slot >= 0 && slot < (long long)a.n_pages * a.page) {
+        const long long page = slot >> 32 ? slot / a.page : (long long)((uint32_t)slot / (uint32_t)a.page);
+        row = page * a.page_stride + (slot - page * a.page) * a.pos_stride;
+      } else if (slot != -1) {
+        atomicOr(a.err, ERR_PAGE);
+      }
+      s_row[side] = row;
+    }
+  };
+
+  Item mine[ROPE_ITEMS];
+#pragma unroll
+  for (int k = 0; k < ROPE_ITEMS; ++k) mine[k] = item(tid + k * ROPE_THREADS);
+  int ahead = blockIdx.x, ld_stage = 0, stage = 0, side = 0;
+  auto load_next = [&]() {
+    if (ahead < a.n_tokens) {
+#pragma unroll
+      for (int k = 0; k < ROPE_ITEMS; ++k) {
+        if (mine[k].d == -2) continue;
+        const IO* src = mine[k].src + ahead * mine[k].stride;
+        copy(place(ld_stage, k, 0), src);
+        if (!ADJACENT && mine[k].d >= 0) copy(place(ld_stage, k, 1), src + a.rot / 2);
+      }
+      ahead += gridDim.x;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++ld_stage == ROPE_STAGES) ld_stage = 0;
+  };
+  look(blockIdx.x);
+#pragma unroll 1
+  for (int i = 0; i < ROPE_STAGES - 1; ++i) load_next();
+  angles(0);
+  look(blockIdx.x + gridDim.x);
+  __syncthreads();
+#pragma unroll 1
+  for (int t = blockIdx.x; t < a.n_tokens; t += gridDim.x) {
+    load_next();
+    asm volatile("cp.async.wait_group %0;" ::"n"(ROPE_STAGES - 1) : "memory");
+    const long long row = s_row[side];
 #pragma unroll
     for (int k = 0; k < ROPE_ITEMS; ++k) {
-      const int it = base + k * ROPE_THREADS;
-      if (it >= items) continue;
-      if (it < qk) {
-        const int h = it / per_head, i = it - h * per_head, d = i < rotated ? i * W : a.rot + (i - rotated) * W;
-        if (i < rotated) {
-          if constexpr (ADJACENT) {
-#pragma unroll
-            for (int e = 0; e + 1 < W; e += 2) {
-              const float2 c = cs[(d + e) / 2];
-              const float u = x[k][0][e], v = x[k][0][e + 1];
-              x[k][0][e] = u * c.x - v * c.y;
-              x[k][0][e + 1] = u * c.y + v * c.x;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < W; ++e) {
-              const float2 c = cs[d + e];
-              const float u = x[k][0][e], v = x[k][1][e];
-              x[k][0][e] = u * c.x - v * c.y;
-              x[k][1][e] = u * c.y + v * c.x;
-            }
-          }
-        }
-        if (h < a.nq) {
-          IO* dst = (IO*)a.q_out + t * a.qo_stride + h * a.hd + d;
-          store_w<W>(dst, x[k][0], bad);
-          if (!ADJACENT && i < rotated) store_w<W>(dst + a.rot / 2, x[k][1], bad);
-        } else if (row >= 0) {
-          KV* dst = (KV*)a.kc + row + (h - a.nq) * a.head_stride + d;
-          store_w<W>(dst, x[k][0], bad);
-          if (!ADJACENT && i < rotated) store_w<W>(dst + a.rot / 2, x[k][1], bad);
-        }
-      } else if (row >= 0) {
-        const int e = (it - qk) * W, h = e / a.hd;
-        store_w<W>((KV*)a.vc + row + h * a.head_stride + (e - h * a.hd), x[k][0], bad);
-      }
+      R r[2];
+      r[0] = *place(stage, k, 0);
+      if (!ADJACENT) r[1] = *place(stage, k, 1);
+      write(mine[k], t, r, s_cs[side], row);
     }
+#pragma unroll 1
+    for (int it = tid + ROPE_ITEMS * ROPE_THREADS; it < items; it += ROPE_THREADS) {  // of very many heads
+      const Item m = item(it);
+      if (!m.is_q && row < 0) continue;
+      R r[2];
+      const IO* src = m.src + t * m.stride;
+      r[0] = *reinterpret_cast<const R*>(src);
+      if (!ADJACENT && m.d >= 0) r[1] = *reinterpret_cast<const R*>(src + a.rot / 2);
+      write(m, t, r, s_cs[side], row);
+    }
+    if (++stage == ROPE_STAGES) stage = 0;
+    side ^= 1;
+    angles(side);
+    look(t + 2 * gridDim.x);
+    __syncthreads();
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (bad) atomicOr(a.err, ERR_RANGE);
 }
 
 template <typename IO, typename KV, int W>
 cudaError_t launch_rope_w(const RopeArgs& a, cudaStream_t s) {
-  return a.adjacent ? launch_k(rope_append_kernel<IO, KV, W, true>, dim3(a.n_tokens), dim3(ROPE_THREADS), 0, s, false, a)
-                    : launch_k(rope_append_kernel<IO, KV, W, false>, dim3(a.n_tokens), dim3(ROPE_THREADS), 0, s, false, a);
+  int dev = 0, nsm = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) || (e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev))) return e;
+  const dim3 grid(a.n_tokens < nsm * ROPE_CTAS_PER_SM ? a.n_tokens : nsm * ROPE_CTAS_PER_SM);
+  constexpr int ring = ROPE_STAGES * ROPE_ITEMS * 2 * ROPE_THREADS * 16;
+  auto kernel = a.adjacent ? rope_append_kernel<IO, KV, W, true> : rope_append_kernel<IO, KV, W, false>;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring))) return e;
+  return launch_k(kernel, grid, dim3(ROPE_THREADS), ring, s, false, a);
 }
 // W: 16 bytes of io where the rotated halves (or pairs) and the rest divide into such vectors, half of that (16-bit
 // types) or single pairs else.
