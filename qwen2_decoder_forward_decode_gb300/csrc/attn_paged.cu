@@ -38,7 +38,8 @@ namespace {
 template <typename T, int HD, int HB, typename IO>
 struct MmaCfg {
   static constexpr bool F32IO = std::is_same<IO, float>::value;
-  static constexpr int NW = 8, RW = 16, NT = NW * 32;
+  // 16 positions a product; two products a tile for short heads, whose tiles would else be all latency
+  static constexpr int NW = 8, R = HD <= 64 ? 2 : 1, RW = 16 * R, NT = NW * 32;
   static constexpr bool three = F32IO && sizeof(T) == 2 && !std::is_same<T, f16>::value;
   static constexpr int NQ = !F32IO ? 1 : three ? 3 : 2, NP = three ? 3 : 2;
   using Ld = Loader<T, HD, RW, NW>;
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(256, 1) paged_mma_kernel(const PagedAttnArgs a
   using C = MmaCfg<T, HD, HB, IO>;
   using Ld = typename C::Ld;
   using Fin = Finish<IO, HB, HD, C::NT>;
-  constexpr int NW = C::NW, NS = C::NS, NQ = C::NQ, NP = C::NP, CS = comb_stride(HD), TILE = Ld::TILE, V = Ld::V;
+  constexpr int NW = C::NW, NS = C::NS, R = C::R, NQ = C::NQ, NP = C::NP, CS = comb_stride(HD), TILE = Ld::TILE, V = Ld::V;
   using Raw = typename std::conditional<C::F32IO, float2, uint32_t>::type;  // two query elements
   constexpr int NKK = HD / 16, NA = HB == 8 ? (NQ + 1) / 2 : NQ, NPA = HB == 8 ? (NP + 1) / 2 : NP;  // products per step
   static_assert(NS >= 2 && C::SMEM >= PA_JOIN * HB * CS * 4, "the ring, and the parts of a join in its place");
@@ -158,28 +159,34 @@ __global__ void __launch_bounds__(256, 1) paged_mma_kernel(const PagedAttnArgs a
       const uint32_t mask = s_mask[warp][stage];
       if (mask) {
         const uint32_t ks = ring + stage * Ld::STAGE, vs = ks + Ld::STAGE / 2;
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float c[2 * R][4];
+#pragma unroll
+        for (int i = 0; i < 2 * R; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
         const int mi = lane >> 3, r8 = lane & 7;
 #pragma unroll
         for (int kk = 0; kk < NKK; ++kk) {
-          uint32_t b[4];  // keys 0 - 7 and 8 - 15, dimensions kk * 16 .. + 15
-          ldmatrix_x4(b, ks + Ld::at((mi >> 1) * 8 + r8, kk * 2 + (mi & 1)));
 #pragma unroll
-          for (int n = 0; n < NA; ++n) {
-            mma_t(c[0], qa[n][kk], b[0], b[1], T());
-            mma_t(c[1], qa[n][kk], b[2], b[3], T());
+          for (int rr = 0; rr < R; ++rr) {
+            uint32_t b[4];  // keys 0 - 7 and 8 - 15 of 16, dimensions kk * 16 .. + 15
+            ldmatrix_x4(b, ks + Ld::at(rr * 16 + (mi >> 1) * 8 + r8, kk * 2 + (mi & 1)));
+#pragma unroll
+            for (int n = 0; n < NA; ++n) {
+              mma_t(c[2 * rr], qa[n][kk], b[0], b[1], T());
+              mma_t(c[2 * rr + 1], qa[n][kk], b[2], b[3], T());
+            }
           }
         }
-        uint32_t pa[NPA][4];
+        uint32_t pa[R][NPA][4];
 #pragma unroll
         for (int half = 0; half < HB / 8; ++half) {
-          float s[4];  // positions 2 tig, 2 tig + 1, and + 8
+          float s[4 * R];  // positions 2 tig, 2 tig + 1, and + 8, + 16, ...
+          float top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 4 * R; ++i) {
             const float x = HB == 8 ? c[i >> 1][i & 1] + c[i >> 1][2 + (i & 1)] : c[i >> 1][2 * half + (i & 1)];
             s[i] = (mask >> (2 * tig + (i & 1) + 8 * (i >> 1))) & 1 ? x * sc[half] : -INFINITY;
+            top = fmaxf(top, s[i]);
           }
-          float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const float mn = fmaxf(m[half], top);
@@ -197,29 +204,35 @@ __global__ void __launch_bounds__(256, 1) paged_mma_kernel(const PagedAttnArgs a
             m[half] = mn;
           }
           const float ref = (mn == -INFINITY ? 0.f : mn) - PA_BIAS;
-          float e[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = ex2(s[i] - ref);
-          l[half] += (e[0] + e[1]) + (e[2] + e[3]);
-          uint32_t lo[4], hi[4];
-          split<T, NP>(e[0], e[1], lo);
-          split<T, NP>(e[2], e[3], hi);
+          for (int rr = 0; rr < R; ++rr) {
+            float e[4];
 #pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const int n = HB == 8 ? i / 2 : i, rw = HB == 8 ? i & 1 : half;
-            pa[n][rw] = lo[i];
-            pa[n][2 + rw] = hi[i];
+            for (int i = 0; i < 4; ++i) e[i] = ex2(s[4 * rr + i] - ref);
+            l[half] += (e[0] + e[1]) + (e[2] + e[3]);
+            uint32_t lo[4], hi[4];
+            split<T, NP>(e[0], e[1], lo);
+            split<T, NP>(e[2], e[3], hi);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              const int n = HB == 8 ? i / 2 : i, rw = HB == 8 ? i & 1 : half;
+              pa[rr][n][rw] = lo[i];
+              pa[rr][n][2 + rw] = hi[i];
+            }
+            if (HB == 8 && NP & 1) pa[rr][NPA - 1][1] = pa[rr][NPA - 1][3] = 0u;
           }
-          if (HB == 8 && NP & 1) pa[NPA - 1][1] = pa[NPA - 1][3] = 0u;
         }
 #pragma unroll
         for (int dd = 0; dd < NKK; ++dd) {
-          uint32_t b[4];  // dimensions dd * 16 .. + 7 and + 8 .. + 15
-          ldmatrix_x4_t(b, vs + Ld::at((mi & 1) * 8 + r8, dd * 2 + (mi >> 1)));
 #pragma unroll
-          for (int n = 0; n < NPA; ++n) {
-            mma_t(o[2 * dd], pa[n], b[0], b[1], T());
-            mma_t(o[2 * dd + 1], pa[n], b[2], b[3], T());
+          for (int rr = 0; rr < R; ++rr) {
+            uint32_t b[4];  // dimensions dd * 16 .. + 7 and + 8 .. + 15
+            ldmatrix_x4_t(b, vs + Ld::at(rr * 16 + (mi & 1) * 8 + r8, dd * 2 + (mi >> 1)));
+#pragma unroll
+            for (int n = 0; n < NPA; ++n) {
+              mma_t(o[2 * dd], pa[rr][n], b[0], b[1], T());
+              mma_t(o[2 * dd + 1], pa[rr][n], b[2], b[3], T());
+            }
           }
         }
       }
