@@ -417,8 +417,9 @@ qw_status qw_op_rope_append(const qw_paged_kv *cache, int32_t n_tokens, int32_t 
  *       16 bytes. out may be q (with the same stride).
  *   lse fp32 [n_seqs][n_heads], or NULL
  *   workspace at least qw_op_paged_attention_workspace() bytes, 16-byte aligned, zeroed once
- *       before its first use (cudaMemset); every call leaves it ready for the next. Calls
- *       that may run at the same time need workspaces of their own.
+ *       before its first use (cudaMemset); every call leaves it ready for the next, of any
+ *       shape and also of qw_op_token_logprobs. Calls that may run at the same time, captured
+ *       graphs of them included, need workspaces of their own.
  * io_dtype QW_F32 with any cache type, or the cache's own type; sums are fp32. Any n_heads that is
  * a multiple of the cache's n_kv_heads. The result does not depend on the run: equal inputs give
  * equal bits on equal devices. */
@@ -442,7 +443,8 @@ qw_status qw_op_paged_attention(const qw_paged_kv *cache, int32_t n_seqs, int32_
  *   ids, logprobs, ranks [n_rows][n_ids], n_ids 0 .. 8 (0: all three may be NULL); ranks may be NULL
  *   entropy [n_rows] or NULL
  *   top_ids, top_logprobs [n_rows][top_k], top_k 0 .. min(32, vocab) (0: both may be NULL)
- *   workspace as for qw_op_paged_attention, of qw_op_token_logprobs_workspace() bytes. */
+ *   workspace at least qw_op_token_logprobs_workspace() bytes, with the rules of
+ *       qw_op_paged_attention's. Equal inputs give equal bits on equal devices. */
 size_t qw_op_token_logprobs_workspace(int32_t n_rows, int32_t vocab, int32_t top_k);
 qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t vocab, const void *logits,
                                int64_t row_stride, const int32_t *ids, int32_t n_ids, float *logprobs, int32_t *ranks,

@@ -87,19 +87,24 @@ __global__ void __launch_bounds__(256, 1) paged_mma_kernel(const PagedAttnArgs a
   int stage = 0, ahead = NS - 1;  // tiles still to be requested before the first is used
   Place pend[2];
   int n_pend = 0;
-  for (bool left = true; left;) {
-    const int t0 = p.t, t1 = min(p.nt, r.end - p.v - V);
-    // the unit's queries, columns 2 tig, 2 tig + 1 and 2 tig + 8, 2 tig + 9 of every 16: requested here, used
-    // after the first tile's requests
-    Raw xq[HB / 8][NKK][2];
+  // a unit's queries, columns 2 tig, 2 tig + 1 and 2 tig + 8, 2 tig + 9 of every 16: requested before the unit
+  // ahead of it ends, used after its first tile has come
+  Raw xq[HB / 8][NKK][2];
+  auto fetch_q = [&](const Place& u) {
+    const int g = u.u / n_hb, hb = u.u - g * n_hb;
 #pragma unroll
     for (int half = 0; half < HB / 8; ++half) {
-      const int g = p.u / n_hb, h = (p.u - g * n_hb) * HB + gid + 8 * half;
-      const IO* q = (const IO*)a.q + p.b * a.q_stride + (g * group + h) * a.hd + 2 * tig;
+      const int h = hb * HB + gid + 8 * half;
+      const IO* q = (const IO*)a.q + u.b * a.q_stride + (g * group + h) * a.hd + 2 * tig;
 #pragma unroll
       for (int i = 0; i < 2 * NKK; ++i)
         xq[half][i / 2][i % 2] = h < group && i * 8 < a.hd ? *reinterpret_cast<const Raw*>(q + i * 8) : Raw{};
     }
+  };
+  fetch_q(p);
+#pragma unroll 1
+  for (bool left = true; left;) {
+    const int t0 = p.t, t1 = min(p.nt, r.end - p.v - V);
     bool fresh = true;
     uint32_t qa[NA][NKK][4];  // A fragments: pieces of rows gid and gid + 8
     float sc[2];
@@ -269,12 +274,14 @@ __global__ void __launch_bounds__(256, 1) paged_mma_kernel(const PagedAttnArgs a
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       if (tig == 0) *reinterpret_cast<float2*>(cw + (gid + 8 * half) * CS + HD) = make_float2(m[half], sum);
     }
-    if (Fin::template unit<NW>(a, r, p, n_hb, comb, t0, t1)) {
-      pend[n_pend] = p;
-      ++n_pend;
-    }
+    const Place done = p;
     p.t = t1 - 1;
     left = advance<TILE, V>(a, n_units, r.end, p);
+    if (left) fetch_q(p);
+    if (Fin::template unit<NW>(a, r, done, n_hb, comb, t0, t1)) {
+      pend[n_pend] = done;
+      ++n_pend;
+    }
   }
   cp_wait<0>();
   if (n_pend) Fin::template join<V>(a, r, pend, n_pend, n_hb, reinterpret_cast<float*>(pa_smem));
@@ -301,7 +308,7 @@ size_t part_floats(int n_heads, int n_kv_heads, int head_dim) {
   const int hb = n_heads / n_kv_heads <= 8 ? 8 : 16, hd = head_dim <= 32 ? 32 : head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
   return (size_t)hb * comb_stride(hd);
 }
-constexpr size_t COUNTER_BYTES = 4 * PA_MAX_CTAS * sizeof(unsigned int);
+static_assert(4 * PA_MAX_CTAS * sizeof(unsigned int) <= OP_COUNTER_BYTES, "counters");
 
 }  // namespace
 }  // namespace paged
@@ -314,7 +321,7 @@ extern "C" {
 
 size_t qw_op_paged_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
   if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || head_dim < 8 || head_dim % 8 || head_dim > PA_MAX_HD) return 0;
-  return COUNTER_BYTES + 2 * PA_MAX_CTAS * part_floats(n_heads, n_kv_heads, head_dim) * sizeof(float);
+  return OP_COUNTER_BYTES + 2 * PA_MAX_CTAS * part_floats(n_heads, n_kv_heads, head_dim) * sizeof(float);
 }
 
 qw_status qw_op_paged_attention(const qw_paged_kv* cache, int32_t n_seqs, int32_t n_heads, const int32_t* block_table,
@@ -331,8 +338,8 @@ qw_status qw_op_paged_attention(const qw_paged_kv* cache, int32_t n_seqs, int32_
   if (n_seqs > 65535 || n_heads > 4096) return op_fail(QW_ERR_UNSUPPORTED, "more than 65535 sequences or 4096 heads");
   if ((int64_t)max_blocks * c.page_size > (int64_t)1 << 30)
     return op_fail(QW_ERR_UNSUPPORTED, "max_blocks * page_size above 2^30");
-  // the tile list's numbers are 31-bit: tiles of at least 64 positions, and a weight of at most 5 a unit
-  if ((int64_t)n_seqs * n_heads * ((int64_t)max_blocks * c.page_size / 64 + 6) > 0x7fffffffll)
+  // the tile list's numbers are 31-bit: tiles of at least 32 positions, and a weight of at most 5 a unit
+  if ((int64_t)n_seqs * n_heads * ((int64_t)max_blocks * c.page_size / 32 + 6) > 0x7fffffffll)
     return op_fail(QW_ERR_UNSUPPORTED, "n_seqs * n_heads * max_blocks * page_size too large");
   if (!std::isfinite(scale)) return op_fail(QW_ERR_INVALID_ARG, "scale not finite");
   if (n_seqs == 0) return QW_OK;
@@ -351,7 +358,7 @@ qw_status qw_op_paged_attention(const qw_paged_kv* cache, int32_t n_seqs, int32_
     return op_cuda_fail(e, "device query");
   PagedAttnArgs a{c.k, c.v, c.page_stride, c.head_stride, c.pos_stride, n_seqs, n_heads, c.n_kv_heads, c.head_dim,
                   c.page_size, c.n_pages, max_blocks, block_table, lens, q, out, q_stride, out_stride, scale, lse,
-                  (unsigned int*)workspace, (float*)((char*)workspace + COUNTER_BYTES), err_dev};
+                  (unsigned int*)workspace, (float*)((char*)workspace + OP_COUNTER_BYTES), err_dev};
   cudaStream_t s = (cudaStream_t)cuda_stream;
   const int ctas = nsm < PA_MAX_CTAS ? nsm : PA_MAX_CTAS;
   if (c.dtype == QW_F32 || c.head_dim > 128) e = launch_simt(c.dtype, io_dtype, ctas, a, s);

@@ -698,7 +698,7 @@ cudaError_t launch_logprobs(LogprobArgs a, int nsm, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(logprob_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
   return e ? e : launch_k(logprob_kernel<T>, dim3(grid), dim3(LP_NT), ring, s, false, a);
 }
-constexpr size_t LP_COUNTER_BYTES = 2 * LP_MAX_CTAS * sizeof(unsigned int);
+static_assert(2 * LP_MAX_CTAS * sizeof(unsigned int) <= OP_COUNTER_BYTES, "counters");
 
 }  // namespace
 }  // namespace qw
@@ -709,7 +709,7 @@ extern "C" {
 
 size_t qw_op_token_logprobs_workspace(int32_t n_rows, int32_t vocab, int32_t top_k) {
   if (n_rows < 0 || vocab < 1 || top_k < 0 || top_k > LP_MAX_TOP) return 0;
-  return LP_COUNTER_BYTES + 2 * LP_MAX_CTAS * sizeof(LogprobPart);
+  return OP_COUNTER_BYTES + 2 * LP_MAX_CTAS * sizeof(LogprobPart);
 }
 
 qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t vocab, const void* logits,
@@ -742,7 +742,7 @@ qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t voc
   if ((e = cudaGetDevice(&dev)) || (e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)))
     return op_cuda_fail(e, "device query");
   const LogprobArgs a{logits, row_stride, n_rows, vocab, n_ids, top_k, 0, 0, ids, logprobs, ranks, entropy, top_ids,
-                      top_logprobs, (unsigned int*)workspace, (LogprobPart*)((char*)workspace + LP_COUNTER_BYTES), err_dev};
+                      top_logprobs, (unsigned int*)workspace, (LogprobPart*)((char*)workspace + OP_COUNTER_BYTES), err_dev};
   cudaStream_t s = (cudaStream_t)cuda_stream;
   e = logits_dtype == QW_F32   ? launch_logprobs<float>(a, nsm, s)
       : logits_dtype == QW_F16 ? launch_logprobs<f16>(a, nsm, s) : launch_logprobs<bf16>(a, nsm, s);

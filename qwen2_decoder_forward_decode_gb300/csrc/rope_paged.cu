@@ -325,6 +325,7 @@ qw_status qw_op_rope_append(const qw_paged_kv* cache, int32_t n_tokens, int32_t 
   if (adjacent != 0 && adjacent != 1) return op_fail(QW_ERR_INVALID_ARG, "adjacent must be 0 or 1");
   if (!std::isfinite(mscale)) return op_fail(QW_ERR_INVALID_ARG, "mscale not finite");
   if (n_heads > 4096 || c.n_kv_heads > 4096) return op_fail(QW_ERR_UNSUPPORTED, "more than 4096 heads");
+  if (n_tokens > 1 << 30) return op_fail(QW_ERR_UNSUPPORTED, "more than 2^30 tokens");
   if (n_tokens == 0) return QW_OK;
   if (!positions || !slots || !turns || !err_dev) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
   if (((uintptr_t)slots | (uintptr_t)turns) & 7) return op_fail(QW_ERR_INVALID_ARG, "slots or turns not 8-byte aligned");

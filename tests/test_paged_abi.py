@@ -102,6 +102,15 @@ def test_plan_refusals(over):
     refused(lambda: plan(**over), 1)
 
 
+def test_sizes_beyond_32_bits_are_refused():
+    refused(lambda: plan(tokens=(1 << 30) + 1), 2)
+    refused(lambda: plan(n_pages=(1 << 30) + 1), 2)
+    refused(lambda: release(n_pages=(1 << 30) + 1), 2)
+    refused(lambda: rope(n_tokens=(1 << 30) + 1), 2)
+    refused(lambda: attn(n_seqs=60000, max_blocks=1 << 16), 2, "too large")
+    refused(lambda: logprobs(rows=1 << 20, vocab=1 << 24, stride=1 << 24), 2, "too large")
+
+
 def test_release_refuses_no_flags():
     refused(lambda: release(done=None), 1)
 

@@ -143,3 +143,23 @@ def test_prefill_decode_and_release(io, cache, hd, page):
     used = [int(s.table[b, j]) for b in range(n) for j in range(ref.pages_of(len(keys[b]), page))]
     free = s.free[:int(s.n_free)].tolist()
     assert sorted(used + free) == list(range(s.n_pages))
+
+
+def test_attention_and_log_probabilities_share_a_workspace_in_turn():
+    from qwen2_decoder_forward_decode_gb300 import binding
+    s = Serving(5, 4, 2, 64, 16, 200, 40, 3000, "f32", "f16")
+    s.new.copy_(torch.tensor([600, 1, 0, 33, 500], dtype=torch.int32))
+    s.qkv.normal_(generator=torch.Generator("cuda").manual_seed(2))
+    s.append()
+    s.attend()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (s.out, s.lse, s.lp, s.ent, s.top_ids)]
+    n = max(s.ws.numel(), s.lws.numel())
+    s.ws = s.lws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        for t in (s.out, s.lse, s.lp, s.ent, s.top_ids):
+            t.zero_()
+        s.attend()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (s.out, s.lse, s.lp, s.ent, s.top_ids)))
+    assert int(s.err) == 0 and binding.DEV_PAGE == 32
