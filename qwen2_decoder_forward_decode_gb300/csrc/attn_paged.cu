@@ -164,9 +164,13 @@ __global__ void __launch_bounds__(256, 1) paged_mma_kernel(const PagedAttnArgs a
       const uint32_t mask = s_mask[warp][stage];
       if (mask) {
         const uint32_t ks = ring + stage * Ld::STAGE, vs = ks + Ld::STAGE / 2;
-        float c[2 * R][4];
+        // lower pieces have sums of their own: the additions cut, and would do so twice as often at the top
+        constexpr int NC = NA > 1 ? 2 : 1;
+        float c[NC][2 * R][4];
 #pragma unroll
-        for (int i = 0; i < 2 * R; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+          for (int i = 0; i < 2 * R; ++i) c[n][i][0] = c[n][i][1] = c[n][i][2] = c[n][i][3] = 0.f;
         const int mi = lane >> 3, r8 = lane & 7;
 #pragma unroll
         for (int kk = 0; kk < NKK; ++kk) {
@@ -176,10 +180,16 @@ __global__ void __launch_bounds__(256, 1) paged_mma_kernel(const PagedAttnArgs a
             ldmatrix_x4(b, ks + Ld::at(rr * 16 + (mi >> 1) * 8 + r8, kk * 2 + (mi & 1)));
 #pragma unroll
             for (int n = 0; n < NA; ++n) {
-              mma_t(c[2 * rr], qa[n][kk], b[0], b[1], T());
-              mma_t(c[2 * rr + 1], qa[n][kk], b[2], b[3], T());
+              mma_t(c[n ? NC - 1 : 0][2 * rr], qa[n][kk], b[0], b[1], T());
+              mma_t(c[n ? NC - 1 : 0][2 * rr + 1], qa[n][kk], b[2], b[3], T());
             }
           }
+        }
+        if constexpr (NC > 1) {
+#pragma unroll
+          for (int i = 0; i < 2 * R; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[0][i][k] += c[NC - 1][i][k];
         }
         uint32_t pa[R][NPA][4];
 #pragma unroll
@@ -188,7 +198,7 @@ __global__ void __launch_bounds__(256, 1) paged_mma_kernel(const PagedAttnArgs a
           float top = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 4 * R; ++i) {
-            const float x = HB == 8 ? c[i >> 1][i & 1] + c[i >> 1][2 + (i & 1)] : c[i >> 1][2 * half + (i & 1)];
+            const float x = HB == 8 ? c[0][i >> 1][i & 1] + c[0][i >> 1][2 + (i & 1)] : c[0][i >> 1][2 * half + (i & 1)];
             s[i] = (mask >> (2 * tig + (i & 1) + 8 * (i >> 1))) & 1 ? x * sc[half] : -INFINITY;
             top = fmaxf(top, s[i]);
           }
@@ -243,7 +253,7 @@ __global__ void __launch_bounds__(256, 1) paged_mma_kernel(const PagedAttnArgs a
       }
       __syncwarp();
       if (++stage == NS) stage = 0;
-      if (t == t1 || (C::F32IO && ++since == PA_FLUSH)) {  // o to the warp's place in comb, added to what is there
+      if (t == t1 || (C::F32IO && ++since == PA_FLUSH / NPA)) {  // o to the warp's place in comb, added to what is there
         since = 0;
 #pragma unroll
         for (int half = 0; half < HB / 8; ++half) {

@@ -18,8 +18,8 @@ constexpr int PA_MAX_CTAS = 160;   // persistent CTAs the workspace has room for
 constexpr int PA_WHOLE = 3;         // units of at most so many tiles are not split
 constexpr int PA_GROUP = 10;       // parts merged at once: 152 CTAs are at most 16 groups
 constexpr int PA_JOIN = 20;        // states a join holds: two groups, or the group sums of two units (18)
-constexpr int PA_FLUSH = 16;         // tiles that the tensor cores sum up for an fp32 caller (their additions cut,
-                                   // so the error of a long sum grows with its length: 1.6e-6 for 64 tiles)
+constexpr int PA_FLUSH = 16;         // products that the tensor cores sum up for an fp32 caller (their additions cut,
+                                   // so a long sum's error grows with its length: 1.6e-6 for 100)
 constexpr float PA_BIAS = 10.f;    // probabilities are kept times 2^10: their fp16 halves stay normal
                                    // numbers down to 2^-24 of the largest
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
