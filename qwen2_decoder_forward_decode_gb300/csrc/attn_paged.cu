@@ -8,16 +8,16 @@
 //
 // What bounds it: every key and value is used by the few query heads of its group only, about 2 flops
 // per byte and head, so HBM. Everything else serves to keep loads in flight on every SM:
-//   - One CTA per SM. The tiles of all sequences and KV heads form one list (sequence, unit, tile),
-//     cut into equal consecutive ranges, one per CTA, from the lengths on the device: ragged batches
-//     and single long sequences load every SM alike, and a captured graph follows the lengths.
-//   - Each of the CTA's 8 warps owns the same rows of every tile and copies them itself (cp.async,
-//     16 bytes a lane) into its own ring of stages, looking the rows' pages up one tile ahead. Warps
-//     meet only where a unit ends; the ring runs on into the next unit meanwhile.
+//   - One CTA of 8 warps per SM (two of 4 warps on the CUDA cores, see there). The tiles of all sequences
+//     and KV heads form one list (sequence, unit, tile), cut into equal consecutive ranges, one per CTA,
+//     from the lengths on the device: ragged batches and single long sequences load every SM alike, and
+//     a captured graph follows the lengths.
+//   - Each of the CTA's warps owns the same rows of every tile and copies them itself (cp.async, 16 bytes a
+//     lane) into its own ring of stages, looking the rows' pages up one tile ahead. Warps meet only where
+//     a unit ends; the ring runs on into the next unit meanwhile.
 //   - A unit that one CTA covers is finished there. The parts of a split unit go to the workspace; the
-//     last CTA to arrive merges them, in groups of PA_GROUP CTAs first where there are more (a single
-//     CTA reading every part of a long sequence would be bound by latency). The order of every sum is
-//     fixed by the lengths, so results repeat bit by bit.
+//     CTAs that arrive last merge them, as a tree (one CTA reading every part of a long sequence would be
+//     bound by latency). The order of every sum is fixed by the lengths, so results repeat bit by bit.
 #include "attn_paged.cuh"
 
 #include <cmath>
@@ -50,14 +50,14 @@ struct MmaCfg {
 };
 
 template <typename T, int HD, int HB, typename IO>
-__global__ void __launch_bounds__(256, 1) paged_mma_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel(const PagedAttnArgs a) {
   using C = MmaCfg<T, HD, HB, IO>;
   using Ld = typename C::Ld;
-  using Fin = Finish<IO, HB, HD, C::NT>;
+  using Fin = Finish<IO, HB, HD, C::NT, C::SMEM>;
   constexpr int NW = C::NW, NS = C::NS, R = C::R, NQ = C::NQ, NP = C::NP, CS = comb_stride(HD), TILE = Ld::TILE, V = Ld::V;
   using Raw = typename std::conditional<C::F32IO, float2, uint32_t>::type;  // two query elements
   constexpr int NKK = HD / 16, NA = HB == 8 ? (NQ + 1) / 2 : NQ, NPA = HB == 8 ? (NP + 1) / 2 : NP;  // products per step
-  static_assert(NS >= 2 && C::SMEM >= PA_JOIN * HB * CS * 4, "the ring, and the parts of a join in its place");
+  static_assert(NS >= 2, "ring");
   extern __shared__ __align__(128) unsigned char pa_smem[];
   __shared__ uint32_t s_mask[NW][NS];  // rows of a stage that exist
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
@@ -318,7 +318,7 @@ size_t part_floats(int n_heads, int n_kv_heads, int head_dim) {
   const int hb = n_heads / n_kv_heads <= 8 ? 8 : 16, hd = head_dim <= 32 ? 32 : head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
   return (size_t)hb * comb_stride(hd);
 }
-static_assert(4 * PA_MAX_CTAS * sizeof(unsigned int) <= OP_COUNTER_BYTES, "counters");
+static_assert(PA_LEVELS * 2 * PA_MAX_CTAS * sizeof(unsigned int) <= OP_COUNTER_BYTES, "counters");
 
 }  // namespace
 }  // namespace paged
@@ -370,8 +370,8 @@ qw_status qw_op_paged_attention(const qw_paged_kv* cache, int32_t n_seqs, int32_
                   c.page_size, c.n_pages, max_blocks, block_table, lens, q, out, q_stride, out_stride, scale, lse,
                   (unsigned int*)workspace, (float*)((char*)workspace + OP_COUNTER_BYTES), err_dev};
   cudaStream_t s = (cudaStream_t)cuda_stream;
-  const int ctas = nsm < PA_MAX_CTAS ? nsm : PA_MAX_CTAS;
-  if (c.dtype == QW_F32 || c.head_dim > 128) e = launch_simt(c.dtype, io_dtype, ctas, a, s);
+  const int ctas = nsm < PA_MAX_CTAS / 2 ? nsm : PA_MAX_CTAS / 2;
+  if (c.dtype == QW_F32 || c.head_dim > 128) e = launch_simt(c.dtype, io_dtype, 2 * ctas, a, s);
   else if (c.dtype == QW_F16)
     e = io_dtype == QW_F32 ? launch_16bit<f16, float>(ctas, a, s) : launch_16bit<f16, f16>(ctas, a, s);
   else

@@ -14,10 +14,9 @@ namespace qw {
 namespace paged {
 
 constexpr int PA_MAX_HD = 256;
-constexpr int PA_MAX_CTAS = 160;   // persistent CTAs the workspace has room for
-constexpr int PA_WHOLE = 3;         // units of at most so many tiles are not split
-constexpr int PA_GROUP = 10;       // parts merged at once: 152 CTAs are at most 16 groups
-constexpr int PA_JOIN = 20;        // states a join holds: two groups, or the group sums of two units (18)
+constexpr int PA_MAX_CTAS = 320;   // CTAs the workspace has room for
+constexpr int PA_WHOLE = 3;        // units of at most so many tiles are not split
+constexpr int PA_LEVELS = 4;       // of a join
 constexpr int PA_FLUSH = 16;         // products that the tensor cores sum up for an fp32 caller (their additions cut,
                                    // so a long sum's error grows with its length: 1.6e-6 for 100)
 constexpr float PA_BIAS = 10.f;    // probabilities are kept times 2^10: their fp16 halves stay normal
@@ -34,12 +33,12 @@ struct PagedAttnArgs {
   long long q_stride, out_stride;
   float scale;
   float* lse;
-  unsigned int* counters;  // [2][2 * PA_MAX_CTAS], zero between calls
+  unsigned int* counters;  // [PA_LEVELS][2 * PA_MAX_CTAS], zero between calls
   float* part;             // [2 * PA_MAX_CTAS][HB][HD + 8]
   int* err;
 };
 
-__host__ __device__ constexpr int comb_stride(int hd) { return hd + 8; }  // o, then m and l
+__host__ __device__ constexpr int comb_stride(int hd) { return hd + 4; }  // o, then m and l
 
 // two elements at an even index
 __device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
@@ -274,9 +273,12 @@ struct Loader {
 // All code that runs once per unit or per CTA is kept short (loops, one out-of-line join): a first version
 // with everything inlined and unrolled was 130 KB per kernel, and its instruction misses cost 8 us at
 // every unit's end and 10 us in the join.
-template <typename IO, int HB, int HD, int NT>
+template <typename IO, int HB, int HD, int NT, int SMEM>
 struct Finish {
   static constexpr int CS = comb_stride(HD), N4 = HB * HD / 4;
+  // parts merged at once: of two units, they fit the kernel's shared memory
+  static constexpr int GROUP_FIT = SMEM / (2 * HB * CS * 4), GROUP = GROUP_FIT > 10 ? 10 : GROUP_FIT;
+  static_assert(GROUP * GROUP * GROUP * GROUP >= PA_MAX_CTAS, "levels");
 
   struct Acc {  // 4 output elements of one head
     float4 o;
@@ -342,43 +344,39 @@ struct Finish {
     return !whole;
   }
 
-  // Joins the CTA's split units (at most two, places pend[0 .. n)), both at once: announces its parts, and
-  // merges a unit's parts if it is the last to: first those of PA_GROUP consecutive CTAs, then the groups'
-  // sums. The parts are fetched into shared memory (buf, all of the kernel's) together. Done once at
-  // the CTA's end: an announcement takes a memory fence and an atomic's round trip, about 1 us, the merge
-  // of a level 2 us.
+  // Joins the CTA's split units (at most two, places pend[0 .. n)), both at once, in a tree: at level 0 the parts of
+  // GROUP consecutive CTAs, counted from the unit's first, at level 1 the sums of GROUP groups, and so on. A CTA
+  // announces its part and merges the group if it is the last to; the group's first slot takes the sum. The
+  // parts are fetched into shared memory (buf, all of the kernel's) together. Done once at the CTA's
+  // end: an announcement takes a memory fence and an atomic's round trip, about 1 us, a level 2 us.
   template <int V>
   static __device__ __forceinline__ void join(const PagedAttnArgs& a, const Range& r, const Place* pend, int n, int n_hb, float* buf) {
     constexpr int S4 = HB * CS / 4;
-    // what is merged next: states of CTAs from, from + step, ...; the unit's first slot; its CTAs and groups
-    __shared__ int s_from[2], s_step[2], s_count[2], s_first[2], s_c0[2], s_groups[2], s_last[2];
+    // what is merged next: states of CTAs from, from + step, ...; the unit's first slot and its CTAs
+    __shared__ int s_from[2], s_count[2], s_first[2], s_c0[2], s_c1[2], s_last[2];
     const int c = blockIdx.x, w = threadIdx.x / 32;
     const bool speaker = threadIdx.x % 32 == 0 && w < n;
     if (threadIdx.x < 2) s_last[threadIdx.x] = s_count[threadIdx.x] = 0;
     __syncthreads();
     if (speaker) {
       const Place& p = pend[w];
-      const int c0 = cta_of(r, p.v + V), c1 = cta_of(r, p.v + V + p.nt - 1), g0 = c - (c - c0) % PA_GROUP;
-      s_c0[w] = c0;
-      s_from[w] = g0;
-      s_step[w] = 1;
-      s_count[w] = min(PA_GROUP, c1 - g0 + 1);
-      s_first[w] = slot_of(r, p, c0);
-      s_groups[w] = (c1 - c0) / PA_GROUP + 1;
+      s_c0[w] = cta_of(r, p.v + V);
+      s_c1[w] = cta_of(r, p.v + V + p.nt - 1);
+      s_first[w] = slot_of(r, p, s_c0[w]);
+      s_last[w] = 1;
     }
+    int step = 1;
 #pragma unroll 1
-    for (int level = 0; level < 2; ++level) {
-      if (speaker && (level == 0 || s_last[w])) {
-        const int slot = level || s_from[w] == s_c0[w] ? s_first[w] : 2 * s_from[w];
-        if (level) {
-          s_from[w] = s_c0[w];
-          s_step[w] = PA_GROUP;
-          s_count[w] = s_groups[w];
-        }
-        unsigned int* counter = a.counters + level * 2 * PA_MAX_CTAS + slot;
+    for (int level = 0; level < PA_LEVELS; ++level, step *= GROUP) {
+      if (speaker && s_last[w]) {
+        const int c0 = s_c0[w], from = c - (c - c0) % (step * GROUP), count = min(GROUP, (s_c1[w] - from) / step + 1);
+        s_from[w] = from;
+        s_count[w] = count;
+        unsigned int* counter = a.counters + level * 2 * PA_MAX_CTAS + (from == c0 ? s_first[w] : 2 * from);
         __threadfence();  // (the CTA's parts, written before the last barrier)
-        s_last[w] = atomicAdd(counter, 1u) == (unsigned)s_count[w] - 1u;
-        if (s_last[w]) *counter = 0u;
+        const bool last = atomicAdd(counter, 1u) == (unsigned)count - 1u;
+        if (last) *counter = 0u;
+        s_last[w] = last;
         __threadfence();
       }
       __syncthreads();
@@ -386,7 +384,7 @@ struct Finish {
       if (n0 + n1 == 0) return;
 #pragma unroll 1
       for (int part = w; part < n0 + n1; part += NT / 32) {  // a warp a state
-        const int k = part >= n0, cta = s_from[k] + (part - (k ? n0 : 0)) * s_step[k];
+        const int k = part >= n0, cta = s_from[k] + (part - (k ? n0 : 0)) * step;
         const float* src = slot_ptr(a, cta == s_c0[k] ? s_first[k] : 2 * cta);
         float* dst = buf + part * HB * CS;
 #pragma unroll 4
@@ -395,13 +393,13 @@ struct Finish {
       cp_commit();
       cp_wait<0>();
       __syncthreads();
-      const bool done0 = level || s_groups[0] == 1, done1 = n1 == 0 || level || s_groups[1] == 1;
+      const bool done0 = n0 == 0 || s_c1[0] - s_c0[0] < step * GROUP, done1 = n1 == 0 || s_c1[1] - s_c0[1] < step * GROUP;
 #pragma unroll 1
       for (int i = n0 ? threadIdx.x : N4 + threadIdx.x; i < (n1 ? 2 * N4 : N4); i += NT) {
         const int k = i >= N4, i4 = i - k * N4, h = i4 / (HD / 4), d = (i4 - h * (HD / 4)) * 4;
         const Acc s = sum(buf + (k ? n0 * HB * CS : 0), k ? n1 : n0, h, d);
         if (k ? done1 : done0) write_out(a, pend[k], n_hb, h, d, s);
-        else put(slot_ptr(a, s_from[k] == s_c0[k] ? s_first[k] : 2 * s_from[k]), h, d, s);  // the group's first slot
+        else put(slot_ptr(a, s_from[k] == s_c0[k] ? s_first[k] : 2 * s_from[k]), h, d, s);
       }
       __syncthreads();
       if (threadIdx.x == 0) {

@@ -23,7 +23,7 @@ inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 // Both operators with a workspace keep their counters (zero between calls) in its first bytes, so that one workspace
 // can serve them in turn.
-constexpr size_t OP_COUNTER_BYTES = 8192;
+constexpr size_t OP_COUNTER_BYTES = 16384;
 
 // Every pointer must be memory of the current device: a host pointer or another device's would
 // fault in the kernel. Managed memory passes. Null pointers are skipped (optional arguments).
