@@ -24,6 +24,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace qw {
 namespace {
@@ -86,9 +87,14 @@ template <typename T> struct Logits;
 template <> struct Logits<float> {
   static constexpr int N = 4;
   static __device__ __forceinline__ uint32_t minus_inf() { return 0xff800000u; }
-  static __device__ __forceinline__ float top(const uint4& r) {
-    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
-  }
+  // maximum of the vectors that were added
+  struct Top {
+    float m = -INFINITY;
+    __device__ __forceinline__ void add(const uint4& r) {
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w))));
+    }
+    __device__ __forceinline__ float value() const { return m; }
+  };
   static __device__ __forceinline__ void pairs(const uint4& r, f32x2* p) {
     p[0] = pack2(max_nan(__uint_as_float(r.x), LP_FLOOR), max_nan(__uint_as_float(r.y), LP_FLOOR));
     p[1] = pack2(max_nan(__uint_as_float(r.z), LP_FLOOR), max_nan(__uint_as_float(r.w), LP_FLOOR));
@@ -115,10 +121,13 @@ __device__ __forceinline__ uint32_t next16(uint32_t b) { return (b & 0x7fff) == 
 template <typename T, typename T2>
 struct Logits16 {
   static constexpr int N = 8;
-  static __device__ __forceinline__ float top(const uint4& r) {
-    const T2 m = __hmax2(__hmax2(as_pair<T2>(r.x), as_pair<T2>(r.y)), __hmax2(as_pair<T2>(r.z), as_pair<T2>(r.w)));
-    return fmaxf(__low2float(m), __high2float(m));
-  }
+  struct Top {
+    T2 m = as_pair<T2>(std::is_same<T, bf16>::value ? 0xff80ff80u : 0xfc00fc00u);  // -inf
+    __device__ __forceinline__ void add(const uint4& r) {
+      m = __hmax2(m, __hmax2(__hmax2(as_pair<T2>(r.x), as_pair<T2>(r.y)), __hmax2(as_pair<T2>(r.z), as_pair<T2>(r.w))));
+    }
+    __device__ __forceinline__ float value() const { return fmaxf(__low2float(m), __high2float(m)); }
+  };
   // Counts of both halves in one sum of masks: a true half adds 0xffff, so the sum of lo low and hi high ones is
   // (lo - hi) 2^16 - lo.
   struct Count {
@@ -490,11 +499,10 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
       asm volatile("cp.async.wait_group %0;" ::"n"(LP_NS - 1) : "memory");
       b.take(a, row, batch, stage_ptr(stage));
       if (++stage == LP_NS) stage = 0;
-      float top = -INFINITY;
+      typename Batch<T>::Lg::Top tops;
 #pragma unroll
-      for (int i = 0; i < LP_VPT; ++i) {
-        top = fmaxf(top, Batch<T>::Lg::top(b.r[i]));
-      }
+      for (int i = 0; i < LP_VPT; ++i) tops.add(b.r[i]);
+      const float top = tops.value();
       most = fmaxf(most, top);
       if (top * LP_LOG2E > m) {
         const float to = top * LP_LOG2E, d = m - to, f = ex2(d);
@@ -514,8 +522,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
         Batch<T>::Lg::pairs(b.r[i], x);
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) {
-          f32x2 d = ref;
-          fma2(d, x[e], l2e);
+          const f32x2 d = fma2_to(x[e], l2e, ref);
           const float2 v = unpack2(d);
           const f32x2 p = pack2(ex2(v.x), ex2(v.y));
           s2 = add2(s2, p);
@@ -535,8 +542,9 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
           // before t in its own vector were counted when the row began
           const typename Batch<T>::Lg::Thr here = Batch<T>::Lg::thr(z), next = Batch<T>::Lg::thr_above(z);
           typename Batch<T>::Lg::Count count;
+          const int v = b.id(LP_VPT - 1) + N <= t ? LP_VPT : b.id(0) + N > t ? 0 : (t - b.j0 - N) / (LP_NT * N) + 1;  // vectors before t
 #pragma unroll
-          for (int i = 0; i < LP_VPT; ++i) count.add(b.r[i], b.id(i) + N <= t ? here : next);
+          for (int i = 0; i < LP_VPT; ++i) count.add(b.r[i], i < v ? here : next);
           int above = count.total();
           above = __reduce_add_sync(0xffffffffu, above);
           if (lane == 0 && above) atomicAdd(&sh.above[q], above);
