@@ -18,6 +18,12 @@
 //   - A unit that one CTA covers is finished there. The parts of a split unit go to the workspace; the
 //     CTAs that arrive last merge them, as a tree (one CTA reading every part of a long sequence would be
 //     bound by latency). The order of every sum is fixed by the lengths, so results repeat bit by bit.
+// Measured (12 query and 2 KV heads of 128, fp16 cache, fp32 queries, unless stated): 256 sequences of 1 to 8192
+// positions, 28 and 4 heads, bf16: 326 us, 6.5 TB/s; one sequence of 131071: 34 us, 3.9 TB/s, of which 5 us pass
+// before the first tile and 8 us in the join's two levels; 16 sequences of 256 to 2048: 12.9 us (3.7 us of
+// traffic); one of 178: 6.7 us (lengths, table and first rows are loads that wait for one another). Instructions
+// matter off the main loop: with everything inlined and unrolled, 130 KB a kernel, their misses cost 8 us
+// at every unit's end and 10 us in the join.
 #include "attn_paged.cuh"
 
 #include <cmath>

@@ -270,9 +270,7 @@ struct Loader {
 
 // ---- the end of a unit -------------------------------------------------------------------------------------
 
-// All code that runs once per unit or per CTA is kept short (loops, one out-of-line join): a first version
-// with everything inlined and unrolled was 130 KB per kernel, and its instruction misses cost 8 us at
-// every unit's end and 10 us in the join.
+// All code that runs once per unit or per CTA is kept short: loops, one out-of-line sum of states.
 template <typename IO, int HB, int HD, int NT, int SMEM>
 struct Finish {
   static constexpr int CS = comb_stride(HD), N4 = HB * HD / 4;
