@@ -435,7 +435,7 @@ qw_status qw_op_paged_attention(const qw_paged_kv *cache, int32_t n_seqs, int32_
  *   ranks[i]    = 1 + the tokens with a larger logit, or the same and a lower id
  *   entropy     = - sum_j p_j ln p_j in nats (p = softmax(z); 0 where p_j is 0)
  *   top_ids, top_logprobs: the top_k tokens in that order, and their log probabilities
- * A logit of -inf is a token of probability 0. A row that holds a NaN or +inf, or nothing but
+ * A logit of -inf is a token of probability 0; a log probability beyond fp32 is -inf. A row that holds a NaN or +inf, or nothing but
  * -inf, has no distribution: QW_DEV_NONFINITE is set, logprobs, entropy and top_logprobs are NaN,
  * ranks 0 and top_ids -1. An id of -1 marks no token (logprob 0, rank 0); any other id outside
  * [0, vocab) gives NaN and rank 0 and sets QW_DEV_TOKEN.

@@ -41,10 +41,10 @@ constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
 typedef unsigned long long u64;
 
 struct LogprobPart {  // of a row that several CTAs share
-  float m, s, w;
+  float m, s, w, top;
   int nan;
   int above[LP_MAX_IDS];
-  int n, pad[3];
+  int n, pad[2];
   u64 key[LP_MAX_TOP];
 };
 
@@ -85,11 +85,18 @@ constexpr u64 LP_NO_BAR = 0x007fffffffffffffull;  // the key of (-inf, id 0): ev
 //
 // pair(u): the logits of word u (two for 16-bit types) as packed fp32, with -inf raised to a finite value whose
 // exponential is 0 (so that d * exp(d) is 0 as well); a NaN stays.
-constexpr float LP_FLOOR = -1e38f;  // (finite after the product with log2 e and the difference)
+// Rows whose maximum lies so low that the floor would count, or so high that products with log2(e) overflow (masks
+// of the type's lowest value that leave nothing), are summed again, slowly.
+constexpr float LP_FLOOR = -1e28f;  // (times log2(e), and that times 2^31 logits, is finite)
+template <typename T>
+__device__ __forceinline__ bool extreme(float most) {
+  return !(most < 5e27f && most > (std::is_same<T, f16>::value ? -65000.f : -5e27f));
+}
 template <typename T> struct Logits;
 template <> struct Logits<float> {
   static constexpr int N = 4;
   static __device__ __forceinline__ uint32_t minus_inf() { return 0xff800000u; }
+  static __device__ __forceinline__ float floor() { return LP_FLOOR; }
   // maximum of the vectors that were added
   struct Top {
     float m = -INFINITY;
@@ -154,8 +161,9 @@ struct Logits16 {
 };
 template <> struct Logits<bf16> : Logits16<bf16, __nv_bfloat162> {
   static __device__ __forceinline__ uint32_t minus_inf() { return 0xff80ff80u; }
+  static __device__ __forceinline__ float floor() { return to_f32(__float2bfloat16_rn(LP_FLOOR)); }
   static __device__ __forceinline__ f32x2 pair(uint32_t u) {
-    const __nv_bfloat162 h = __hmax2_nan(as_pair<__nv_bfloat162>(u), __float2bfloat162_rn(LP_FLOOR));
+    const __nv_bfloat162 h = __hmax2_nan(as_pair<__nv_bfloat162>(u), __float2bfloat162_rn(floor()));
     const uint32_t v = *reinterpret_cast<const uint32_t*>(&h);
     return pack2(bf_lo(v), bf_hi(v));
   }
@@ -165,8 +173,9 @@ template <> struct Logits<bf16> : Logits16<bf16, __nv_bfloat162> {
 };
 template <> struct Logits<f16> : Logits16<f16, __half2> {
   static __device__ __forceinline__ uint32_t minus_inf() { return 0xfc00fc00u; }
+  static __device__ __forceinline__ float floor() { return -65504.f; }
   static __device__ __forceinline__ f32x2 pair(uint32_t u) {
-    const float2 t = __half22float2(__hmax2_nan(as_pair<__half2>(u), __float2half2_rn(-65504.f)));
+    const float2 t = __half22float2(__hmax2_nan(as_pair<__half2>(u), __float2half2_rn(floor())));
     return pack2(t.x, t.y);
   }
   static __device__ __forceinline__ void pairs(const uint4& r, f32x2* p) {
@@ -184,7 +193,7 @@ struct Shared {
   uint16_t top[LP_GROUPS][LP_NT];  // upper 16 bits of the ordered maxima
   uint16_t work[LP_WORK];        // group * LP_NT + thread
   int n_work;
-  float red[3][LP_NW];
+  float red[4][LP_NW];
   int above[LP_MAX_IDS], nan;
   int id[2][LP_MAX_IDS], equal[2][LP_MAX_IDS];  // of the row and the next, by turns; equal: see fetch_ids
   float given[2][LP_MAX_IDS];
@@ -365,17 +374,40 @@ __device__ __forceinline__ void select_top(const LogprobArgs& a, Shared& sh, int
   compact(sh, top_k);
 }
 
-// Writes a row's results from its state (the list sorted in sh). All threads.
+// ln sum exp(z - most) and the entropy of a row with extreme values, from the definition. All threads.
 template <typename T>
-__device__ __forceinline__ void finish_row(const LogprobArgs& a, Shared& sh, int row, float m, float s, float w, bool nan, int turn) {
+__device__ __noinline__ void slow_sums(const LogprobArgs& a, Shared& sh, int row, float most, float& ln_s, float& entropy, bool& nan) {
+  const T* z = (const T*)a.logits + (long long)row * a.row_stride;
+  float s = 0.f, w = 0.f;
+  int bad = 0;
+#pragma unroll 1
+  for (int j = threadIdx.x; j < a.vocab; j += LP_NT) {
+    const float x = to_f32(z[j]), d = x - most, e = expf(d);
+    bad |= x != x;
+    s += e;
+    if (e > 0.f) w = fmaf(d, e, w);
+  }
+  nan = __syncthreads_or(bad);
+  s = block_sum(s, sh.red[0]);
+  w = block_sum(w, sh.red[0]);
+  ln_s = logf(s);
+  entropy = ln_s - w / s;
+}
+
+// Writes a row's results from its state (most: its largest logit; the list sorted in sh). All threads.
+template <typename T>
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, Shared& sh, int row, float most, float m, float s, float w, bool nan,
+                                           int turn) {
   const int tid = threadIdx.x;
-  const bool odd = nan || s != s || !(m < INFINITY) || m == -INFINITY;  // no distribution
-  // ln p = (log2(e) z - m - log2 S) ln 2: the product and the difference are one rounding
-  const float log2_s = odd ? NAN : log2f(s);
-  auto logprob = [&](float z) { return (fmaf(z, LP_LOG2E, -m) - log2_s) * LP_LN2; };
+  // s and w are relative to m, the product log2(e) most as it was rounded: log2(e) most - m is exact, and brings
+  // ln s to most
+  float ln_s = (log2f(s) - fmaf(most, LP_LOG2E, -m)) * LP_LN2, entropy = (log2f(s) - w / s) * LP_LN2;
+  if (fabsf(most) < INFINITY && extreme<T>(most)) slow_sums<T>(a, sh, row, most, ln_s, entropy, nan);
+  const bool odd = nan || !(fabsf(most) < INFINITY);  // no distribution
+  auto logprob = [&](float z) { return z - most - ln_s; };
   if (tid == 0) {
     if (odd) atomicOr(a.err, ERR_NONFINITE);
-    if (a.entropy) a.entropy[row] = odd ? NAN : (log2_s - w / s) * LP_LN2;
+    if (a.entropy) a.entropy[row] = odd ? NAN : entropy;
   }
   if (tid < a.n_ids) {
     const int t = sh.id[turn][tid];
@@ -507,8 +539,9 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
       for (int i = 0; i < LP_VPT; ++i) tops.add(b.r[i]);
       const float top = tops.value();
       most = fmaxf(most, top);
-      if (top * LP_LOG2E > m) {
-        const float to = top * LP_LOG2E, d = m - to, f = ex2(d);
+      const float to = fmaxf(top, Batch<T>::Lg::floor()) * LP_LOG2E;
+      if (to > m) {
+        const float d = m - to, f = ex2(d);
         if (m == -INFINITY) s = w = 0.f;
         else {
           w = fmaf(d, s, w) * f;
@@ -516,8 +549,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
         }
         m = to;
       }
-      const float minus = m == -INFINITY ? 0.f : -m;
-      const f32x2 ref = pack2(minus, minus), l2e = pack2(LP_LOG2E, LP_LOG2E);
+      const f32x2 ref = pack2(-m, -m), l2e = pack2(LP_LOG2E, LP_LOG2E);
       f32x2 s2 = pack2(s, 0.f), w2 = pack2(w, 0.f);
 #pragma unroll
       for (int i = 0; i < LP_VPT; ++i) {
@@ -564,11 +596,18 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
     // the CTA's state of the row
     if (a.top_k) select_top<T>(a, sh, row, b0, b1, per, most);
     float mm = warp_max(m);
-    if (lane == 0) sh.red[0][warp] = mm;
+    most = warp_max(most);
+    if (lane == 0) {
+      sh.red[0][warp] = mm;
+      sh.red[3][warp] = most;
+    }
     if (nan) sh.nan = 1;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < LP_NW; ++i) mm = fmaxf(mm, sh.red[0][i]);
+    for (int i = 0; i < LP_NW; ++i) {
+      mm = fmaxf(mm, sh.red[0][i]);
+      most = fmaxf(most, sh.red[3][i]);
+    }
     {
       const float d = m == -INFINITY ? 0.f : m - mm, f = m == -INFINITY ? 0.f : ex2(d);
       w = warp_sum(fmaf(d, s, w) * f);
@@ -597,6 +636,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
         mine->m = mm;
         mine->s = s;
         mine->w = w;
+        mine->top = most;
         mine->nan = nan;
         mine->n = sh.n;
       }
@@ -618,12 +658,22 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
         // every thread takes the parts c0 + tid, + LP_NT, ...: the same order of sums at every run
         mm = -INFINITY;
 #pragma unroll 1
-        for (int c = c0 + tid; c <= c1; c += LP_NT) mm = fmaxf(mm, __ldcg(&slot_of(c)->m));
+        for (int c = c0 + tid; c <= c1; c += LP_NT) {
+          mm = fmaxf(mm, __ldcg(&slot_of(c)->m));
+          most = fmaxf(most, __ldcg(&slot_of(c)->top));
+        }
         mm = warp_max(mm);
-        if (lane == 0) sh.red[0][warp] = mm;
+        most = warp_max(most);
+        if (lane == 0) {
+          sh.red[0][warp] = mm;
+          sh.red[3][warp] = most;
+        }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < LP_NW; ++i) mm = fmaxf(mm, sh.red[0][i]);
+        for (int i = 0; i < LP_NW; ++i) {
+          mm = fmaxf(mm, sh.red[0][i]);
+          most = fmaxf(most, sh.red[3][i]);
+        }
         s = w = 0.f;
 #pragma unroll 1
         for (int c = c0 + tid; c <= c1; c += LP_NT) {
@@ -683,7 +733,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
         }
       }
     }
-    if (write) finish_row<T>(a, sh, row, mm, s, w, nan, turn);
+    if (write) finish_row<T>(a, sh, row, most, mm, s, w, nan, turn);
     __syncthreads();
     at += b1 - b0;
     turn ^= 1;

@@ -66,12 +66,14 @@ class Call:
             m = z.max()
             e = np.exp(z - m)
             S = e.sum()
-            lse = m + math.log(S)
+            ln_s = math.log(S)  # (z - m - ln S, not z - (m + ln S): at 3e38 a step of 64 bits is 4e22)
             p = e / S
-            H = -np.sum(np.where(p > 0, p * (np.maximum(z, -1e30) - lse), 0.0))
+            with np.errstate(invalid="ignore"):
+                H = math.log(S) - np.sum(np.where(p > 0, p * (z - m), 0.0))
             # S: positive terms summed in at most 400 steps on one path, at 8 standard deviations of half a
             # step, and exponentials good to 2^-22: 8 * 20 * 2^-24 + 2^-22 = 9.8e-6; z - m, ln S and their
             # difference: a step each
+            near = lambda got, v: got == np.float32(v - m - ln_s) or abs(got - (v - m - ln_s)) <= tol(v)  # noqa: E731 (beyond fp32: -inf)
             tol = lambda v: 1e-5 + ref.U * (abs(v - m) + abs(math.log(S)))  # noqa: E731
             order = np.lexsort((np.arange(self.vocab), -(z + 0.0)))
             place = np.empty(self.vocab, dtype=np.int64)
@@ -80,7 +82,7 @@ class Call:
                 if not in_range[i]:
                     assert (lp[r, i] == 0 if t == -1 else np.isnan(lp[r, i])) and (not ranks or rk[r, i] == 0)
                     continue
-                assert lp[r, i] == z[t] if z[t] == -np.inf else abs(lp[r, i] - (z[t] - lse)) <= tol(z[t]), (r, i)
+                assert lp[r, i] == z[t] if z[t] == -np.inf else near(lp[r, i], z[t]), (r, i)
                 assert not ranks or rk[r, i] == place[t], (r, i)
             # W / S has the relative errors of both sums, and W / S = ln S - H
             assert not entropy or abs(ent[r] - H) <= 1e-5 * (2 + 2 * abs(H) + abs(math.log(S))), r
@@ -88,7 +90,7 @@ class Call:
                 np.testing.assert_array_equal(ti[r], order[:self.k], err_msg=f"row {r}")
                 for i in range(self.k):
                     v = z[order[i]]
-                    assert tl[r, i] == v if v == -np.inf else abs(tl[r, i] - (v - lse)) <= tol(v), (r, i)
+                    assert tl[r, i] == v if v == -np.inf else near(tl[r, i], v), (r, i)
 
 
 def logits(rng, rows, vocab, hot=6):
@@ -167,6 +169,30 @@ def test_optional_outputs():
         c = Call(logits(rng, 4, 20000), "f32", rng.integers(0, 20000, (4, n_ids)), k)
         c.run(ranks, entropy)
         c.check(0, ranks and n_ids > 0, entropy)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("vocab", [40, 9000, 70001])
+def test_rows_masked_with_the_lowest_value(dtype, vocab):
+    """Masks of the type's lowest value instead of -inf, alone and next to it, rows that leave nothing, and logits
+    so large that their product with log2(e) is not finite."""
+    rng = np.random.default_rng(vocab)
+    low, high = float(torch.finfo(ref.torch_dtype(dtype)).min), float(torch.finfo(ref.torch_dtype(dtype)).max)
+    some = rng.random(vocab) < 0.03
+    some[vocab // 2] = True
+    z = [np.full(vocab, low), np.where(some, low, -np.inf), np.where(some, rng.standard_normal(vocab), low), np.where(some, low, rng.standard_normal(vocab)),
+         np.where(np.arange(vocab) % 3 == 0, -np.inf, np.where(some, 2.0, low)), np.where(some, high, 1.0), np.where(some, high, low), np.where(some, high / 2, high),
+         np.where(some, low / 2, low), np.where(some, low * 0.25, -np.inf), np.where(some, high, -np.inf)]
+    c = Call(np.stack(z), dtype, [[vocab // 2, 0, vocab - 1, 1]] * len(z), 32)
+    c.run()
+    c.check()
+    z[3][5] = np.nan  # a NaN counts in a row of extreme values too
+    z[5][vocab - 3] = np.nan
+    z[0][vocab // 3] = np.nan
+    from qwen2_decoder_forward_decode_gb300 import binding
+    c = Call(np.stack(z), dtype, [[vocab // 2, 0]] * len(z), 3)
+    c.run()
+    c.check(err=binding.DEV_NONFINITE)
 
 
 def test_large_values():
