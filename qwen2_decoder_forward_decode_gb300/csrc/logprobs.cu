@@ -10,6 +10,7 @@
 // logit (1024 rows of 152064 bf16: 62 us for one likely id, 76 with a second, unlikely one whose rank counts
 // every logit, 96 with 20 top tokens as well: 3.3 TB/s). One row takes 11.5 us, a chain of latencies: ids,
 // batch, bound, second look, join.
+// Short rows go to logprobs_rows.cu, whose row end has no barriers.
 //   - All rows' batches (256 threads x 8 vectors of 16 bytes) form one list, cut into equal consecutive ranges,
 //     one per CTA, three CTAs an SM. A row that a cut divides is joined by the last of its CTAs to arrive;
 //     every sum's order is fixed, results repeat bit by bit.
@@ -21,24 +22,19 @@
 //     maximum reaches it, hardly more than top_k of them, are read again and their logits at or above the
 //     bound sorted. (Lists that were kept while streaming, with a rising threshold, cost 50 us of 134 for
 //     1024 rows of 152064: the warps met to raise it.)
-#include "common.cuh"
+#include "logprobs.cuh"
 #include "op_util.h"
 
 #include <math.h>
 
 #include <algorithm>
-#include <type_traits>
 
 namespace qw {
-namespace {
 
 constexpr int LP_NT = 256, LP_NW = LP_NT / 32, LP_VPT = 8, LP_NS = 2;  // threads, warps, a batch's 16-byte vectors a thread, ring
-constexpr int LP_MAX_IDS = 8, LP_MAX_TOP = 32;
 constexpr int LP_CTAS_PER_SM = 3, LP_MAX_CTAS = 640;
 constexpr int LP_END = 5;         // what a row's end costs, in batches
 constexpr int LP_CAP = 384;       // keys in the list and the pushed ones
-constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
-typedef unsigned long long u64;
 
 struct LogprobPart {  // of a row that several CTAs share
   float m, s, w, top;
@@ -48,140 +44,7 @@ struct LogprobPart {  // of a row that several CTAs share
   u64 key[LP_MAX_TOP];
 };
 
-struct LogprobArgs {
-  const void* logits;
-  long long row_stride;
-  int n_rows, vocab, n_ids, top_k, batches;  // batches of a row
-  int pieces;  // > 0: rows are cut into so many pieces of their own and CTAs take whole pieces; 0: see Cuts
-  const int* ids;
-  float* logprobs;
-  int* ranks;
-  float* entropy;
-  int* top_ids;
-  float* top_logprobs;
-  unsigned int* counters;  // [2 * LP_MAX_CTAS], zero between calls
-  LogprobPart* parts;      // [2 * LP_MAX_CTAS]
-  int* err;
-};
-
-// (logit, lower id first) as an integer; -0 counts as 0
-__device__ __forceinline__ uint32_t order_bits(float z) {
-  const uint32_t u = __float_as_uint(z + 0.f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float order_value(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
-__device__ __forceinline__ u64 order_key(float z, int j) { return (u64)order_bits(z) << 32 | (0xffffffffu - (uint32_t)j); }
-__device__ __forceinline__ float key_value(u64 k) { return order_value((uint32_t)(k >> 32)); }
-
-__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
-constexpr u64 LP_NO_BAR = 0x007fffffffffffffull;  // the key of (-inf, id 0): every finite logit's is above
-
-// ---- 16 bytes of logits ------------------------------------------------------------------------------------
-//
-// pair(u): the logits of word u (two for 16-bit types) as packed fp32, with -inf raised to a finite value whose
-// exponential is 0 (so that d * exp(d) is 0 as well); a NaN stays.
-// Rows whose maximum lies so low that the floor would count, or so high that products with log2(e) overflow (masks
-// of the type's lowest value that leave nothing), are summed again, slowly.
-constexpr float LP_FLOOR = -1e28f;  // (times log2(e), and that times 2^31 logits, is finite)
-template <typename T>
-__device__ __forceinline__ bool extreme(float most) {
-  return !(most < 5e27f && most > (std::is_same<T, f16>::value ? -65000.f : -5e27f));
-}
-template <typename T> struct Logits;
-template <> struct Logits<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ uint32_t minus_inf() { return 0xff800000u; }
-  static __device__ __forceinline__ float floor() { return LP_FLOOR; }
-  // maximum of the vectors that were added
-  struct Top {
-    float m = -INFINITY;
-    __device__ __forceinline__ void add(const uint4& r) {
-      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w))));
-    }
-    __device__ __forceinline__ float value() const { return m; }
-  };
-  static __device__ __forceinline__ void pairs(const uint4& r, f32x2* p) {
-    p[0] = pack2(max_nan(__uint_as_float(r.x), LP_FLOOR), max_nan(__uint_as_float(r.y), LP_FLOOR));
-    p[1] = pack2(max_nan(__uint_as_float(r.z), LP_FLOOR), max_nan(__uint_as_float(r.w), LP_FLOOR));
-  }
-  // counts of logits at or above a threshold, a vector at a time
-  struct Count {
-    int n = 0;
-    __device__ __forceinline__ void add(const uint4& r, float thr) {
-      n += (__uint_as_float(r.x) >= thr) + (__uint_as_float(r.y) >= thr) + (__uint_as_float(r.z) >= thr) + (__uint_as_float(r.w) >= thr);
-    }
-    __device__ __forceinline__ int total() const { return n; }
-  };
-  typedef float Thr;
-  static __device__ __forceinline__ Thr thr(float z) { return z; }
-  static __device__ __forceinline__ Thr thr_above(float z) {  // the next larger value
-    const uint32_t bits = order_bits(z);
-    return order_value(bits == 0x80000000u ? 0x80000001u : bits + 1);
-  }
-};
-template <typename T2>
-__device__ __forceinline__ T2 as_pair(uint32_t u) { return *reinterpret_cast<const T2*>(&u); }
-// the next larger value of a 16-bit float's bits (0 and -0: the smallest positive one)
-__device__ __forceinline__ uint32_t next16(uint32_t b) { return (b & 0x7fff) == 0 ? 1u : b & 0x8000 ? b - 1 : b + 1; }
-template <typename T, typename T2>
-struct Logits16 {
-  static constexpr int N = 8;
-  struct Top {
-    T2 m = as_pair<T2>(std::is_same<T, bf16>::value ? 0xff80ff80u : 0xfc00fc00u);  // -inf
-    __device__ __forceinline__ void add(const uint4& r) {
-      m = __hmax2(m, __hmax2(__hmax2(as_pair<T2>(r.x), as_pair<T2>(r.y)), __hmax2(as_pair<T2>(r.z), as_pair<T2>(r.w))));
-    }
-    __device__ __forceinline__ float value() const { return fmaxf(__low2float(m), __high2float(m)); }
-  };
-  // Counts of both halves in one sum of masks: a true half adds 0xffff, so the sum of lo low and hi high ones is
-  // (lo - hi) 2^16 - lo.
-  struct Count {
-    uint32_t n = 0;
-    __device__ __forceinline__ void add(const uint4& r, T2 thr) {
-      n += __hge2_mask(as_pair<T2>(r.x), thr) + __hge2_mask(as_pair<T2>(r.y), thr);
-      n += __hge2_mask(as_pair<T2>(r.z), thr) + __hge2_mask(as_pair<T2>(r.w), thr);
-    }
-    __device__ __forceinline__ int total() const {
-      const uint32_t lo = -n & 0xffffu;
-      return (int)(2 * lo) - (int16_t)((n + lo) >> 16);
-    }
-  };
-  typedef T2 Thr;
-  static __device__ __forceinline__ uint32_t bits(float z) {
-    const T h = from_f32<T>(z);
-    return *reinterpret_cast<const uint16_t*>(&h);
-  }
-  static __device__ __forceinline__ T2 thr(float z) { return as_pair<T2>(bits(z) * 0x10001u); }
-  static __device__ __forceinline__ T2 thr_above(float z) { return as_pair<T2>(next16(bits(z)) * 0x10001u); }
-};
-template <> struct Logits<bf16> : Logits16<bf16, __nv_bfloat162> {
-  static __device__ __forceinline__ uint32_t minus_inf() { return 0xff80ff80u; }
-  static __device__ __forceinline__ float floor() { return to_f32(__float2bfloat16_rn(LP_FLOOR)); }
-  static __device__ __forceinline__ f32x2 pair(uint32_t u) {
-    const __nv_bfloat162 h = __hmax2_nan(as_pair<__nv_bfloat162>(u), __float2bfloat162_rn(floor()));
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(&h);
-    return pack2(bf_lo(v), bf_hi(v));
-  }
-  static __device__ __forceinline__ void pairs(const uint4& r, f32x2* p) {
-    p[0] = pair(r.x); p[1] = pair(r.y); p[2] = pair(r.z); p[3] = pair(r.w);
-  }
-};
-template <> struct Logits<f16> : Logits16<f16, __half2> {
-  static __device__ __forceinline__ uint32_t minus_inf() { return 0xfc00fc00u; }
-  static __device__ __forceinline__ float floor() { return -65504.f; }
-  static __device__ __forceinline__ f32x2 pair(uint32_t u) {
-    const float2 t = __half22float2(__hmax2_nan(as_pair<__half2>(u), __float2half2_rn(floor())));
-    return pack2(t.x, t.y);
-  }
-  static __device__ __forceinline__ void pairs(const uint4& r, f32x2* p) {
-    p[0] = pair(r.x); p[1] = pair(r.y); p[2] = pair(r.z); p[3] = pair(r.w);
-  }
-};
+namespace {
 
 constexpr int LP_GROUPS = 8;  // groups of a row's batches, of which each thread keeps a maximum
 constexpr int LP_WORK = 128;   // groups that are read again at a time
@@ -268,24 +131,6 @@ struct Batch {
     for (int i = 0; i < LP_VPT; ++i) r[i] = *reinterpret_cast<const uint4*>(stage + i * LP_NT * 16);
   }
 };
-
-// the logits of a vector
-__device__ __forceinline__ void unpack(const uint4& r, float* x, float) {
-  x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y); x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
-}
-__device__ __forceinline__ void unpack(const uint4& r, float* x, bf16) {
-  x[0] = bf_lo(r.x); x[1] = bf_hi(r.x); x[2] = bf_lo(r.y); x[3] = bf_hi(r.y);
-  x[4] = bf_lo(r.z); x[5] = bf_hi(r.z); x[6] = bf_lo(r.w); x[7] = bf_hi(r.w);
-}
-__device__ __forceinline__ void unpack(const uint4& r, float* x, f16) {
-  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = __half22float2(as_pair<__half2>(u[i]));
-    x[2 * i] = t.x;
-    x[2 * i + 1] = t.y;
-  }
-}
 
 // A bound on the top_k-th largest logit from the thread maxima, in steps of their upper 16 bits: the largest that
 // top_k threads reach. 0x7f (-inf's) or less where fewer have a finite maximum. All threads.
@@ -761,6 +606,16 @@ cudaError_t launch_logprobs(LogprobArgs a, int nsm, cudaStream_t s) {
 }
 static_assert(2 * LP_MAX_CTAS * sizeof(unsigned int) <= OP_COUNTER_BYTES, "counters");
 
+// Whether a warp a row (logprobs_rows.cu) is faster. A warp takes 6 us and 0.8 a KB of row, for as many rows as the GPU
+// has warps; the CTAs 9 us for every row that each of them gets, almost whatever its length. us here and there, 20 top
+// tokens: 16 rows of 2 KB 8.9 and 7.0, of 4 KB 8.7 and 8.7, of 8 KB 8.8 and 12.5; 1024 rows of 8 KB 24 and 13, of 16 KB 25 and
+// 20; 4096 rows of 2 KB 79 and 12.9, of 16 KB 84 and 40, of 32 KB 83 and 66 (without top tokens 43 and 47). The limit
+// also keeps a lane's chain of additions short: 24 KB of 16-bit logits are 192 on a path.
+bool rows_for_warps(int dtype, int n_rows, int vocab, int nsm) {
+  const long long rounds = ((long long)n_rows + nsm * LP_CTAS_PER_SM - 1) / (nsm * LP_CTAS_PER_SM);
+  return (long long)vocab * (long long)dtype_size(dtype) <= std::min(4096 * rounds, 24576ll);
+}
+
 }  // namespace
 }  // namespace qw
 
@@ -805,7 +660,8 @@ qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t voc
   const LogprobArgs a{logits, row_stride, n_rows, vocab, n_ids, top_k, 0, 0, ids, logprobs, ranks, entropy, top_ids,
                       top_logprobs, (unsigned int*)workspace, (LogprobPart*)((char*)workspace + OP_COUNTER_BYTES), err_dev};
   cudaStream_t s = (cudaStream_t)cuda_stream;
-  e = logits_dtype == QW_F32   ? launch_logprobs<float>(a, nsm, s)
+  e = rows_for_warps(logits_dtype, n_rows, vocab, nsm) ? launch_logprobs_rows(logits_dtype, a, nsm, s)
+      : logits_dtype == QW_F32 ? launch_logprobs<float>(a, nsm, s)
       : logits_dtype == QW_F16 ? launch_logprobs<f16>(a, nsm, s) : launch_logprobs<bf16>(a, nsm, s);
   if (e) return op_cuda_fail(e, "token logprobs launch");
   return QW_OK;

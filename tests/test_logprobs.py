@@ -195,6 +195,48 @@ def test_rows_masked_with_the_lowest_value(dtype, vocab):
     c.check(err=binding.DEV_NONFINITE)
 
 
+def _short_rows(rng, vocab, kind):
+    j = np.arange(vocab)
+    return {"random": lambda: rng.standard_normal(vocab) * 2, "equal": lambda: np.full(vocab, -3.25), "two values": lambda: (j % 3 == 1) * 1.0, "ascending": lambda: j / vocab * 8,
+            "masked": lambda: np.where(rng.random(vocab) < 0.9, -np.inf, rng.standard_normal(vocab)), "one finite": lambda: np.where(j == vocab // 2, 1.5, -np.inf),
+            "tiny": lambda: rng.integers(-3, 4, vocab) * 2.0 ** -23, "nan": lambda: np.where(j == vocab - 1, np.nan, 0.5), "inf": lambda: np.where(j == vocab // 3, np.inf, 0.5),
+            "empty": lambda: np.full(vocab, -np.inf), "lowest": lambda: np.where(rng.random(vocab) < 0.5, -65504.0, -np.inf)}[kind]()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("vocab,rows,gap,offset", [(1, 5, 0, 0), (31, 3, 2, 1), (257, 5000, 1, 3), (1024, 700, 0, 0), (1025, 460, 3, 2), (2049, 1000, 0, 5), (4999, 1900, 1, 0), (6143, 3200, 0, 1),
+                                                     (6145, 3200, 0, 0), (12287, 3200, 0, 0)])
+def test_many_short_rows(dtype, vocab, rows, gap, offset):
+    """Rows of a few KB, in numbers where one warp has a row and beyond: the first ones against the definition, the others, their
+    repeats, bit by bit against them (8 periods apart: a row's start within 16 bytes decides the order of its sums)."""
+    from qwen2_decoder_forward_decode_gb300 import binding
+    rng = np.random.default_rng(vocab)
+    kinds = ["random", "equal", "two values", "ascending", "masked", "one finite", "tiny", "nan", "inf", "empty", "lowest", "random", "random"]
+    n = min(rows, len(kinds))
+    z = np.stack([_short_rows(rng, vocab, k) for k in kinds[:n]])
+    ids = np.stack([rng.integers(0, vocab, n), rng.integers(0, vocab, n), np.full(n, vocab - 1), np.full(n, -1), np.zeros(n)], axis=1)
+    top = min(vocab, 32)
+    repeat = np.arange(rows) % n
+    c = Call(z[repeat], dtype, ids[repeat], top, gap, offset)
+    c.run()
+    torch.cuda.synchronize()
+    first = min(8 * n, rows)
+    # longer rows may be cut, at different places: two results near one truth, each by the bounds of check(), where
+    # |ln p| = (m - z) + ln S and ln S, H <= ln vocab
+    cut = vocab * c.buf.element_size() > 24576
+    for t, bound in ((c.lp, 1e-5), (c.ranks, 0), (c.ent, 1e-5 * (2 + 3 * math.log(vocab))), (c.top_ids, 0), (c.top_lp, 1e-5)):
+        got, again = t[:first][torch.arange(first, rows, device="cuda") % first], t[first:rows]
+        same = got.view(torch.int32) == again.view(torch.int32)
+        if cut and bound:
+            same |= (got.double() - again.double()).abs() <= 2 * (bound + ref.U * got.double().abs())
+        assert same.all()
+        assert (t[rows:] == 55).all()
+        t[first:] = 55
+    c.rows = first
+    odd = any(np.isnan(r).any() or (r == np.inf).any() or (r == -np.inf).all() for r in c.z[:n])
+    c.check(err=binding.DEV_NONFINITE if odd else 0)
+
+
 def test_large_values():
     rng = np.random.default_rng(0)
     for shift, scale in ((1e4, 1.0), (-3e4, 1.0), (0.0, 300.0)):
