@@ -35,13 +35,13 @@ constexpr int LP_NT = 256, LP_NW = LP_NT / 32, LP_VPT = 8, LP_NS = 2;  // thread
 constexpr int LP_CTAS_PER_SM = 3, LP_MAX_CTAS = 640;
 constexpr int LP_END = 5;         // what a row's end costs, in batches
 constexpr int LP_CAP = 384;       // keys in the list and the pushed ones
+constexpr int LP_EARLY = 3;       // keys of the parts that a thread fetches before it knows their bound
 
-struct LogprobPart {  // of a row that several CTAs share
+struct alignas(16) LogprobPart {  // of a row that several CTAs share
   float m, s, w, top;
-  int nan;
   int above[LP_MAX_IDS];
-  int n, pad[2];
-  u64 key[LP_MAX_TOP];
+  int nan, pad[3];
+  u64 key[LP_MAX_TOP];  // its likeliest tokens, 0 behind the last
 };
 
 namespace {
@@ -478,15 +478,11 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
       auto slot_of = [&](int c) { return a.parts + (c == c0 ? first : 2 * c); };
       LogprobPart* mine = slot_of(blockIdx.x);
       if (tid == 0) {
-        mine->m = mm;
-        mine->s = s;
-        mine->w = w;
-        mine->top = most;
+        *reinterpret_cast<float4*>(&mine->m) = make_float4(mm, s, w, most);
         mine->nan = nan;
-        mine->n = sh.n;
       }
       if (tid < a.n_ids) mine->above[tid] = sh.above[tid];
-      if (tid < sh.n) mine->key[tid] = sh.buf[sh.side][tid];
+      if (tid < a.top_k) mine->key[tid] = tid < sh.n ? sh.buf[sh.side][tid] : 0;
       __syncthreads();
       if (tid == 0) {
         __threadfence();
@@ -500,47 +496,71 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
       __syncthreads();
       write = sh.last;
       if (write) {
-        // every thread takes the parts c0 + tid, + LP_NT, ...: the same order of sums at every run
-        mm = -INFINITY;
-#pragma unroll 1
-        for (int c = c0 + tid; c <= c1; c += LP_NT) {
-          mm = fmaxf(mm, __ldcg(&slot_of(c)->m));
-          most = fmaxf(most, __ldcg(&slot_of(c)->top));
+        // Everything of the parts is fetched at once. Every thread takes the parts c0 + tid, + LP_NT, ...: the same
+        // order of sums at every run.
+        const int parts = c1 - c0 + 1, top_k = a.top_k;
+        u64 early[LP_EARLY];
+#pragma unroll
+        for (int k = 0; k < LP_EARLY; ++k) {
+          const int i = tid + k * LP_NT, c = i / LP_MAX_TOP, e = i % LP_MAX_TOP;
+          early[k] = c < parts && e < top_k ? __ldcg(&slot_of(c0 + c)->key[e]) : 0;
         }
-        mm = warp_max(mm);
-        most = warp_max(most);
+        // j parts whose q-th keys reach a key have j q >= top_k keys that do: the j-th largest of all q-th keys bounds the
+        // list from below. With q near twice the mean a part has, about 2 top_k keys reach it.
+        const int asked = min(parts, LP_CAP), q = min(top_k, (2 * top_k + asked - 1) / asked), jth = q ? (top_k + q - 1) / q : 0;
+        u64* qth = sh.buf[sh.side ^ 1];
+        float pm = -INFINITY, ps = 0.f, pw = 0.f, pt = -INFINITY;
+#pragma unroll 1
+        for (int c = tid; c < parts; c += LP_NT) {
+          const LogprobPart* p = slot_of(c0 + c);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(&p->m));
+          const int4 n0 = __ldcg(reinterpret_cast<const int4*>(p->above)), n1 = __ldcg(reinterpret_cast<const int4*>(p->above) + 1);
+          const int bad = __ldcg(&p->nan);
+          if (q && c < asked) qth[c] = __ldcg(&p->key[q - 1]);
+          const int n[LP_MAX_IDS] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+#pragma unroll
+          for (int e = 0; e < LP_MAX_IDS; ++e)
+            if (e < a.n_ids && n[e]) atomicAdd(&sh.above[e], n[e]);
+          if (bad) sh.nan = 1;
+          pt = fmaxf(pt, v.w);
+          if (v.x > -INFINITY) {
+            const float to = fmaxf(pm, v.x), d0 = pm == -INFINITY ? 0.f : pm - to, d1 = v.x - to, f0 = ex2(d0), f1 = ex2(d1);
+            pw = fmaf(d0, ps, pw) * f0 + fmaf(d1, v.y, v.z) * f1;
+            ps = fmaf(ps, f0, v.y * f1);
+            pm = to;
+          }
+        }
+        mm = warp_max(pm);
+        most = warp_max(pt);
         if (lane == 0) {
           sh.red[0][warp] = mm;
           sh.red[3][warp] = most;
         }
+        if (tid == 0) sh.bar = 0;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < LP_NW; ++i) {
           mm = fmaxf(mm, sh.red[0][i]);
           most = fmaxf(most, sh.red[3][i]);
         }
-        s = w = 0.f;
-#pragma unroll 1
-        for (int c = c0 + tid; c <= c1; c += LP_NT) {
-          const LogprobPart* p = slot_of(c);
-          const float pm = __ldcg(&p->m), ps = __ldcg(&p->s), pw = __ldcg(&p->w);
-          if (__ldcg(&p->nan)) sh.nan = 1;
-          if (pm > -INFINITY) {
-            const float d = pm - mm, f = ex2(d);
-            w = fmaf(fmaf(d, ps, pw), f, w);
-            s = fmaf(ps, f, s);
-          }
-#pragma unroll 1
-          for (int q = 0; q < a.n_ids; ++q) {
-            const int n = __ldcg(&p->above[q]);
-            if (n) atomicAdd(&sh.above[q], n);
-          }
+        {
+          const float d = pm == -INFINITY ? 0.f : pm - mm, f = pm == -INFINITY ? 0.f : ex2(d);
+          w = warp_sum(fmaf(d, ps, pw) * f);
+          s = warp_sum(ps * f);
         }
-        s = warp_sum(s);
-        w = warp_sum(w);
         if (lane == 0) {
           sh.red[1][warp] = s;
           sh.red[2][warp] = w;
+        }
+        if (q) {
+#pragma unroll 1
+          for (int c = tid; c < asked; c += LP_NT) {
+            const u64 key = qth[c];
+            int larger = 0;
+#pragma unroll 4
+            for (int x = 0; x < asked; ++x) larger += qth[x] > key;
+            if (key && larger == jth - 1) sh.bar = key;
+          }
         }
         __syncthreads();
         s = w = 0.f;
@@ -550,30 +570,36 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __
           w += sh.red[2][i];
         }
         nan = sh.nan;
-        // the parts' lists: at least top_k keys are not below the largest of the full lists' last keys
-        if (a.top_k) {
-          if (tid == 0) sh.bar = 0;
-          __syncthreads();
-          for (int c = c0 + tid; c <= c1; c += LP_NT) {
-            const LogprobPart* p = slot_of(c);
-            if (__ldcg(&p->n) == a.top_k) atomicMax(&sh.bar, __ldcg(&p->key[a.top_k - 1]));
-          }
-          __syncthreads();
+        if (q) {
           const u64 bar = sh.bar;
-          // so many parts at a time that they fit next to the best ones even if all their keys are taken
-          constexpr int step = (LP_CAP - LP_MAX_TOP) / LP_MAX_TOP;
-          for (int c = c0; c <= c1; c += step) {
-            const int n = min(step, c1 - c + 1);
+          auto push = [&](u64 key) {
+            if (!key || key < bar) return;
+            const int to = atomicAdd(&sh.n, 1);
+            if (to < LP_CAP) sh.buf[sh.side][to] = key;
+          };
+#pragma unroll
+          for (int k = 0; k < LP_EARLY; ++k) push(early[k]);
 #pragma unroll 1
-            for (int i = tid; i < n * LP_MAX_TOP; i += LP_NT) {
-              const LogprobPart* p = slot_of(c + i / LP_MAX_TOP);
-              const u64 key = i % LP_MAX_TOP < a.top_k ? __ldcg(&p->key[i % LP_MAX_TOP]) : 0;
-              if (i % LP_MAX_TOP < __ldcg(&p->n) && key >= bar) sh.buf[sh.side][atomicAdd(&sh.n, 1)] = key;
+          for (int i = tid + LP_EARLY * LP_NT; i < parts * LP_MAX_TOP; i += LP_NT)
+            if (i % LP_MAX_TOP < top_k) push(__ldcg(&slot_of(c0 + i / LP_MAX_TOP)->key[i % LP_MAX_TOP]));
+          __syncthreads();
+          const int listed = sh.n;
+          __syncthreads();
+          if (listed <= LP_CAP) {
+            compact(sh, top_k);
+          } else {  // more keys than have room: some parts at a time, next to the best ones
+            if (tid == 0) sh.n = 0;
+            __syncthreads();
+            constexpr int step = (LP_CAP - LP_MAX_TOP) / LP_MAX_TOP;
+#pragma unroll 1
+            for (int c = 0; c < parts; c += step) {
+              const int n = min(step, parts - c);
+#pragma unroll 1
+              for (int i = tid; i < n * LP_MAX_TOP; i += LP_NT)
+                if (i % LP_MAX_TOP < top_k) push(__ldcg(&slot_of(c0 + c + i / LP_MAX_TOP)->key[i % LP_MAX_TOP]));
+              __syncthreads();
+              compact(sh, top_k);
             }
-            __syncthreads();
-            const int listed = sh.n;
-            __syncthreads();
-            if (c + step > c1 || listed > LP_MAX_TOP) compact(sh, a.top_k);
           }
         }
       }

@@ -237,6 +237,19 @@ def test_many_short_rows(dtype, vocab, rows, gap, offset):
     c.check(err=binding.DEV_NONFINITE if odd else 0)
 
 
+@pytest.mark.parametrize("dtype,vocab", [("f32", 400003), ("bf16", 800001), ("f32", 4000001)])
+@pytest.mark.parametrize("kind", ["random", "ascending", "descending", "equal", "one finite", "few finite"])
+def test_a_row_of_many_parts(dtype, vocab, kind):
+    """About 50 and 450 parts are joined: lists that all reach the bound, that hardly any does, that are empty."""
+    rng = np.random.default_rng(vocab)
+    j = np.arange(vocab)
+    z = {"random": lambda: rng.standard_normal(vocab), "ascending": lambda: j / vocab * 8, "descending": lambda: j / vocab * -8, "equal": lambda: np.full(vocab, 0.5),
+         "one finite": lambda: np.where(j == vocab // 2, 1.5, -np.inf), "few finite": lambda: np.where(j % (vocab // 20) == 7, 0.25, -np.inf)}[kind]()
+    c = Call(z[None], dtype, [[0, vocab - 1, vocab // 2, 7, -1]], 32)
+    c.run()
+    c.check()
+
+
 def test_large_values():
     rng = np.random.default_rng(0)
     for shift, scale in ((1e4, 1.0), (-3e4, 1.0), (0.0, 300.0)):
