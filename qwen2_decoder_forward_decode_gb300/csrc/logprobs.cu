@@ -132,16 +132,25 @@ struct Batch {
   }
 };
 
-// A bound on the top_k-th largest logit from the thread maxima, in steps of their upper 16 bits: the largest that
-// top_k threads reach. 0x7f (-inf's) or less where fewer have a finite maximum. All threads.
-__device__ __forceinline__ uint32_t top_bound(float tmax, int top_k) {
-  const uint32_t key = order_bits(tmax) >> 16;
-  uint32_t bound = 0;
-#pragma unroll 1
-  for (uint32_t bit = 0x8000u; bit; bit >>= 1)
-    if (__syncthreads_count(key >= (bound | bit)) >= top_k) bound |= bit;
-  return bound;
+// A bound on the top_k-th largest logit from the thread maxima, in steps of their upper 15 bits: the largest that
+// top_k threads reach, at least the lowest finite logit's. By one warp: a search by all of them met at 16 barriers.
+// All threads; the list is empty.
+__device__ __forceinline__ uint32_t top_bound(Shared& sh, float tmax, int top_k) {
+  uint16_t* all = reinterpret_cast<uint16_t*>(sh.buf[sh.side ^ 1]);
+  all[threadIdx.x] = (uint16_t)(order_bits(tmax) >> 17);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const uint4 v = reinterpret_cast<const uint4*>(all)[threadIdx.x];
+    uint32_t keys[4] = {v.x, v.y, v.z, v.w}, most = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) most = max(most, max(keys[i] & 0xffffu, keys[i] >> 16));
+    const uint32_t bound = max(keys_bound<4>(keys, most, top_k), 0x40u);
+    if (threadIdx.x == 0) sh.bar = bound;
+  }
+  __syncthreads();
+  return (uint32_t)sh.bar;
 }
+static_assert(LP_NT == 32 * 8 && LP_MAX_TOP <= 32, "eight keys a lane");
 
 // The sorted top_k (or fewer, of finite logits) of batches b0 .. b1 - 1 of a row, into the empty list. tmax: the
 // thread's maximum of them; sh.top: its groups' (group: (batch - b0) / per). All threads.
@@ -149,12 +158,12 @@ template <typename T>
 __device__ __forceinline__ void select_top(const LogprobArgs& a, Shared& sh, int row, int b0, int b1, int per, float tmax) {
   constexpr int N = Logits<T>::N;
   const int tid = threadIdx.x, top_k = a.top_k;
-  const uint32_t bound = max(top_bound(tmax, top_k), 0x80u);  // (finite logits only)
+  const uint32_t bound = top_bound(sh, tmax, top_k);
   const T* z = (const T*)a.logits + (long long)row * a.row_stride;
   const int shift = (int)((uintptr_t)z % 16) / (int)sizeof(T);
   int hits = 0;  // the thread's groups that reach the bound
-  for (int g = 0; g * per < b1 - b0; ++g) hits |= (sh.top[g][tid] >= bound) << g;
-  u64 bar = ((u64)bound << 48) - 1;
+  for (int g = 0; g * per < b1 - b0; ++g) hits |= (sh.top[g][tid] >= 2 * bound) << g;
+  u64 bar = ((u64)bound << 49) - 1;
 #pragma unroll 1
   for (bool more = true; more;) {
     if (tid == 0) sh.n_work = 0;
@@ -327,7 +336,7 @@ struct Cuts {
 template <typename T>
 __global__ void __launch_bounds__(LP_NT, LP_CTAS_PER_SM) logprob_kernel(const __grid_constant__ LogprobArgs a) {
   constexpr int N = Batch<T>::N;
-  __shared__ Shared sh;
+  __shared__ __align__(16) Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   extern __shared__ __align__(16) unsigned char lp_ring[];
   const Cuts cuts(a);

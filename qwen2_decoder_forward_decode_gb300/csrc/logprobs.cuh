@@ -171,5 +171,26 @@ __device__ __forceinline__ void unpack(const uint4& r, float* x, f16) {
   }
 }
 
+// The largest 15-bit key that top_k of a warp's keys reach. keys: the lane's, in pairs (their upper bits are set here);
+// most: the largest of them. top_k <= 32. The whole warp.
+template <int W>
+__device__ __forceinline__ uint32_t keys_bound(uint32_t* keys, uint32_t most, int top_k) {
+  // top_k <= 32 lanes reach the least of the lanes' maxima: what it has in common with the largest is the bound's
+  const uint32_t lo = __reduce_min_sync(0xffffffffu, most), hi = __reduce_max_sync(0xffffffffu, most);
+  uint32_t bit = lo == hi ? 0u : 0x80000000u >> __clz(lo ^ hi), bound = bit ? hi & ~(2u * bit - 1u) : hi;
+#pragma unroll
+  for (int i = 0; i < W; ++i) keys[i] |= 0x80008000u;
+#pragma unroll 1
+  for (; bit; bit >>= 1) {
+    // a half's top bit outlasts the subtraction if the half reaches the candidate
+    const uint32_t v = (bound | bit) * 0x10001u;
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) n += (keys[i] - v) >> 15 & 0x10001u;
+    if ((int)__reduce_add_sync(0xffffffffu, (n & 0xffffu) + (n >> 16)) >= top_k) bound |= bit;
+  }
+  return bound;
+}
+
 }  // namespace
 }  // namespace qw

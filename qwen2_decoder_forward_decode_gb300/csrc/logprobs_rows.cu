@@ -110,21 +110,7 @@ __device__ __forceinline__ uint32_t top_bound(const WarpShared& sh, int top_k, i
   uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) most = max(most, max(keys[i] & 0xffffu, keys[i] >> 16));
-  // top_k <= 32 lanes reach the least of the lanes' maxima: what it has in common with the largest is the bound's
-  const uint32_t lo = __reduce_min_sync(0xffffffffu, most), hi = __reduce_max_sync(0xffffffffu, most);
-  uint32_t bit = lo == hi ? 0u : 0x80000000u >> __clz(lo ^ hi), bound = bit ? hi & ~(2u * bit - 1u) : hi;
-#pragma unroll
-  for (int i = 0; i < W; ++i) keys[i] |= 0x80008000u;
-#pragma unroll 1
-  for (; bit; bit >>= 1) {
-    // a half's top bit outlasts the subtraction if the half reaches the candidate
-    const uint32_t v = (bound | bit) * 0x10001u;
-    uint32_t n = 0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) n += (keys[i] - v) >> 15 & 0x10001u;
-    if ((int)__reduce_add_sync(0xffffffffu, (n & 0xffffu) + (n >> 16)) >= top_k) bound |= bit;
-  }
-  bound = max(bound, 0x40u);
+  const uint32_t bound = max(keys_bound<W>(keys, most, top_k), 0x40u);
   const uint32_t v = bound * 0x10001u;
   hits = 0;
 #pragma unroll
