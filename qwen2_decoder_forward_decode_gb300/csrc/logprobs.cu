@@ -5,10 +5,10 @@
 // entropy is ln S - W / S. A larger maximum m' turns S into S e^(m - m') and W into (W + (m - m') S) e^(m - m'),
 // so one pass with running values does. Tokens are ordered by (logit, lower id first) as one 64-bit key.
 //
-// What bounds it: each logit is read once, so HBM for fp32 logits (1024 rows of 151936: 136 us, 4.6 TB/s; without top
-// tokens 110 us, 5.7 TB/s); 16-bit ones arrive twice as fast and are bound by the SMs' instructions, 9 to 14 a
+// What bounds it: each logit is read once, so HBM for fp32 logits (1024 rows of 151936: 131 us, 4.7 TB/s; without top
+// tokens 106 us, 5.9 TB/s); 16-bit ones arrive twice as fast and are bound by the SMs' instructions, 9 to 14 a
 // logit (1024 rows of 152064 bf16: 62 us for one likely id, 76 with a second, unlikely one whose rank counts
-// every logit, 96 with 20 top tokens as well: 3.3 TB/s). One row takes 11.5 us, a chain of latencies: ids,
+// every logit, 94 with 20 top tokens as well: 3.3 TB/s). One row takes 10 to 12 us, a chain of latencies: ids,
 // batch, bound, second look, join.
 // Short rows go to logprobs_rows.cu, whose row end has no barriers.
 //   - All rows' batches (256 threads x 8 vectors of 16 bytes) form one list, cut into equal consecutive ranges,
@@ -22,6 +22,9 @@
 //     maximum reaches it, hardly more than top_k of them, are read again and their logits at or above the
 //     bound sorted. (Lists that were kept while streaming, with a rising threshold, cost 50 us of 134 for
 //     1024 rows of 152064: the warps met to raise it.)
+//   - The join of a divided row takes one round trip to the L2 cache for all of its parts and a bound that about 2 top_k
+//     of their keys reach (with the counts fetched id by id and a bound that let 400 keys in, 2 rows of 152064 fp32 and 32
+//     top tokens took 23.5 us, not 12.4).
 #include "logprobs.cuh"
 #include "op_util.h"
 
