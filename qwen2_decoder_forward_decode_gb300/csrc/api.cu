@@ -1003,9 +1003,15 @@ qw_status qw_read_logprobs(qw_model* m, int32_t seq, const int32_t* ids, int32_t
   constexpr size_t ws_at = (sizeof(Row) + 255) / 256 * 256;
   const size_t ws_bytes = qw_op_token_logprobs_workspace(1, m->d.V, 32);
   if (!m->lp_block) {
-    QW_CUDA(cudaMalloc(&m->lp_block, ws_at + ws_bytes));
-    const cudaError_t e = cudaMemset(m->lp_block, 0, ws_at + ws_bytes);
-    if (e) return cuda_fail(e, "cudaMemset");
+    void* block = nullptr;
+    QW_CUDA(cudaMalloc(&block, ws_at + ws_bytes));
+    // on the model's stream: one that does not wait for the default stream would run ahead of a plain memset
+    const cudaError_t e = cudaMemsetAsync(block, 0, ws_at + ws_bytes, m->stream);
+    if (e) {
+      cudaFree(block);
+      return cuda_fail(e, "cudaMemsetAsync");
+    }
+    m->lp_block = block;
   }
   Row* r = (Row*)m->lp_block;
   Row h{};

@@ -313,3 +313,36 @@ def test_a_model_reads_the_log_probabilities_of_its_last_step():
             assert m.position(1) == 11
         finally:
             m.close()
+
+
+def test_the_first_log_probabilities_of_a_model_do_not_wait_for_the_default_stream():
+    """A model with a stream of its own, work pending on the default stream when the scratch is made: the clear must be in
+    the model's stream, before the ids and the kernel, and not behind the pending work."""
+    from qwen2_decoder_forward_decode_gb300 import DeviceWeights, Model
+    from synth import SHAPES, make_prompt, make_weights
+    s = SHAPES["tiny"]
+    w = DeviceWeights(make_weights(s), 0)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        m = Model(s, w, 32)
+        try:
+            m.prefill(make_prompt(s, 9))
+            z = m.logits().astype(np.float64)
+            lse = z.max() + math.log(np.exp(z - z.max()).sum())
+            order = np.lexsort((np.arange(len(z)), -z))
+            pending = torch.cuda.Event()
+            torch.cuda._sleep(10 ** 9)  # about half a second
+            pending.record()
+            got = m.logprobs([7, 200, 31], top_k=5)
+            assert not pending.query(), "the default stream's work was over before the call"
+            torch.cuda.synchronize()
+            again = m.logprobs([7, 200, 31], top_k=5)
+            for lp, ranks, ent, top_ids, top_lp in (got, again):
+                np.testing.assert_allclose(lp, z[[7, 200, 31]] - lse, rtol=0, atol=2e-5)
+                assert ranks.tolist() == [1 + int(np.where(order == t)[0][0]) for t in (7, 200, 31)]
+                assert top_ids.tolist() == order[:5].tolist()
+                np.testing.assert_allclose(top_lp, z[order[:5]] - lse, rtol=0, atol=2e-5)
+                p = np.exp(z - lse)
+                assert abs(ent + (p * (z - lse)).sum()) < 1e-4
+        finally:
+            m.close()
