@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel
   using Raw = typename std::conditional<C::F32IO, float2, uint32_t>::type;  // two query elements
   constexpr int NKK = HD / 16, NA = HB == 8 ? (NQ + 1) / 2 : NQ, NPA = HB == 8 ? (NP + 1) / 2 : NP;  // products per step
   static_assert(NS >= 2, "ring");
+  static_assert(TILE >= least_tile(sizeof(T) == 4, HD) && V <= PA_MAX_WEIGHT, "length of the list of tiles");
   extern __shared__ __align__(128) unsigned char pa_smem[];
   __shared__ uint32_t s_mask[NW][NS];  // rows of a stage that exist
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
@@ -354,8 +355,9 @@ qw_status qw_op_paged_attention(const qw_paged_kv* cache, int32_t n_seqs, int32_
   if (n_seqs > 65535 || n_heads > 4096) return op_fail(QW_ERR_UNSUPPORTED, "more than 65535 sequences or 4096 heads");
   if ((int64_t)max_blocks * c.page_size > (int64_t)1 << 30)
     return op_fail(QW_ERR_UNSUPPORTED, "max_blocks * page_size above 2^30");
-  // the tile list's numbers are 31-bit: tiles of at least 32 positions, and a weight of at most 5 a unit
-  if ((int64_t)n_seqs * n_heads * ((int64_t)max_blocks * c.page_size / 32 + 6) > 0x7fffffffll)
+  // the tile list's numbers are 31-bit: a unit (at most one a head) has its tiles, the last one cut, and its weight
+  const int64_t unit = (int64_t)max_blocks * c.page_size / least_tile(c.dtype == QW_F32, c.head_dim) + 1 + PA_MAX_WEIGHT;
+  if ((int64_t)n_seqs * n_heads * unit > 0x7fffffffll)
     return op_fail(QW_ERR_UNSUPPORTED, "n_seqs * n_heads * max_blocks * page_size too large");
   if (!std::isfinite(scale)) return op_fail(QW_ERR_INVALID_ARG, "scale not finite");
   if (n_seqs == 0) return QW_OK;

@@ -17,6 +17,9 @@ constexpr int PA_MAX_HD = 256;
 constexpr int PA_MAX_CTAS = 320;   // CTAs the workspace has room for
 constexpr int PA_WHOLE = 3;        // units of at most so many tiles are not split
 constexpr int PA_LEVELS = 4;       // of a join
+constexpr int PA_MAX_WEIGHT = 4;   // of a unit's end in the list of tiles, in tiles
+// positions of the kernels' tiles, at least: bounds the length of the list of tiles (each kernel asserts both)
+__host__ __device__ constexpr int least_tile(bool f32_cache, int head_dim) { return f32_cache && head_dim > 128 ? 16 : 32; }
 constexpr int PA_FLUSH = 16;         // products that the tensor cores sum up for an fp32 caller (their additions cut,
                                    // so a long sum's error grows with its length: 1.6e-6 for 100)
 constexpr float PA_BIAS = 10.f;    // probabilities are kept times 2^10: their fp16 halves stay normal

@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(SimtCfg<T, HD, HB>::NT, 2) paged_simt_kernel(c
   constexpr int PG = G4 >= 32 ? 1 : 32 / G4;    // lanes that share a group, by position
   constexpr int GL = G4 >= 32 ? G4 / 32 : 1;    // groups a lane owns
   static_assert(NS >= 2, "ring");
+  static_assert(TILE >= least_tile(sizeof(T) == 4, HD) && V <= PA_MAX_WEIGHT, "length of the list of tiles");
   extern __shared__ __align__(128) unsigned char pa_smem[];
   __shared__ uint32_t s_mask[NW][NS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

@@ -111,6 +111,21 @@ def test_sizes_beyond_32_bits_are_refused():
     refused(lambda: logprobs(rows=1 << 20, vocab=1 << 24, stride=1 << 24), 2, "too large")
 
 
+def test_tile_lists_beyond_31_bits_are_refused():
+    """Tables that share pages can hold any lengths. Tiles have 16 positions in fp32 caches of more than 128
+    dimensions, at least 32 else: the same shape is within the range there."""
+    def status(dtype, hd, n_seqs):
+        kv = cache(dtype=dtype, head_dim=hd, n_kv_heads=1, page_stride=16 * hd, head_stride=0, pos_stride=hd)
+        with pytest.raises(binding.QwError) as e:  # (in range: refused for its addresses, or for want of a GPU)
+            attn(kv, n_seqs=n_seqs, n_heads=63, max_blocks=1 << 16, io=dtype, q_stride=63 * hd, out_stride=63 * hd)
+        return e.value.status, str(e.value)
+    for hd in (136, 256):
+        assert status(0, hd, 1024)[0] == 2 and "too large" in status(0, hd, 1024)[1]
+        assert status(0, hd, 521)[0] == 2 and status(0, hd, 520)[0] != 2  # 63 * 2^16 tiles: 2^31 is 520.1 times that
+        assert status(2, hd, 1024)[0] != 2 and status(1, hd, 1024)[0] != 2
+    assert status(0, 128, 1040)[0] != 2 and status(0, 128, 1041)[0] == 2
+
+
 def test_release_refuses_no_flags():
     refused(lambda: release(done=None), 1)
 
