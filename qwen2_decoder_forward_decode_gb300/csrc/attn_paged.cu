@@ -320,10 +320,12 @@ cudaError_t launch_16bit(int ctas, const PagedAttnArgs& a, cudaStream_t s) {
   return a.hd <= 64 ? launch_mma<T, 64, 16, IO>(ctas, a, s) : launch_mma<T, 128, 16, IO>(ctas, a, s);
 }
 
-// floats of one part: the largest instance that the shape may take
+// floats of one part: of the largest instance that the shape may take, whatever its types (launch_16bit's HB and HD; the
+// CUDA cores' HB is at most 8, their HD at most this one)
 size_t part_floats(int n_heads, int n_kv_heads, int head_dim) {
-  const int hb = n_heads / n_kv_heads <= 8 ? 8 : 16, hd = head_dim <= 32 ? 32 : head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-  return (size_t)hb * comb_stride(hd);
+  const bool wide = n_heads / n_kv_heads > 8;
+  const int hd = head_dim <= 32 && !wide ? 32 : head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+  return (size_t)(wide ? 16 : 8) * comb_stride(hd);
 }
 static_assert(PA_LEVELS * 2 * PA_MAX_CTAS * sizeof(unsigned int) <= OP_COUNTER_BYTES, "counters");
 

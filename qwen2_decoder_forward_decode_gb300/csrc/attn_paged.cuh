@@ -37,7 +37,7 @@ struct PagedAttnArgs {
   float scale;
   float* lse;
   unsigned int* counters;  // [PA_LEVELS][2 * PA_MAX_CTAS], zero between calls
-  float* part;             // [2 * PA_MAX_CTAS][HB][HD + 8]
+  float* part;             // [2 * PA_MAX_CTAS][HB][comb_stride(HD)]
   int* err;
 };
 

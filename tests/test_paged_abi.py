@@ -158,6 +158,15 @@ def test_workspace_sizes(L):
     assert L.qw_op_token_logprobs_workspace(4, 1000, 33) == 0
 
 
+@pytest.mark.parametrize("group", [1, 4, 8, 9, 16, 40])
+@pytest.mark.parametrize("hd", [8, 32, 40, 64, 96, 128, 136, 256])
+def test_the_attention_workspace_holds_every_part(L, group, hd):
+    """640 parts of the kernel's heads and dimensions (16-bit caches: 64 dimensions at least for groups of more than 8
+    heads), each with a maximum and a sum in a row of 4 more, and the counters."""
+    pad = next(x for x in (32, 64, 128, 256) if hd <= x and (x > 32 or group <= 8))
+    assert L.qw_op_paged_attention_workspace(2 * group, 2, hd) >= 16384 + 640 * (16 if group > 8 else 8) * (pad + 4) * 4
+
+
 def test_model_logprobs_refuses_a_null_model(L):
     assert L.qw_read_logprobs(None, 0, None, 0, None, None, None, 0, None, None) == 1
 

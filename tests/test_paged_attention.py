@@ -258,3 +258,16 @@ def test_a_captured_call_follows_the_device_lengths_and_tables():
         c.out.fill_(3.0)
         g.replay()
         c.check(kv=lambda b, h: (c.c.k[b][:lens[b], h], c.c.v[b][:lens[b], h]))
+
+
+@pytest.mark.parametrize("io,cache", TYPES)
+@pytest.mark.parametrize("nq,hd", [(16, 32), (9, 8), (40, 16)])
+def test_large_groups_of_short_heads_stay_in_their_workspace(io, cache, nq, hd):
+    """Split units of groups above 8 heads and at most 32 dimensions, whose parts are padded to 64."""
+    c = Call([9000, 3, 0, 4000], nq, 1, hd, 16, io, cache)
+    size = c.ws.numel()
+    c.ws = torch.cat([c.ws, torch.full((1 << 20,), 77, dtype=torch.uint8, device="cuda")])
+    for _ in range(2):
+        c.run()
+        c.check()
+    assert (c.ws[size:] == 77).all() and (c.ws[:16384] == 0).all()
