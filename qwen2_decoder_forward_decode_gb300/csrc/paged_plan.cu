@@ -230,7 +230,9 @@ cudaError_t launch_plan(K kernel, Args a, int64_t items, bool aliased, cudaStrea
   const size_t smem = (size_t)2 * (a.n + 1) * sizeof(int);
   cudaError_t e = cudaSuccess;
   int dev = 0, nsm = 0, ctas = 1;
-  if (smem > 40 * 1024 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) return e;
+  // the same limit in every call: it is the kernel's, and a smaller one could come between another thread's setting and launch
+  constexpr int most = 2 * (PLAN_MAX_SEQS + 1) * (int)sizeof(int);
+  if (smem > 40 * 1024 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most))) return e;
   if (items > PLAN_SMALL) {
     if ((e = cudaGetDevice(&dev)) || (e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev))) return e;
     const int64_t want = (items + 4 * PLAN_THREADS - 1) / (4 * PLAN_THREADS);

@@ -239,3 +239,33 @@ def test_host_memory_is_refused():
     with pytest.raises(binding.QwError) as e:
         p.run()
     assert e.value.status == 1 and "device memory" in str(e.value)
+
+
+def test_batches_of_many_sizes_from_several_threads():
+    """The kernels' shared memory grows with the number of sequences: calls of other sizes in other host threads must not
+    change what a launch is allowed."""
+    import threading
+    from qwen2_decoder_forward_decode_gb300 import binding
+    L = binding.lib()
+    plans = [Plan([5] * n, [0] * (n - 9) + [1] * 9, 16, 1, 9) for n in (16384, 6000, 16384, 6000, 9000)]
+    streams, done = [torch.cuda.Stream() for _ in plans], dev([0] * 16384)
+    torch.cuda.synchronize()
+    failed = []
+
+    def loop(p, stream):
+        ptr = lambda *names: [getattr(p, n).data_ptr() for n in names]  # noqa: E731
+        plan = [len(p.lens), p.page, p.n_pages, p.blocks, p.max_tokens] + ptr("tlens", "tnew", "tfree", "tn_free", "ttable", "lens_out", "n_free_out", "cu", "positions", "slots", "err")
+        other = torch.zeros(len(p.lens) + 1, dtype=torch.int32, device="cuda")
+        back = [len(p.lens), p.page, p.n_pages, p.blocks] + ptr("tlens") + [done.data_ptr()] + ptr("ttable", "tfree", "tn_free") + [other.data_ptr(), other.data_ptr() + 4 * len(p.lens)] + ptr("err")
+        for _ in range(5000):  # (prepared calls: the more of a thread's time is in the library, the nearer they come)
+            if L.qw_op_page_plan(*plan, stream.cuda_stream) or L.qw_op_page_release(*back, stream.cuda_stream):
+                failed.append((len(p.lens), L.qw_last_error()))
+
+    threads = [threading.Thread(target=loop, args=a) for a in zip(plans, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, (len(failed), failed[0])
+    for p in plans:
+        p.check()
