@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel
   int stage = 0, ahead = NS - 1;  // tiles still to be requested before the first is used
   Place pend[2];
   int n_pend = 0;
+  const float sc = a.scale * LOG2E;
   // a unit's queries, columns 2 tig, 2 tig + 1 and 2 tig + 8, 2 tig + 9 of every 16: requested before the unit
   // ahead of it ends, used after its first tile has come
   Raw xq[HB / 8][NKK][2];
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel
     const int t0 = p.t, t1 = min(p.nt, r.end - p.v - V);
     bool fresh = true;
     uint32_t qa[NA][NKK][4];  // A fragments: pieces of rows gid and gid + 8
-    float sc[2];
+    float undo[2];                // of the queries' power of two
     float o[HD / 8][4], m[HB / 8], l[HB / 8], m_there[HB / 8];
     bool there = false;  // part of o is in comb already, relative to m_there
     int since = 0;
@@ -141,19 +142,22 @@ __global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel
         for (int half = 0; half < HB / 8; ++half) {
           float up = 1.f, down = 1.f;
           if constexpr (C::F32IO) {
-            // fp32 queries times a power of two that puts the row's largest at 2^10: the pieces stay normal
+            // fp32 queries times a power of two that keeps the pieces normal: fp16 pieces with the row's largest at
+            // 2^10, whatever its size; bf16 pieces, whose range is fp32's own, with only small ones raised to 2^-50, so
+            // that no product overflows that would not in fp32. The scores undo it before they are scaled.
             float top = 0.f;
 #pragma unroll
             for (int i = 0; i < 2 * NKK; ++i) top = fmaxf(top, fmaxf(fabsf(xq[half][i / 2][i % 2].x), fabsf(xq[half][i / 2][i % 2].y)));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-            if (ex > -100 && ex < 100) {
-              up = __uint_as_float((uint32_t)(127 + 10 - ex) << 23);
-              down = __uint_as_float((uint32_t)(127 - 10 + ex) << 23);
+            if (ex < 128) {  // (a row with an infinity passes as it is)
+              const int shift = std::is_same<T, f16>::value ? min(10 - ex, 126) : max(-50 - ex, 0);
+              up = __uint_as_float((uint32_t)(127 + shift) << 23);
+              down = __uint_as_float((uint32_t)(127 - shift) << 23);
             }
           }
-          sc[half] = a.scale * LOG2E * down;
+          undo[half] = down;
 #pragma unroll
           for (int kk = 0; kk < NKK; ++kk)
 #pragma unroll
@@ -166,7 +170,7 @@ __global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel
               if (HB == 8 && NQ & 1) qa[NA - 1][kk][2 * c + 1] = 0u;
             }
         }
-        if (HB == 8) sc[1] = sc[0];
+        if (HB == 8) undo[1] = undo[0];
       }
       const uint32_t mask = s_mask[warp][stage];
       if (mask) {
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel
 #pragma unroll
           for (int i = 0; i < 4 * R; ++i) {
             const float x = HB == 8 ? c[0][i >> 1][i & 1] + c[0][i >> 1][2 + (i & 1)] : c[0][i >> 1][2 * half + (i & 1)];
-            s[i] = (mask >> (2 * tig + (i & 1) + 8 * (i >> 1))) & 1 ? x * sc[half] : -INFINITY;
+            s[i] = (mask >> (2 * tig + (i & 1) + 8 * (i >> 1))) & 1 ? (C::F32IO ? x * undo[half] : x) * sc : -INFINITY;
             top = fmaxf(top, s[i]);
           }
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));

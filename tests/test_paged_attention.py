@@ -271,3 +271,34 @@ def test_large_groups_of_short_heads_stay_in_their_workspace(io, cache, nq, hd):
         c.run()
         c.check()
     assert (c.ws[size:] == 77).all() and (c.ws[:16384] == 0).all()
+
+
+@pytest.mark.parametrize("io,cache,hd", [("f32", "f16", 128), ("f32", "f16", 32), ("f32", "bf16", 64), ("f32", "bf16", 128), ("f32", "f32", 64), ("f32", "f16", 256), ("f32", "f32", 256)])
+@pytest.mark.parametrize("nq", [4, 20])
+@pytest.mark.parametrize("e", [-124, -101, -99, 99, 101, 119])
+def test_queries_of_any_exponent(io, cache, hd, nq, e):
+    """Queries of 2^e, with scales that undo it: finite scores of finite numbers, near the ends of fp32's range too."""
+    c = Call([300, 77], nq, 2, hd, 16, io, cache, q_scale=2.0 ** (e + 1), scale=float(np.float32(2.0 ** -e / math.sqrt(hd))))
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("hd,nq", [(64, 4), (128, 4), (64, 20), (256, 4)])
+@pytest.mark.parametrize("cache", ["bf16", "f32"])
+@pytest.mark.parametrize("e_k,e_q", [(112, -112), (115, 0), (-110, 0), (-100, 110)])
+def test_keys_of_any_exponent(cache, hd, nq, e_k, e_q):
+    """Keys of 2^e_k under queries of 2^e_q, with scales that undo both."""
+    c = Call([300, 77], nq, 2, hd, 16, "f32", cache, q_scale=2.0 ** (e_q + 1), scale=float(np.float32(2.0 ** -(e_k + e_q) / math.sqrt(hd))))
+    c.c.tk.mul_(2.0 ** e_k)  # (a power of two: exact)
+    c.c.k = [k * 2.0 ** e_k for k in c.c.k]
+    c.run()
+    c.check()
+
+
+def test_zero_and_subnormal_queries():
+    for cache in ("f16", "bf16", "f32"):
+        c = Call([300, 77], 4, 2, 64, 16, "f32", cache, q_scale=2.0 ** -130, scale=2.0 ** 126)
+        c.tq[1] = 0.0
+        c.q[1] = 0.0
+        c.run()
+        c.check()
