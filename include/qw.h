@@ -410,7 +410,7 @@ qw_status qw_op_rope_append(const qw_paged_kv *cache, int32_t n_tokens, int32_t 
  * A NaN among the keys, values or queries makes every output that it reaches NaN, an infinity
  * makes it infinite or NaN; other heads and sequences are not touched. A length that is negative or
  * beyond max_blocks pages is cut to that range, the positions of a page outside [0, n_pages)
- * are left out, and both set QW_DEV_PAGE.
+ * are left out (out 0 and lse -inf if none remains), and both set QW_DEV_PAGE.
  *   block_table [n_seqs][max_blocks], max_blocks * page_size at most 2^30; lens [n_seqs]
  *   q   [n_seqs][n_heads][head_dim] of io_dtype, heads contiguous, q_stride elements between
  *       sequences; out the same with out_stride; both 16-byte aligned, strides multiples of

@@ -307,11 +307,22 @@ struct Finish {
     return a;
   }
 
+  // Whether any position of a sequence lies in a page of the cache. (Asked where no score was above -inf.)
+  static __device__ __noinline__ bool any_page(const PagedAttnArgs& a, int b, int len) {
+#pragma unroll 1
+    for (int blk = 0; (long long)blk * a.page < len; ++blk) {
+      const int id = __ldg(a.table + (size_t)b * a.max_blocks + blk);
+      if (id >= 0 && id < a.n_pages) return true;
+    }
+    return false;
+  }
+
   static __device__ __forceinline__ void write_out(const PagedAttnArgs& a, const Place& p, int n_hb, int h, int d, const Acc& s) {
     const int group = a.nq / a.nkv, g = p.u / n_hb, hg = (p.u - g * n_hb) * HB + h;
     if (hg >= group || d >= a.hd) return;
     const int head = g * group + hg;
-    const float inv = 1.f / s.l;  // (l = 0: every score was -inf, and 0 / 0 is the formula's NaN)
+    // l = 0: every score was -inf, and 0 / 0 is the formula's NaN; or no position was left: 0, as for length 0
+    const float inv = s.l == 0.f && !any_page(a, p.b, p.len) ? 1.f : 1.f / s.l;
     store4((IO*)a.out + p.b * a.out_stride + head * a.hd + d, make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv));
     if (d == 0 && a.lse) a.lse[(size_t)p.b * a.nq + head] = (s.m - PA_BIAS + log2f(s.l)) * LN2;
   }

@@ -302,3 +302,34 @@ def test_zero_and_subnormal_queries():
         c.q[1] = 0.0
         c.run()
         c.check()
+
+
+@pytest.mark.parametrize("io,cache,hd", [("f32", "f16", 128), ("bf16", "bf16", 64), ("f16", "f16", 32), ("f32", "bf16", 128), ("f32", "f32", 32), ("f32", "f32", 256), ("bf16", "bf16", 256)])
+@pytest.mark.parametrize("nq", [4, 20])
+def test_a_sequence_with_no_page_left_is_empty(io, cache, hd, nq):
+    """Tables without a page of the cache, of one tile and of many CTAs, give what length 0 gives; a long sequence with
+    only its last page keeps that one."""
+    from qwen2_decoder_forward_decode_gb300 import binding
+    lens = [5000, 40, 5, 3000, 4000, 0]
+    c = Call(lens, nq, 2, hd, 16, io, cache)
+    c.c.ttable[0] = -7
+    c.c.ttable[2] = c.c.n_pages
+    c.c.ttable[4, :249] = 10 ** 6
+    c.run()
+    kept = {0: slice(0), 2: slice(0), 4: slice(3984, 4000)}
+    c.check(err=binding.DEV_PAGE, kv=lambda b, h: (c.c.k[b][kept.get(b, slice(None)), h], c.c.v[b][kept.get(b, slice(None)), h]))
+    assert (c.out[[0, 2, 5], :nq * hd] == 0).all() and (c.lse[[0, 2, 5]] == -math.inf).all()
+
+
+@pytest.mark.parametrize("io,cache,hd", [("f32", "f16", 128), ("bf16", "bf16", 64), ("f32", "f32", 32)])
+def test_scores_of_minus_infinity_are_no_empty_sequence(io, cache, hd):
+    """Every score -inf where positions are there, next to pages that are left out: still 0 / 0."""
+    from qwen2_decoder_forward_decode_gb300 import binding
+    c = Call([3000, 40], 2, 1, hd, 16, io, cache)
+    c.tq[:2, :2 * hd] = c.tq[:2, :2 * hd].abs() + 0.1
+    c.c.ttable[0, 1:] = -1
+    c.c.tk[int(c.c.table[0, 0]), 0, :, 3] = -math.inf
+    c.run()
+    torch.cuda.synchronize()
+    assert int(c.err) == binding.DEV_PAGE
+    assert c.out[0, :2 * hd].isnan().all() and c.out[1, :2 * hd].isfinite().all()
