@@ -333,8 +333,9 @@ typedef struct {
  *                cu_tokens[b] <= t < cu_tokens[b + 1]
  *   positions    [max_tokens]: lens[b] + t - cu_tokens[b]; 0 behind the last token
  *   slots        [max_tokens]: the token's slot in the cache; -1 behind the last token
- * If the step does not fit (too few free pages, more than max_tokens tokens or max_blocks pages
- * of a sequence, a negative length or count, n_free outside [0, n_pages]) QW_DEV_CAPACITY is
+ * If the step does not fit (too few free pages, more than max_tokens tokens, more than max_blocks
+ * pages or 2^31 - 1 positions of a sequence, a negative length or count, n_free outside
+ * [0, n_pages]) QW_DEV_CAPACITY is
  * set and the step is empty: lens_out = lens, n_free_out = n_free, cu_tokens 0, positions 0,
  * slots -1. A page id outside [0, n_pages) gives slot -1 and sets QW_DEV_PAGE. n_seqs <= 16384,
  * n_pages and max_tokens <= 2^30.

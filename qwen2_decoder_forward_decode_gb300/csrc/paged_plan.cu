@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(const PlanArgs 
   if (!a.items) pdl_wait();  // (the launch that reads what this one overwrites)
   if (tid == 0) s_bad = 0;
   const int n_free = *a.n_free;
-  const long long room = (long long)a.max_blocks * a.page;
+  const long long room = min((long long)a.max_blocks * a.page, 0x7fffffffll);  // (lengths are 32-bit)
   __syncthreads();
   block_scan2(a.n, cu, pg, [&](int i, uint32_t& t, uint32_t& p) {
     const int len = a.lens[i], add = a.n_new ? a.n_new[i] : 1;

@@ -269,3 +269,21 @@ def test_batches_of_many_sizes_from_several_threads():
     assert not failed, (len(failed), failed[0])
     for p in plans:
         p.check()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_lengths_end_at_31_bits(in_place):
+    """Tables whose rows hold more positions than a length can count: the last length fits, the next does not."""
+    from qwen2_decoder_forward_decode_gb300 import binding
+    p = Plan([2 ** 31 - 2, 5], [1, 1], 2 ** 20, 4096, 8, in_place=in_place)
+    p.run()
+    p.check()
+    assert int(p.lens_out[0]) == 2 ** 31 - 1
+    for lens, new in (([2 ** 31 - 1, 5], [1, 1]), ([2 ** 31 - 2, 5], [2, 1]), ([5, 2 ** 30], [1, 2 ** 30])):
+        p = Plan(lens, new, 2 ** 20, 4096, 8, in_place=in_place)
+        p.run()
+        table, lens_out, cu, positions, slots, n_free, err = p.got()
+        assert err == binding.DEV_CAPACITY
+        np.testing.assert_array_equal(table, p.table)
+        assert lens_out.tolist() == lens and n_free == p.n_free
+        assert (cu == 0).all() and (positions == 0).all() and (slots == -1).all()
