@@ -285,10 +285,10 @@ qw_status qw_op_gemm_swiglu_f16(int32_t M, int32_t N, int32_t K, const void *A,
  *
  * Conventions of these calls:
  *   - All pointers are device pointers on the current device unless marked host; a pointer to
- *     host memory or to another device's is refused (QW_ERR_INVALID_ARG). The stream belongs
- *     to the current device. Nothing is allocated and nothing synchronises; every call may be
- *     captured into a CUDA graph, which then reads the lengths, tables and counts that the
- *     device memory holds at each replay.
+ *     host memory or to another device's is refused (QW_ERR_INVALID_ARG), and so is one that is
+ *     not aligned to its elements. The stream belongs to the current device. Nothing is allocated
+ *     and nothing synchronises; every call may be captured into a CUDA graph, which then reads
+ *     the lengths, tables and counts that the device memory holds at each replay.
  *   - What only the device can see (lengths, page ids, slots, token ids) is checked there:
  *     a bad value is never used as an address, and its QW_DEV_* bit is OR-ed into err_dev
  *     (device int32, required, never cleared by the library).

@@ -687,7 +687,8 @@ qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t voc
   if (!aligned16(workspace)) return op_fail(QW_ERR_INVALID_ARG, "workspace not 16-byte aligned");
   if (workspace_bytes < qw_op_token_logprobs_workspace(n_rows, vocab, top_k))
     return op_fail(QW_ERR_INVALID_ARG, "workspace too small");
-  qw_status st = op_check_device({logits, n_ids ? ids : nullptr, n_ids ? logprobs : nullptr, n_ids ? ranks : nullptr,
+  const void* allocation = (const void*)((uintptr_t)logits & ~(uintptr_t)3);  // (16-bit rows may begin between)
+  qw_status st = op_check_device({allocation, n_ids ? ids : nullptr, n_ids ? logprobs : nullptr, n_ids ? ranks : nullptr,
                                   entropy, top_k ? top_ids : nullptr, top_k ? top_logprobs : nullptr, workspace,
                                   err_dev});
   if (st) return st;

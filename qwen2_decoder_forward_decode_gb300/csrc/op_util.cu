@@ -4,6 +4,8 @@
 namespace qw {
 
 qw_status op_check_device(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if ((uintptr_t)p & 3) return op_fail(QW_ERR_INVALID_ARG, "a pointer is not aligned to 4 bytes");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e) {

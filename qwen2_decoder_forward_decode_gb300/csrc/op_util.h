@@ -26,7 +26,8 @@ inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 constexpr size_t OP_COUNTER_BYTES = 16384;
 
 // Every pointer must be memory of the current device: a host pointer or another device's would
-// fault in the kernel. Managed memory passes. Null pointers are skipped (optional arguments).
+// fault in the kernel. Managed memory passes. Null pointers are skipped (optional arguments). A pointer that is not
+// aligned to 4 bytes would fault too: all elements but 16-bit ones have 4 or 8.
 qw_status op_check_device(std::initializer_list<const void*> ptrs);
 
 // Shape, strides and alignment of a paged cache; on success *norm is the cache with the strides

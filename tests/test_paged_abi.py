@@ -150,6 +150,21 @@ def test_nothing_to_do_is_no_error():
     logprobs(rows=0, logits=None)
 
 
+@pytest.mark.parametrize("call,names", [
+    (attn, ("table", "lens", "lse", "err")), (rope, ("positions", "err")), (logprobs, ("ids", "lp", "ranks", "entropy", "top_ids", "top_lp", "err")),
+    (plan, ("lens", "new", "free", "n_free", "table", "lens_out", "n_free_out", "cu", "positions", "err")),
+    (release, ("lens", "done", "table", "free", "n_free", "lens_out", "n_free_out", "err")),
+])
+def test_pointers_between_two_elements_are_refused(call, names):
+    for name in names:
+        for off in (1, 2, 3):
+            refused(lambda: call(**{name: P + off}), 1, "aligned")
+    with pytest.raises(binding.QwError) as e:  # 16-bit logits may begin at any of them: refused for other reasons only
+        logprobs(dtype=2, logits=P + 2)
+    assert "aligned" not in str(e.value)
+    refused(lambda: logprobs(dtype=2, logits=P + 1), 1, "misaligned")
+
+
 def test_workspace_sizes(L):
     assert L.qw_op_paged_attention_workspace(12, 2, 128) > 0
     assert L.qw_op_paged_attention_workspace(12, 5, 128) == 0
