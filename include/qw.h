@@ -416,6 +416,7 @@ qw_status qw_op_rope_append(const qw_paged_kv *cache, int32_t n_tokens, int32_t 
  *   q   [n_seqs][n_heads][head_dim] of io_dtype, heads contiguous, q_stride elements between
  *       sequences; out the same with out_stride; both 16-byte aligned, strides multiples of
  *       16 bytes. out may be q (with the same stride).
+ *   scale of a magnitude of at most 2^127
  *   lse fp32 [n_seqs][n_heads], or NULL
  *   workspace at least qw_op_paged_attention_workspace() bytes, 16-byte aligned, zeroed once
  *       before its first use (cudaMemset); every call leaves it ready for the next, of any

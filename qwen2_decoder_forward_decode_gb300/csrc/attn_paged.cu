@@ -365,7 +365,8 @@ qw_status qw_op_paged_attention(const qw_paged_kv* cache, int32_t n_seqs, int32_
   const int64_t unit = (int64_t)max_blocks * c.page_size / least_tile(c.dtype == QW_F32, c.head_dim) + 1 + PA_MAX_WEIGHT;
   if ((int64_t)n_seqs * n_heads * unit > 0x7fffffffll)
     return op_fail(QW_ERR_UNSUPPORTED, "n_seqs * n_heads * max_blocks * page_size too large");
-  if (!std::isfinite(scale)) return op_fail(QW_ERR_INVALID_ARG, "scale not finite");
+  // (the kernels take scale * log2(e), which must be finite too: else scores of 0 would be NaN)
+  if (!(std::fabs(scale) <= 0x1p127f)) return op_fail(QW_ERR_INVALID_ARG, "scale not finite, or above 2^127");
   if (n_seqs == 0) return QW_OK;
   if (!block_table || !lens || !workspace || !err_dev) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
   const int64_t width = (int64_t)n_heads * c.head_dim;

@@ -126,6 +126,15 @@ def test_tile_lists_beyond_31_bits_are_refused():
     assert status(0, 128, 1040)[0] != 2 and status(0, 128, 1041)[0] == 2
 
 
+def test_scales_that_overflow_in_base_2_are_refused():
+    for scale in (3e38, -3e38, 2.0 ** 127 * (1 + 2.0 ** -23), -math.inf):
+        refused(lambda: attn(scale=scale), 1, "scale")
+    for scale in (2.0 ** 127, -2.0 ** 127):
+        with pytest.raises(binding.QwError) as e:  # (refused for its addresses, or for want of a GPU)
+            attn(scale=scale)
+        assert "scale" not in str(e.value)
+
+
 def test_release_refuses_no_flags():
     refused(lambda: release(done=None), 1)
 

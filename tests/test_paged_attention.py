@@ -333,3 +333,13 @@ def test_scores_of_minus_infinity_are_no_empty_sequence(io, cache, hd):
     torch.cuda.synchronize()
     assert int(c.err) == binding.DEV_PAGE
     assert c.out[0, :2 * hd].isnan().all() and c.out[1, :2 * hd].isfinite().all()
+
+
+@pytest.mark.parametrize("io,cache,hd", [("f32", "f16", 128), ("bf16", "bf16", 64), ("f32", "f32", 32)])
+def test_the_largest_scale_leaves_scores_of_zero(io, cache, hd):
+    """Queries of 0 have scores of 0 under any scale: the mean of the values."""
+    c = Call([300, 77], 4, 2, hd, 16, io, cache, scale=2.0 ** 127)
+    c.tq[:2, :4 * hd] = 0.0
+    c.q[:] = 0.0
+    c.run()
+    c.check()
