@@ -287,3 +287,34 @@ def test_lengths_end_at_31_bits(in_place):
         np.testing.assert_array_equal(table, p.table)
         assert lens_out.tolist() == lens and n_free == p.n_free
         assert (cu == 0).all() and (positions == 0).all() and (slots == -1).all()
+
+
+def test_large_steps_in_place_captured():
+    """Steps that take all SMs and update the lengths and the free count in place, as one graph: plan, then release."""
+    from qwen2_decoder_forward_decode_gb300 import binding
+    rng = np.random.default_rng(1)
+    lens, new = rng.integers(0, 3000, 60).tolist(), rng.integers(100, 700, 60).tolist()
+    p = Plan(lens, new, 1, max(a + b for a, b in zip(lens, new)), sum(new) + 50, in_place=True)
+    assert p.max_tokens > 8192 and p.n_pages > 8192
+    done = rng.integers(0, 2, 60).tolist()
+    tdone = dev(done)
+    kept = [(t, t.clone()) for t in (p.tlens, p.tn_free, p.ttable, p.tfree)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.run()
+        s = torch.cuda.current_stream().cuda_stream
+        lens_mid, free_mid = p.tlens.clone(), p.tn_free.clone()
+        binding.page_release(60, p.page, p.n_pages, p.blocks, p.tlens.data_ptr(), tdone.data_ptr(), p.ttable.data_ptr(), p.tfree.data_ptr(), p.tn_free.data_ptr(), p.tlens.data_ptr(),
+                             p.tn_free.data_ptr(), p.err.data_ptr(), s)
+    table, lens2, free, cu, positions, slots = ref.plan(lens, new, p.page, p.table, p.free, p.max_tokens)
+    back, left = release_want(lens2, done, p.page, table, free, p.n_pages)
+    for _ in range(3):
+        for t, was in kept:
+            t.copy_(was)
+        g.replay()
+        got = p.got()
+        for a, b in zip((got[0], got[2], got[3], got[4]), (table, cu, positions, slots)):
+            np.testing.assert_array_equal(a, b)
+        assert lens_mid[:60].tolist() == lens2 and int(free_mid) == len(free)
+        assert got[1].tolist() == left and got[5:] == [len(back), 0]
+        np.testing.assert_array_equal(p.tfree.cpu().numpy()[:len(back)], back)

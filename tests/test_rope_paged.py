@@ -163,3 +163,13 @@ def test_on_another_stream_and_captured():
     with torch.cuda.stream(side):
         s.run()
     s.check()
+
+
+@pytest.mark.parametrize("io,cache", [("f32", "f32"), ("f32", "f16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("adjacent", [0, 1])
+@pytest.mark.parametrize("n,nq,nkv,hd,rot,in_place", [(2000, 12, 2, 64, 64, True), (700, 64, 8, 128, 2, False), (3, 300, 60, 256, 64, False), (40, 128, 128, 72, 72, True), (1217, 2, 1, 16, 6, False)])
+def test_more_tokens_than_blocks_and_more_heads_than_threads(io, cache, adjacent, n, nq, nkv, hd, rot, in_place):
+    """Several tokens a block, in a ring; more elements of a token than the ring has places."""
+    s = Step(n, nq, nkv, hd, rot, adjacent, io, cache, in_place=in_place)
+    s.run()
+    s.check()
