@@ -422,7 +422,9 @@ qw_status qw_op_rope_append(const qw_paged_kv *cache, int32_t n_tokens, int32_t 
  *       before its first use (cudaMemset); every call leaves it ready for the next, of any
  *       shape and also of qw_op_token_logprobs. Calls that may run at the same time, captured
  *       graphs of them included, need workspaces of their own.
- * io_dtype QW_F32 with any cache type, or the cache's own type; sums are fp32. Any n_heads that is
+ * io_dtype QW_F32 with any cache type, or the cache's own type; sums are fp32 and divided at the
+ * end, so values whose sum over the positions passes 2^118 overflow to infinities. Over an fp16
+ * cache an fp32 query keeps 22 bits, of its head's largest element. Any n_heads that is
  * a multiple of the cache's n_kv_heads. The result does not depend on the run: equal inputs give
  * equal bits on equal devices. */
 size_t qw_op_paged_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
@@ -437,9 +439,9 @@ qw_status qw_op_paged_attention(const qw_paged_kv *cache, int32_t n_seqs, int32_
  *   ranks[i]    = 1 + the tokens with a larger logit, or the same and a lower id
  *   entropy     = - sum_j p_j ln p_j in nats (p = softmax(z); 0 where p_j is 0)
  *   top_ids, top_logprobs: the top_k tokens in that order, and their log probabilities
- * A logit of -inf is a token of probability 0; a log probability beyond fp32 is -inf. A row that holds a NaN or +inf, or nothing but
- * -inf, has no distribution: QW_DEV_NONFINITE is set, logprobs, entropy and top_logprobs are NaN,
- * ranks 0 and top_ids -1. An id of -1 marks no token (logprob 0, rank 0); any other id outside
+ * A logit of -inf is a token of probability 0; a log probability beyond fp32 is -inf. A row that
+ * holds a NaN or +inf, or nothing but -inf, has no distribution: QW_DEV_NONFINITE is set, logprobs,
+ * entropy and top_logprobs are NaN, ranks 0 and top_ids -1. An id of -1 marks no token (logprob 0, rank 0); any other id outside
  * [0, vocab) gives NaN and rank 0 and sets QW_DEV_TOKEN.
  *   logits [n_rows][row_stride >= vocab] of logits_dtype, aligned to its own size
  *   ids, logprobs, ranks [n_rows][n_ids], n_ids 0 .. 8 (0: all three may be NULL); ranks may be NULL

@@ -18,8 +18,8 @@
 //   - A unit that one CTA covers is finished there. The parts of a split unit go to the workspace; the
 //     CTAs that arrive last merge them, as a tree (one CTA reading every part of a long sequence would be
 //     bound by latency). The order of every sum is fixed by the lengths, so results repeat bit by bit.
-// Measured (12 query and 2 KV heads of 128, fp16 cache, fp32 queries, unless stated): 256 sequences of 1 to 8192
-// positions, 28 and 4 heads, bf16: 326 us, 6.5 TB/s; one sequence of 131071: 34 us, 3.9 TB/s, of which 5 us pass
+// Measured in a CUDA graph (a lone call costs the host about 3 us from C, 10 to 14 from Python; 12 query and 2 KV heads of 128,
+// fp16 cache, fp32 queries, unless stated): 256 sequences of 1 to 8192 positions, 28 and 4 heads, bf16: 326 us, 6.5 TB/s; one sequence of 131071: 34 us, 3.9 TB/s, of which 5 us pass
 // before the first tile and 8 us in the join's two levels; 16 sequences of 256 to 2048: 12.9 us (3.7 us of
 // traffic); one of 178: 6.7 us (lengths, table and first rows are loads that wait for one another). Instructions
 // matter off the main loop: with everything inlined and unrolled, 130 KB a kernel, their misses cost 8 us
@@ -41,6 +41,11 @@ namespace {
 // fed as sums of pieces of the cache's type: with HB = 8, rows 0 - 7 hold the first piece and rows
 // 8 - 15 the second, so two pieces cost what one does; bf16 caches of fp32 callers take a third piece
 // (8 digits each) as a second product. Groups of more than 8 heads use HB = 16, one product per piece.
+// What is rounded to fewer bits than fp32: an fp32 caller's queries and probabilities over fp16 caches to two pieces (22
+// bits of the row's largest element, the smallest step 2^-34 of it), the probabilities of 16-bit callers to two
+// pieces too (22 bits; bf16 16, for outputs of 8); exponentials are ex2's, good to 2^-22. The fp32 caller of a bf16
+// cache with groups of more than 8 heads of 128 keeps three pieces of 16 rows: 210 bytes a thread spill (with at most 8
+// heads 20 bytes).
 template <typename T, int HD, int HB, typename IO>
 struct MmaCfg {
   static constexpr bool F32IO = std::is_same<IO, float>::value;

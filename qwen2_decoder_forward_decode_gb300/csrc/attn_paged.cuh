@@ -230,7 +230,9 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs& a, int n_units,
 // ---- the rows of a tile ----------------------------------------------------------------------------------
 
 // Each warp's rows of a tile, requested by the warp itself. Stage layout: K [RW][HD], V [RW][HD] of T, the
-// 16-byte chunks of row r permuted by chunk ^ (r & 7), so that 8 rows' same chunk lie in distinct banks.
+// 16-byte chunks of row r permuted by chunk ^ (r & 7), so that 8 rows' same chunk lie in distinct banks. (Rows of 64 bytes,
+// 16-bit heads of at most 32 dimensions, have 4 chunks only: rows r and r + 4 share banks, and an ldmatrix takes twice the
+// accesses. 100 sequences of up to 8000 positions, 8 and 2 heads of 32, bf16: 38 us for 16 us of traffic.)
 template <typename T, int HD, int RW, int NW>
 struct Loader {
   static constexpr int TILE = RW * NW, CH = HD * (int)sizeof(T) / 16, CE = 16 / (int)sizeof(T);

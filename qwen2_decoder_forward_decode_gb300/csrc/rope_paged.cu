@@ -64,7 +64,10 @@ __device__ __forceinline__ void store_w(T* p, const float* x, bool& bad) {
 // them itself (cp.async) into its places of a ring, ROPE_STAGES - 1 tokens ahead, and reads them back itself. The
 // rot / 2 (cos, sin) pairs, which all heads share, are computed a token ahead.
 // What bounds it: every element is read and written once, HBM for long prefills and latency for decode steps.
-// 16 tokens take 2.7 us, 8191 tokens of 36 bf16 heads of 128 25.5 us, 5.9 TB/s. A CTA a token, with the same angles and vectors, took
+// In a CUDA graph (a lone call costs the host about 3 us from C, 10 to 14 from Python) 16 tokens take 2.7 us, 8191 tokens of 36
+// bf16 heads of 128, half of each rotated in adjacent pairs, 25.5 us, 5.9 TB/s. The 16-bit instances of pairs in halves hold two
+// vectors an item and spill (144 bytes a thread, fp16 128): the same tokens take 37.7 us, rotated as a whole 36.0 (adjacent
+// 29.1); fp32 to fp16, without spills, 50.3 and 52.4 us for 42.1 us of traffic. A CTA a token, with the same angles and vectors, took
 // 46 us (the chain position - angle - barrier - store, 4 us, is not hidden); tokens ahead in registers
 // instead of the ring 35 us (spills); three stages with three CTAs an SM 26.5 us.
 constexpr int ROPE_THREADS = 256, ROPE_ITEMS = 3, ROPE_STAGES = 2, ROPE_CTAS_PER_SM = 4;
