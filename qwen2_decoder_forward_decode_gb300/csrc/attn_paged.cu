@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel
     uint32_t qa[NA][NKK][4];  // A fragments: pieces of rows gid and gid + 8
     float undo[2];                // of the queries' power of two
     float o[HD / 8][4], m[HB / 8], l[HB / 8], m_there[HB / 8];
+    bool any = false;    // position so far
     bool there = false;  // part of o is in comb already, relative to m_there
     int since = 0;
 #pragma unroll
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel
       }
       const uint32_t mask = s_mask[warp][stage];
       if (mask) {
+        any = true;
         const uint32_t ks = ring + stage * Ld::STAGE, vs = ks + Ld::STAGE / 2;
         // lower pieces have sums of their own: the additions cut, and would do so twice as often at the top
         constexpr int NC = NA > 1 ? 2 : 1;
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel
       float sum = l[half];
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (tig == 0) *reinterpret_cast<float2*>(cw + (gid + 8 * half) * CS + HD) = make_float2(m[half], sum);
+      if (tig == 0) *reinterpret_cast<float2*>(cw + (gid + 8 * half) * CS + HD) = make_float2(state_max(m[half], any), sum);
     }
     const Place done = p;
     p.t = t1 - 1;

@@ -5,6 +5,7 @@
 #include "common.cuh"
 #include "op_util.h"
 
+#include <cfloat>
 #include <math.h>
 
 #include <cmath>
@@ -275,6 +276,10 @@ struct Loader {
 
 // ---- the end of a unit -------------------------------------------------------------------------------------
 
+// The maximum of a warp's state: -inf for no position at all (pages outside the cache), the lowest finite number, which
+// weighs as little next to others, for positions whose scores are all -inf.
+__device__ __forceinline__ float state_max(float m, bool any) { return any ? fmaxf(m, -FLT_MAX) : m; }
+
 // All code that runs once per unit or per CTA is kept short: loops, one out-of-line sum of states.
 template <typename IO, int HB, int HD, int NT, int SMEM>
 struct Finish {
@@ -309,22 +314,12 @@ struct Finish {
     return a;
   }
 
-  // Whether any position of a sequence lies in a page of the cache. (Asked where no score was above -inf.)
-  static __device__ __noinline__ bool any_page(const PagedAttnArgs& a, int b, int len) {
-#pragma unroll 1
-    for (int blk = 0; (long long)blk * a.page < len; ++blk) {
-      const int id = __ldg(a.table + (size_t)b * a.max_blocks + blk);
-      if (id >= 0 && id < a.n_pages) return true;
-    }
-    return false;
-  }
-
   static __device__ __forceinline__ void write_out(const PagedAttnArgs& a, const Place& p, int n_hb, int h, int d, const Acc& s) {
     const int group = a.nq / a.nkv, g = p.u / n_hb, hg = (p.u - g * n_hb) * HB + h;
     if (hg >= group || d >= a.hd) return;
     const int head = g * group + hg;
-    // l = 0: every score was -inf, and 0 / 0 is the formula's NaN; or no position was left: 0, as for length 0
-    const float inv = s.l == 0.f && !any_page(a, p.b, p.len) ? 1.f : 1.f / s.l;
+    // l = 0: no position was left, and out is 0 as for length 0; or every score was -inf, and 0 / 0 is the formula's NaN
+    const float inv = s.l == 0.f && s.m == -INFINITY ? 1.f : 1.f / s.l;
     store4((IO*)a.out + p.b * a.out_stride + head * a.hd + d, make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv));
     if (d == 0 && a.lse) a.lse[(size_t)p.b * a.nq + head] = (s.m - PA_BIAS + log2f(s.l)) * LN2;
   }

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(SimtCfg<T, HD, HB>::NT, 2) paged_simt_kernel(c
       *reinterpret_cast<float2*>(qs + i) =
           h0 + h < group && d < a.hd ? load2((const IO*)a.q + p.b * a.q_stride + (g * group + h0 + h) * a.hd + d) : make_float2(0.f, 0.f);
     }
-    bool fresh = true;
+    bool fresh = true, any = false;  // any: position so far
     f32x2 o[GL][4][HB / 2];  // pairs of heads
 #pragma unroll
     for (int i = 0; i < GL; ++i)
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(SimtCfg<T, HD, HB>::NT, 2) paged_simt_kernel(c
       }
       const uint32_t mask = s_mask[warp][stage];
       if (mask) {
+        any = true;
         const unsigned char *ks = ring_p + stage * Ld::STAGE, *vs = ks + Ld::STAGE / 2;
         f32x2 dot[HB];
 #pragma unroll
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(SimtCfg<T, HD, HB>::NT, 2) paged_simt_kernel(c
 #pragma unroll
       for (int y = 1; y < RW; y <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
       if (pos == 0) {
-        cw[(part * HPL + i) * CS + HD] = m[i];
+        cw[(part * HPL + i) * CS + HD] = state_max(m[i], any);
         cw[(part * HPL + i) * CS + HD + 1] = sum;
       }
     }

@@ -343,3 +343,49 @@ def test_the_largest_scale_leaves_scores_of_zero(io, cache, hd):
     c.q[:] = 0.0
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("io,cache,hd", [("f32", "f16", 128), ("f32", "f32", 32)])
+def test_scores_of_minus_infinity_weigh_nothing_next_to_others(io, cache, hd):
+    """A long sequence whose scores are -inf but for one page: tiles, warps and blocks without a finite score are joined to one
+    with some; another without any score of its own but -inf, next to pages that are left out, in many blocks."""
+    from qwen2_decoder_forward_decode_gb300 import binding
+    c = Call([6000, 6000, 40], 4, 2, hd, 16, io, cache)
+    c.tq[:3, :4 * hd] = c.tq[:3, :4 * hd].abs() + 0.1
+    c.q = c.tq[:3, :4 * hd].double().cpu().numpy().reshape(3, 4, hd)
+    kept = slice(3 * 16, 4 * 16)
+    if cache == "f32":  # (products with the lower pieces of 16-bit caches give NaN for infinite keys)
+        for j, page in enumerate(c.c.table[0]):
+            if j != 3:
+                c.c.tk[int(page), :, :, 3] = -math.inf
+    else:
+        c.c.ttable[0, :3], c.c.ttable[0, 4:375] = -1, -1
+    c.c.ttable[1, :370] = -1
+    for page in c.c.table[1, 370:375]:
+        c.c.tk[int(page), :, :, 3] = -math.inf
+    c.run()
+    torch.cuda.synchronize()
+    assert int(c.err) == binding.DEV_PAGE and c.out[1, :4 * hd].isnan().all()
+    c.c.k[1], c.c.v[1] = c.c.k[1][:0], c.c.v[1][:0]
+    c.out[1, :4 * hd], c.lse[1] = 0.0, -math.inf  # (checked above; the others by the formula)
+    c.check(err=binding.DEV_PAGE, kv=lambda b, h: (c.c.k[b][kept if b == 0 else slice(None), h], c.c.v[b][kept if b == 0 else slice(None), h]))
+
+
+@pytest.mark.parametrize("io,cache,hd", [("f32", "f16", 128), ("f32", "f32", 32)])
+def test_a_long_table_of_no_pages_takes_no_longer_than_one_of_pages(io, cache, hd):
+    """2^22 positions in pages of one, all outside the cache, and as many in the one page that it has."""
+    from qwen2_decoder_forward_decode_gb300 import binding
+    c = Call([1], 2, 1, hd, 1, io, cache, blocks=1 << 22)
+    c.c.tlens[0] = 1 << 22
+    took = []
+    for page in (int(c.c.table[0, 0]), -1):
+        c.c.ttable.fill_(page)
+        for _ in range(2):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            c.run()
+            b.record()
+            torch.cuda.synchronize()
+        took.append(a.elapsed_time(b))
+    assert int(c.err) == binding.DEV_PAGE and (c.out[0] == 0).all() and (c.lse[0] == -math.inf).all()
+    assert took[1] < 2 * took[0] + 1, took
