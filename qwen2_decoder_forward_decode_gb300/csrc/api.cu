@@ -14,6 +14,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -49,6 +50,15 @@ constexpr int ATTN_CHUNK_MIN = 32;
 
 void qw::set_error_message(const char* msg) { g_err = msg; }
 void qw::set_error_message(const char* where, const char* what) { g_err = std::string(where) + ": " + what; }
+
+cudaError_t qw::raise_smem_limit(const void* kernel, size_t bytes) {
+  static std::mutex mutex;
+  std::lock_guard<std::mutex> lock(mutex);
+  cudaFuncAttributes a;
+  const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+  if (e || (size_t)a.maxDynamicSharedSizeBytes >= bytes) return e;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
 
 struct qw_model {
   Dims d;

@@ -652,11 +652,8 @@ cudaError_t launch_attn_batched(int nq, int nkv, int hd, int nsplit, int chunk_m
 
 cudaError_t attn_set_attributes(size_t smem) {
   if (smem <= 48 * 1024) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<f16>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e) return e;
-  return cudaFuncSetAttribute(attn_decode_kernel<float>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = raise_smem_limit((const void*)attn_decode_kernel<f16>, smem);
+  return e ? e : raise_smem_limit((const void*)attn_decode_kernel<float>, smem);
 }
 
 }  // namespace qw

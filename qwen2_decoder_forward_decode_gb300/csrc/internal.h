@@ -48,6 +48,9 @@ struct Finalize {
 // ---- api.cu ----
 void set_error_message(const char* msg);  // message returned by qw_last_error on this thread
 void set_error_message(const char* where, const char* what);  // "where: what"
+// Allows a kernel `bytes` of dynamic shared memory on the current device. The limit is the kernel's, shared by all models
+// and threads of the process: it is only ever raised.
+cudaError_t raise_smem_limit(const void* kernel, size_t bytes);
 // bytes of workspace qw_op_decode_attention uses for this shape and KV type (kv_dtype a
 // qw_dtype); the per-KV-head counters occupy its last n_kv_heads * 4 bytes
 size_t op_attn_workspace_exact(int kv_dtype, int n_heads, int n_kv_heads, int head_dim, int kv_stride);

@@ -1258,7 +1258,7 @@ size_t megastep_work_floats(const Dims& d) {  // x, act, the attention partials,
 
 
 cudaError_t megastep_set_attributes(const Dims& d) {
-  return cudaFuncSetAttribute(megastep_fn(d), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)megastep_smem(d));
+  return raise_smem_limit(megastep_fn(d), megastep_smem(d));
 }
 
 int megastep_threads() { return mk::THREADS; }

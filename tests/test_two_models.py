@@ -1,0 +1,57 @@
+"""Two models alive in one process: the second's sizes must not change what the first may launch."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def run(m, s, seqs=1):
+    """Prefill and three decode steps; the logits of every step."""
+    from synth import make_prompt
+    out = []
+    for q in range(seqs):
+        m.prefill(make_prompt(s, 9 + q), seq=q)
+    for _ in range(3):
+        m.decode_step()
+        out += [m.logits(seq=q) for q in range(seqs)]
+    return out
+
+
+@pytest.mark.parametrize("first,cap,second,cap2,seqs", [
+    ("hd128_bf16", 64, "gqa2_hd128_bf16", 64, 1),  # the persistent step kernel: a hidden vector in shared memory
+    ("gqa2_hd128_bf16", 64, "hd128_bf16", 64, 1),
+    ("small_f32", 8192, "small_f32", 6400, 1),     # the CUDA-core attention: a chunk of the capacity in shared memory
+    ("small_f32", 6400, "small_f32", 8192, 1),
+    ("small_bf16", 8192, "small_bf16", 6400, 3),   # the batched step
+])
+def test_a_second_model_leaves_the_first_its_launches(first, cap, second, cap2, seqs):
+    from qwen2_decoder_forward_decode_gb300 import DeviceWeights, Model
+    from synth import SHAPES, make_weights
+    weights = {n: DeviceWeights(make_weights(SHAPES[n]), 1 if SHAPES[n].dtype == "bf16" else 0) for n in {first, second}}
+
+    def model(name, c):
+        return Model(SHAPES[name], weights[name], c, max_seqs=seqs)
+
+    alone = []
+    for name, c in ((first, cap), (second, cap2)):
+        m = model(name, c)
+        try:
+            alone.append(run(m, SHAPES[name], seqs))
+        finally:
+            m.close()
+    a, b = model(first, cap), model(second, cap2)
+    try:
+        both = [run(a, SHAPES[first], seqs), run(b, SHAPES[second], seqs)]
+    finally:
+        a.close()
+        b.close()
+    for want, got in zip(alone, both):
+        for x, y in zip(want, got):
+            np.testing.assert_array_equal(x, y)
