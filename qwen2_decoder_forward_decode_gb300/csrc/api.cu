@@ -30,6 +30,7 @@ qw_status fail(qw_status s, const std::string& msg) {
 }
 
 qw_status cuda_fail(cudaError_t e, const char* where) {
+  cudaGetLastError();  // reported here: the next launch that asks for the last error must not find it
   return fail(QW_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(e));
 }
 

@@ -8,17 +8,11 @@ qw_status op_check_device(std::initializer_list<const void*> ptrs) {
     if ((uintptr_t)p & 3) return op_fail(QW_ERR_INVALID_ARG, "a pointer is not aligned to 4 bytes");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e) {
-    cudaGetLastError();
-    return op_cuda_fail(e, "cudaGetDevice");
-  }
+  if (e) return op_cuda_fail(e, "cudaGetDevice");
   for (const void* p : ptrs) {
     if (!p) continue;
     cudaPointerAttributes a;
-    if ((e = cudaPointerGetAttributes(&a, p))) {
-      cudaGetLastError();
-      return op_cuda_fail(e, "cudaPointerGetAttributes");
-    }
+    if ((e = cudaPointerGetAttributes(&a, p))) return op_cuda_fail(e, "cudaPointerGetAttributes");
     if (a.type == cudaMemoryTypeManaged) continue;
     if (a.type != cudaMemoryTypeDevice) return op_fail(QW_ERR_INVALID_ARG, "a pointer is not device memory");
     if (a.device != dev) return op_fail(QW_ERR_INVALID_ARG, "a pointer belongs to another device than the current one");

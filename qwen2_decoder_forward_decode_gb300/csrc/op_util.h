@@ -13,6 +13,7 @@ inline qw_status op_fail(qw_status s, const char* msg) {
   return s;
 }
 inline qw_status op_cuda_fail(cudaError_t e, const char* where) {
+  cudaGetLastError();  // reported here: the next launch that asks for the last error must not find it
   set_error_message(where, cudaGetErrorString(e));
   return QW_ERR_CUDA;
 }

@@ -55,3 +55,38 @@ def test_a_second_model_leaves_the_first_its_launches(first, cap, second, cap2, 
     for want, got in zip(alone, both):
         for x, y in zip(want, got):
             np.testing.assert_array_equal(x, y)
+
+
+def test_a_failed_call_leaves_no_error_to_the_next():
+    """An operator whose launch fails (the default stream, while a stream that waits for it is captured) reports it; a model's
+    prefill after it has none to report."""
+    import ctypes
+    import test_paged_plan
+    from qwen2_decoder_forward_decode_gb300 import DeviceWeights, Model, binding
+    from synth import SHAPES, make_prompt, make_weights
+    rt = next((ctypes.CDLL(n) for n in {line.split()[-1] for line in open("/proc/self/maps") if "libcudart.so" in line}), None)
+    if rt is None:
+        pytest.skip("no shared CUDA runtime to make a stream with")
+    s = SHAPES["small_f32"]
+    m = Model(s, DeviceWeights(make_weights(s), 0), 64)
+    p = test_paged_plan.Plan([3, 16], [1, 1], 16, 4, 2)
+    torch.cuda.synchronize()
+    try:
+        want = m.prefill(make_prompt(s, 40))
+        stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+        assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
+        assert rt.cudaStreamBeginCapture(stream, 1) == 0  # (this thread's calls only)
+        try:
+            with pytest.raises(binding.QwError) as e:
+                with torch.cuda.stream(torch.cuda.default_stream()):
+                    p.run()
+        finally:
+            assert rt.cudaStreamEndCapture(stream, ctypes.byref(graph)) != 0  # (the capture has failed, too)
+            rt.cudaGetLastError()
+            assert rt.cudaStreamDestroy(stream) == 0
+        assert e.value.status == 5 and "launch" in str(e.value)
+        assert m.prefill(make_prompt(s, 40)) == want
+        p.run()
+        p.check()
+    finally:
+        m.close()
