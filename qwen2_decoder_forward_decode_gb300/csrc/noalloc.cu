@@ -22,6 +22,7 @@ std::mutex g_mu;
 void* g_scratch_addr[MAX_DEVICES] = {};  // device address of g_attn_scratch, per device
 
 qw_status fail(qw_status s, const char* msg) {
+  if (s == QW_ERR_CUDA) cudaGetLastError();  // reported here: the next launch that asks for the last error must not find it
   qw::set_error_message(msg);
   return s;
 }

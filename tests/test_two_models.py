@@ -57,36 +57,45 @@ def test_a_second_model_leaves_the_first_its_launches(first, cap, second, cap2, 
             np.testing.assert_array_equal(x, y)
 
 
-def test_a_failed_call_leaves_no_error_to_the_next():
-    """An operator whose launch fails (the default stream, while a stream that waits for it is captured) reports it; a model's
-    prefill after it has none to report."""
-    import ctypes
+class default_stream_refused:
+    """A stream that waits for the default one is captured: launches on the default stream fail meanwhile."""
+
+    def __enter__(self):
+        import ctypes
+        self.rt = next((ctypes.CDLL(n) for n in {line.split()[-1] for line in open("/proc/self/maps") if "libcudart.so" in line}), None)
+        if self.rt is None:
+            pytest.skip("no shared CUDA runtime to make a stream with")
+        self.stream, self.graph = ctypes.c_void_p(), ctypes.c_void_p()
+        self.byref = ctypes.byref
+        assert self.rt.cudaStreamCreate(ctypes.byref(self.stream)) == 0
+        assert self.rt.cudaStreamBeginCapture(self.stream, 1) == 0  # (this thread's calls only)
+
+    def __exit__(self, *exc):
+        if self.rt.cudaStreamEndCapture(self.stream, self.byref(self.graph)) == 0:  # (a failed launch ends the capture, a failed query does not)
+            self.rt.cudaGraphDestroy(self.graph)
+        self.rt.cudaGetLastError()
+        assert self.rt.cudaStreamDestroy(self.stream) == 0
+
+
+@pytest.mark.parametrize("op", ["plan", "decode attention"])
+def test_a_failed_call_leaves_no_error_to_the_next(op):
+    """An operator whose launch fails reports it; a model's prefill after it has none to report."""
     import test_paged_plan
     from qwen2_decoder_forward_decode_gb300 import DeviceWeights, Model, binding
     from synth import SHAPES, make_prompt, make_weights
-    rt = next((ctypes.CDLL(n) for n in {line.split()[-1] for line in open("/proc/self/maps") if "libcudart.so" in line}), None)
-    if rt is None:
-        pytest.skip("no shared CUDA runtime to make a stream with")
     s = SHAPES["small_f32"]
     m = Model(s, DeviceWeights(make_weights(s), 0), 64)
     p = test_paged_plan.Plan([3, 16], [1, 1], 16, 4, 2)
+    q, k, v, out = (torch.zeros(n, device="cuda") for n in (64, 32 * 16, 32 * 16, 64))
+    call = {"plan": p.run, "decode attention": lambda: binding.decode_attention_noalloc(0, 4, 1, 16, 20, 32, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None)}[op]
     torch.cuda.synchronize()
     try:
         want = m.prefill(make_prompt(s, 40))
-        stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
-        assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
-        assert rt.cudaStreamBeginCapture(stream, 1) == 0  # (this thread's calls only)
-        try:
-            with pytest.raises(binding.QwError) as e:
-                with torch.cuda.stream(torch.cuda.default_stream()):
-                    p.run()
-        finally:
-            assert rt.cudaStreamEndCapture(stream, ctypes.byref(graph)) != 0  # (the capture has failed, too)
-            rt.cudaGetLastError()
-            assert rt.cudaStreamDestroy(stream) == 0
-        assert e.value.status == 5 and "launch" in str(e.value)
+        with default_stream_refused(), pytest.raises(binding.QwError) as e:
+            call()
+        assert e.value.status == 5
         assert m.prefill(make_prompt(s, 40)) == want
-        p.run()
-        p.check()
+        call()
+        p.run() if op != "plan" else p.check()
     finally:
         m.close()
