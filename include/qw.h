@@ -335,8 +335,7 @@ typedef struct {
  *   slots        [max_tokens]: the token's slot in the cache; -1 behind the last token
  * If the step does not fit (too few free pages, more than max_tokens tokens, more than max_blocks
  * pages or 2^31 - 1 positions of a sequence, a negative length or count, n_free outside
- * [0, n_pages]) QW_DEV_CAPACITY is
- * set and the step is empty: lens_out = lens, n_free_out = n_free, cu_tokens 0, positions 0,
+ * [0, n_pages]) QW_DEV_CAPACITY is set and the step is empty: lens_out = lens, n_free_out = n_free, cu_tokens 0, positions 0,
  * slots -1. A page id outside [0, n_pages) gives slot -1 and sets QW_DEV_PAGE. n_seqs <= 16384,
  * n_pages and max_tokens <= 2^30.
  * With n_seqs = 0 the outputs are those of an empty step. max_tokens = 0 is allowed. */
@@ -441,8 +440,8 @@ qw_status qw_op_paged_attention(const qw_paged_kv *cache, int32_t n_seqs, int32_
  *   top_ids, top_logprobs: the top_k tokens in that order, and their log probabilities
  * A logit of -inf is a token of probability 0; a log probability beyond fp32 is -inf. A row that
  * holds a NaN or +inf, or nothing but -inf, has no distribution: QW_DEV_NONFINITE is set, logprobs,
- * entropy and top_logprobs are NaN, ranks 0 and top_ids -1. An id of -1 marks no token (logprob 0, rank 0); any other id outside
- * [0, vocab) gives NaN and rank 0 and sets QW_DEV_TOKEN.
+ * entropy and top_logprobs are NaN, ranks 0 and top_ids -1. An id of -1 marks no token (logprob 0,
+ * rank 0); any other id outside [0, vocab) gives NaN and rank 0 and sets QW_DEV_TOKEN.
  *   logits [n_rows][row_stride >= vocab] of logits_dtype, aligned to its own size
  *   ids, logprobs, ranks [n_rows][n_ids], n_ids 0 .. 8 (0: all three may be NULL); ranks may be NULL
  *   entropy [n_rows] or NULL

@@ -11,7 +11,7 @@
 // PLAN_SMALL tokens, or a release of as many table entries, takes one CTA; more are spread over the SMs.
 // Outputs that alias inputs (lengths and the free count) are then written by a second, small kernel, since
 // a CTA may still be reading when another writes. Measured in a CUDA graph (a lone call costs the host about 3 us from C, 10 to 12
-// from Python): 512 sequences with one token each 5.1 us (in place 4.3), 64 prompts of 117 000 tokens together 6.2 us (in
+// from Python): 512 sequences with one token each 5.1 us (in place no more), 64 prompts of 117 000 tokens together 6.2 us (in
 // place, with the second kernel, 8.2), 512 sequences of which a third give 37 000 pages back 4.3 us (in place 5.6);
 // one CTA for everything took 117 us for the prompts.
 #include "common.cuh"
