@@ -6,7 +6,7 @@
 // so one pass with running values does. Tokens are ordered by (logit, lower id first) as one 64-bit key.
 //
 // Precision: sums and differences are fp32, exponentials ex2's, good to 2^-22: a log probability is good to about a step of fp32 of
-// itself (2e-9 to 4e-8 of a row's norm against 64 bits, as a plain fp32 form), a near-certain token's to 1e-7 absolute.
+// itself (2e-9 to 1.1e-7 of a row's norm against 64 bits, a plain fp32 form 2e-9 to 5e-8), a near-certain token's to 1e-7 absolute.
 //
 // Times are in a CUDA graph; a lone call costs the host about 3 us from C, 10 to 14 from Python.
 // What bounds it: each logit is read once, so HBM for fp32 logits (1024 rows of 151936: 131 us, 4.7 TB/s; without top
