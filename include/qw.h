@@ -281,7 +281,9 @@ qw_status qw_op_gemm_swiglu_f16(int32_t M, int32_t N, int32_t K, const void *A,
  * token goes, qw_op_rope_append rotates the queries and keys and writes keys and values
  * there, qw_op_paged_attention reads the pages back for one new token per sequence, and
  * qw_op_token_logprobs turns the step's logits into log probabilities.
- * qw_op_page_release returns the pages of finished sequences.
+ * qw_op_page_release returns the pages of finished sequences. Where several sequences go on from one prompt (samples, beams),
+ * qw_op_page_fork lets them share its pages, qw_op_shared_attention reads them once, qw_op_beam_select chooses how the beams go
+ * on, and qw_op_page_copy and qw_op_page_compact move pages.
  *
  * Conventions of these calls:
  *   - All pointers are device pointers on the current device unless marked host; a pointer to
@@ -358,6 +360,60 @@ qw_status qw_op_page_release(int32_t n_seqs, int32_t page_size, int32_t n_pages,
                              int32_t *free_pages, const int32_t *n_free, int32_t *lens_out,
                              int32_t *n_free_out, int32_t *err_dev, void *cuda_stream);
 
+/* Forks sequences, and ends those that nobody goes on from: sequence i of the n_out new ones is a copy of the old
+ * sequence parents[i] (-1: an empty one) that shares its pages. shares[p] is the number of holders of page p (rows of
+ * block tables) beyond the first: 0 for pages of one holder and for free ones, so that pages from qw_op_page_plan need no
+ * entry. A last page that is partly filled is written by the next append, so only the lowest child of its parent keeps
+ * it; every other child, in order, takes a page from the end of free_pages[0 .. n_free[0] - 1] for it:
+ *   lens_out [n_out], table_out [n_out][max_blocks]: the new sequences; entries behind a sequence's pages are not written
+ *   copy_src, copy_dst, copy_len [n_out]: that child's old and new last page and its positions, for qw_op_page_copy; -1, -1
+ *       and 0 where nothing is to be copied
+ *   shares_out [n_pages]; may be shares
+ *   free_out [n_pages]: the free pages that were not taken, in their order, then the pages whose last holder ended, in
+ *       ascending order; may be free_pages. n_free_out [1] their number; may be n_free
+ * A sequence ends where no child names it: with parents[i] = i or -1 the call returns the pages of finished sequences to
+ * the list (qw_op_page_release does so for pages that nobody shares). Of the pages in parents' tables shares counts
+ * other holders too, such as a kept prompt's. lens_out and table_out must be other memory than lens and block_table.
+ * If there are too few free pages, a length is negative or beyond max_blocks pages, or n_free is outside [0, n_pages],
+ * QW_DEV_CAPACITY is set and nothing is forked, ended or taken: lens_out 0, nothing to copy, shares, list and count as they
+ * were. A parent outside [-1, n_seqs) counts as -1, a page id outside [0, n_pages) is copied and not counted; both set
+ * QW_DEV_PAGE. n_seqs and n_out <= 16384, n_pages <= 2^30.
+ * workspace: at least qw_op_page_fork_workspace() bytes, 16-byte aligned, zeroed once before its first use; every call leaves
+ * it ready for the next with the same n_pages. Calls that may run at the same time need workspaces of their own. */
+size_t qw_op_page_fork_workspace(int32_t n_pages);
+qw_status qw_op_page_fork(int32_t n_seqs, int32_t n_out, int32_t page_size, int32_t n_pages, int32_t max_blocks,
+                          const int32_t *lens, const int32_t *block_table, const int32_t *parents, const int32_t *shares,
+                          const int32_t *free_pages, const int32_t *n_free, int32_t *lens_out, int32_t *table_out,
+                          int32_t *shares_out, int32_t *free_out, int32_t *n_free_out, int32_t *copy_src,
+                          int32_t *copy_dst, int32_t *copy_len, void *workspace, size_t workspace_bytes,
+                          int32_t *err_dev, void *cuda_stream);
+
+/* Compacts the pool: pages that are not among free_pages[0 .. n_free[0] - 1] are live, L of them. The i-th highest live
+ * page of an id >= L moves to the i-th lowest free page of an id < L, i < n_moves[0] = min(their number, max_moves):
+ *   move_src, move_dst [max_moves]: the moves, -1 behind the last. qw_op_page_copy carries them out (in every cache of
+ *       the pool, before anything else reads it)
+ *   table_out [n_seqs][max_blocks]: the tables with the moved pages' new ids; may be block_table
+ *   shares_out [n_pages]: the pages' counts (see qw_op_page_fork) carried along; may be shares. Both NULL: no page is shared
+ *   free_out [n_pages]: the free pages afterwards in descending order, so that the lowest are taken first; may be free_pages.
+ *       Their number stays n_free[0]
+ * Other tables of the same pool can be rewritten from the moves. If a page is on the list twice or outside
+ * [0, n_pages) (QW_DEV_PAGE), or n_free or a length is out of range (QW_DEV_CAPACITY), nothing moves and the outputs are
+ * the inputs. A table entry outside [0, n_pages) stays and sets QW_DEV_PAGE. n_pages and max_moves <= 2^30.
+ * workspace: at least qw_op_page_compact_workspace() bytes, with the rules of qw_op_page_fork's. */
+size_t qw_op_page_compact_workspace(int32_t n_pages);
+qw_status qw_op_page_compact(int32_t n_seqs, int32_t page_size, int32_t n_pages, int32_t max_blocks, int32_t max_moves,
+                             const int32_t *lens, const int32_t *block_table, const int32_t *shares,
+                             const int32_t *free_pages, const int32_t *n_free, int32_t *table_out, int32_t *shares_out,
+                             int32_t *free_out, int32_t *move_src, int32_t *move_dst, int32_t *n_moves, void *workspace,
+                             size_t workspace_bytes, int32_t *err_dev, void *cuda_stream);
+
+/* Copies pages inside n_caches caches (host array; the layers of one model, which have the same type, extents and
+ * strides; at most 128): for every i < n with src[i] != -1 the first len[i] positions (len NULL: all) of page src[i], in all
+ * heads, keys and values, to page dst[i]. No two entries have the same dst, and no dst is a src. A page outside
+ * [0, n_pages), or a length outside [0, page_size], copies nothing and sets QW_DEV_PAGE. */
+qw_status qw_op_page_copy(const qw_paged_kv *caches, int32_t n_caches, int32_t n, const int32_t *src, const int32_t *dst,
+                          const int32_t *len, int32_t *err_dev, void *cuda_stream);
+
 /* How rotary frequencies are stretched for contexts longer than the trained one. With r the
  * rotated dimensions, w_i = theta^(-2i/r), i < r/2, and L = orig_len:
  *   QW_ROPE_NONE    w_i
@@ -432,6 +488,26 @@ qw_status qw_op_paged_attention(const qw_paged_kv *cache, int32_t n_seqs, int32_
                                 int64_t q_stride, float scale, void *out, int64_t out_stride, float *lse,
                                 void *workspace, size_t workspace_bytes, int32_t *err_dev, void *cuda_stream);
 
+/* The same for groups of sequences that begin alike (samples or beams of one prompt, users of one system prompt): what is
+ * shared is read once for the group. Group g is the sequences cu_seqs[g] .. cu_seqs[g + 1] - 1 (cu_seqs[0] = 0,
+ * cu_seqs[n_groups] = n_seqs, some may be empty), and each of them shares its first shared_lens[b] positions with the
+ * group's first sequence, whose table says where they lie (whatever its own length is): out and lse are those of
+ * qw_op_paged_attention where every table holds these positions. shared_lens is one number in a group, or 0 for sequences
+ * that share nothing; a sequence shorter than that is computed from its own table alone.
+ * A sequence that claims to share another number of positions than the group's first sets QW_DEV_PAGE and misses them.
+ * Bounds of groups that do not ascend from 0 to n_seqs set QW_DEV_PAGE, and all outputs are 0, lse -inf.
+ *   cu_seqs [n_groups + 1], 1 <= n_groups <= n_seqs; shared_lens [n_seqs]
+ *   workspace at least qw_op_shared_attention_workspace() bytes, with the rules of qw_op_paged_attention's, which it
+ *       serves too
+ * Probabilities of 16-bit callers are rounded to the cache's type over the shared positions (not in lse); an fp32 caller's
+ * keep 22 bits and more, as there. Equal inputs give equal bits on equal devices. */
+size_t qw_op_shared_attention_workspace(int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+qw_status qw_op_shared_attention(const qw_paged_kv *cache, int32_t n_seqs, int32_t n_heads, const int32_t *block_table,
+                                 int32_t max_blocks, const int32_t *lens, int32_t n_groups, const int32_t *cu_seqs,
+                                 const int32_t *shared_lens, int32_t io_dtype, const void *q, int64_t q_stride, float scale,
+                                 void *out, int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
+                                 int32_t *err_dev, void *cuda_stream);
+
 /* Log probabilities of given tokens, with their ranks, the entropy and the likeliest tokens, of
  * n_rows rows of logits [LSA Decoding: softmax of the logits]. For a row z:
  *   logprobs[i] = z_t - ln sum_j exp(z_j) for t = ids[i], i < n_ids
@@ -454,7 +530,36 @@ qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t voc
                                float *entropy, int32_t top_k, int32_t *top_ids, float *top_logprobs, void *workspace,
                                size_t workspace_bytes, int32_t *err_dev, void *cuda_stream);
 
-/* The same for the logits of sequence seq's last step, into host memory (all pointers host, sizes
+/* A step of beam search for n_groups groups of n_beams beams [LSA Decoding: softmax of the logits]: row w = g * n_beams + i is
+ * beam i of group g, scores[w] the sum of its tokens' log probabilities. The beam can go on with any token t of a logit
+ * above -inf, and its score becomes scores[w] + z_t - ln sum_j exp(z_j); an ended beam (ended[w] != 0) stays as it is, a
+ * single candidate with its own score and the token end_id. The n_out best of a group, by weights[w] * score, in order; equal
+ * ones by the lower beam, then the larger logit, then the lower id. The order is that of the scores in 64 bits.
+ *   logits [n_groups * n_beams][row_stride >= vocab] of logits_dtype, aligned to its own size
+ *   scores [rows]; -inf: a beam that is not there. weights [rows], positive, such as a power of 1 / length; NULL: 1
+ *   ended [rows] or NULL: none. end_id: the token that ends a beam, or -1
+ *   parents, tokens, scores_out, ended_out [n_groups * n_out]: the candidate's row, token, score, and whether it has ended
+ *       (its parent had, or its token is end_id); ended_out may be NULL. If there are fewer candidates than n_out, the rest
+ *       is parent -1, token -1, score -inf, ended 1
+ *   history, history_out [rows][width] and [n_groups * n_out][width], lens, lens_out [rows] and [n_groups * n_out]: the tokens of
+ *       the beams so far in the order of the new beams, each with its token behind (an ended beam's stays), and their
+ *       numbers; all NULL: none. What lies behind a history is not written. A history that is full, or a length outside
+ *       [0, width], sets QW_DEV_CAPACITY; the history then stays as long as it is
+ * A row whose logits hold a NaN or +inf, or nothing but -inf, whose score is NaN or +inf, or whose weight is not positive and
+ * finite, has no candidates and sets QW_DEV_NONFINITE (the logits of ended and absent beams are not looked at).
+ * The outputs are other memory than the inputs. parents can go to qw_op_page_fork as they are.
+ * At most 65535 groups, 32 beams, 32 candidates, 2^21 tokens. workspace: at least qw_op_beam_select_workspace() bytes, 16-byte
+ * aligned; it need not be zeroed. Calls that may run at the same time need workspaces of their own. Equal inputs
+ * give equal bits on equal devices. */
+size_t qw_op_beam_select_workspace(int32_t n_groups, int32_t n_beams, int32_t vocab, int32_t n_out);
+qw_status qw_op_beam_select(int32_t logits_dtype, int32_t n_groups, int32_t n_beams, int32_t vocab, const void *logits,
+                            int64_t row_stride, const float *scores, const float *weights, const int32_t *ended,
+                            int32_t end_id, int32_t n_out, int32_t *parents, int32_t *tokens, float *scores_out,
+                            int32_t *ended_out, int32_t width, const int32_t *history, const int32_t *lens,
+                            int32_t *history_out, int32_t *lens_out, void *workspace, size_t workspace_bytes,
+                            int32_t *err_dev, void *cuda_stream);
+
+/* The same as qw_op_token_logprobs for the logits of sequence seq's last step, into host memory (all pointers host, sizes
  * and NULL rules as above, one row; entropy one float). The scratch is allocated by the first
  * call and released by qw_destroy. Synchronises. Errors: QW_ERR_INVALID_ARG for a sequence that
  * is not active, QW_ERR_TOKEN_RANGE for an id outside [0, vocab), QW_ERR_NUMERIC for

@@ -102,10 +102,19 @@ def lib():
         "qw_op_gemm_swiglu_f16": ([I32, I32, I32, VP, VP, VP, VP, VP, VP], I32),
         "qw_op_page_plan": ([I32] * 5 + [VP] * 12, I32),
         "qw_op_page_release": ([I32] * 4 + [VP] * 9, I32),
+        "qw_op_page_fork_workspace": ([I32], SZ),
+        "qw_op_page_fork": ([I32] * 5 + [VP] * 15 + [SZ, VP, VP], I32),
+        "qw_op_page_compact_workspace": ([I32], SZ),
+        "qw_op_page_compact": ([I32] * 5 + [VP] * 12 + [SZ, VP, VP], I32),
+        "qw_op_page_copy": ([P(PagedKV), I32, I32, VP, VP, VP, VP, VP], I32),
         "qw_rope_turns": ([I32, F64, I32, F64, F64, F64, F64, P(ctypes.c_uint64), pf], I32),
         "qw_op_rope_append": ([P(PagedKV), I32, I32, I32, VP, VP, VP, I32, I32, F32C] + [VP, I64] * 4 + [VP, VP], I32),
         "qw_op_paged_attention_workspace": ([I32, I32, I32], SZ),
         "qw_op_paged_attention": ([P(PagedKV), I32, I32, VP, I32, VP, I32, VP, I64, F32C, VP, I64, VP, VP, SZ, VP, VP], I32),
+        "qw_op_shared_attention_workspace": ([I32, I32, I32, I32], SZ),
+        "qw_op_shared_attention": ([P(PagedKV), I32, I32, VP, I32, VP, I32, VP, VP, I32, VP, I64, F32C, VP, I64, VP, VP, SZ, VP, VP], I32),
+        "qw_op_beam_select_workspace": ([I32] * 4, SZ),
+        "qw_op_beam_select": ([I32] * 4 + [VP, I64, VP, VP, VP, I32, I32, VP, VP, VP, VP, I32] + [VP] * 5 + [SZ, VP, VP], I32),
         "qw_op_token_logprobs_workspace": ([I32, I32, I32], SZ),
         "qw_op_token_logprobs": ([I32, I32, I32, VP, I64, VP, I32, VP, VP, VP, I32, VP, VP, VP, SZ, VP, VP], I32),
         "qw_read_logprobs": ([VP, I32, pi, I32, pf, pi, pf, I32, pi, pf], I32),
@@ -128,7 +137,10 @@ def exported_symbols():
             "qw_set_timeline", "qw_read_timeline",
             "qw_op_decode_attention_workspace", "qw_op_decode_attention",
             "qw_op_decode_attention_noalloc", "qw_op_decode_attention_noalloc_limit", "qw_op_gemm_f16",
-            "qw_op_gemm_swiglu_f16", "qw_op_page_plan", "qw_op_page_release", "qw_rope_turns",
+            "qw_op_gemm_swiglu_f16", "qw_op_page_plan", "qw_op_page_release",
+            "qw_op_page_fork_workspace", "qw_op_page_fork", "qw_op_page_compact_workspace", "qw_op_page_compact",
+            "qw_op_page_copy", "qw_op_shared_attention_workspace", "qw_op_shared_attention",
+            "qw_op_beam_select_workspace", "qw_op_beam_select", "qw_rope_turns",
             "qw_op_rope_append", "qw_op_paged_attention_workspace", "qw_op_paged_attention",
             "qw_op_token_logprobs_workspace", "qw_op_token_logprobs", "qw_read_logprobs"]
 
@@ -363,6 +375,42 @@ def page_release(n_seqs, page_size, n_pages, max_blocks, lens_ptr, done_ptr, tab
                                    n_free_ptr, lens_out_ptr, n_free_out_ptr, err_ptr, stream))
 
 
+def page_fork_workspace(n_pages):
+    return int(lib().qw_op_page_fork_workspace(n_pages))
+
+
+def page_fork(n_seqs, n_out, page_size, n_pages, max_blocks, lens_ptr, table_ptr, parents_ptr, shares_ptr, free_ptr,
+              n_free_ptr, lens_out_ptr, table_out_ptr, shares_out_ptr, free_out_ptr, n_free_out_ptr, copy_src_ptr,
+              copy_dst_ptr, copy_len_ptr, ws_ptr, ws_bytes, err_ptr, stream=None):
+    """Makes every new sequence a copy of its parent that shares its pages, and frees the pages that nobody holds."""
+    check(lib().qw_op_page_fork(n_seqs, n_out, page_size, n_pages, max_blocks, lens_ptr, table_ptr, parents_ptr, shares_ptr,
+                                free_ptr, n_free_ptr, lens_out_ptr, table_out_ptr, shares_out_ptr, free_out_ptr,
+                                n_free_out_ptr, copy_src_ptr, copy_dst_ptr, copy_len_ptr, ws_ptr, ws_bytes, err_ptr, stream))
+
+
+def page_compact_workspace(n_pages):
+    return int(lib().qw_op_page_compact_workspace(n_pages))
+
+
+def page_compact(n_seqs, page_size, n_pages, max_blocks, max_moves, lens_ptr, table_ptr, shares_ptr, free_ptr, n_free_ptr,
+                 table_out_ptr, shares_out_ptr, free_out_ptr, src_ptr, dst_ptr, n_moves_ptr, ws_ptr, ws_bytes, err_ptr,
+                 stream=None):
+    """Moves the highest live pages of the pool into its lowest free ones (the moves go to page_copy)."""
+    check(lib().qw_op_page_compact(n_seqs, page_size, n_pages, max_blocks, max_moves, lens_ptr, table_ptr, shares_ptr,
+                                   free_ptr, n_free_ptr, table_out_ptr, shares_out_ptr, free_out_ptr, src_ptr, dst_ptr,
+                                   n_moves_ptr, ws_ptr, ws_bytes, err_ptr, stream))
+
+
+def paged_kv_array(caches):
+    """The caches of several layers (PagedKV) as one array for page_copy."""
+    return (PagedKV * len(caches))(*caches)
+
+
+def page_copy(caches, n_caches, n, src_ptr, dst_ptr, len_ptr, err_ptr, stream=None):
+    """Copies pages, or their first positions, inside every cache of the array from paged_kv_array."""
+    check(lib().qw_op_page_copy(caches, n_caches, n, src_ptr, dst_ptr, len_ptr, err_ptr, stream))
+
+
 def rope_turns(rot_dim, theta, scaling="none", factor=1.0, orig_len=0.0, low=1.0, high=None):
     """Rotary frequencies as 64-bit fractions of a turn (uint64 [rot_dim / 2]) and the factor of cos and
     sin, for rope_append. scaling is a key of ROPE_SCALING; high defaults to 32 turns ("yarn") or 4
@@ -395,6 +443,31 @@ def paged_attention(cache, n_seqs, n_heads, table_ptr, max_blocks, lens_ptr, io_
     check(lib().qw_op_paged_attention(ctypes.byref(cache), n_seqs, n_heads, table_ptr, max_blocks, lens_ptr, io_dtype,
                                       q_ptr, q_stride, scale, out_ptr, out_stride, lse_ptr, ws_ptr, ws_bytes, err_ptr,
                                       stream))
+
+
+def shared_attention_workspace(n_seqs, n_heads, n_kv_heads, head_dim):
+    return int(lib().qw_op_shared_attention_workspace(n_seqs, n_heads, n_kv_heads, head_dim))
+
+
+def shared_attention(cache, n_seqs, n_heads, table_ptr, max_blocks, lens_ptr, n_groups, cu_ptr, shared_ptr, io_dtype, q_ptr,
+                     q_stride, scale, out_ptr, out_stride, lse_ptr, ws_ptr, ws_bytes, err_ptr, stream=None):
+    """Attention of one new token per sequence, for groups of sequences whose first positions are the same pages."""
+    check(lib().qw_op_shared_attention(ctypes.byref(cache), n_seqs, n_heads, table_ptr, max_blocks, lens_ptr, n_groups,
+                                       cu_ptr, shared_ptr, io_dtype, q_ptr, q_stride, scale, out_ptr, out_stride, lse_ptr,
+                                       ws_ptr, ws_bytes, err_ptr, stream))
+
+
+def beam_select_workspace(n_groups, n_beams, vocab, n_out):
+    return int(lib().qw_op_beam_select_workspace(n_groups, n_beams, vocab, n_out))
+
+
+def beam_select(logits_dtype, n_groups, n_beams, vocab, logits_ptr, row_stride, scores_ptr, weights_ptr, ended_ptr, end_id,
+                n_out, parents_ptr, tokens_ptr, scores_out_ptr, ended_out_ptr, width, history_ptr, lens_ptr,
+                history_out_ptr, lens_out_ptr, ws_ptr, ws_bytes, err_ptr, stream=None):
+    """The best continuations of each group's beams, and the beams' token histories in their order."""
+    check(lib().qw_op_beam_select(logits_dtype, n_groups, n_beams, vocab, logits_ptr, row_stride, scores_ptr, weights_ptr,
+                                  ended_ptr, end_id, n_out, parents_ptr, tokens_ptr, scores_out_ptr, ended_out_ptr, width,
+                                  history_ptr, lens_ptr, history_out_ptr, lens_out_ptr, ws_ptr, ws_bytes, err_ptr, stream))
 
 
 def token_logprobs_workspace(n_rows, vocab, top_k):

@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel
   const int group = a.nq / a.nkv, n_hb = (group + HB - 1) / HB, n_units = a.nkv * n_hb;
   float* comb = reinterpret_cast<float*>(pa_smem + NS * NW * Ld::STAGE);
   const uint32_t ring = smem_addr(pa_smem) + warp * NS * Ld::STAGE;
+  if (a.state) pdl_trigger();  // (the shared beginning's attention goes on beside this one)
   Place ld;
   const Range r = find_range<IO, TILE, V, C::NT>(a, n_units, ld);
   if (r.begin >= r.end) return;
@@ -331,6 +332,8 @@ cudaError_t launch_16bit(int ctas, const PagedAttnArgs& a, cudaStream_t s) {
   return a.hd <= 64 ? launch_mma<T, 64, 16, IO>(ctas, a, s) : launch_mma<T, 128, 16, IO>(ctas, a, s);
 }
 
+}  // namespace
+
 // floats of one part: of the largest instance that the shape may take, whatever its types (launch_16bit's HB and HD; the
 // CUDA cores' HB is at most 8, their HD at most this one)
 size_t part_floats(int n_heads, int n_kv_heads, int head_dim) {
@@ -340,7 +343,35 @@ size_t part_floats(int n_heads, int n_kv_heads, int head_dim) {
 }
 static_assert(PA_LEVELS * 2 * PA_MAX_CTAS * sizeof(unsigned int) <= OP_COUNTER_BYTES, "counters");
 
-}  // namespace
+cudaError_t launch_paged(int cache_dtype, int io_dtype, int nsm, const PagedAttnArgs& a, cudaStream_t s) {
+  const int ctas = nsm < PA_MAX_CTAS / 2 ? nsm : PA_MAX_CTAS / 2;
+  if (cache_dtype == QW_F32 || a.hd > 128) return launch_simt(cache_dtype, io_dtype, 2 * ctas, a, s);
+  if (cache_dtype == QW_F16)
+    return io_dtype == QW_F32 ? launch_16bit<f16, float>(ctas, a, s) : launch_16bit<f16, f16>(ctas, a, s);
+  return io_dtype == QW_F32 ? launch_16bit<bf16, float>(ctas, a, s) : launch_16bit<bf16, bf16>(ctas, a, s);
+}
+
+qw_status check_attention(const qw_paged_kv* cache, qw_paged_kv* norm, int32_t n_seqs, int32_t n_heads, int32_t max_blocks,
+                          int32_t io_dtype, float scale) {
+  qw_paged_kv c;
+  qw_status st = op_check_cache(cache, &c);
+  if (st) return st;
+  if ((st = op_check_io(io_dtype, c.dtype))) return st;
+  if (n_seqs < 0 || max_blocks < 1 || n_heads < 1 || n_heads % c.n_kv_heads)
+    return op_fail(QW_ERR_INVALID_ARG, "bad attention shape");
+  if (n_seqs > 65535 || n_heads > 4096) return op_fail(QW_ERR_UNSUPPORTED, "more than 65535 sequences or 4096 heads");
+  if ((int64_t)max_blocks * c.page_size > (int64_t)1 << 30)
+    return op_fail(QW_ERR_UNSUPPORTED, "max_blocks * page_size above 2^30");
+  // the tile list's numbers are 31-bit: a unit (at most one a head) has its tiles, the last one cut, and its weight
+  const int64_t unit = (int64_t)max_blocks * c.page_size / least_tile(c.dtype == QW_F32, c.head_dim) + 1 + PA_MAX_WEIGHT;
+  if ((int64_t)n_seqs * n_heads * unit > 0x7fffffffll)
+    return op_fail(QW_ERR_UNSUPPORTED, "n_seqs * n_heads * max_blocks * page_size too large");
+  // (the kernels take scale * log2(e), which must be finite too: else scores of 0 would be NaN)
+  if (!(std::fabs(scale) <= 0x1p127f)) return op_fail(QW_ERR_INVALID_ARG, "scale not finite, or above 2^127");
+  *norm = c;
+  return QW_OK;
+}
+
 }  // namespace paged
 }  // namespace qw
 
@@ -360,20 +391,8 @@ qw_status qw_op_paged_attention(const qw_paged_kv* cache, int32_t n_seqs, int32_
                                 void* workspace, size_t workspace_bytes, int32_t* err_dev, void* cuda_stream) {
   set_error_message("");
   qw_paged_kv c;
-  qw_status st = op_check_cache(cache, &c);
+  qw_status st = check_attention(cache, &c, n_seqs, n_heads, max_blocks, io_dtype, scale);
   if (st) return st;
-  if ((st = op_check_io(io_dtype, c.dtype))) return st;
-  if (n_seqs < 0 || max_blocks < 1 || n_heads < 1 || n_heads % c.n_kv_heads)
-    return op_fail(QW_ERR_INVALID_ARG, "bad attention shape");
-  if (n_seqs > 65535 || n_heads > 4096) return op_fail(QW_ERR_UNSUPPORTED, "more than 65535 sequences or 4096 heads");
-  if ((int64_t)max_blocks * c.page_size > (int64_t)1 << 30)
-    return op_fail(QW_ERR_UNSUPPORTED, "max_blocks * page_size above 2^30");
-  // the tile list's numbers are 31-bit: a unit (at most one a head) has its tiles, the last one cut, and its weight
-  const int64_t unit = (int64_t)max_blocks * c.page_size / least_tile(c.dtype == QW_F32, c.head_dim) + 1 + PA_MAX_WEIGHT;
-  if ((int64_t)n_seqs * n_heads * unit > 0x7fffffffll)
-    return op_fail(QW_ERR_UNSUPPORTED, "n_seqs * n_heads * max_blocks * page_size too large");
-  // (the kernels take scale * log2(e), which must be finite too: else scores of 0 would be NaN)
-  if (!(std::fabs(scale) <= 0x1p127f)) return op_fail(QW_ERR_INVALID_ARG, "scale not finite, or above 2^127");
   if (n_seqs == 0) return QW_OK;
   if (!block_table || !lens || !workspace || !err_dev) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
   const int64_t width = (int64_t)n_heads * c.head_dim;
@@ -390,14 +409,8 @@ qw_status qw_op_paged_attention(const qw_paged_kv* cache, int32_t n_seqs, int32_
     return op_cuda_fail(e, "device query");
   PagedAttnArgs a{c.k, c.v, c.page_stride, c.head_stride, c.pos_stride, n_seqs, n_heads, c.n_kv_heads, c.head_dim,
                   c.page_size, c.n_pages, max_blocks, block_table, lens, q, out, q_stride, out_stride, scale, lse,
-                  (unsigned int*)workspace, (float*)((char*)workspace + OP_COUNTER_BYTES), err_dev};
-  cudaStream_t s = (cudaStream_t)cuda_stream;
-  const int ctas = nsm < PA_MAX_CTAS / 2 ? nsm : PA_MAX_CTAS / 2;
-  if (c.dtype == QW_F32 || c.head_dim > 128) e = launch_simt(c.dtype, io_dtype, 2 * ctas, a, s);
-  else if (c.dtype == QW_F16)
-    e = io_dtype == QW_F32 ? launch_16bit<f16, float>(ctas, a, s) : launch_16bit<f16, f16>(ctas, a, s);
-  else
-    e = io_dtype == QW_F32 ? launch_16bit<bf16, float>(ctas, a, s) : launch_16bit<bf16, bf16>(ctas, a, s);
+                  (unsigned int*)workspace, (float*)((char*)workspace + OP_COUNTER_BYTES), err_dev, nullptr, nullptr};
+  e = launch_paged(c.dtype, io_dtype, nsm, a, (cudaStream_t)cuda_stream);
   if (e) return op_cuda_fail(e, "paged attention launch");
   return QW_OK;
 }

@@ -40,6 +40,10 @@ struct PagedAttnArgs {
   unsigned int* counters;  // [PA_LEVELS][2 * PA_MAX_CTAS], zero between calls
   float* part;             // [2 * PA_MAX_CTAS][HB][comb_stride(HD)]
   int* err;
+  // for attention that computes a shared beginning elsewhere, else null: the first positions of a sequence that are left
+  // out (none of them where the sequence is shorter), and the states [n_seqs][nq][comb_stride(hd)] that replace out and lse
+  const int* skip;
+  float* state;
 };
 
 __host__ __device__ constexpr int comb_stride(int hd) { return hd + 4; }  // o, then m and l
@@ -104,22 +108,34 @@ __device__ __forceinline__ void split(float a, float b, uint32_t* piece) {
 
 // ---- the list of tiles ---------------------------------------------------------------------------------
 
-__device__ __forceinline__ int seq_len(const PagedAttnArgs& a, int b, bool& bad) {
+// the positions of a sequence that are attended to, and in `from` the first of them
+__device__ __forceinline__ int seq_len(const PagedAttnArgs& a, int b, int& from, bool& bad) {
   const long long room = (long long)a.max_blocks * a.page;
-  const int len = __ldg(a.lens + b);
+  int len = __ldg(a.lens + b);
   bad = len < 0 || len > room;
-  return len < 0 ? 0 : len > room ? (int)room : len;
+  len = len < 0 ? 0 : len > room ? (int)room : len;
+  from = 0;
+  if (a.skip) {
+    const int skip = __ldg(a.skip + b);
+    bad |= skip < 0 || skip > room;
+    if (skip > 0 && skip <= len) from = skip;
+  }
+  return len - from;
+}
+__device__ __forceinline__ int seq_len(const PagedAttnArgs& a, int b, int& from) {
+  bool bad;
+  return seq_len(a, b, from, bad);
 }
 __device__ __forceinline__ int seq_len(const PagedAttnArgs& a, int b) {
-  bool bad;
-  return seq_len(a, b, bad);
+  int from;
+  return seq_len(a, b, from);
 }
 
 // The list weighs a unit's end (the merge of the warps, the next queries) like V tiles, in front of its own.
-// A place is tile t of nt of unit u of sequence b; v: where the list has the unit. All numbers of the
+// A place is tile t of nt of unit u of sequence b, whose len positions begin at `from`; v: where the list has the unit. All numbers of the
 // list fit 31 bits (the host refuses shapes that could hold more).
 struct Place {
-  int b, u, t, nt, len, v;
+  int b, u, t, nt, len, v, from;
 };
 
 // The next tile; false behind the list's end `end` (as a number of the list).
@@ -132,7 +148,7 @@ __device__ __forceinline__ bool advance(const PagedAttnArgs& a, int n_units, int
   if (++p.u < n_units) return true;
   p.u = 0;
   do {
-    p.len = seq_len(a, ++p.b);
+    p.len = seq_len(a, ++p.b, p.from);
     p.nt = (p.len + TILE - 1) / TILE;
   } while (p.nt == 0 && p.b + 1 < a.n_seqs);
   return true;
@@ -163,7 +179,8 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs& a, int n_units,
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     bool bad;
-    const int len = seq_len(a, b, bad);
+    int from;
+    const int len = seq_len(a, b, from, bad);
     if (len) mine += V + (len + TILE - 1) / TILE;
     empty |= len == 0;
     if (bad && blockIdx.x == 0) atomicOr(a.err, ERR_PAGE);
@@ -181,6 +198,12 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs& a, int n_units,
 #pragma unroll 1
     for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
       if (seq_len(a, b) > 0) continue;
+      if (a.state) {
+#pragma unroll 1
+        for (int h = tid; h < a.nq; h += NT)
+          *reinterpret_cast<float2*>(a.state + ((size_t)b * a.nq + h) * comb_stride(a.hd) + a.hd) = make_float2(-INFINITY, 0.f);
+        continue;
+      }
 #pragma unroll 1
       for (int i = 4 * tid; i < width; i += 4 * NT) store4((IO*)a.out + b * a.out_stride + i, make_float4(0.f, 0.f, 0.f, 0.f));
       if (a.lse)
@@ -209,10 +232,11 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs& a, int n_units,
       if (x < base || x >= base + mine) continue;
 #pragma unroll 1
       for (int b = b0; b < b1; ++b) {
-        const int len = seq_len(a, b), nt = (len + TILE - 1) / TILE, unit = nt ? V + nt : 0;
+        int from;
+        const int len = seq_len(a, b, from), nt = (len + TILE - 1) / TILE, unit = nt ? V + nt : 0;
         if (x < at + unit * n_units) {
           const int u = (x - at) / unit, v = at + u * unit;
-          s_at[k] = Place{b, u, nt <= PA_WHOLE ? 0 : max(0, x - v - V), nt, len, v};
+          s_at[k] = Place{b, u, nt <= PA_WHOLE ? 0 : max(0, x - v - V), nt, len, v, from};
           break;
         }
         at += unit * n_units;
@@ -243,8 +267,9 @@ struct Loader {
   static_assert((CH & (CH - 1)) == 0, "chunks are permuted by exclusive or");
   // byte offset of the lane's row (lanes 0 .. RW - 1) in the caches, or -1: no such row
   static __device__ __forceinline__ long long row(const PagedAttnArgs& a, const Place& p, int n_hb, int warp, int lane) {
-    const int j = p.t * TILE + warp * RW + lane;
+    int j = p.t * TILE + warp * RW + lane;
     if (lane >= RW || j >= p.len) return -1;
+    j += p.from;
     const int blk = j / a.page, id = __ldg(a.table + (size_t)p.b * a.max_blocks + blk);
     if (id < 0 || id >= a.n_pages) {
       if (p.u == 0) atomicOr(a.err, ERR_PAGE);
@@ -314,18 +339,23 @@ struct Finish {
     return a;
   }
 
+  // a state's row: o [hd], then m and l
+  static __device__ __forceinline__ void put(float* row, int hd, int d, const Acc& s) {
+    *reinterpret_cast<float4*>(row + d) = s.o;
+    if (d == 0) *reinterpret_cast<float2*>(row + hd) = make_float2(s.m, s.l);
+  }
   static __device__ __forceinline__ void write_out(const PagedAttnArgs& a, const Place& p, int n_hb, int h, int d, const Acc& s) {
     const int group = a.nq / a.nkv, g = p.u / n_hb, hg = (p.u - g * n_hb) * HB + h;
     if (hg >= group || d >= a.hd) return;
     const int head = g * group + hg;
+    if (a.state) {
+      put(a.state + ((size_t)p.b * a.nq + head) * comb_stride(a.hd), a.hd, d, s);
+      return;
+    }
     // l = 0: no position was left, and out is 0 as for length 0; or every score was -inf, and 0 / 0 is the formula's NaN
     const float inv = s.l == 0.f && s.m == -INFINITY ? 1.f : 1.f / s.l;
     store4((IO*)a.out + p.b * a.out_stride + head * a.hd + d, make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv));
     if (d == 0 && a.lse) a.lse[(size_t)p.b * a.nq + head] = (s.m - PA_BIAS + log2f(s.l)) * LN2;
-  }
-  static __device__ __forceinline__ void put(float* slot, int h, int d, const Acc& s) {
-    *reinterpret_cast<float4*>(slot + h * CS + d) = s.o;
-    if (d == 0) *reinterpret_cast<float2*>(slot + h * CS + HD) = make_float2(s.m, s.l);
   }
 
   // Part slots: a CTA's range cuts at most two units, the one it begins with (slot 2 c) and the one that it
@@ -347,7 +377,7 @@ struct Finish {
       const int h = i4 / (HD / 4), d = (i4 - h * (HD / 4)) * 4;
       const Acc s = sum(comb, NW, h, d);
       if (whole) write_out(a, p, n_hb, h, d, s);
-      else put(slot, h, d, s);
+      else put(slot + h * CS, HD, d, s);
     }
     __syncthreads();
     return !whole;
@@ -408,7 +438,7 @@ struct Finish {
         const int k = i >= N4, i4 = i - k * N4, h = i4 / (HD / 4), d = (i4 - h * (HD / 4)) * 4;
         const Acc s = sum(buf + (k ? n0 * HB * CS : 0), k ? n1 : n0, h, d);
         if (k ? done1 : done0) write_out(a, pend[k], n_hb, h, d, s);
-        else put(slot_ptr(a, s_from[k] == s_c0[k] ? s_first[k] : 2 * s_from[k]), h, d, s);
+        else put(slot_ptr(a, s_from[k] == s_c0[k] ? s_first[k] : 2 * s_from[k]) + h * CS, HD, d, s);
       }
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -422,6 +452,13 @@ struct Finish {
 
 // attn_paged_simt.cu: fp32 caches, and heads of more than 128 dimensions
 cudaError_t launch_simt(int cache_dtype, int io_dtype, int ctas, const PagedAttnArgs& a, cudaStream_t s);
+// attn_paged.cu: the kernel that the shape takes, and the floats of its parts in the workspace
+cudaError_t launch_paged(int cache_dtype, int io_dtype, int nsm, const PagedAttnArgs& a, cudaStream_t s);
+size_t part_floats(int n_heads, int n_kv_heads, int head_dim);
+// Shapes and pointers of attention over a paged cache, as both entry points check them; *norm is the cache with the strides
+// along extents of 1 set to 0.
+qw_status check_attention(const qw_paged_kv* cache, qw_paged_kv* norm, int32_t n_seqs, int32_t n_heads, int32_t max_blocks,
+                          int32_t io_dtype, float scale);
 
 template <typename K>
 cudaError_t launch(K kernel, int threads, int smem, int ctas, const PagedAttnArgs& a, cudaStream_t s) {

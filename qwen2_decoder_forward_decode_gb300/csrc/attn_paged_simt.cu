@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(SimtCfg<T, HD, HB>::NT, 2) paged_simt_kernel(c
   float* ps = qs + HB * HD + warp * (RW + 1) * HB;  // [RW][HB] probabilities, then [HB] factors
   unsigned char* ring_p = pa_smem + warp * NS * Ld::STAGE;
   const uint32_t ring = smem_addr(ring_p);
+  if (a.state) pdl_trigger();  // (the shared beginning's attention goes on beside this one)
   Place ld;
   const Range r = find_range<IO, TILE, V, C::NT>(a, n_units, ld);
   if (r.begin >= r.end) return;

@@ -1,0 +1,253 @@
+// Decode attention of groups of sequences that share a beginning, over a paged cache ("LLM Speedrun: Architecture":
+// Attention, Grouped Query Attention): samples and beams of one prompt, or users of one system prompt.
+//
+// Mathematics: the state (m, l, o) of a set of positions is the maximum score m (base 2), l = sum 2^(s - m) and
+// o = sum 2^(s - m) V. States of disjoint sets merge as M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i. So
+// the shared positions are read once for all rows (sequence, head) of a group and KV head, and each sequence's own
+// positions by themselves:
+//   1. the own positions: the kernels of attn_paged.cu with each sequence's first positions left out and their states
+//      kept in fp32;
+//   2. the shared ones: matrix products of up to 128 rows with blocks of keys and values (attn_shared_tc.cu; fp32 caches
+//      and longer heads on the CUDA cores, attn_shared_simt.cu). All blocks of all groups form one list that is cut into
+//      equal ranges, one a CTA;
+//   3. the join: a warp a row, or a CTA a row where rows are few and their parts many.
+// The second launch goes on beside the first (programmatic dependent launch: it waits for it at its end only), the third
+// is in place when the second ends.
+#include "attn_shared.cuh"
+
+#include <algorithm>
+
+namespace qw {
+namespace shared_attn {
+namespace {
+
+constexpr int JN_THREADS = 256, JN_WARPS = JN_THREADS / 32;
+
+struct JoinArgs {
+  SharedArgs s;
+  Geometry geo;
+};
+
+// The sum of states, NV groups of 4 dimensions a lane.
+template <int NV>
+struct Sum {
+  float m, l;
+  float4 o[NV];
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void add(float m2, float l2, const float4* x) {  // (its o is not looked at where m2 is -inf)
+    if (m2 == -INFINITY) return;
+    const float top = fmaxf(m, m2), f = m == -INFINITY ? 0.f : ex2(m - top), w = ex2(m2 - top);
+    m = top;
+    l = fmaf(w, l2, l * f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      o[i].x = fmaf(w, x[i].x, o[i].x * f);
+      o[i].y = fmaf(w, x[i].y, o[i].y * f);
+      o[i].z = fmaf(w, x[i].z, o[i].z * f);
+      o[i].w = fmaf(w, x[i].w, o[i].w * f);
+    }
+  }
+};
+
+template <int NV, int WPR>  // WPR: warps of a row
+__device__ __forceinline__ bool join_row(const JoinArgs& ja, int row, int part, Sum<NV>& sum) {
+  const SharedArgs& a = ja.s;
+  const PagedAttnArgs& p = a.p;
+  const int lane = threadIdx.x & 31, b = row / p.nq, h = row - b * p.nq;
+  sum.clear();
+  auto take = [&](const float* s, int hd) {
+    const float2 ml = *reinterpret_cast<const float2*>(s + hd);
+    float4 x[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      x[i] = 4 * lane + 128 * i < p.hd ? *reinterpret_cast<const float4*>(s + 4 * lane + 128 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    sum.add(ml.x, ml.y, x);
+  };
+  const SharedHead head = *a.head;
+  if (head.bad) return false;
+  if (part == 0) take(p.state + (size_t)row * comb_stride(p.hd), p.hd);
+  int lo = 0, hi = a.n_groups;  // the last group that begins at or before b
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.cu + mid) <= b) lo = mid;
+    else hi = mid;
+  }
+  const int first = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1), grp = p.nq / p.nkv;
+  const int pre = __ldg(p.skip + first), mine = __ldg(p.skip + b), len = __ldg(p.lens + b);
+  const long long room = (long long)p.max_blocks * p.page;
+  if (pre <= 0 || pre > room || mine != pre || len < pre) {
+    // the sequence has no shared part, or one that its group's first sequence does not have: then positions are missing
+    if (part == 0 && lane == 0 && h == 0 && mine != pre && mine > 0 && mine <= len) atomicOr(p.err, ERR_PAGE);
+    return true;
+  }
+  const int nt = ((end - first) * grp + ja.geo.mt - 1) / ja.geo.mt, nb = (pre + ja.geo.bk - 1) / ja.geo.bk;
+  const int kv = h / grp, i = (b - first) * grp + (h - kv * grp), tile = i / ja.geo.mt;
+  const int v = a.at[lo] + (kv * nt + tile) * (SH_WEIGHT + nb);
+  const Range r{head.each, head.rest, 0, 0};
+  const int c0 = cta_of(r, v + SH_WEIGHT), c1 = cta_of(r, v + SH_WEIGHT + nb - 1);
+  if (c0 == c1) {
+    if (part == 0) take(a.whole + (size_t)row * comb_stride(p.hd), p.hd);
+    return true;
+  }
+#pragma unroll 4
+  for (int c = c0 + part; c <= c1; c += WPR) {
+    const int slot = 2 * c + (c == c0 && cut(r, c) < v ? 1 : 0);
+    take(a.parts + ((size_t)slot * ja.geo.mt + (i - tile * ja.geo.mt)) * comb_stride(ja.geo.hd), ja.geo.hd);
+  }
+  return true;
+}
+
+template <int NV, typename IO>
+__device__ __forceinline__ void write_row(const PagedAttnArgs& p, int row, const Sum<NV>& s) {
+  const int lane = threadIdx.x & 31, b = row / p.nq, h = row - b * p.nq;
+  // l = 0: no position was left, and out is 0; or every score was -inf, and 0 / 0 is the formula's NaN
+  const float inv = s.l == 0.f && s.m == -INFINITY ? 1.f : 1.f / s.l;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int d = 4 * lane + 128 * i;
+    if (d < p.hd)
+      paged::store4((IO*)p.out + b * p.out_stride + h * p.hd + d,
+                    make_float4(s.o[i].x * inv, s.o[i].y * inv, s.o[i].z * inv, s.o[i].w * inv));
+  }
+  if (lane == 0 && p.lse) p.lse[row] = (s.m - PA_BIAS + log2f(s.l)) * paged::LN2;
+}
+
+template <int NV, int WPR, typename IO>
+__global__ void __launch_bounds__(JN_THREADS) join_kernel(const JoinArgs ja) {
+  const PagedAttnArgs& p = ja.s.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = p.n_seqs * p.nq;
+  pdl_wait();
+  Sum<NV> sum;
+  if constexpr (WPR == 1) {
+#pragma unroll 1
+    for (int row = blockIdx.x * JN_WARPS + warp; row < rows; row += gridDim.x * JN_WARPS) {
+      join_row<NV, 1>(ja, row, 0, sum);
+      write_row<NV, IO>(p, row, sum);
+    }
+  } else {
+    static_assert(WPR == JN_WARPS, "a CTA a row");
+    __shared__ float2 s_ml[JN_WARPS];
+    __shared__ float4 s_o[JN_WARPS][NV * 32];
+    const int row = blockIdx.x;
+    join_row<NV, WPR>(ja, row, warp, sum);
+    if (lane == 0) s_ml[warp] = make_float2(sum.m, sum.l);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s_o[warp][32 * i + lane] = sum.o[i];
+    __syncthreads();
+    if (warp) return;
+#pragma unroll 1
+    for (int w = 1; w < JN_WARPS; ++w) {
+      float4 x[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) x[i] = s_o[w][32 * i + lane];
+      sum.add(s_ml[w].x, s_ml[w].y, x);
+    }
+    write_row<NV, IO>(p, row, sum);
+  }
+}
+
+template <int NV, typename IO>
+cudaError_t launch_join(const JoinArgs& ja, int nsm, cudaStream_t s) {
+  const int rows = ja.s.p.n_seqs * ja.s.p.nq;
+  if (rows <= 8 * nsm) return launch_k(join_kernel<NV, JN_WARPS, IO>, dim3(rows), dim3(JN_THREADS), 0, s, true, ja);
+  const int ctas = std::min((rows + JN_WARPS - 1) / JN_WARPS, 16 * nsm);
+  return launch_k(join_kernel<NV, 1, IO>, dim3(ctas), dim3(JN_THREADS), 0, s, true, ja);
+}
+template <typename IO>
+cudaError_t launch_join(const JoinArgs& ja, int nsm, cudaStream_t s) {
+  return ja.s.p.hd <= 128 ? launch_join<1, IO>(ja, nsm, s) : launch_join<2, IO>(ja, nsm, s);
+}
+
+// The workspace: the counters and parts of attn_paged.cu, the head and the groups' places, states, parts.
+struct Layout {
+  size_t head, at, own, whole, parts, bytes;
+};
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+Layout layout(int n_seqs, int n_heads, int n_kv_heads, int head_dim) {
+  Layout y;
+  y.head = up256(OP_COUNTER_BYTES + 2 * paged::PA_MAX_CTAS * paged::part_floats(n_heads, n_kv_heads, head_dim) * sizeof(float));
+  y.at = y.head + 256;
+  y.own = y.at + up256((size_t)n_seqs * sizeof(int));
+  const size_t states = up256((size_t)n_seqs * n_heads * comb_stride(head_dim) * sizeof(float));
+  y.whole = y.own + states;
+  y.parts = y.whole + states;
+  size_t most = 0;
+  for (int type : {(int)QW_F32, (int)QW_F16}) {  // of both kernels that the shape may take
+    const Geometry g = geometry(type, head_dim, SH_MAX_CTAS);
+    most = std::max(most, (size_t)2 * g.ctas * g.mt * comb_stride(g.hd) * sizeof(float));
+  }
+  y.bytes = y.parts + most;
+  return y;
+}
+
+}  // namespace
+}  // namespace shared_attn
+}  // namespace qw
+
+using namespace qw;
+using namespace qw::shared_attn;
+
+extern "C" {
+
+size_t qw_op_shared_attention_workspace(int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
+  if (n_seqs < 0 || n_seqs > 65535 || n_heads > 4096 || !qw_op_paged_attention_workspace(n_heads, n_kv_heads, head_dim)) return 0;
+  return layout(n_seqs < 1 ? 1 : n_seqs, n_heads, n_kv_heads, head_dim).bytes;
+}
+
+qw_status qw_op_shared_attention(const qw_paged_kv* cache, int32_t n_seqs, int32_t n_heads, const int32_t* block_table,
+                                 int32_t max_blocks, const int32_t* lens, int32_t n_groups, const int32_t* cu_seqs,
+                                 const int32_t* shared_lens, int32_t io_dtype, const void* q, int64_t q_stride, float scale,
+                                 void* out, int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes,
+                                 int32_t* err_dev, void* cuda_stream) {
+  set_error_message("");
+  qw_paged_kv c;
+  qw_status st = paged::check_attention(cache, &c, n_seqs, n_heads, max_blocks, io_dtype, scale);
+  if (st) return st;
+  if (n_groups < 0 || n_groups > n_seqs) return op_fail(QW_ERR_INVALID_ARG, "n_groups must be at most n_seqs");
+  if (n_seqs == 0) return QW_OK;
+  if (n_groups == 0) return op_fail(QW_ERR_INVALID_ARG, "sequences without a group");
+  const Geometry least = geometry(c.dtype, c.head_dim, 1);
+  const int64_t tiles = ((int64_t)n_seqs * (n_heads / c.n_kv_heads) + least.mt - 1) / least.mt + n_groups;
+  if (tiles * c.n_kv_heads * ((int64_t)max_blocks * c.page_size / least.bk + 1 + SH_WEIGHT) > 0x7fffffffll)
+    return op_fail(QW_ERR_UNSUPPORTED, "n_seqs * n_heads * max_blocks * page_size too large");
+  if (!block_table || !lens || !cu_seqs || !shared_lens || !workspace || !err_dev) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
+  const int64_t width = (int64_t)n_heads * c.head_dim;
+  if ((st = op_check_rows(q, q_stride, width, io_dtype, "q"))) return st;
+  if ((st = op_check_rows(out, out_stride, width, io_dtype, "out"))) return st;
+  if (out == q && out_stride != q_stride) return op_fail(QW_ERR_INVALID_ARG, "out may be q with the same stride only");
+  if (!aligned16(workspace)) return op_fail(QW_ERR_INVALID_ARG, "workspace not 16-byte aligned");
+  const Layout y = layout(n_seqs, n_heads, c.n_kv_heads, c.head_dim);
+  if (workspace_bytes < y.bytes) return op_fail(QW_ERR_INVALID_ARG, "workspace too small");
+  if ((st = op_check_device({c.k, c.v, block_table, lens, cu_seqs, shared_lens, q, out, lse, workspace, err_dev}))) return st;
+  int dev = 0, nsm = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) || (e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)))
+    return op_cuda_fail(e, "device query");
+  char* ws = (char*)workspace;
+  JoinArgs ja;
+  ja.s.p = PagedAttnArgs{c.k, c.v, c.page_stride, c.head_stride, c.pos_stride, n_seqs, n_heads, c.n_kv_heads, c.head_dim,
+                         c.page_size, c.n_pages, max_blocks, block_table, lens, q, out, q_stride, out_stride, scale, lse,
+                         (unsigned int*)ws, (float*)(ws + OP_COUNTER_BYTES), err_dev, shared_lens, (float*)(ws + y.own)};
+  ja.s.n_groups = n_groups;
+  ja.s.cu = cu_seqs;
+  ja.s.head = (SharedHead*)(ws + y.head);
+  ja.s.at = (int*)(ws + y.at);
+  ja.s.whole = (float*)(ws + y.whole);
+  ja.s.parts = (float*)(ws + y.parts);
+  ja.geo = geometry(c.dtype, c.head_dim, nsm);
+  cudaStream_t s = (cudaStream_t)cuda_stream;
+  if ((e = paged::launch_paged(c.dtype, io_dtype, nsm, ja.s.p, s))) return op_cuda_fail(e, "shared attention launch");
+  e = c.dtype != QW_F32 && c.head_dim <= 128 ? launch_shared_tc(c.dtype, io_dtype, ja.geo.ctas, ja.s, s)
+                                             : launch_shared_simt(c.dtype, io_dtype, ja.geo.ctas, ja.s, s);
+  if (e) return op_cuda_fail(e, "shared attention launch");
+  e = io_dtype == QW_F32 ? launch_join<float>(ja, nsm, s) : io_dtype == QW_F16 ? launch_join<f16>(ja, nsm, s) : launch_join<bf16>(ja, nsm, s);
+  if (e) return op_cuda_fail(e, "shared attention launch");
+  return QW_OK;
+}
+
+}  // extern "C"

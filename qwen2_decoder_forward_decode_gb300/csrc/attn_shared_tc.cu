@@ -1,0 +1,439 @@
+// The shared positions of attn_shared.cu on the 5th-generation tensor cores (tcgen05, TMEM): 16-bit caches, heads of at most
+// 128 dimensions.
+//
+// A unit is 128 rows (sequence, head) of one group and KV head. Blocks of 128 positions stream past them:
+//   warps 0 .. 3    producers: a warp copies 32 positions' keys or values (cp.async, 16 bytes a lane, pages looked up by
+//                   the lane that owns the position) into a ring of tiles, swizzled as the tensor cores read them. Pages of any
+//                   size and stride serve, which a tensor map's boxes do not. The order is the one in which the tiles are
+//                   consumed: K_0, K_1, V_0, K_2, V_1, ...
+//   warp 12         issues the products: S_j = Q K_j^T into buffer j % 2, a block ahead, and O_j = P_j V_j with P_j from TMEM.
+//   warps 4 .. 11   softmax. Warps w and w + 4 share TMEM lanes, one row a lane: the first takes positions 0 .. 63 of every
+//                   block, the other 64 .. 127, and they trade maxima through shared memory. They write P_j over S_j, and
+//                   then add O_{j-1} to their half of the row's output in registers, a fp32 sum that rounds (the tensor
+//                   cores' additions cut: over thousands of positions 1e-6 of the norm) and needs no rescaling in TMEM.
+// The warps meet at a unit's ends only: there the softmax warps put the rows' queries into shared memory.
+//
+// Precision: fp32 callers' queries and probabilities are sums of pieces of the cache's type, two of fp16 (22 bits of the row's
+// largest element), three of bf16. A 16-bit caller's probabilities are rounded once to its own type, whose bits the
+// output has too; their sum l takes them before that. Exponentials are ex2's, good to 2^-22.
+//
+// Every wait is bounded: on expiry ERR_TIMEOUT is set, the CTA stops issuing work, waits (bounded) for what it issued, and
+// releases its TMEM.
+#include <math.h>
+
+#include "attn_shared.cuh"
+#include "tc_common.cuh"
+
+namespace qw {
+namespace shared_attn {
+namespace {
+
+using paged::Pair;
+using paged::split;
+
+constexpr int MT = 128, BK = 128, THREADS = 512, PRODUCERS = 4, MMA_WARP = 12, MASKS = 16;
+
+template <typename T, int HD, typename IO>
+struct Cfg {
+  static constexpr bool F32IO = std::is_same<IO, float>::value, BF = std::is_same<T, bf16>::value, three = F32IO && BF;
+  static constexpr int NQ = !F32IO ? 1 : three ? 3 : 2, NP = NQ;  // pieces of queries and probabilities
+  static constexpr int TILE = BK * HD * 2;                        // bytes of a tile; HD / 64 boxes [128 rows][64 columns]
+  static constexpr int Q_BYTES = NQ * MT * HD * 2;
+  // q_full, s_full[2], p_full[2], o_full[2], done, pair[4], full[NS], empty[NS]
+  static constexpr int NBAR = 12;
+  static constexpr int SMALL = (NBAR + 2 * 8) * 8 + 16 + MT * 4 + 2 * 2 * MT * 4 + MASKS * 16;
+  static constexpr int NS_FIT = (232448 - Q_BYTES - SMALL) / TILE, NS = NS_FIT > 8 ? 8 : NS_FIT;
+  static constexpr int OFF_RING = Q_BYTES, OFF_SMALL = OFF_RING + NS * TILE, SMEM = OFF_SMALL + SMALL;
+  static constexpr int AHEAD = NS - 1 < 4 ? NS - 1 : 4;  // tiles in flight
+  // TMEM columns: S buffers (P pieces 0 and 1 over them), third pieces, O
+  static constexpr int P3 = 256, O_COL = three ? 384 : 256, NO = three ? 1 : 2;
+  static_assert(NS >= 4, "ring");
+  static_assert(O_COL + NO * 128 <= 512, "TMEM");
+};
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// 16 columns of this thread's TMEM lane, completed by tmem_wait_st
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+template <typename T, int HD, typename IO>
+__global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs a) {
+  using C = Cfg<T, HD, IO>;
+  constexpr int NS = C::NS, NQ = C::NQ, NP = C::NP;
+  extern __shared__ __align__(1024) unsigned char sh_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  const uint32_t base = smem_addr(sh_smem);
+  uint64_t* bars = (uint64_t*)(sh_smem + C::OFF_SMALL);
+  const uint32_t q_full = smem_addr(bars), s_full0 = q_full + 8, p_full0 = q_full + 24, o_full0 = q_full + 40, done = q_full + 56,
+                 pair0 = q_full + 64, full0 = q_full + 96, empty0 = full0 + 64;
+  uint32_t* tmem_slot = (uint32_t*)(bars + C::NBAR + 16);
+  volatile int* s_abort = (volatile int*)(tmem_slot + 1);
+  float* undo = (float*)(tmem_slot + 4);                    // [MT] of the queries' power of two
+  float* xch = undo + MT;                                   // [block parity][half][row]
+  uint32_t* masks = (uint32_t*)(xch + 4 * MT);              // [block % MASKS][4] positions that exist
+  if (base & 1023) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicOr(a.p.err, ERR_LAYOUT);
+    pdl_wait();
+    return;
+  }
+  Unit p;
+  const Range r = find_groups<MT, BK, THREADS>(a, p, sh_smem);
+  if (r.begin >= r.end) {
+    pdl_wait();  // (this grid ends after the one before it)
+    return;
+  }
+  if (threadIdx.x == 0) {
+    *s_abort = 0;
+    mbar_init(q_full, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full0 + 8 * i, 1);
+      mbar_init(p_full0 + 8 * i, 8);
+      mbar_init(o_full0 + 8 * i, 1);
+    }
+    mbar_init(done, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(pair0 + 8 * i, 2);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full0 + 8 * i, PRODUCERS);
+      mbar_init(empty0 + 8 * i, 1);
+    }
+    mbar_fence_init();
+  }
+  if (warp == MMA_WARP) tc::tmem_alloc(smem_addr(tmem_slot), 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int* err = a.p.err;
+
+  if (warp < PRODUCERS) {
+    setmaxnreg_dec<56>();
+    // ---- producers
+    constexpr int CH = HD / 8, RP = 32 / CH;  // chunks of a row, rows a step
+    const int ch = lane % CH, r0 = lane / CH;
+    const bool col = ch * 8 < a.p.hd;
+    const char *kl = (const char*)a.p.k + ch * 16, *vl = (const char*)a.p.v + ch * 16;
+    int n = 0, told = 0, block = 0;  // tiles requested, tiles announced, blocks begun
+    bool ok = true;
+    auto announce = [&](int upto) {  // (their copies have landed)
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0)
+        for (int i = told; i < upto; ++i) mbar_arrive(full0 + 8 * (i % NS));
+      told = upto;
+    };
+    auto request = [&](const char* src, long long off, uint32_t mask) {
+      const int s = n % NS;
+      if (n >= NS) {
+        const uint32_t par = (n / NS & 1) ^ 1;
+        if (!mbar_test(empty0 + 8 * s, par)) {
+          paged::cp_wait<0>();
+          if (told < n) announce(n);
+          if (!tc::mbar_wait(empty0 + 8 * s, par, err)) *s_abort = 1;
+        }
+      }
+      if (*s_abort) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      const uint32_t dst = base + C::OFF_RING + s * C::TILE + (ch >> 3) * (BK * 128);
+      if (off < 0) off = 0;
+#pragma unroll
+      for (int i = 0; i < 32 / RP; ++i) {
+        const int row = i * RP + r0;
+        const long long o = __shfl_sync(0xffffffffu, off, row);
+        paged::cp_async16_or_zero(dst + (warp * 32 + row) * 128 + (((ch & 7) ^ (row & 7)) << 4), src + o, (mask >> row & 1) && col);
+      }
+      paged::cp_commit();
+      ++n;
+      if (n - told > C::AHEAD) {
+        paged::cp_wait<C::AHEAD>();
+        announce(n - C::AHEAD);
+      }
+    };
+    do {
+      const int kv = p.u / p.nt, t1 = min(p.nb, r.end - p.v - SH_WEIGHT);
+      long long v_off = 0;
+      uint32_t v_mask = 0;
+#pragma unroll 1
+      for (int t = p.t; t < t1 && ok; ++t) {
+        const long long off = position_of<T>(a, p, kv, t * BK + warp * 32 + lane);
+        const uint32_t mask = __ballot_sync(0xffffffffu, off >= 0);
+        if (lane == 0) masks[(block % MASKS) * 4 + warp] = mask;
+        ++block;
+        request(kl, off, mask);
+        if (t > p.t && ok) request(vl, v_off, v_mask);
+        v_off = off;
+        v_mask = mask;
+      }
+      if (ok) request(vl, v_off, v_mask);
+    } while (ok && next_unit<MT, BK>(a, r.end, p));
+    paged::cp_wait<0>();
+    if (told < n) announce(n);
+  } else if (warp >= 12) {
+    setmaxnreg_dec<40>();
+    if (warp == MMA_WARP && lane == 0) {
+      // ---- issues the products
+      constexpr uint32_t kind = C::BF ? 1u << 7 | 1u << 10 : 0u;
+      constexpr uint32_t idS = tc::idesc_f16(MT, BK) | kind, idO = tc::idesc_f16_bmn(MT, HD) | kind;
+      int n = 0, block = 0, units = 0;  // tiles, blocks and units so far
+      bool ok = true;
+      do {
+        const int t1 = min(p.nb, r.end - p.v - SH_WEIGHT), nb = t1 - p.t;
+        if (!(ok = tc::mbar_wait(q_full, units & 1, err))) break;
+        ++units;
+        auto tile = [&](uint32_t& addr) {
+          const int s = n % NS;
+          if (!tc::mbar_wait(full0 + 8 * s, n / NS & 1, err)) return false;
+          tc::tc_fence_after();
+          addr = base + C::OFF_RING + s * C::TILE;
+          return true;
+        };
+        auto release = [&]() { tc::mma_commit(empty0 + 8 * (n++ % NS)); };
+        auto issue_s = [&](int j) {  // j: block of all
+          uint32_t k;
+          if (!tile(k)) return false;
+#pragma unroll
+          for (int i = NQ - 1; i >= 0; --i)  // the lowest piece first
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk)
+              tc::mma_f16(tmem + (j & 1) * 128, tc::smem_desc_sw128(base + i * MT * HD * 2 + (kk >> 2) * MT * 128 + (kk & 3) * 32),
+                          tc::smem_desc_sw128(k + (kk >> 2) * BK * 128 + (kk & 3) * 32), idS, i < NQ - 1 || kk > 0);
+          tc::mma_commit(s_full0 + 8 * (j & 1));
+          release();
+          return true;
+        };
+        ok = issue_s(block);
+        for (int j = 0; j < nb && ok; ++j, ++block) {
+          if (*s_abort) ok = false;
+          // S of the next block goes where P of the last one was, whose product was issued before
+          if (ok && j + 1 < nb) ok = issue_s(block + 1);
+          if (!ok || !(ok = tc::mbar_wait(p_full0 + 8 * (block & 1), block >> 1 & 1, err))) break;
+          uint32_t v;
+          if (!(ok = tile(v))) break;
+          const uint32_t o = tmem + C::O_COL + (block & 1) * (C::NO - 1) * 128;
+#pragma unroll
+          for (int i = NP - 1; i >= 0; --i) {
+            const uint32_t pc = tmem + (i < 2 ? (block & 1) * 128 + i * 64 : C::P3 + (block & 1) * 64);
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk)
+              tc::mma_f16_tmem_a(o, pc + kk * 8, tc::smem_desc_sw128_mn(v + kk * 2048, BK * 128, 1024), idO, i < NP - 1 || kk > 0);
+          }
+          tc::mma_commit(o_full0 + 8 * (block & 1));
+          release();
+        }
+      } while (ok && next_unit<MT, BK>(a, r.end, p));
+      if (!ok) *s_abort = 1;
+      tc::mma_commit(done);  // arrives once all products issued above are done
+      tc::mbar_wait(done, 0, err);
+    }
+  } else {
+    setmaxnreg_inc<208>();
+    // ---- softmax
+    constexpr int OC = HD / 2;  // output columns of a thread
+    const int quarter = warp & 3, half = (warp - 4) >> 2, row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16), pair = pair0 + 8 * quarter;
+    const float sc = fabsf(a.p.scale) * paged::LOG2E, sign = a.p.scale > 0.f ? 1.f : a.p.scale < 0.f ? -1.f : 0.f;
+    int block = 0, trades = 0;
+    bool ok = true;
+    auto trade = [&](float mine) -> float {  // the partner's value
+      xch[(2 * (trades & 1) + half) * MT + row] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair);
+      if (!tc::mbar_wait(pair, trades & 1, err)) ok = false;
+      const float other = xch[(2 * (trades & 1) + (half ^ 1)) * MT + row];
+      ++trades;
+      return other;
+    };
+    do {
+      const int kv = p.u / p.nt, tile = p.u - kv * p.nt, t1 = min(p.nb, r.end - p.v - SH_WEIGHT), nb = t1 - p.t;
+      {  // the unit's queries, 16 rows a warp; zeros for rows that take no part
+        constexpr int DL = HD / 32;  // dimensions of a lane
+        const int d0 = lane * DL;
+        const uint32_t at = base + (d0 >> 6) * (MT * 128) + (d0 & 7) * 2;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int rr = (warp - 4) * 16 + i;
+          const Row row_i = row_of(a, p, kv, tile * MT + rr);
+          float x[DL];
+#pragma unroll
+          for (int d = 0; d < DL; ++d) x[d] = 0.f;
+          if (row_i.in && d0 < a.p.hd) {
+            const IO* q = (const IO*)a.p.q + row_i.b * a.p.q_stride + row_i.h * a.p.hd + d0;
+#pragma unroll
+            for (int d = 0; d < DL; d += 2) {
+              const float2 two = paged::load2(q + d);
+              x[d] = two.x * sign;
+              x[d + 1] = two.y * sign;
+            }
+          }
+          float up = 1.f, down = 1.f;
+          if constexpr (C::F32IO) {
+            // a power of two that keeps the pieces normal: fp16 pieces with the row's largest at 2^10, whatever its size; bf16
+            // pieces, whose range is fp32's own, with only small ones raised to 2^-50. The scores undo it.
+            float top = 0.f;
+#pragma unroll
+            for (int d = 0; d < DL; ++d) top = fmaxf(top, fabsf(x[d]));
+            top = warp_max(top);
+            const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+            if (ex < 128) {  // (a row with an infinity passes as it is)
+              const int shift = C::BF ? max(-50 - ex, 0) : min(10 - ex, 126);
+              up = __uint_as_float((uint32_t)(127 + shift) << 23);
+              down = __uint_as_float((uint32_t)(127 - shift) << 23);
+            }
+          }
+          if (lane == 0) undo[rr] = down;
+          const uint32_t dst = at + rr * 128 + ((((d0 >> 3) & 7) ^ (rr & 7)) << 4);
+          uint32_t w[DL / 2][NQ];
+#pragma unroll
+          for (int d = 0; d < DL; d += 2) split<T, NQ>(x[d] * up, x[d + 1] * up, w[d / 2]);
+#pragma unroll
+          for (int i2 = 0; i2 < NQ; ++i2) {
+            if constexpr (DL == 4)
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + i2 * MT * HD * 2), "r"(w[0][i2]), "r"(w[1][i2]) : "memory");
+            else
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + i2 * MT * HD * 2), "r"(w[0][i2]) : "memory");
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      float o[OC];
+#pragma unroll
+      for (int i = 0; i < OC; ++i) o[i] = 0.f;
+      float m = -INFINITY, l = 0.f, f_last = 1.f, c = 0.f;
+      bool any = false;
+      auto fold = [&](int j) {  // O of block j, whose probabilities moved the reference by f_last
+        if (!tc::mbar_wait(o_full0 + 8 * (j & 1), j >> 1 & 1, err)) {
+          ok = false;
+          return;
+        }
+        tc::tc_fence_after();
+        if (__any_sync(0xffffffffu, f_last != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < OC; ++i) o[i] *= f_last;
+        }
+        const uint32_t from = lanes + C::O_COL + (j & 1) * (C::NO - 1) * 128 + half * OC;
+#pragma unroll
+        for (int i = 0; i < OC; i += 32) {
+          float x[32];
+          tc::tmem_ld32(from + i, x);
+#pragma unroll
+          for (int d = 0; d < 32; ++d) o[i + d] += x[d];
+        }
+        tc::tc_fence_before();
+      };
+#pragma unroll 1
+      for (int j = 0; j < nb; ++j, ++block) {
+        const int b = block & 1;
+        if (*s_abort || !tc::mbar_wait(s_full0 + 8 * b, block >> 1 & 1, err)) ok = false;
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc::tc_fence_after();
+        if (j == 0) c = fmaxf(C::F32IO ? sc * undo[row] : sc, 1e-38f);  // (not 0: masked scores stay -inf)
+        uint32_t u[64];
+        tc::tmem_ld32_nowait(lanes + b * 128 + 64 * half, u);
+        tc::tmem_ld32_nowait(lanes + b * 128 + 64 * half + 32, u + 32);
+        tc::tmem_wait_ld();
+        const uint2 mask = *reinterpret_cast<const uint2*>(masks + (block % MASKS) * 4 + 2 * half);
+        const uint32_t* all = masks + (block % MASKS) * 4;
+        any |= (all[0] | all[1] | all[2] | all[3]) != 0;
+        if ((mask.x & mask.y) != 0xffffffffu) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (!(mask.x >> i & 1)) u[i] = 0xff800000u;
+            if (!(mask.y >> i & 1)) u[32 + i] = 0xff800000u;
+          }
+        }
+        float top[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(u[i]);
+#pragma unroll
+        for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(u[i]));
+        const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), other = trade(mine);
+        if (C::three && j > 0) fold(block - 1);  // (one O buffer: it is read before P is handed over)
+        const float mn = fmaxf(m, fmaxf(mine, other) * c), f = mn > m ? ex2(m - mn) : 1.f;
+        l *= f;
+        m = mn;
+        const float ref = (mn == -INFINITY ? 0.f : mn) - PA_BIAS;
+        const f32x2 c2 = pack2(c, c), r2 = pack2(-ref, -ref);
+        f32x2 acc[2] = {0ull, 0ull};
+#pragma unroll
+        for (int i0 = 0; i0 < 32; i0 += 16) {
+          uint32_t pp[NP][16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = unpack2(fma2_to(pack2(__uint_as_float(u[2 * (i0 + i)]), __uint_as_float(u[2 * (i0 + i) + 1])), c2, r2));
+            const float p0 = ex2(e.x), p1 = ex2(e.y);
+            acc[i & 1] = add2(acc[i & 1], pack2(p0, p1));
+            uint32_t w[NP];
+            split<T, NP>(p0, p1, w);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) pp[k][i] = w[k];
+          }
+#pragma unroll
+          for (int k = 0; k < NP; ++k) tmem_st16(lanes + (k < 2 ? b * 128 + 64 * k : C::P3 + b * 64) + 32 * half + i0, pp[k]);
+        }
+        const float2 s0 = unpack2(acc[0]), s1 = unpack2(acc[1]);
+        l += (s0.x + s0.y) + (s1.x + s1.y);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full0 + 8 * b);
+        if (!C::three && j > 0) fold(block - 1);
+        f_last = f;
+      }
+      if (!ok) break;
+      fold(block - 1);
+      l += trade(l);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const Row mine = row_of(a, p, kv, tile * MT + row);
+      if (mine.in) {
+        const bool whole = nb == p.nb;
+        float* dst = state_of<MT, HD>(a, r, p, whole, mine, row);
+        const int width = whole ? a.p.hd : HD;
+#pragma unroll
+        for (int i = 0; i < OC; i += 4)
+          if (half * OC + i < width)
+            *reinterpret_cast<float4*>(dst + half * OC + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        if (half == 0) *reinterpret_cast<float2*>(dst + width) = make_float2(paged::state_max(m, any), l);
+      }
+    } while (next_unit<MT, BK>(a, r.end, p));
+    if (!ok) *s_abort = 1;
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+  pdl_wait();  // (this grid ends after the one before it)
+}
+
+template <typename T, int HD, typename IO>
+cudaError_t run(int ctas, const SharedArgs& a, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(shared_tc_kernel<T, HD, IO>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<T, HD, IO>::SMEM);
+  return e ? e : launch_k(shared_tc_kernel<T, HD, IO>, dim3(ctas), dim3(THREADS), Cfg<T, HD, IO>::SMEM, s, true, a);
+}
+template <typename T, typename IO>
+cudaError_t run(int ctas, const SharedArgs& a, cudaStream_t s) {
+  return a.p.hd <= 64 ? run<T, 64, IO>(ctas, a, s) : run<T, 128, IO>(ctas, a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_shared_tc(int cache_dtype, int io_dtype, int ctas, const SharedArgs& a, cudaStream_t s) {
+  if (cache_dtype == QW_F16) return io_dtype == QW_F32 ? run<f16, float>(ctas, a, s) : run<f16, f16>(ctas, a, s);
+  return io_dtype == QW_F32 ? run<bf16, float>(ctas, a, s) : run<bf16, bf16>(ctas, a, s);
+}
+
+}  // namespace shared_attn
+}  // namespace qw
