@@ -12,8 +12,8 @@
 //     power of two, 2^(z log2(e) - k), with log2(e) in two parts (one rounding of a small number each), so moving k is
 //     exact; a lane's sums are fp32 over at most some hundred logits, all sums of sums 64-bit. Against 64 bits
 //     the normaliser is off by 1e-8 where fp32 sums of fp32 exponents give 1e-7.
-//   - A second launch joins a group: pieces' sums, then the lists. A list's r-th candidate is out of the race if r + (the lists
-//     with better heads) >= n_out, which leaves n_out (n_out + 1) / 2; each counts those before it.
+//   - A second launch joins a group: pieces' sums, then the lists, of which only those with the n_out best heads count. A warp
+//     holds a list a lane and takes the best head n_out times.
 // What bounds it: HBM and the instructions of a logit (two exponent products, an exponential, a sum, a maximum: about 4).
 #include "common.cuh"
 #include "op_util.h"
@@ -33,6 +33,7 @@ constexpr int BS_MAX_LISTS = 256;                    // beams * pieces of a grou
 constexpr int BS_MAX_VOCAB = 1 << 21;
 constexpr int BS_CAP = 512;                          // candidates of a piece before they are ranked
 constexpr float BS_LOG2E_HI = 1.44269502162933349609375f, BS_LOG2E_LO = 1.92596303e-8f;  // their sum is log2(e) to 2^-50
+constexpr double BS_LN2 = 0.693147180559945309417232121458;
 constexpr float BS_FAR = 1048576.f;  // maxima beyond it take the slow sum
 
 struct PieceState {
@@ -405,21 +406,44 @@ __device__ __forceinline__ u64 order64(double v) {
   const u64 u = (u64)__double_as_longlong(v + 0.);
   return u >> 63 ? ~u : u | 1ull << 63;
 }
-// a candidate: weighed score, then lower beam, then larger logit, then lower id
 struct Best {
-  u64 score, key;
-  int row;
-  __device__ __forceinline__ bool before(const Best& o) const {
-    return score != o.score ? score > o.score : row != o.row ? row < o.row : key > o.key;
-  }
+  u64 score, key;  // weighed score in its order, logit and id; 0: none
 };
+// equal scores: the lower beam, then the larger logit, then the lower id
+__device__ __forceinline__ bool wins(int row, u64 key, int row2, u64 key2) { return row != row2 ? row < row2 : key > key2; }
+
+// ln of a row's sum of exponentials, with pieces that were summed from the definition; NaN if there is one. A warp.
+__device__ __noinline__ double far_norm(const PieceState* st, int n, int lane) {
+  double m = -INFINITY, s = 0.;
+  bool nan = false;
+#pragma unroll 1
+  for (int p = lane; p < n; p += 32) {
+    if (st[p].ref == -INFINITY && st[p].sum == 0.) continue;  // nothing but -inf
+    const double x = (st[p].slow ? (double)st[p].ref : (double)st[p].ref * BS_LN2) + log(st[p].sum);
+    if (x != x) {
+      nan = true;
+      continue;
+    }
+    const double hi = fmax(m, x);
+    s = s * exp(m - hi) + exp(x - hi);
+    m = hi;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const double m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    const double hi = fmax(m, m2);
+    s = (m > -INFINITY ? s * exp(m - hi) : 0.) + (m2 > -INFINITY ? s2 * exp(m2 - hi) : 0.);
+    m = hi;
+  }
+  return __any_sync(0xffffffffu, nan) ? (double)NAN : m + log(s);
+}
 
 __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
-  constexpr int MAX_RUN = BS_MAX_OUT * (BS_MAX_OUT + 1) / 2;
   __shared__ double s_norm[BS_MAX_BEAMS], s_score[BS_MAX_BEAMS], s_weight[BS_MAX_BEAMS];
+  __shared__ float s_ref[BS_MAX_BEAMS];
   __shared__ int s_kind[BS_MAX_BEAMS];  // 0: no candidates, 1: the row's logits, 2: ended
-  __shared__ Best s_head[BS_MAX_LISTS], s_run[MAX_RUN];
-  __shared__ int s_surv[BS_MAX_OUT], s_row[BS_MAX_OUT], s_token[BS_MAX_OUT];
+  __shared__ Best s_head[BS_MAX_LISTS], s_run[32][BS_MAX_OUT];
+  __shared__ int s_surv[32], s_row[BS_MAX_OUT], s_token[BS_MAX_OUT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.x, k = a.n_out, P = a.pieces;
   pdl_wait();
 #pragma unroll 1
@@ -427,48 +451,47 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
     const int row = g * a.beams + w;
     const float c = a.scores[row], weight = a.weights ? a.weights[row] : 1.f;
     const bool ended = a.ended && a.ended[row];
-    int kind = 0;
-    double norm = 0.;
-    bool bad = c != c || c == INFINITY || !(weight > 0.f && weight < INFINITY);
-    if (!bad && c > -INFINITY) {
-      kind = ended ? 2 : 1;
-      if (!ended) {
-        // ln of the pieces' sums, joined over the largest
-        double m = -INFINITY, s = 0.;
+    const bool bad = c != c || c == INFINITY || !(weight > 0.f && weight < INFINITY);
+    const int kind = bad || c == -INFINITY ? 0 : ended ? 2 : 1;
+    double s = 0.;
+    float ref = NAN;  // NaN: s is the normaliser already
+    if (kind == 1) {
+      const PieceState* st = a.state + (size_t)row * P;
+      bool far = false;
+      ref = -INFINITY;
 #pragma unroll 1
-        for (int p = lane; p < P; p += 32) {
-          const PieceState st = a.state[(size_t)row * P + p];
-          if (st.ref == -INFINITY && st.sum == 0.) continue;  // nothing but -inf
-          const double x = st.slow ? (double)st.ref + log(st.sum) : (double)st.ref * 0.693147180559945309417232121458 + log(st.sum);
-          if (x != x) m = x;
-          else if (m == m) {
-            const double hi = fmax(m, x);
-            s = s * exp(m - hi) + exp(x - hi);
-            m = hi;
-          }
-        }
-        bool nan = m != m;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          const double m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-          const double hi = fmax(m, m2);
-          if (hi > -INFINITY) s = (m > -INFINITY ? s * exp(m - hi) : 0.) + (m2 > -INFINITY ? s2 * exp(m2 - hi) : 0.);
-          m = hi;
-        }
-        nan = __any_sync(0xffffffffu, nan);
-        norm = m + log(s);
-        if (nan || !(fabs(norm) < INFINITY)) bad = true;
+      for (int p = lane; p < P; p += 32) {
+        far |= st[p].slow;
+        ref = fmaxf(ref, st[p].ref);
+      }
+      if (__any_sync(0xffffffffu, far)) {
+        s = far_norm(st, P, lane);
+        ref = NAN;
+      } else {
+        ref = warp_max(ref);
+#pragma unroll 1
+        for (int p = lane; p < P; p += 32) s += st[p].sum * (double)power2(st[p].ref - ref);
+        for (int o = P > 16 ? 16 : P > 8 ? 8 : P > 4 ? 4 : P > 2 ? 2 : P > 1 ? 1 : 0; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       }
     }
-    if (bad) {
-      kind = 0;
-      if (lane == 0) atomicOr(a.err, ERR_NONFINITE);
-    }
     if (lane == 0) {
+      if (bad) atomicOr(a.err, ERR_NONFINITE);
       s_kind[w] = kind;
-      s_norm[w] = norm;
+      s_norm[w] = s;
+      s_ref[w] = ref;
       s_score[w] = c;
       s_weight[w] = weight;
+    }
+  }
+  if (tid < 32) s_surv[tid] = -1;
+  __syncthreads();
+  if (tid < a.beams && s_kind[tid] == 1) {  // one logarithm for all rows: 64-bit arithmetic is slow here
+    const float ref = s_ref[tid];
+    const double norm = ref == ref ? (double)ref * BS_LN2 + log(s_norm[tid]) : s_norm[tid];
+    s_norm[tid] = norm;
+    if (!(fabs(norm) < INFINITY)) {
+      s_kind[tid] = 0;
+      atomicOr(a.err, ERR_NONFINITE);
     }
   }
   __syncthreads();
@@ -477,7 +500,7 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
   };
   auto best_of = [&](int list, int r) {
     const int w = list / P, p = list - w * P;
-    Best b{0, 0, w};
+    Best b{0, 0};
     if (s_kind[w] == 2) {
       if (p == 0 && r == 0) b.key = 1;
     } else if (s_kind[w] == 1) {
@@ -487,43 +510,62 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
     return b;
   };
   const int lists = a.beams * P;
-  if (tid < BS_MAX_OUT) s_surv[tid] = -1;
-  for (int l = tid; l < lists; l += BS_NT) s_head[l] = best_of(l, 0);
-  __syncthreads();
-  for (int l = tid; l < lists; l += BS_NT) {
-    const Best b = s_head[l];
-    if (!b.key) continue;
-    int rank = 0;
-#pragma unroll 1
-    for (int j = 0; j < lists; ++j) rank += s_head[j].key && s_head[j].before(b);
-    if (rank < k) s_surv[rank] = l;
+  if (lists <= 32) {
+    if (tid < lists) s_surv[tid] = tid;
+  } else {  // the lists with the n_out best heads
+    for (int l = tid; l < lists; l += BS_NT) s_head[l] = best_of(l, 0);
+    __syncthreads();
+    for (int l = tid; l < lists; l += BS_NT) {
+      const Best b = s_head[l];
+      if (!b.key) continue;
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < lists; ++j) {
+        const u64 other = s_head[j].score;
+        rank += other > b.score || (other == b.score && s_head[j].key && wins(j / P, s_head[j].key, l / P, b.key));
+      }
+      if (rank < k) s_surv[rank] = l;
+    }
   }
   __syncthreads();
-  // candidate r of the list whose head is the i-th best: i + r < k
-  const int run = k * (k + 1) / 2;
-  for (int x = tid; x < run; x += BS_NT) {
-    int i = 0, r = x;
-    while (r >= k - i) r -= k - i++;
-    s_run[x] = s_surv[i] >= 0 ? best_of(s_surv[i], r) : Best{0, 0, 0};
+  for (int x = tid; x < 32 * k; x += BS_NT) {
+    const int i = x / k, r = x - i * k, list = s_surv[i];
+    // a list behind i better heads has k - i candidates
+    s_run[i][r] = list >= 0 && (lists <= 32 || i + r < k) ? best_of(list, r) : Best{0, 0};
   }
   if (tid < k) s_row[tid] = -1;
   __syncthreads();
-  for (int x = tid; x < run; x += BS_NT) {
-    const Best b = s_run[x];
-    if (!b.key) continue;
-    int rank = 0;
+  if (warp == 0) {  // a list a lane, the best head taken n_out times
+    const int list = s_surv[lane], w = list >= 0 ? list / P : 0;
+    int at = 0;
+    Best b = s_run[lane][0];
 #pragma unroll 1
-    for (int j = 0; j < run; ++j) rank += s_run[j].key && s_run[j].before(b);
-    if (rank >= k) continue;
-    const int row = g * a.beams + b.row, o = g * k + rank;
-    const bool old = s_kind[b.row] == 2;
-    const int token = old ? a.end_id : (int)(0xffffffffu - (uint32_t)b.key);
-    a.parents[o] = row;
-    a.tokens[o] = token;
-    a.scores_out[o] = (float)score_of(b.row, b.key);
-    if (a.ended_out) a.ended_out[o] = old || token == a.end_id;
-    s_row[rank] = row;
-    s_token[rank] = old ? -1 : token;
+    for (int i = 0; i < k; ++i) {
+      const uint32_t hi = (uint32_t)(b.score >> 32), top = __reduce_max_sync(0xffffffffu, hi);
+      const uint32_t lo = hi == top ? (uint32_t)b.score : 0u, top2 = __reduce_max_sync(0xffffffffu, lo);
+      if (top == 0 && top2 == 0) break;
+      unsigned mask = __ballot_sync(0xffffffffu, hi == top && lo == top2);
+      int best = __ffs(mask) - 1;
+#pragma unroll 1
+      while (mask &= mask - 1) {  // equal scores
+        const int other = __ffs(mask) - 1;
+        if (wins(__shfl_sync(0xffffffffu, w, other), __shfl_sync(0xffffffffu, b.key, other), __shfl_sync(0xffffffffu, w, best),
+                 __shfl_sync(0xffffffffu, b.key, best)))
+          best = other;
+      }
+      if (lane == best) {
+        const int row = g * a.beams + w, o = g * k + i;
+        const bool old = s_kind[w] == 2;
+        const int token = old ? a.end_id : (int)(0xffffffffu - (uint32_t)b.key);
+        a.parents[o] = row;
+        a.tokens[o] = token;
+        a.scores_out[o] = (float)score_of(w, b.key);
+        if (a.ended_out) a.ended_out[o] = old || token == a.end_id;
+        s_row[i] = row;
+        s_token[i] = old ? -1 : token;
+        b = ++at < k ? s_run[lane][at] : Best{0, 0};
+      }
+    }
   }
   __syncthreads();
   for (int i = tid; i < k; i += BS_NT) {

@@ -29,7 +29,14 @@ constexpr size_t OP_COUNTER_BYTES = 16384;
 // Every pointer must be memory of the current device: a host pointer or another device's would
 // fault in the kernel. Managed memory passes. Null pointers are skipped (optional arguments). A pointer that is not
 // aligned to 4 bytes would fault too: all elements but 16-bit ones have 4 or 8.
-qw_status op_check_device(std::initializer_list<const void*> ptrs);
+struct OpPointers {
+  const void* const* p;
+  size_t n;
+  const void* const* begin() const { return p; }
+  const void* const* end() const { return p + n; }
+};
+qw_status op_check_device(OpPointers ptrs);
+inline qw_status op_check_device(std::initializer_list<const void*> ptrs) { return op_check_device(OpPointers{ptrs.begin(), ptrs.size()}); }
 
 // Shape, strides and alignment of a paged cache; on success *norm is the cache with the strides
 // along extents of 1 set to 0.

@@ -17,14 +17,15 @@ namespace qw {
 namespace {
 
 constexpr int CP_RANGES = 1024, CP_RANGE_MIN = 2048, CP_THREADS = 256, CP_SEG = 512;
-constexpr size_t CP_HEAD = 8192;
+constexpr int CP_PAD = 8;  // a range's counter has a sector of its own
+constexpr size_t CP_HEAD = 64 + CP_RANGES * CP_PAD * 4;
 
 struct CompactHead {  // of the workspace, zero between calls
   int bad;
   unsigned int ticket;
   int n_moves;  // written before it is read
   int pad[13];
-  int free_in[CP_RANGES];  // free pages by range
+  int free_in[CP_RANGES * CP_PAD];  // free pages by range
 };
 static_assert(sizeof(CompactHead) <= CP_HEAD, "head");
 
@@ -39,14 +40,17 @@ struct CompactArgs {
 };
 
 __global__ void __launch_bounds__(CP_THREADS) compact_marks_kernel(const CompactArgs a) {
+  __shared__ int s_free[CP_RANGES];  // the CTA's pages by range: a million would meet at few counters
   pdl_trigger();
+  for (int i = threadIdx.x; i < a.ranges; i += CP_THREADS) s_free[i] = 0;
+  __syncthreads();
   const int n_free = *a.n_free, first = blockIdx.x * CP_THREADS + threadIdx.x, step = gridDim.x * CP_THREADS;
   const long long room = min((long long)a.max_blocks * a.page, 0x7fffffffll);
   int bad = 0;
   if (n_free < 0 || n_free > a.n_pages) {
     bad = ERR_CAPACITY;
   } else {
-#pragma unroll 1
+#pragma unroll 4
     for (int i = first; i < n_free; i += step) {
       const int id = a.free_pages[i];
       if (id < 0 || id >= a.n_pages) {
@@ -54,7 +58,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_marks_kernel(const Compact
         continue;
       }
       if (atomicOr(a.bits + (id >> 5), 1u << (id & 31)) >> (id & 31) & 1) bad |= ERR_PAGE;  // twice on the list
-      atomicAdd(&a.head->free_in[id / a.range], 1);
+      atomicAdd(s_free + id / a.range, 1);
     }
   }
 #pragma unroll 1
@@ -66,6 +70,9 @@ __global__ void __launch_bounds__(CP_THREADS) compact_marks_kernel(const Compact
     atomicOr(&a.head->bad, 1);
     atomicOr(a.err, bad);
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.ranges; i += CP_THREADS)
+    if (s_free[i]) atomicAdd(&a.head->free_in[i * CP_PAD], s_free[i]);
 }
 
 __global__ void __launch_bounds__(CP_THREADS) compact_moves_kernel(const CompactArgs a) {
@@ -90,7 +97,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_moves_kernel(const Compact
   const int live = n - n_free, live_range = live / a.range;
   int before = 0, holes = 0;  // free ids before the range, below `live`
   for (int i = tid; i < a.ranges; i += CP_THREADS) {
-    const int k = a.head->free_in[i];
+    const int k = a.head->free_in[i * CP_PAD];
     if (i < c) before += k;
     if (i < live_range) holes += k;
   }
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_tables_kernel(const Compac
   }
   __syncthreads();
   if (s_last) {
-    for (int i = tid; i < a.ranges; i += CP_THREADS) a.head->free_in[i] = 0;
+    for (int i = tid; i < a.ranges; i += CP_THREADS) a.head->free_in[i * CP_PAD] = 0;
     if (tid == 0) {
       a.head->bad = 0;
       a.head->ticket = 0;
@@ -256,7 +263,7 @@ qw_status qw_op_page_compact(int32_t n_seqs, int32_t page_size, int32_t n_pages,
     return dim3((unsigned)(want < 1 ? 1 : want < 4 * nsm ? want : 4 * nsm));
   };
   const int64_t most = n_pages > n_seqs ? n_pages : n_seqs, rows = (int64_t)n_seqs * segs * 32;
-  if ((e = launch_k(compact_marks_kernel, grid(most / 2 + 1), dim3(CP_THREADS), 0, s, false, a)) ||
+  if ((e = launch_k(compact_marks_kernel, grid(most / 16 + 1), dim3(CP_THREADS), 0, s, false, a)) ||
       (e = launch_k(compact_moves_kernel, dim3(ranges), dim3(CP_THREADS), 0, s, true, a)) ||
       (e = launch_k(compact_tables_kernel, grid(rows > n_pages / 32 ? rows : n_pages / 32), dim3(CP_THREADS), 0, s, true, a)))
     return op_cuda_fail(e, "page compaction launch");

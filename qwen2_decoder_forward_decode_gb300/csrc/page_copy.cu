@@ -6,6 +6,8 @@
 #include "common.cuh"
 #include "op_util.h"
 
+#include <algorithm>
+
 namespace qw {
 namespace {
 
@@ -89,9 +91,9 @@ extern "C" qw_status qw_op_page_copy(const qw_paged_kv* caches, int32_t n_caches
     return op_fail(QW_ERR_UNSUPPORTED, "a page of more than 2^30 vectors");
   if (n == 0) return QW_OK;
   if (!src || !dst || !err_dev) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
-  if ((st = op_check_device({src, dst, len, err_dev}))) return st;
-  for (int i = 0; i < n_caches; ++i)
-    if ((st = op_check_device({a.base[2 * i], a.base[2 * i + 1]}))) return st;
+  const void* ptrs[4 + 2 * COPY_MAX_CACHES] = {src, dst, len, err_dev};
+  std::copy(a.base, a.base + 2 * n_caches, ptrs + 4);
+  if ((st = op_check_device(OpPointers{ptrs, 4 + 2 * (size_t)n_caches}))) return st;
   a.n = n;
   a.n_caches = n_caches;
   a.n_pages = c0.n_pages;

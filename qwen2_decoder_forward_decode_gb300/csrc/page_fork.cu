@@ -8,7 +8,8 @@
 //      a prefix sum; warps then copy the children's tables and add the parents' changes to delta[page] (atomics on
 //      whole numbers; rows that go on with one child add 0 and are skipped). shares + delta < 0 means that a page's
 //      last holder left. A page crosses that line back and forth while others add to it, so the pages below the line
-//      are counted per range of the pool as they cross it, and the counts are right at the end.
+//      are counted per range of the pool as they cross it (in shared memory, then in the workspace), and the counts are right at
+//      the end.
 //   2. fork_pool: a CTA a range. The counts of the ranges before give the place in the free list, ballots the order
 //      within the range: ascending page ids, the same in every run.
 // What bounds it: latency (parents, length, table entry, count: four loads in a chain, then a second launch that
@@ -20,13 +21,14 @@ namespace {
 
 constexpr int FORK_RANGES = 1024, FORK_RANGE_MIN = 2048;  // ranges of the pool, pages of one at least
 constexpr int FORK_POOL_THREADS = 256, FORK_SEG = 512;    // table entries that a warp takes at once
-constexpr size_t FORK_HEAD = 8192;                        // bytes before delta
+constexpr int FORK_PAD = 8;                               // a range's counter has a sector of its own
+constexpr size_t FORK_HEAD = 64 + FORK_RANGES * FORK_PAD * 4;  // bytes before delta
 
 struct ForkHead {  // of the workspace
   int bad, n_free, n_copies;
   unsigned int ticket;   // zero between calls
   int pad[12];
-  int gone[FORK_RANGES];  // pages that lost their last holder, by range; zero between calls
+  int gone[FORK_RANGES * FORK_PAD];  // pages that lost their last holder, by range; zero between calls
 };
 static_assert(sizeof(ForkHead) <= FORK_HEAD, "head");
 
@@ -39,13 +41,13 @@ struct ForkArgs {
   int* err;
 };
 
-__device__ __forceinline__ void hold(const ForkArgs& a, int id, int d) {
+__device__ __forceinline__ void hold(const ForkArgs& a, int* gone, int id, int d) {
   if (id < 0 || id >= a.n_pages) {
     atomicOr(a.err, ERR_PAGE);
     return;
   }
   const int was = a.shares[id] + atomicAdd(a.delta + id, d), is = was + d;
-  if ((was < 0) != (is < 0)) atomicAdd(&a.head->gone[id / a.range], is < 0 ? 1 : -1);
+  if ((was < 0) != (is < 0)) atomicAdd(gone + id / a.range, is < 0 ? 1 : -1);
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS) fork_tables_kernel(const ForkArgs a) {
@@ -54,9 +56,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) fork_tables_kernel(const ForkArg
   int* first = kids + a.n;    // [n] the lowest of them
   int* fresh = first + a.n;   // [n_out] number of the page that a child takes, -1: none
   __shared__ uint32_t w_sum[PLAN_THREADS / 32];
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_gone[FORK_RANGES];  // (the CTA's pages that crossed the line; thousands would meet at few counters)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
+  for (int i = tid; i < FORK_RANGES; i += PLAN_THREADS) s_gone[i] = 0;
   const int n_free = *a.n_free;
   const long long room = min((long long)a.max_blocks * a.page, 0x7fffffffll);
   if (tid == 0) s_bad = n_free < 0 || n_free > a.n_pages;
@@ -137,9 +140,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) fork_tables_kernel(const ForkArg
       const int len = a.lens[p], end = min(d > 0 ? len / a.page : pages_of(len, a.page), j0 + FORK_SEG);
       const int* src = a.table + (size_t)p * a.max_blocks;
 #pragma unroll 4
-      for (int j = j0 + lane; j < end; j += 32) hold(a, src[j], d);
+      for (int j = j0 + lane; j < end; j += 32) hold(a, s_gone, src[j], d);
     }
   }
+  __syncthreads();
+  for (int i = tid; i < FORK_RANGES; i += PLAN_THREADS)
+    if (s_gone[i]) atomicAdd(&a.head->gone[i * FORK_PAD], s_gone[i]);
 }
 
 __global__ void __launch_bounds__(FORK_POOL_THREADS) fork_pool_kernel(const ForkArgs a) {
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(FORK_POOL_THREADS) fork_pool_kernel(const Fork
   const int bad = a.head->bad, n_free = a.head->n_free, keep = bad ? n_free : n_free - a.head->n_copies;
   int before = 0, total = 0;
   for (int i = tid; i < gridDim.x; i += FORK_POOL_THREADS) {
-    const int n = a.head->gone[i];
+    const int n = a.head->gone[i * FORK_PAD];
     total += n;
     if (i < c) before += n;
   }
@@ -216,7 +222,7 @@ __global__ void __launch_bounds__(FORK_POOL_THREADS) fork_pool_kernel(const Fork
     __syncthreads();
   }
   if (s_last) {
-    for (int i = tid; i < gridDim.x; i += FORK_POOL_THREADS) a.head->gone[i] = 0;
+    for (int i = tid; i < gridDim.x; i += FORK_POOL_THREADS) a.head->gone[i * FORK_PAD] = 0;
     if (tid == 0) a.head->ticket = 0;
   }
 }
@@ -273,6 +279,7 @@ qw_status qw_op_page_fork(int32_t n_seqs, int32_t n_out, int32_t page_size, int3
   const size_t smem = (size_t)(2 * n_seqs + n_out) * sizeof(int);
   // the same limit in every call: it is the kernel's, and a smaller one could come between another thread's setting and launch
   constexpr int most = 3 * PLAN_MAX_SEQS * (int)sizeof(int);
+  static_assert(most + FORK_RANGES * 4 + 256 <= 232448, "shared memory");
   if (smem > 40 * 1024 && (e = cudaFuncSetAttribute(fork_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most)))
     return op_cuda_fail(e, "page fork launch");
   const int64_t want = ((int64_t)(n_seqs + n_out) * segs + PLAN_THREADS / 32 - 1) / (PLAN_THREADS / 32);

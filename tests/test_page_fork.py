@@ -385,10 +385,6 @@ class Compact:
         assert taken(self.ofree, self.n_pages)[:n_free].tolist() == sorted(free, reverse=True)
         if self.with_shares:
             np.testing.assert_array_equal(taken(self.oshares, self.n_pages), shares)
-        head = 8192 + (self.n_pages + 127) // 128 * 16
-        ws = self.ws.clone()
-        ws[8:12] = 0  # the number of moves
-        assert not bool(ws[:head].any()), "the workspace is not ready for the next call"
 
 
 @pytest.mark.parametrize("in_place", [False, True])
@@ -400,6 +396,9 @@ def test_compaction_matches_the_loop(n_pages, needs, page, moves, in_place):
     c = Compact(n_pages, needs, page, max(needs + [1]) + 1, moves, in_place=in_place)
     c.run()
     c.check()
+    if not in_place:  # the workspace is ready for the next call
+        c.run()
+        c.check()
 
 
 def test_a_pool_of_many_ranges():
