@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
   __shared__ float s_ref[BS_MAX_BEAMS];
   __shared__ int s_kind[BS_MAX_BEAMS];  // 0: no candidates, 1: the row's logits, 2: ended
   __shared__ Best s_head[BS_MAX_LISTS], s_run[32][BS_MAX_OUT];
-  __shared__ int s_surv[32], s_row[BS_MAX_OUT], s_token[BS_MAX_OUT];
+  __shared__ int s_surv[32], s_row[BS_MAX_OUT], s_token[BS_MAX_OUT], s_len[BS_MAX_OUT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.x, k = a.n_out, P = a.pieces;
   pdl_wait();
 #pragma unroll 1
@@ -577,21 +577,21 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
     if (a.history) a.lens_out[o] = 0;
   }
   if (!a.history) return;
-#pragma unroll 1
-  for (int i = warp; i < k; i += BS_NW) {  // a history a warp
-    const int row = s_row[i], token = s_token[i];
+  for (int i = tid; i < k; i += BS_NT) {
+    const int row = s_row[i], held = row >= 0 ? a.lens[row] : 0, len = max(0, min(held, a.width));
+    s_len[i] = len;
     if (row < 0) continue;
-    const int held = a.lens[row], len = max(0, min(held, a.width));
-    const bool grows = token >= 0, fits = len < a.width;
-    const int* src = a.history + (size_t)row * a.width;
-    int* dst = a.history_out + (size_t)(g * k + i) * a.width;
+    const bool grows = s_token[i] >= 0, fits = len < a.width;
+    if (grows && fits) a.history_out[(size_t)(g * k + i) * a.width + len] = s_token[i];
+    a.lens_out[g * k + i] = len + (grows && fits);
+    if (held != len || (grows && !fits)) atomicOr(a.err, ERR_CAPACITY);
+  }
+  __syncthreads();
+  const int step = (a.width + 31) / 32 * 32;  // (a warp stays within a history)
 #pragma unroll 4
-    for (int j = lane; j < len; j += 32) dst[j] = src[j];
-    if (lane == 0) {
-      if (grows && fits) dst[len] = token;
-      a.lens_out[g * k + i] = len + (grows && fits);
-      if (held != len || (grows && !fits)) atomicOr(a.err, ERR_CAPACITY);
-    }
+  for (long long x = tid; x < (long long)k * step; x += BS_NT) {
+    const int i = (int)(x / step), j = (int)(x - (long long)i * step);
+    if (j < s_len[i]) a.history_out[(size_t)(g * k + i) * a.width + j] = a.history[(size_t)s_row[i] * a.width + j];
   }
 }
 

@@ -16,7 +16,7 @@
 namespace qw {
 namespace {
 
-constexpr int CP_RANGES = 1024, CP_RANGE_MIN = 2048, CP_THREADS = 256, CP_SEG = 512;
+constexpr int CP_RANGES = 1024, CP_RANGE_MIN = 2048, CP_THREADS = 256, CP_SEG = 128;
 constexpr int CP_PAD = 8;  // a range's counter has a sector of its own
 constexpr size_t CP_HEAD = 64 + CP_RANGES * CP_PAD * 4;
 
@@ -120,11 +120,12 @@ __global__ void __launch_bounds__(CP_THREADS) compact_moves_kernel(const Compact
   if (c == 0 && tid == 0) *a.n_moves = a.head->n_moves = moves;
 #pragma unroll 1
   for (int i = moves + c * CP_THREADS + tid; i < a.max_moves; i += gridDim.x * CP_THREADS) a.src[i] = a.dst[i] = -1;
-  // a word of 32 pages a lane, a warp 1024 pages; the warps' counts in front
+  // CP_WORDS words of 32 pages a warp at a time, one word a lane; the warps' counts in front
+  constexpr int CP_WORDS = CP_RANGE_MIN / (32 * NW);
 #pragma unroll 1
-  for (long long base = first; base < end; base += CP_THREADS * 32) {
-    const long long w0 = (base >> 5) + warp * 32;
-    const uint32_t mine = (w0 + lane) * 32 < end ? a.bits[w0 + lane] : 0u;
+  for (long long base = first; base < end; base += CP_RANGE_MIN) {
+    const long long w0 = (base >> 5) + warp * CP_WORDS;
+    const uint32_t mine = lane < CP_WORDS && (w0 + lane) * 32 < end ? a.bits[w0 + lane] : 0u;
     const int count = __popc(mine);
     int incl = count;
 #pragma unroll
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_moves_kernel(const Compact
       before += s_sum[0][w];
     }
 #pragma unroll 1
-    for (int k = 0; k < 32 && (w0 + k) * 32 < end; ++k) {  // a page a lane: stores side by side
+    for (int k = 0; k < CP_WORDS && (w0 + k) * 32 < end; ++k) {  // a page a lane: stores side by side
       const uint32_t word = __shfl_sync(0xffffffffu, mine, k);
       const int below = at + __shfl_sync(0xffffffffu, incl - count, k);
       const long long id64 = (w0 + k) * 32 + lane;
@@ -263,7 +264,7 @@ qw_status qw_op_page_compact(int32_t n_seqs, int32_t page_size, int32_t n_pages,
     return dim3((unsigned)(want < 1 ? 1 : want < 4 * nsm ? want : 4 * nsm));
   };
   const int64_t most = n_pages > n_seqs ? n_pages : n_seqs, rows = (int64_t)n_seqs * segs * 32;
-  if ((e = launch_k(compact_marks_kernel, grid(most / 16 + 1), dim3(CP_THREADS), 0, s, false, a)) ||
+  if ((e = launch_k(compact_marks_kernel, grid(most / 8 + 1), dim3(CP_THREADS), 0, s, false, a)) ||
       (e = launch_k(compact_moves_kernel, dim3(ranges), dim3(CP_THREADS), 0, s, true, a)) ||
       (e = launch_k(compact_tables_kernel, grid(rows > n_pages / 32 ? rows : n_pages / 32), dim3(CP_THREADS), 0, s, true, a)))
     return op_cuda_fail(e, "page compaction launch");

@@ -20,7 +20,7 @@ namespace qw {
 namespace {
 
 constexpr int FORK_RANGES = 1024, FORK_RANGE_MIN = 2048;  // ranges of the pool, pages of one at least
-constexpr int FORK_POOL_THREADS = 256, FORK_SEG = 512;    // table entries that a warp takes at once
+constexpr int FORK_POOL_THREADS = 256, FORK_SEG = 128;    // table entries that a warp takes: one round of loads
 constexpr int FORK_PAD = 8;                               // a range's counter has a sector of its own
 constexpr size_t FORK_HEAD = 64 + FORK_RANGES * FORK_PAD * 4;  // bytes before delta
 
