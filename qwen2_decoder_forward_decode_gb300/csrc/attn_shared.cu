@@ -7,8 +7,9 @@
 // positions by themselves:
 //   1. the own positions: the kernels of attn_paged.cu with each sequence's first positions left out and their states
 //      kept in fp32;
-//   2. the shared ones: matrix products of up to 128 rows with blocks of keys and values (attn_shared_tc.cu; fp32 caches
-//      and longer heads on the CUDA cores, attn_shared_simt.cu). All blocks of all groups form one list that is cut into
+//   2. the shared ones: matrix products of up to 256 rows with blocks of keys and values on the tensor cores
+//      (attn_shared_pair.cu, for fp32 callers attn_shared_tc.cu; fp32 caches and longer heads on the CUDA cores,
+//      attn_shared_simt.cu). All blocks of all groups form one list that is cut into
 //      equal ranges, one a CTA;
 //   3. the join: a warp a row, or a CTA a row where rows are few and their parts many.
 // The second launch goes on beside the first (programmatic dependent launch: it waits for it at its end only), the third
@@ -85,19 +86,28 @@ __device__ __forceinline__ bool join_row(const JoinArgs& ja, int row, int part, 
     if (part == 0 && lane == 0 && h == 0 && mine != pre && mine > 0 && mine <= len) atomicOr(p.err, ERR_PAGE);
     return true;
   }
-  const int nt = ((end - first) * grp + ja.geo.mt - 1) / ja.geo.mt, nb = (pre + ja.geo.bk - 1) / ja.geo.bk;
-  const int kv = h / grp, i = (b - first) * grp + (h - kv * grp), tile = i / ja.geo.mt;
-  const int v = a.at[lo] + (kv * nt + tile) * (SH_WEIGHT + nb);
+  const int rows = (end - first) * grp, mt = ja.geo.mt, nt = (rows + mt - 1) / mt, nb = (pre + ja.geo.bk - 1) / ja.geo.bk;
+  const int kv = h / grp, i = (b - first) * grp + (h - kv * grp), tile = i / mt;
+  const bool pair = mt == 256;
+  const int big = pair ? 2 : 1, cost = pair ? block_cost<256>(rows, tile) : 1;  // numbers of a block, in full tiles and in this one
+  const bool halves = cost < big;                                               // even and odd blocks have states of their own
+  const int numbers = pair ? head_numbers<256>(rows, nt, nb) : head_numbers<128>(rows, nt, nb);
+  const int v = a.at[lo] + kv * numbers + tile * (SH_WEIGHT + big * nb);
   const Range r{head.each, head.rest, 0, 0};
-  const int c0 = cta_of(r, v + SH_WEIGHT), c1 = cta_of(r, v + SH_WEIGHT + nb - 1);
+  const int c0 = cta_of(r, v + SH_WEIGHT), c1 = cta_of(r, v + SH_WEIGHT + cost * (nb - 1));
   if (c0 == c1) {
-    if (part == 0) take(a.whole + (size_t)row * comb_stride(p.hd), p.hd);
+    if (part == 0) {
+      take(a.whole + (size_t)row * comb_stride(p.hd), p.hd);
+      if (halves) take(a.whole + ((size_t)p.n_seqs * p.nq + row) * comb_stride(p.hd), p.hd);
+    }
     return true;
   }
 #pragma unroll 4
   for (int c = c0 + part; c <= c1; c += WPR) {
     const int slot = 2 * c + (c == c0 && cut(r, c) < v ? 1 : 0);
-    take(a.parts + ((size_t)slot * ja.geo.mt + (i - tile * ja.geo.mt)) * comb_stride(ja.geo.hd), ja.geo.hd);
+    const float* s = a.parts + ((size_t)slot * mt + (i - tile * mt)) * comb_stride(ja.geo.hd);
+    take(s, ja.geo.hd);
+    if (halves) take(s + (size_t)(mt / 2) * comb_stride(ja.geo.hd), ja.geo.hd);
   }
   return true;
 }
@@ -175,10 +185,10 @@ Layout layout(int n_seqs, int n_heads, int n_kv_heads, int head_dim) {
   y.own = y.at + up256((size_t)n_seqs * sizeof(int));
   const size_t states = up256((size_t)n_seqs * n_heads * comb_stride(head_dim) * sizeof(float));
   y.whole = y.own + states;
-  y.parts = y.whole + states;
+  y.parts = y.whole + 2 * states;
   size_t most = 0;
-  for (int type : {(int)QW_F32, (int)QW_F16}) {  // of both kernels that the shape may take
-    const Geometry g = geometry(type, head_dim, SH_MAX_CTAS);
+  for (int io : {(int)QW_F32, (int)QW_F16}) {  // of the kernels that the shape may take: io is the cache's type or fp32
+    const Geometry g = geometry(io == QW_F32 ? QW_F32 : QW_F16, io, head_dim, SH_MAX_CTAS);
     most = std::max(most, (size_t)2 * g.ctas * g.mt * comb_stride(g.hd) * sizeof(float));
   }
   y.bytes = y.parts + most;
@@ -211,9 +221,9 @@ qw_status qw_op_shared_attention(const qw_paged_kv* cache, int32_t n_seqs, int32
   if (n_groups < 0 || n_groups > n_seqs) return op_fail(QW_ERR_INVALID_ARG, "n_groups must be at most n_seqs");
   if (n_seqs == 0) return QW_OK;
   if (n_groups == 0) return op_fail(QW_ERR_INVALID_ARG, "sequences without a group");
-  const Geometry least = geometry(c.dtype, c.head_dim, 1);
+  const Geometry least = geometry(c.dtype, io_dtype, c.head_dim, 1);
   const int64_t tiles = ((int64_t)n_seqs * (n_heads / c.n_kv_heads) + least.mt - 1) / least.mt + n_groups;
-  if (tiles * c.n_kv_heads * ((int64_t)max_blocks * c.page_size / least.bk + 1 + SH_WEIGHT) > 0x7fffffffll)
+  if (tiles * c.n_kv_heads * (2 * ((int64_t)max_blocks * c.page_size / least.bk + 1) + SH_WEIGHT) > 0x7fffffffll)
     return op_fail(QW_ERR_UNSUPPORTED, "n_seqs * n_heads * max_blocks * page_size too large");
   if (!block_table || !lens || !cu_seqs || !shared_lens || !workspace || !err_dev) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
   const int64_t width = (int64_t)n_heads * c.head_dim;
@@ -239,11 +249,12 @@ qw_status qw_op_shared_attention(const qw_paged_kv* cache, int32_t n_seqs, int32
   ja.s.at = (int*)(ws + y.at);
   ja.s.whole = (float*)(ws + y.whole);
   ja.s.parts = (float*)(ws + y.parts);
-  ja.geo = geometry(c.dtype, c.head_dim, nsm);
+  ja.geo = geometry(c.dtype, io_dtype, c.head_dim, nsm);
   cudaStream_t s = (cudaStream_t)cuda_stream;
   if ((e = paged::launch_paged(c.dtype, io_dtype, nsm, ja.s.p, s))) return op_cuda_fail(e, "shared attention launch");
-  e = c.dtype != QW_F32 && c.head_dim <= 128 ? launch_shared_tc(c.dtype, io_dtype, ja.geo.ctas, ja.s, s)
-                                             : launch_shared_simt(c.dtype, io_dtype, ja.geo.ctas, ja.s, s);
+  e = c.dtype == QW_F32 || c.head_dim > 128 ? launch_shared_simt(c.dtype, io_dtype, ja.geo.ctas, ja.s, s)
+      : io_dtype == QW_F32                  ? launch_shared_tc(c, ja.geo.ctas, ja.s, s)
+                                            : launch_shared_pair(c, ja.geo.ctas, ja.s, s);
   if (e) return op_cuda_fail(e, "shared attention launch");
   e = io_dtype == QW_F32 ? launch_join<float>(ja, nsm, s) : io_dtype == QW_F16 ? launch_join<f16>(ja, nsm, s) : launch_join<bf16>(ja, nsm, s);
   if (e) return op_cuda_fail(e, "shared attention launch");

@@ -26,16 +26,24 @@ struct SharedArgs {
   const int* cu;
   SharedHead* head;
   int* at;       // [n_groups] where the list has the group
-  float* whole;  // [n_seqs][nq][comb_stride(hd)] states of units that one CTA covers
+  float* whole;  // [2][n_seqs][nq][comb_stride(hd)] states of units that one CTA covers, see state_of
   float* parts;  // [2 * CTAs][rows of a tile][comb_stride(HD)] of the others
 };
 
 // A unit is a tile of MT rows (sequence, head of the KV head) of one group and KV head, over the group's shared positions in
-// blocks of BK. Neighbouring units read the same keys and values.
+// blocks of BK. Neighbouring units read the same keys and values. A block counts as many numbers of the list as the unit has
+// halves of MT rows where the kernel takes 256 rows (their products are what bounds it), else one.
 struct Unit {
   int g, lo, rows, nt, pre, nb;  // the group: first sequence, rows of a KV head, their tiles, shared positions, their blocks
-  int u, t, v;                   // unit kv * nt + tile of the group, block, where the list has the unit
+  int u, t, v, c;                // unit kv * nt + tile of the group, block, where the list has the unit, numbers a block
 };
+template <int MT>
+__host__ __device__ __forceinline__ int block_cost(int rows, int tile) { return MT == 256 && rows - tile * MT > MT / 2 ? 2 : 1; }
+// numbers of one KV head's units
+template <int MT>
+__host__ __device__ __forceinline__ int head_numbers(int rows, int nt, int nb) {
+  return nt * SH_WEIGHT + ((nt - 1) * block_cost<MT>(MT, 0) + block_cost<MT>(rows, nt - 1)) * nb;
+}
 
 // The group g; its numbers in the list, 0 if it has nothing to do. bad: its bounds or its length are out of range.
 template <int MT, int BK>
@@ -52,16 +60,20 @@ __device__ __forceinline__ int load_group(const SharedArgs& a, int g, Unit& p, b
   p.nt = (p.rows + MT - 1) / MT;
   p.pre = pre;
   p.nb = (pre + BK - 1) / BK;
-  return p.nb ? a.p.nkv * p.nt * (SH_WEIGHT + p.nb) : 0;
+  p.c = block_cost<MT>(p.rows, 0);
+  return p.nb ? a.p.nkv * head_numbers<MT>(p.rows, p.nt, p.nb) : 0;
 }
 
 // The next unit; false behind the list's end `end`.
 template <int MT, int BK>
 __device__ __forceinline__ bool next_unit(const SharedArgs& a, int end, Unit& p) {
   p.t = 0;
-  p.v += SH_WEIGHT + p.nb;
+  p.v += SH_WEIGHT + p.c * p.nb;
   if (p.v >= end) return false;
-  if (++p.u < a.p.nkv * p.nt) return true;
+  if (++p.u < a.p.nkv * p.nt) {
+    p.c = block_cost<MT>(p.rows, p.u % p.nt);
+    return true;
+  }
   p.u = 0;
   bool bad;
   int g = p.g;
@@ -69,8 +81,12 @@ __device__ __forceinline__ bool next_unit(const SharedArgs& a, int end, Unit& p)
   return true;
 }
 
+// the unit's blocks from p.t on that lie before the list's end `end`
+__device__ __forceinline__ int blocks_of(const Unit& p, int end) { return min(p.nb, (end - p.v - SH_WEIGHT + p.c - 1) / p.c) - p.t; }
+
 // The CTA's range of the list and its first unit; CTA 0 leaves the cuts and the groups' places for the join. A cut that
-// falls on a unit's weight moves to the unit's beginning. scratch: shared memory, free again when the call returns.
+// falls on a unit's weight moves to the unit's beginning, one inside a block to the next block. scratch: shared memory, free
+// again when the call returns.
 constexpr int SH_SCRATCH = 256;
 template <int MT, int BK, int NT>
 __device__ __forceinline__ Range find_groups(const SharedArgs& a, Unit& first, void* scratch) {
@@ -125,10 +141,12 @@ __device__ __forceinline__ Range find_groups(const SharedArgs& a, Unit& first, v
         for (int k = 0; k < 2; ++k) {
           const int x = cut(r, c + k);
           if (x < at || x >= at + n) continue;
-          const int unit = SH_WEIGHT + p.nb;
-          p.u = (x - at) / unit;
-          p.v = at + p.u * unit;
-          p.t = max(0, x - p.v - SH_WEIGHT);
+          const int per_head = n / a.p.nkv, kv = (x - at) / per_head, big = SH_WEIGHT + block_cost<MT>(MT, 0) * p.nb;
+          const int in = x - at - kv * per_head, tile = min(in / big, p.nt - 1);
+          p.u = kv * p.nt + tile;
+          p.v = at + kv * per_head + tile * big;
+          p.c = block_cost<MT>(p.rows, tile);
+          p.t = (max(0, x - p.v - SH_WEIGHT) + p.c - 1) / p.c;
           s_at[k] = p;
         }
       at += n;
@@ -137,8 +155,10 @@ __device__ __forceinline__ Range find_groups(const SharedArgs& a, Unit& first, v
   __syncthreads();
   if (c < ctas) {
     first = s_at[0];
-    r.begin = first.v + (first.t ? SH_WEIGHT + first.t : 0);
-    r.end = c + 1 == ctas ? total : s_at[1].v + (s_at[1].t ? SH_WEIGHT + s_at[1].t : 0);
+    auto place = [](const Unit& x) { return x.v + (x.t ? SH_WEIGHT + x.c * x.t : 0); };
+    r.begin = place(first);
+    r.end = c + 1 == ctas ? total : place(s_at[1]);
+    if (first.t == first.nb) next_unit<MT, BK>(a, r.end, first);
   }
   __syncthreads();
   return r;
@@ -160,11 +180,12 @@ __device__ __forceinline__ Row row_of(const SharedArgs& a, const Unit& p, int kv
   return r;
 }
 
-// Where a row's state goes: part slots are 2 c for the unit that CTA c begins with, 2 c + 1 for one that it begins
-// later and does not finish.
+// Where a row's state goes, i its number in the tile: part slots are 2 c for the unit that CTA c begins with, 2 c + 1 for
+// one that it begins later and does not finish. second: the state of the odd blocks, where a tile's halves take the even and
+// the odd blocks of the same rows (i is then of the upper half, too).
 template <int MT, int HD>
-__device__ __forceinline__ float* state_of(const SharedArgs& a, const Range& r, const Unit& p, bool whole, const Row& row, int i) {
-  if (whole) return a.whole + ((size_t)row.b * a.p.nq + row.h) * comb_stride(a.p.hd);
+__device__ __forceinline__ float* state_of(const SharedArgs& a, const Range& r, const Unit& p, bool whole, const Row& row, int i, bool second = false) {
+  if (whole) return a.whole + ((size_t)((second ? a.p.n_seqs : 0) + row.b) * a.p.nq + row.h) * comb_stride(a.p.hd);
   const int slot = 2 * blockIdx.x + (cut(r, blockIdx.x) < p.v ? 1 : 0);
   return a.parts + ((size_t)slot * MT + i) * comb_stride(HD);
 }
@@ -185,14 +206,16 @@ __device__ __forceinline__ long long position_of(const SharedArgs& a, const Unit
 struct Geometry {
   int mt, bk, hd, ctas;
 };
-inline Geometry geometry(int cache_dtype, int hd, int nsm) {
+inline Geometry geometry(int cache_dtype, int io_dtype, int hd, int nsm) {
   const int n = nsm < SH_MAX_CTAS ? nsm : SH_MAX_CTAS;
-  if (cache_dtype != QW_F32 && hd <= 128) return Geometry{128, 128, hd <= 64 ? 64 : 128, n};
+  if (cache_dtype != QW_F32 && hd <= 128) return Geometry{io_dtype == QW_F32 ? 128 : 256, 128, hd <= 64 ? 64 : 128, n};
   return Geometry{64, 64, hd <= 64 ? 64 : hd <= 128 ? 128 : 256, hd <= 128 ? 2 * n : n};
 }
 
-// attn_shared_tc.cu: 16-bit caches, heads of at most 128 dimensions; attn_shared_simt.cu: the others
-cudaError_t launch_shared_tc(int cache_dtype, int io_dtype, int ctas, const SharedArgs& a, cudaStream_t s);
+// 16-bit caches, heads of at most 128 dimensions: attn_shared_tc.cu for fp32 callers, attn_shared_pair.cu for 16-bit ones;
+// attn_shared_simt.cu: the others
+cudaError_t launch_shared_tc(const qw_paged_kv& cache, int ctas, const SharedArgs& a, cudaStream_t s);
+cudaError_t launch_shared_pair(const qw_paged_kv& cache, int ctas, const SharedArgs& a, cudaStream_t s);
 cudaError_t launch_shared_simt(int cache_dtype, int io_dtype, int ctas, const SharedArgs& a, cudaStream_t s);
 
 }  // namespace shared_attn

@@ -1,0 +1,334 @@
+// The shared positions of attn_shared.cu on the 5th-generation tensor cores (tcgen05, TMEM) for 16-bit callers, heads of at
+// most 128 dimensions.
+//
+// Two chains of products run side by side, so that one's products fill the time of the other's softmax: S = Q K^T (128 rows x
+// 128 positions), P = 2^(S - m) written over it, O += P V, all in TMEM. A unit of more than 128 rows has its first 128 in
+// chain A and the others in chain B, over the same blocks of keys and values; one of fewer rows has its even blocks in A and
+// its odd ones in B, with a state each.
+//   warps 0 .. 3     producers (attn_shared_tc.cuh)
+//   warp 12          issues the products: S_A, S_B, then in turn PV_A, the next S_A, PV_B, the next S_B
+//   warps 4 .. 7     softmax of chain A, 8 .. 11 of chain B: one row a lane, its 128 scores in registers
+// O stays in TMEM. Its reference m moves only when a row's maximum exceeds it by more than 2^5; then the warp rescales its
+// rows of O, which is safe: S of a block is issued after the chain's last P V, so that is done when S arrives. P is at most
+// 2^15 then, in fp16's range, and keeps its digits down to 2^-24 of the row's largest (PA_BIAS).
+//
+// Precision: probabilities are rounded once to the cache's type, whose bits the output has too; their sum l takes them before
+// that. The tensor cores' additions cut: over 1000 products of 16 positions about 1e-5 of the norm, next to the output's
+// 2^-9 or 2^-12.
+// What bounds it: the products of many rows; HBM and L2 for few.
+//
+// Every wait is bounded: on expiry ERR_TIMEOUT is set, the CTA stops issuing work, waits (bounded) for what it issued, and
+// releases its TMEM.
+#include <math.h>
+
+#include "attn_shared_tc.cuh"
+
+namespace qw {
+namespace shared_attn {
+namespace {
+
+using paged::Pair;
+
+constexpr int MT = 256, BK = TC_BK, THREADS = 512, MMA_WARP = 12;
+constexpr float MOVE_AT = 5.f;  // base-2 growth of a row's maximum that moves its reference
+
+template <int HD>
+struct Cfg {
+  static constexpr int TILE = BK * HD * 2;            // bytes of a tile; HD / 64 boxes [128 rows][64 columns]
+  static constexpr int Q_BYTES = 2 * 128 * HD * 2;    // of both halves
+  // q_full, s_full[2], p_full[2], o_full[2], done, free, full[8], empty[8]
+  static constexpr int NBAR = 10;                     // (one spare: the masks behind are read 16 bytes at a time)
+  static constexpr int SMALL = (NBAR + 2 * 8) * 8 + 16 + TC_MASKS * 16;
+  static constexpr int NS_FIT = (232448 - Q_BYTES - SMALL) / TILE, NS = NS_FIT > 8 ? 8 : NS_FIT;
+  static constexpr int OFF_RING = Q_BYTES, OFF_SMALL = OFF_RING + NS * TILE, SMEM = OFF_SMALL + SMALL;
+  static constexpr int O_COL = 256;                   // TMEM columns: S of both chains (P over them), then O of both
+  static_assert(NS >= 4, "ring");
+  static_assert((OFF_SMALL + (NBAR + 16) * 8 + 16) % 16 == 0, "masks");
+};
+
+// The tiles of a unit of nb blocks in the ring's order K_0, K_1, V_0, K_2, V_1, ..., V_{nb-1}
+__device__ __forceinline__ int k_tile(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int v_tile(int j, int nb) { return j + 1 < nb ? 2 * j + 2 : 2 * nb - 1; }
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_constant__ PageMaps maps, const SharedArgs a) {
+  using C = Cfg<HD>;
+  constexpr int NS = C::NS;
+  constexpr bool BF = std::is_same<T, bf16>::value;
+  extern __shared__ __align__(1024) unsigned char sh_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  const uint32_t base = smem_addr(sh_smem);
+  uint64_t* bars = (uint64_t*)(sh_smem + C::OFF_SMALL);
+  const uint32_t q_full = smem_addr(bars), s_full0 = q_full + 8, p_full0 = q_full + 24, o_full0 = q_full + 40, done = q_full + 56,
+                 idle = q_full + 64, full0 = q_full + 72, empty0 = full0 + 64;
+  uint32_t* tmem_slot = (uint32_t*)(bars + C::NBAR + 16);
+  volatile int* s_abort = (volatile int*)(tmem_slot + 1);
+  uint32_t* masks = tmem_slot + 4;  // [block % TC_MASKS][4] positions that exist
+  if (base & 1023) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicOr(a.p.err, ERR_LAYOUT);
+    pdl_wait();
+    return;
+  }
+  Unit p;
+  const Range r = find_groups<MT, BK, THREADS>(a, p, sh_smem);
+  if (r.begin >= r.end) {
+    pdl_wait();  // (this grid ends after the one before it)
+    return;
+  }
+  if (threadIdx.x == 0) {
+    *s_abort = 0;
+    mbar_init(q_full, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full0 + 8 * i, 1);
+      mbar_init(p_full0 + 8 * i, 4);
+      mbar_init(o_full0 + 8 * i, 1);
+    }
+    mbar_init(done, 1);
+    mbar_init(idle, 8);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full0 + 8 * i, TC_PRODUCERS);
+      mbar_init(empty0 + 8 * i, 1);
+    }
+    mbar_fence_init();
+  }
+  if (warp == MMA_WARP) tc::tmem_alloc(smem_addr(tmem_slot), 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int* err = a.p.err;
+
+  if (warp < TC_PRODUCERS) {
+    setmaxnreg_dec<72>();
+    produce<T, MT, HD, NS>(a, maps, r, p, base + C::OFF_RING, full0, empty0, masks, s_abort);
+  } else if (warp >= 12) {
+    setmaxnreg_dec<56>();
+    if (warp == MMA_WARP && lane == 0) {
+      // ---- issues the products
+      constexpr uint32_t kind = BF ? 1u << 7 | 1u << 10 : 0u;
+      constexpr uint32_t idS = tc::idesc_f16(128, BK) | kind, idO = tc::idesc_f16_bmn(128, HD) | kind;
+      int tile0 = 0, units = 0, steps[2] = {0, 0};  // tiles before the unit, units, steps of each chain so far
+      bool ok = true;
+      do {
+        const int nb = blocks_of(p, r.end);
+        const bool two = p.c == 2;  // both halves have rows
+        if (!(ok = tc::mbar_wait(q_full, units & 1, err))) break;
+        ++units;
+        auto landed = [&](int i, uint32_t& addr) {  // tile i of the unit
+          const int n = tile0 + i, s = n % NS;
+          addr = base + C::OFF_RING + s * C::TILE;
+          return tc::mbar_wait(full0 + 8 * s, n / NS & 1, err);
+        };
+        auto release = [&](int i) { tc::mma_commit(empty0 + 8 * ((tile0 + i) % NS)); };
+        const int n_of[2] = {two ? nb : (nb + 1) / 2, two ? nb : nb / 2};
+        auto block_of = [&](int c, int i) { return two ? i : 2 * i + c; };
+        auto issue_s = [&](int c, int i) {
+          const int j = block_of(c, i);
+          uint32_t k;
+          if (!landed(k_tile(j), k)) return false;
+          tc::tc_fence_after();
+          const uint32_t q = base + (two ? c * 128 * HD * 2 : 0);
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            tc::mma_f16(tmem + c * 128, tc::smem_desc_sw128(q + (kk >> 2) * 128 * 128 + (kk & 3) * 32),
+                        tc::smem_desc_sw128(k + (kk >> 2) * BK * 128 + (kk & 3) * 32), idS, kk > 0);
+          tc::mma_commit(s_full0 + 8 * c);
+          if (!two || c == 1) release(k_tile(j));
+          return true;
+        };
+        ok = issue_s(0, 0) && (n_of[1] == 0 || issue_s(1, 0));
+        for (int i = 0; i < n_of[0] && ok; ++i)
+          for (int c = 0; c < 2 && ok; ++c) {
+            if (i >= n_of[c]) break;
+            if (*s_abort || !tc::mbar_wait(p_full0 + 8 * c, steps[c] & 1, err)) {
+              ok = false;
+              break;
+            }
+            ++steps[c];
+            const int j = block_of(c, i);
+            uint32_t v;
+            if (!(ok = landed(v_tile(j, nb), v))) break;
+            tc::tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk)
+              tc::mma_f16_tmem_a(tmem + C::O_COL + c * 128, tmem + c * 128 + kk * 8, tc::smem_desc_sw128_mn(v + kk * 2048, BK * 128, 1024), idO,
+                                 i > 0 || kk > 0);
+            if (i + 1 == n_of[c]) tc::mma_commit(o_full0 + 8 * c);
+            if (!two || c == 1) release(v_tile(j, nb));
+            if (i + 1 < n_of[c]) ok = issue_s(c, i + 1);
+          }
+        tile0 += 2 * nb;
+      } while (ok && next_unit<MT, BK>(a, r.end, p));
+      if (!ok) *s_abort = 1;
+      tc::mma_commit(done);  // arrives once all products issued above are done
+      tc::mbar_wait(done, 0, err);
+    }
+  } else {
+    setmaxnreg_inc<192>();
+    // ---- softmax: chain c, row `row` of its 128
+    const int c = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), s_at = lanes + c * 128, o_at = lanes + C::O_COL + c * 128;
+    const float sc = fmaxf(fabsf(a.p.scale) * paged::LOG2E, 1e-38f);  // (not 0: masked scores stay -inf)
+    const float sign = a.p.scale > 0.f ? 1.f : a.p.scale < 0.f ? -1.f : 0.f;
+    int block0 = 0, units = 0, steps = 0, segments = 0;
+    bool ok = true;
+    do {
+      const int kv = p.u / p.nt, tile = p.u - kv * p.nt, nb = blocks_of(p, r.end);
+      const bool two = p.c == 2;
+      if (units > 0 && !tc::mbar_wait(idle, (units - 1) & 1, err)) ok = false;  // (all products of the last unit are done)
+      {  // the unit's queries; zeros for rows that take no part
+        constexpr int DL = HD / 32;  // dimensions of a lane
+        const int d0 = lane * DL, rows_w = two ? 32 : 16;
+        const uint32_t at = base + (d0 >> 6) * (128 * 128) + (d0 & 7) * 2;
+#pragma unroll 4
+        for (int i = 0; i < rows_w; ++i) {
+          const int rr = (warp - 4) * rows_w + i;
+          const Row row_i = row_of(a, p, kv, tile * MT + rr);
+          uint32_t w[DL / 2];
+#pragma unroll
+          for (int d = 0; d < DL / 2; ++d) w[d] = 0u;
+          if (row_i.in && d0 < a.p.hd) {
+            const T* q = (const T*)a.p.q + row_i.b * a.p.q_stride + row_i.h * a.p.hd + d0;
+#pragma unroll
+            for (int d = 0; d < DL / 2; ++d) {
+              const float2 two_d = paged::load2(q + 2 * d);
+              w[d] = Pair<T>::pack(two_d.x * sign, two_d.y * sign);
+            }
+          }
+          const uint32_t dst = at + (rr >> 7) * (128 * HD * 2) + (rr & 127) * 128 + ((((d0 >> 3) & 7) ^ (rr & 7)) << 4);
+          if constexpr (DL == 4)
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[0]), "r"(w[1]) : "memory");
+          else
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w[0]) : "memory");
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      float m = -INFINITY, l = 0.f;
+      bool any = false;
+      const int n = two ? nb : c == 0 ? (nb + 1) / 2 : nb / 2;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        if (*s_abort || !tc::mbar_wait(s_full0 + 8 * c, steps & 1, err)) ok = false;
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        ++steps;
+        tc::tc_fence_after();
+        uint32_t u[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tc::tmem_ld32_nowait(s_at + 32 * q, u + 32 * q);
+        tc::tmem_wait_ld();
+        const uint4 mask = *reinterpret_cast<const uint4*>(masks + ((block0 + (two ? i : 2 * i + c)) % TC_MASKS) * 4);
+        any |= (mask.x | mask.y | mask.z | mask.w) != 0u;
+        if ((mask.x & mask.y & mask.z & mask.w) != 0xffffffffu) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            if (!(mask.x >> q & 1)) u[q] = 0xff800000u;
+            if (!(mask.y >> q & 1)) u[32 + q] = 0xff800000u;
+            if (!(mask.z >> q & 1)) u[64 + q] = 0xff800000u;
+            if (!(mask.w >> q & 1)) u[96 + q] = 0xff800000u;
+          }
+        }
+        float top[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) top[q] = __uint_as_float(u[q]);
+#pragma unroll
+        for (int q = 4; q < 128; ++q) top[q & 3] = fmaxf(top[q & 3], __uint_as_float(u[q]));
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+        const bool move = mx > m + MOVE_AT || (m == -INFINITY && mx > m);
+        if (__any_sync(0xffffffffu, move)) {
+          const float f = move ? ex2(m - mx) : 1.f;  // (0 where m is -inf)
+          if (i > 0) {
+#pragma unroll 1
+            for (int d = 0; d < HD; d += 32) {
+              uint32_t o[32];
+              tc::tmem_ld32_nowait(o_at + d, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+              tc::tmem_st32(o_at + d, o);
+            }
+          }
+          if (move) {
+            l *= f;
+            m = mx;
+          }
+        }
+        const float ref = (m == -INFINITY ? 0.f : m) - PA_BIAS;
+        const f32x2 c2 = pack2(sc, sc), r2 = pack2(-ref, -ref);
+        f32x2 acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int q0 = 0; q0 < 64; q0 += 16) {
+          uint32_t pp[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const float2 e = unpack2(fma2_to(pack2(__uint_as_float(u[2 * (q0 + q)]), __uint_as_float(u[2 * (q0 + q) + 1])), c2, r2));
+            const float p0 = ex2(e.x), p1 = ex2(e.y);
+            acc[q & 3] = add2(acc[q & 3], pack2(p0, p1));
+            pp[q] = Pair<T>::pack(p0, p1);
+          }
+          tmem_st16(s_at + q0, pp);
+        }
+        const float2 s0 = unpack2(add2(acc[0], acc[1])), s1 = unpack2(add2(acc[2], acc[3]));
+        l += (s0.x + s0.y) + (s1.x + s1.y);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full0 + 8 * c);
+      }
+      if (ok && n > 0 && !tc::mbar_wait(o_full0 + 8 * c, segments & 1, err)) ok = false;
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (n > 0) ++segments;
+      tc::tc_fence_after();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(idle);
+      block0 += nb;
+      ++units;
+      const int i = two ? c * 128 + row : row;  // of the tile
+      const Row mine = row_of(a, p, kv, tile * MT + i);
+      const bool whole = nb == p.nb;
+      float* dst = mine.in ? state_of<MT, HD>(a, r, p, whole, mine, c * 128 + row, !two && c) : nullptr;
+      const int width = whole ? a.p.hd : HD;
+      if (n > 0) {
+#pragma unroll 1
+        for (int d = 0; d < HD; d += 32) {
+          float o[32];
+          tc::tmem_ld32(o_at + d, o);
+          if (dst)
+#pragma unroll
+            for (int q = 0; q < 32; q += 4)
+              if (d + q < width) *reinterpret_cast<float4*>(dst + d + q) = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+        }
+      }
+      tc::tc_fence_before();
+      if (dst) *reinterpret_cast<float2*>(dst + width) = make_float2(paged::state_max(m, any), l);
+    } while (next_unit<MT, BK>(a, r.end, p));
+    if (!ok) *s_abort = 1;
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+  pdl_wait();  // (this grid ends after the one before it)
+}
+
+template <typename T, int HD>
+cudaError_t run(int ctas, const PageMaps& m, const SharedArgs& a, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(shared_pair_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::SMEM);
+  return e ? e : launch_k(shared_pair_kernel<T, HD>, dim3(ctas), dim3(THREADS), Cfg<HD>::SMEM, s, true, m, a);
+}
+
+}  // namespace
+
+cudaError_t launch_shared_pair(const qw_paged_kv& cache, int ctas, const SharedArgs& a, cudaStream_t s) {
+  PageMaps m{};
+  make_page_maps(cache, m);
+  if (cache.dtype == QW_F16) return a.p.hd <= 64 ? run<f16, 64>(ctas, m, a, s) : run<f16, 128>(ctas, m, a, s);
+  return a.p.hd <= 64 ? run<bf16, 64>(ctas, m, a, s) : run<bf16, 128>(ctas, m, a, s);
+}
+
+}  // namespace shared_attn
+}  // namespace qw

@@ -1,11 +1,8 @@
-// The shared positions of attn_shared.cu on the 5th-generation tensor cores (tcgen05, TMEM): 16-bit caches, heads of at most
-// 128 dimensions.
+// The shared positions of attn_shared.cu on the 5th-generation tensor cores (tcgen05, TMEM) for fp32 callers over 16-bit caches,
+// heads of at most 128 dimensions.
 //
 // A unit is 128 rows (sequence, head) of one group and KV head. Blocks of 128 positions stream past them:
-//   warps 0 .. 3    producers: a warp copies 32 positions' keys or values (cp.async, 16 bytes a lane, pages looked up by
-//                   the lane that owns the position) into a ring of tiles, swizzled as the tensor cores read them. Pages of any
-//                   size and stride serve, which a tensor map's boxes do not. The order is the one in which the tiles are
-//                   consumed: K_0, K_1, V_0, K_2, V_1, ...
+//   warps 0 .. 3    producers (attn_shared_tc.cuh): tiles of keys and values in the order in which they are consumed.
 //   warp 12         issues the products: S_j = Q K_j^T into buffer j % 2, a block ahead, and O_j = P_j V_j with P_j from TMEM.
 //   warps 4 .. 11   softmax. Warps w and w + 4 share TMEM lanes, one row a lane: the first takes positions 0 .. 63 of every
 //                   block, the other 64 .. 127, and they trade maxima through shared memory. They write P_j over S_j, and
@@ -13,16 +10,14 @@
 //                   cores' additions cut: over thousands of positions 1e-6 of the norm) and needs no rescaling in TMEM.
 // The warps meet at a unit's ends only: there the softmax warps put the rows' queries into shared memory.
 //
-// Precision: fp32 callers' queries and probabilities are sums of pieces of the cache's type, two of fp16 (22 bits of the row's
-// largest element), three of bf16. A 16-bit caller's probabilities are rounded once to its own type, whose bits the
-// output has too; their sum l takes them before that. Exponentials are ex2's, good to 2^-22.
+// Precision: queries and probabilities are sums of pieces of the cache's type, two of fp16 (22 bits of the row's largest
+// element), three of bf16, whose products are added up lowest piece first. Exponentials are ex2's, good to 2^-22.
 //
 // Every wait is bounded: on expiry ERR_TIMEOUT is set, the CTA stops issuing work, waits (bounded) for what it issued, and
 // releases its TMEM.
 #include <math.h>
 
-#include "attn_shared.cuh"
-#include "tc_common.cuh"
+#include "attn_shared_tc.cuh"
 
 namespace qw {
 namespace shared_attn {
@@ -31,43 +26,28 @@ namespace {
 using paged::Pair;
 using paged::split;
 
-constexpr int MT = 128, BK = 128, THREADS = 512, PRODUCERS = 4, MMA_WARP = 12, MASKS = 16;
+constexpr int MT = 128, BK = TC_BK, THREADS = 512, MMA_WARP = 12;
 
-template <typename T, int HD, typename IO>
+template <typename T, int HD>
 struct Cfg {
-  static constexpr bool F32IO = std::is_same<IO, float>::value, BF = std::is_same<T, bf16>::value, three = F32IO && BF;
-  static constexpr int NQ = !F32IO ? 1 : three ? 3 : 2, NP = NQ;  // pieces of queries and probabilities
+  static constexpr bool BF = std::is_same<T, bf16>::value, three = BF;
+  static constexpr int NQ = three ? 3 : 2, NP = NQ;  // pieces of queries and probabilities
   static constexpr int TILE = BK * HD * 2;                        // bytes of a tile; HD / 64 boxes [128 rows][64 columns]
   static constexpr int Q_BYTES = NQ * MT * HD * 2;
   // q_full, s_full[2], p_full[2], o_full[2], done, pair[4], full[NS], empty[NS]
   static constexpr int NBAR = 12;
-  static constexpr int SMALL = (NBAR + 2 * 8) * 8 + 16 + MT * 4 + 2 * 2 * MT * 4 + MASKS * 16;
+  static constexpr int SMALL = (NBAR + 2 * 8) * 8 + 16 + MT * 4 + 2 * 2 * MT * 4 + TC_MASKS * 16;
   static constexpr int NS_FIT = (232448 - Q_BYTES - SMALL) / TILE, NS = NS_FIT > 8 ? 8 : NS_FIT;
   static constexpr int OFF_RING = Q_BYTES, OFF_SMALL = OFF_RING + NS * TILE, SMEM = OFF_SMALL + SMALL;
-  static constexpr int AHEAD = NS - 1 < 4 ? NS - 1 : 4;  // tiles in flight
   // TMEM columns: S buffers (P pieces 0 and 1 over them), third pieces, O
   static constexpr int P3 = 256, O_COL = three ? 384 : 256, NO = three ? 1 : 2;
   static_assert(NS >= 4, "ring");
   static_assert(O_COL + NO * 128 <= 512, "TMEM");
 };
 
-template <int N>
-__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-// 16 columns of this thread's TMEM lane, completed by tmem_wait_st
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-template <typename T, int HD, typename IO>
-__global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs a) {
-  using C = Cfg<T, HD, IO>;
+template <typename T, int HD>
+__global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_constant__ PageMaps maps, const SharedArgs a) {
+  using C = Cfg<T, HD>;
   constexpr int NS = C::NS, NQ = C::NQ, NP = C::NP;
   extern __shared__ __align__(1024) unsigned char sh_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -80,7 +60,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs 
   volatile int* s_abort = (volatile int*)(tmem_slot + 1);
   float* undo = (float*)(tmem_slot + 4);                    // [MT] of the queries' power of two
   float* xch = undo + MT;                                   // [block parity][half][row]
-  uint32_t* masks = (uint32_t*)(xch + 4 * MT);              // [block % MASKS][4] positions that exist
+  uint32_t* masks = (uint32_t*)(xch + 4 * MT);              // [block % TC_MASKS][4] positions that exist
   if (base & 1023) {  // the swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) atomicOr(a.p.err, ERR_LAYOUT);
     pdl_wait();
@@ -103,7 +83,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs 
     mbar_init(done, 1);
     for (int i = 0; i < 4; ++i) mbar_init(pair0 + 8 * i, 2);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full0 + 8 * i, PRODUCERS);
+      mbar_init(full0 + 8 * i, TC_PRODUCERS);
       mbar_init(empty0 + 8 * i, 1);
     }
     mbar_fence_init();
@@ -115,71 +95,11 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs 
   const uint32_t tmem = *tmem_slot;
   int* err = a.p.err;
 
-  if (warp < PRODUCERS) {
-    setmaxnreg_dec<56>();
-    // ---- producers
-    constexpr int CH = HD / 8, RP = 32 / CH;  // chunks of a row, rows a step
-    const int ch = lane % CH, r0 = lane / CH;
-    const bool col = ch * 8 < a.p.hd;
-    const char *kl = (const char*)a.p.k + ch * 16, *vl = (const char*)a.p.v + ch * 16;
-    int n = 0, told = 0, block = 0;  // tiles requested, tiles announced, blocks begun
-    bool ok = true;
-    auto announce = [&](int upto) {  // (their copies have landed)
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0)
-        for (int i = told; i < upto; ++i) mbar_arrive(full0 + 8 * (i % NS));
-      told = upto;
-    };
-    auto request = [&](const char* src, long long off, uint32_t mask) {
-      const int s = n % NS;
-      if (n >= NS) {
-        const uint32_t par = (n / NS & 1) ^ 1;
-        if (!mbar_test(empty0 + 8 * s, par)) {
-          paged::cp_wait<0>();
-          if (told < n) announce(n);
-          if (!tc::mbar_wait(empty0 + 8 * s, par, err)) *s_abort = 1;
-        }
-      }
-      if (*s_abort) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      const uint32_t dst = base + C::OFF_RING + s * C::TILE + (ch >> 3) * (BK * 128);
-      if (off < 0) off = 0;
-#pragma unroll
-      for (int i = 0; i < 32 / RP; ++i) {
-        const int row = i * RP + r0;
-        const long long o = __shfl_sync(0xffffffffu, off, row);
-        paged::cp_async16_or_zero(dst + (warp * 32 + row) * 128 + (((ch & 7) ^ (row & 7)) << 4), src + o, (mask >> row & 1) && col);
-      }
-      paged::cp_commit();
-      ++n;
-      if (n - told > C::AHEAD) {
-        paged::cp_wait<C::AHEAD>();
-        announce(n - C::AHEAD);
-      }
-    };
-    do {
-      const int kv = p.u / p.nt, t1 = min(p.nb, r.end - p.v - SH_WEIGHT);
-      long long v_off = 0;
-      uint32_t v_mask = 0;
-#pragma unroll 1
-      for (int t = p.t; t < t1 && ok; ++t) {
-        const long long off = position_of<T>(a, p, kv, t * BK + warp * 32 + lane);
-        const uint32_t mask = __ballot_sync(0xffffffffu, off >= 0);
-        if (lane == 0) masks[(block % MASKS) * 4 + warp] = mask;
-        ++block;
-        request(kl, off, mask);
-        if (t > p.t && ok) request(vl, v_off, v_mask);
-        v_off = off;
-        v_mask = mask;
-      }
-      if (ok) request(vl, v_off, v_mask);
-    } while (ok && next_unit<MT, BK>(a, r.end, p));
-    paged::cp_wait<0>();
-    if (told < n) announce(n);
+  if (warp < TC_PRODUCERS) {
+    setmaxnreg_dec<72>();
+    produce<T, MT, HD, NS>(a, maps, r, p, base + C::OFF_RING, full0, empty0, masks, s_abort);
   } else if (warp >= 12) {
-    setmaxnreg_dec<40>();
+    setmaxnreg_dec<56>();
     if (warp == MMA_WARP && lane == 0) {
       // ---- issues the products
       constexpr uint32_t kind = C::BF ? 1u << 7 | 1u << 10 : 0u;
@@ -187,7 +107,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs 
       int n = 0, block = 0, units = 0;  // tiles, blocks and units so far
       bool ok = true;
       do {
-        const int t1 = min(p.nb, r.end - p.v - SH_WEIGHT), nb = t1 - p.t;
+        const int nb = blocks_of(p, r.end);
         if (!(ok = tc::mbar_wait(q_full, units & 1, err))) break;
         ++units;
         auto tile = [&](uint32_t& addr) {
@@ -236,7 +156,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs 
       tc::mbar_wait(done, 0, err);
     }
   } else {
-    setmaxnreg_inc<208>();
+    setmaxnreg_inc<192>();
     // ---- softmax
     constexpr int OC = HD / 2;  // output columns of a thread
     const int quarter = warp & 3, half = (warp - 4) >> 2, row = quarter * 32 + lane;
@@ -254,7 +174,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs 
       return other;
     };
     do {
-      const int kv = p.u / p.nt, tile = p.u - kv * p.nt, t1 = min(p.nb, r.end - p.v - SH_WEIGHT), nb = t1 - p.t;
+      const int kv = p.u / p.nt, tile = p.u - kv * p.nt, nb = blocks_of(p, r.end);
       {  // the unit's queries, 16 rows a warp; zeros for rows that take no part
         constexpr int DL = HD / 32;  // dimensions of a lane
         const int d0 = lane * DL;
@@ -267,7 +187,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs 
 #pragma unroll
           for (int d = 0; d < DL; ++d) x[d] = 0.f;
           if (row_i.in && d0 < a.p.hd) {
-            const IO* q = (const IO*)a.p.q + row_i.b * a.p.q_stride + row_i.h * a.p.hd + d0;
+            const float* q = (const float*)a.p.q + row_i.b * a.p.q_stride + row_i.h * a.p.hd + d0;
 #pragma unroll
             for (int d = 0; d < DL; d += 2) {
               const float2 two = paged::load2(q + d);
@@ -276,7 +196,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs 
             }
           }
           float up = 1.f, down = 1.f;
-          if constexpr (C::F32IO) {
+          {
             // a power of two that keeps the pieces normal: fp16 pieces with the row's largest at 2^10, whatever its size; bf16
             // pieces, whose range is fp32's own, with only small ones raised to 2^-50. The scores undo it.
             float top = 0.f;
@@ -338,13 +258,13 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs 
         if (*s_abort || !tc::mbar_wait(s_full0 + 8 * b, block >> 1 & 1, err)) ok = false;
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc::tc_fence_after();
-        if (j == 0) c = fmaxf(C::F32IO ? sc * undo[row] : sc, 1e-38f);  // (not 0: masked scores stay -inf)
+        if (j == 0) c = fmaxf(sc * undo[row], 1e-38f);  // (not 0: masked scores stay -inf)
         uint32_t u[64];
         tc::tmem_ld32_nowait(lanes + b * 128 + 64 * half, u);
         tc::tmem_ld32_nowait(lanes + b * 128 + 64 * half + 32, u + 32);
         tc::tmem_wait_ld();
-        const uint2 mask = *reinterpret_cast<const uint2*>(masks + (block % MASKS) * 4 + 2 * half);
-        const uint32_t* all = masks + (block % MASKS) * 4;
+        const uint2 mask = *reinterpret_cast<const uint2*>(masks + (block % TC_MASKS) * 4 + 2 * half);
+        const uint32_t* all = masks + (block % TC_MASKS) * 4;
         any |= (all[0] | all[1] | all[2] | all[3]) != 0;
         if ((mask.x & mask.y) != 0xffffffffu) {
 #pragma unroll
@@ -418,21 +338,19 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const SharedArgs 
   pdl_wait();  // (this grid ends after the one before it)
 }
 
-template <typename T, int HD, typename IO>
-cudaError_t run(int ctas, const SharedArgs& a, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(shared_tc_kernel<T, HD, IO>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<T, HD, IO>::SMEM);
-  return e ? e : launch_k(shared_tc_kernel<T, HD, IO>, dim3(ctas), dim3(THREADS), Cfg<T, HD, IO>::SMEM, s, true, a);
-}
-template <typename T, typename IO>
-cudaError_t run(int ctas, const SharedArgs& a, cudaStream_t s) {
-  return a.p.hd <= 64 ? run<T, 64, IO>(ctas, a, s) : run<T, 128, IO>(ctas, a, s);
+template <typename T, int HD>
+cudaError_t run(int ctas, const PageMaps& m, const SharedArgs& a, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(shared_tc_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<T, HD>::SMEM);
+  return e ? e : launch_k(shared_tc_kernel<T, HD>, dim3(ctas), dim3(THREADS), Cfg<T, HD>::SMEM, s, true, m, a);
 }
 
 }  // namespace
 
-cudaError_t launch_shared_tc(int cache_dtype, int io_dtype, int ctas, const SharedArgs& a, cudaStream_t s) {
-  if (cache_dtype == QW_F16) return io_dtype == QW_F32 ? run<f16, float>(ctas, a, s) : run<f16, f16>(ctas, a, s);
-  return io_dtype == QW_F32 ? run<bf16, float>(ctas, a, s) : run<bf16, bf16>(ctas, a, s);
+cudaError_t launch_shared_tc(const qw_paged_kv& cache, int ctas, const SharedArgs& a, cudaStream_t s) {
+  PageMaps m{};
+  make_page_maps(cache, m);
+  if (cache.dtype == QW_F16) return a.p.hd <= 64 ? run<f16, 64>(ctas, m, a, s) : run<f16, 128>(ctas, m, a, s);
+  return a.p.hd <= 64 ? run<bf16, 64>(ctas, m, a, s) : run<bf16, 128>(ctas, m, a, s);
 }
 
 }  // namespace shared_attn

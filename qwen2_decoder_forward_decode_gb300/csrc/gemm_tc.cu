@@ -785,6 +785,24 @@ bool make_map_kv(void* mv, const void* base, int hd, int keys, int nkv, int cap,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The 16-bit elements of a paged cache, (dimension, position of the page, KV head, page), strides in elements along all but the
+// first; boxes of 64 dimensions x box_rows positions, 128B swizzle. What lies beyond head_dim reads as zeros.
+bool make_map_pages(void* mv, const void* base, const qw_paged_kv& c, int box_rows) {
+  CUtensorMap* m = reinterpret_cast<CUtensorMap*>(mv);
+  EncodeTiledFn f = encode_fn();
+  if (!f) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.n_kv_heads, (cuuint64_t)c.n_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)c.pos_stride * 2, (cuuint64_t)c.head_stride * 2, (cuuint64_t)c.page_stride * 2};
+  for (cuuint64_t& s : strides) {
+    if (s == 0) s = (cuuint64_t)c.head_dim * 2;  // (along an extent of 1)
+    if (s >> 40) return false;
+  }
+  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return f(m, c.dtype == QW_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base), dims,
+           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 constexpr int TC_BN = 256;
 

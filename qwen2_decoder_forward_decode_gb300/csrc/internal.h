@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/qw.h"
+
 namespace qw {
 
 // Device-side error bits (ERR_*) are defined in common.cuh.
@@ -122,6 +124,8 @@ bool make_map(void* map, const void* base, int rows, int cols, int ld, int box_r
 // Tensor map of one layer's fp16 K or V cache [nkv][cap][hd] over its first `keys` positions:
 // boxes of 64 head columns x box_keys positions of one KV head, 128-byte swizzle.
 bool make_map_kv(void* map, const void* base, int hd, int keys, int nkv, int cap, int box_keys);
+// The same for a paged cache (dimension, position, KV head, page), box 64 x box_rows; false where a tensor map cannot say it.
+bool make_map_pages(void* map, const void* base, const qw_paged_kv& c, int box_rows);
 cudaError_t gemm_tc_set_attributes();
 // whether the prefill's tensor-core path launches its kernels with programmatic dependent
 // launch (QW_PREFILL_PDL=0 turns it off)
