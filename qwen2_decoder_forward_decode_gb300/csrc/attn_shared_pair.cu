@@ -6,7 +6,11 @@
 // chain A and the others in chain B, over the same blocks of keys and values; one of fewer rows has its even blocks in A and
 // its odd ones in B, with a state each.
 //   warps 0 .. 3     producers (attn_shared_tc.cuh)
-//   warp 12          issues the products: S_A, S_B, then in turn PV_A, the next S_A, PV_B, the next S_B
+//   warps 12, 13     issue the products of a chain each: S, then in turn P V and the next S. A step's products take the tensor
+//                    cores' queue as a whole, so that the chains stay half a step apart; mixed, both wait for the
+//                    products at the same time and then for the softmax (4000 cycles a block of 256 rows). (One warp for both
+//                    chains is in their way, too: a step's waits and commits take it as long as the products themselves,
+//                    4200 cycles.)
 //   warps 4 .. 7     softmax of chain A, 8 .. 11 of chain B: one row a lane, its 128 scores in registers
 // O stays in TMEM. Its reference m moves only when a row's maximum exceeds it by more than 2^5; then the warp rescales its
 // rows of O, which is safe: S of a block is issued after the chain's last P V, so that is done when S arrives. P is at most
@@ -29,15 +33,15 @@ namespace {
 
 using paged::Pair;
 
-constexpr int MT = 256, BK = TC_BK, THREADS = 512, MMA_WARP = 12;
+constexpr int MT = 256, BK = TC_BK, THREADS = 512, MMA_WARP = 12, TMEM_WARP = 15;  // (a warp whose lanes never part allocates and frees TMEM)
 constexpr float MOVE_AT = 5.f;  // base-2 growth of a row's maximum that moves its reference
 
 template <int HD>
 struct Cfg {
   static constexpr int TILE = BK * HD * 2;            // bytes of a tile; HD / 64 boxes [128 rows][64 columns]
   static constexpr int Q_BYTES = 2 * 128 * HD * 2;    // of both halves
-  // q_full, s_full[2], p_full[2], o_full[2], done, free, full[8], empty[8]
-  static constexpr int NBAR = 10;                     // (one spare: the masks behind are read 16 bytes at a time)
+  // q_full, s_full[2], p_full[2], o_full[2], done[2], idle, full[8], empty[8]
+  static constexpr int NBAR = 10;                     // (with the ring's an even number: the masks behind are read 16 bytes at a time)
   static constexpr int SMALL = (NBAR + 2 * 8) * 8 + 16 + TC_MASKS * 16;
   static constexpr int NS_FIT = (232448 - Q_BYTES - SMALL) / TILE, NS = NS_FIT > 8 ? 8 : NS_FIT;
   static constexpr int OFF_RING = Q_BYTES, OFF_SMALL = OFF_RING + NS * TILE, SMEM = OFF_SMALL + SMALL;
@@ -61,9 +65,10 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
   const uint32_t base = smem_addr(sh_smem);
   uint64_t* bars = (uint64_t*)(sh_smem + C::OFF_SMALL);
   const uint32_t q_full = smem_addr(bars), s_full0 = q_full + 8, p_full0 = q_full + 24, o_full0 = q_full + 40, done = q_full + 56,
-                 idle = q_full + 64, full0 = q_full + 72, empty0 = full0 + 64;
+                 idle = q_full + 72, full0 = q_full + 80, empty0 = full0 + 64;
   uint32_t* tmem_slot = (uint32_t*)(bars + C::NBAR + 16);
   volatile int* s_abort = (volatile int*)(tmem_slot + 1);
+  volatile int* s_turn = (volatile int*)(tmem_slot + 2);  // 1: a chain's products are being issued
   uint32_t* masks = tmem_slot + 4;  // [block % TC_MASKS][4] positions that exist
   if (base & 1023) {  // the swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) atomicOr(a.p.err, ERR_LAYOUT);
@@ -78,6 +83,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
   }
   if (threadIdx.x == 0) {
     *s_abort = 0;
+    *s_turn = 0;
     mbar_init(q_full, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full0 + 8 * i, 1);
@@ -85,14 +91,15 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
       mbar_init(o_full0 + 8 * i, 1);
     }
     mbar_init(done, 1);
-    mbar_init(idle, 8);
+    mbar_init(done + 8, 1);
+    mbar_init(idle, 10);  // the softmax warps and the issuers
     for (int i = 0; i < NS; ++i) {
       mbar_init(full0 + 8 * i, TC_PRODUCERS);
-      mbar_init(empty0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, 2);
     }
     mbar_fence_init();
   }
-  if (warp == MMA_WARP) tc::tmem_alloc(smem_addr(tmem_slot), 512);
+  if (warp == TMEM_WARP) tc::tmem_alloc(smem_addr(tmem_slot), 512);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -104,65 +111,83 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
     produce<T, MT, HD, NS>(a, maps, r, p, base + C::OFF_RING, full0, empty0, masks, s_abort);
   } else if (warp >= 12) {
     setmaxnreg_dec<56>();
-    if (warp == MMA_WARP && lane == 0) {
-      // ---- issues the products
+    if (warp < MMA_WARP + 2 && lane == 0) {
+      // ---- issues the products of chain c
       constexpr uint32_t kind = BF ? 1u << 7 | 1u << 10 : 0u;
       constexpr uint32_t idS = tc::idesc_f16(128, BK) | kind, idO = tc::idesc_f16_bmn(128, HD) | kind;
-      int tile0 = 0, units = 0, steps[2] = {0, 0};  // tiles before the unit, units, steps of each chain so far
+      const int c = warp - MMA_WARP;
+      const uint32_t s_full = s_full0 + 8 * c, p_full = p_full0 + 8 * c, s_col = tmem + c * 128, o_col = tmem + C::O_COL + c * 128;
+      int tile0 = 0, units = 0, steps = 0;  // tiles before the unit, units, steps so far
       bool ok = true;
+      auto turn = [&]() {  // the tensor cores' queue for a whole step: false if the other chain does not give it up
+        if (atomicCAS((int*)s_turn, 0, 1) == 0) return true;
+        const long long t0 = clock64();
+        while (atomicCAS((int*)s_turn, 0, 1) != 0)
+          if (clock64() - t0 > tc::WAIT_BUDGET) {
+            atomicOr(err, ERR_TIMEOUT);
+            return false;
+          }
+        return true;
+      };
       do {
         const int nb = blocks_of(p, r.end);
         const bool two = p.c == 2;  // both halves have rows
         if (!(ok = tc::mbar_wait(q_full, units & 1, err))) break;
         ++units;
         auto landed = [&](int i, uint32_t& addr) {  // tile i of the unit
-          const int n = tile0 + i, s = n % NS;
+          const uint32_t n = tile0 + i, s = n % NS;
           addr = base + C::OFF_RING + s * C::TILE;
           return tc::mbar_wait(full0 + 8 * s, n / NS & 1, err);
         };
-        auto release = [&](int i) { tc::mma_commit(empty0 + 8 * ((tile0 + i) % NS)); };
-        const int n_of[2] = {two ? nb : (nb + 1) / 2, two ? nb : nb / 2};
-        auto block_of = [&](int c, int i) { return two ? i : 2 * i + c; };
-        auto issue_s = [&](int c, int i) {
-          const int j = block_of(c, i);
-          uint32_t k;
-          if (!landed(k_tile(j), k)) return false;
-          tc::tc_fence_after();
-          const uint32_t q = base + (two ? c * 128 * HD * 2 : 0);
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk)
-            tc::mma_f16(tmem + c * 128, tc::smem_desc_sw128(q + (kk >> 2) * 128 * 128 + (kk & 3) * 32),
-                        tc::smem_desc_sw128(k + (kk >> 2) * BK * 128 + (kk & 3) * 32), idS, kk > 0);
-          tc::mma_commit(s_full0 + 8 * c);
-          if (!two || c == 1) release(k_tile(j));
-          return true;
+        auto release = [&](int i) {  // (a tile expects both chains)
+          const uint32_t bar = empty0 + 8 * ((uint32_t)(tile0 + i) % NS);
+          if (!two) mbar_arrive(bar);
+          tc::mma_commit(bar);
         };
-        ok = issue_s(0, 0) && (n_of[1] == 0 || issue_s(1, 0));
-        for (int i = 0; i < n_of[0] && ok; ++i)
-          for (int c = 0; c < 2 && ok; ++c) {
-            if (i >= n_of[c]) break;
-            if (*s_abort || !tc::mbar_wait(p_full0 + 8 * c, steps[c] & 1, err)) {
-              ok = false;
-              break;
-            }
-            ++steps[c];
-            const int j = block_of(c, i);
-            uint32_t v;
-            if (!(ok = landed(v_tile(j, nb), v))) break;
-            tc::tc_fence_after();
+        const uint32_t ql = desc_lo(base) + (two ? c * (128 * HD * 2 >> 4) : 0);
+        auto products_s = [&](uint32_t k) {
+          const uint32_t kl = desc_lo(k);
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)
-              tc::mma_f16_tmem_a(tmem + C::O_COL + c * 128, tmem + c * 128 + kk * 8, tc::smem_desc_sw128_mn(v + kk * 2048, BK * 128, 1024), idO,
-                                 i > 0 || kk > 0);
-            if (i + 1 == n_of[c]) tc::mma_commit(o_full0 + 8 * c);
-            if (!two || c == 1) release(v_tile(j, nb));
-            if (i + 1 < n_of[c]) ok = issue_s(c, i + 1);
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const int at = ((kk >> 2) * 128 * 128 + (kk & 3) * 32) >> 4;
+            mma_ss(s_col, ql + at, kl + at, idS, kk > 0);
           }
+          tc::mma_commit(s_full);
+        };
+        const int step = two ? 1 : 2;
+        int j = two ? 0 : c;
+        bool first = true;
+        uint32_t k, v;
+        if (j < nb && (ok = landed(k_tile(j), k))) {
+          tc::tc_fence_after();
+          if ((ok = turn())) {
+            products_s(k);
+            *s_turn = 0;
+            release(k_tile(j));
+          }
+        }
+        for (; j < nb && ok; j += step) {
+          const bool more = j + step < nb;
+          ok = !*s_abort && tc::mbar_wait(p_full, steps & 1, err) && landed(v_tile(j, nb), v) && (!more || landed(k_tile(j + step), k)) && turn();
+          if (!ok) break;
+          ++steps;
+          tc::tc_fence_after();
+          const uint32_t vl = desc_lo(v, BK * 128);
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) mma_ts(o_col, s_col + kk * 8, vl + kk * (2048 >> 4), idO, !first || kk > 0);
+          first = false;
+          if (more) products_s(k);
+          else tc::mma_commit(o_full0 + 8 * c);
+          *s_turn = 0;
+          release(v_tile(j, nb));
+          if (more) release(k_tile(j + step));
+        }
+        mbar_arrive(idle);  // (so that no issuer is a unit behind)
         tile0 += 2 * nb;
       } while (ok && next_unit<MT, BK>(a, r.end, p));
       if (!ok) *s_abort = 1;
-      tc::mma_commit(done);  // arrives once all products issued above are done
-      tc::mbar_wait(done, 0, err);
+      tc::mma_commit(done + 8 * c);  // arrives once all products issued above are done
+      tc::mbar_wait(done + 8 * c, 0, err);
     }
   } else {
     setmaxnreg_inc<192>();
@@ -234,8 +259,9 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
 #pragma unroll
         for (int q = 0; q < 4; ++q) top[q] = __uint_as_float(u[q]);
 #pragma unroll
-        for (int q = 4; q < 128; ++q) top[q & 3] = fmaxf(top[q & 3], __uint_as_float(u[q]));
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+        for (int q = 4; q < 124; q += 2) top[(q >> 1) & 3] = max3(top[(q >> 1) & 3], __uint_as_float(u[q]), __uint_as_float(u[q + 1]));
+        const float last = max3(__uint_as_float(u[124]), __uint_as_float(u[125]), fmaxf(__uint_as_float(u[126]), __uint_as_float(u[127])));
+        const float mx = max3(max3(top[0], top[1], top[2]), top[3], last) * sc;
         const bool move = mx > m + MOVE_AT || (m == -INFINITY && mx > m);
         if (__any_sync(0xffffffffu, move)) {
           const float f = move ? ex2(m - mx) : 1.f;  // (0 where m is -inf)
@@ -254,6 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
             l *= f;
             m = mx;
           }
+          __syncwarp();
         }
         const float ref = (m == -INFINITY ? 0.f : m) - PA_BIAS;
         const f32x2 c2 = pack2(sc, sc), r2 = pack2(-ref, -ref);
@@ -294,6 +321,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
 #pragma unroll 1
         for (int d = 0; d < HD; d += 32) {
           float o[32];
+          __syncwarp();  // (the lanes' stores part them; TMEM is read by whole warps)
           tc::tmem_ld32(o_at + d, o);
           if (dst)
 #pragma unroll
@@ -306,9 +334,10 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
     } while (next_unit<MT, BK>(a, r.end, p));
     if (!ok) *s_abort = 1;
   }
+  __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == MMA_WARP) {
+  if (warp == TMEM_WARP) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }

@@ -26,7 +26,7 @@ namespace {
 using paged::Pair;
 using paged::split;
 
-constexpr int MT = 128, BK = TC_BK, THREADS = 512, MMA_WARP = 12;
+constexpr int MT = 128, BK = TC_BK, THREADS = 512, MMA_WARP = 12, TMEM_WARP = 15;  // (a warp whose lanes never part allocates and frees TMEM)
 
 template <typename T, int HD>
 struct Cfg {
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
     }
     mbar_fence_init();
   }
-  if (warp == MMA_WARP) tc::tmem_alloc(smem_addr(tmem_slot), 512);
+  if (warp == TMEM_WARP) tc::tmem_alloc(smem_addr(tmem_slot), 512);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -121,12 +121,14 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
         auto issue_s = [&](int j) {  // j: block of all
           uint32_t k;
           if (!tile(k)) return false;
+          const uint32_t ql = desc_lo(base), kl = desc_lo(k);
 #pragma unroll
           for (int i = NQ - 1; i >= 0; --i)  // the lowest piece first
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk)
-              tc::mma_f16(tmem + (j & 1) * 128, tc::smem_desc_sw128(base + i * MT * HD * 2 + (kk >> 2) * MT * 128 + (kk & 3) * 32),
-                          tc::smem_desc_sw128(k + (kk >> 2) * BK * 128 + (kk & 3) * 32), idS, i < NQ - 1 || kk > 0);
+            for (int kk = 0; kk < HD / 16; ++kk) {
+              const int at = ((kk >> 2) * MT * 128 + (kk & 3) * 32) >> 4;
+              mma_ss(tmem + (j & 1) * 128, ql + (i * MT * HD * 2 >> 4) + at, kl + at, idS, i < NQ - 1 || kk > 0);
+            }
           tc::mma_commit(s_full0 + 8 * (j & 1));
           release();
           return true;
@@ -139,13 +141,12 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
           if (!ok || !(ok = tc::mbar_wait(p_full0 + 8 * (block & 1), block >> 1 & 1, err))) break;
           uint32_t v;
           if (!(ok = tile(v))) break;
-          const uint32_t o = tmem + C::O_COL + (block & 1) * (C::NO - 1) * 128;
+          const uint32_t vl = desc_lo(v, BK * 128), o = tmem + C::O_COL + (block & 1) * (C::NO - 1) * 128;
 #pragma unroll
           for (int i = NP - 1; i >= 0; --i) {
             const uint32_t pc = tmem + (i < 2 ? (block & 1) * 128 + i * 64 : C::P3 + (block & 1) * 64);
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)
-              tc::mma_f16_tmem_a(o, pc + kk * 8, tc::smem_desc_sw128_mn(v + kk * 2048, BK * 128, 1024), idO, i < NP - 1 || kk > 0);
+            for (int kk = 0; kk < BK / 16; ++kk) mma_ts(o, pc + kk * 8, vl + kk * (2048 >> 4), idO, i < NP - 1 || kk > 0);
           }
           tc::mma_commit(o_full0 + 8 * (block & 1));
           release();
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(pair);
       if (!tc::mbar_wait(pair, trades & 1, err)) ok = false;
+      __syncwarp();  // (TMEM is read and written by whole warps)
       const float other = xch[(2 * (trades & 1) + (half ^ 1)) * MT + row];
       ++trades;
       return other;
@@ -329,9 +331,10 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
     } while (next_unit<MT, BK>(a, r.end, p));
     if (!ok) *s_abort = 1;
   }
+  __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == MMA_WARP) {
+  if (warp == TMEM_WARP) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
