@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
         }
         for (; j < nb && ok; j += step) {
           const bool more = j + step < nb;
-          ok = !*s_abort && tc::mbar_wait(p_full, steps & 1, err) && landed(v_tile(j, nb), v) && (!more || landed(k_tile(j + step), k)) && turn();
+          // (the tiles landed long ago, mostly: their waits pass while the softmax is at work)
+          ok = !*s_abort && landed(v_tile(j, nb), v) && (!more || landed(k_tile(j + step), k)) && tc::mbar_wait(p_full, steps & 1, err) && turn();
           if (!ok) break;
           ++steps;
           tc::tc_fence_after();
@@ -202,35 +203,41 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
       const int kv = p.u / p.nt, tile = p.u - kv * p.nt, nb = blocks_of(p, r.end);
       const bool two = p.c == 2;
       if (units > 0 && !tc::mbar_wait(idle, (units - 1) & 1, err)) ok = false;  // (all products of the last unit are done)
-      {  // the unit's queries; zeros for rows that take no part
+      const Row mine = row_of(a, p, kv, tile * MT + (two ? c * 128 : 0) + row);
+      if (two || c == 0) {  // the queries of the warp's rows, a row at a time; zeros for rows that take no part
         constexpr int DL = HD / 32;  // dimensions of a lane
-        const int d0 = lane * DL, rows_w = two ? 32 : 16;
-        const uint32_t at = base + (d0 >> 6) * (128 * 128) + (d0 & 7) * 2;
-#pragma unroll 4
-        for (int i = 0; i < rows_w; ++i) {
-          const int rr = (warp - 4) * rows_w + i;
-          const Row row_i = row_of(a, p, kv, tile * MT + rr);
-          uint32_t w[DL / 2];
+        const int d0 = lane * DL;
+        const uint32_t at = base + c * (128 * HD * 2) + (d0 >> 6) * (128 * 128) + ((warp & 3) * 32) * 128 + (d0 & 7) * 2;
+        const long long q_row = mine.in ? mine.b * a.p.q_stride + mine.h * a.p.hd : -1;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += 8) {
+          uint32_t w[8][DL / 2];
 #pragma unroll
-          for (int d = 0; d < DL / 2; ++d) w[d] = 0u;
-          if (row_i.in && d0 < a.p.hd) {
-            const T* q = (const T*)a.p.q + row_i.b * a.p.q_stride + row_i.h * a.p.hd + d0;
+          for (int i = 0; i < 8; ++i) {
+            const long long off = __shfl_sync(0xffffffffu, q_row, i0 + i);
+            const T* q = (const T*)a.p.q + off + d0;
+#pragma unroll
+            for (int d = 0; d < DL / 2; ++d) w[i][d] = off >= 0 && d0 < a.p.hd ? *reinterpret_cast<const uint32_t*>(q + 2 * d) : 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = i0 + i;
+            const uint32_t dst = at + rr * 128 + ((((d0 >> 3) & 7) ^ (rr & 7)) << 4);
 #pragma unroll
             for (int d = 0; d < DL / 2; ++d) {
-              const float2 two_d = paged::load2(q + 2 * d);
-              w[d] = Pair<T>::pack(two_d.x * sign, two_d.y * sign);
+              const float2 x = Pair<T>::unpack(w[i][d]);
+              w[i][d] = Pair<T>::pack(x.x * sign, x.y * sign);
             }
+            if constexpr (DL == 4)
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[i][0]), "r"(w[i][1]) : "memory");
+            else
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w[i][0]) : "memory");
           }
-          const uint32_t dst = at + (rr >> 7) * (128 * HD * 2) + (rr & 127) * 128 + ((((d0 >> 3) & 7) ^ (rr & 7)) << 4);
-          if constexpr (DL == 4)
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[0]), "r"(w[1]) : "memory");
-          else
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w[0]) : "memory");
         }
         fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
       float m = -INFINITY, l = 0.f;
       bool any = false;
       const int n = two ? nb : c == 0 ? (nb + 1) / 2 : nb / 2;
@@ -255,15 +262,37 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
             if (!(mask.w >> q & 1)) u[96 + q] = 0xff800000u;
           }
         }
-        float top[4];
+        // Probabilities over the reference so far, and the block's maximum beside them (its comparisons run beside the
+        // exponentials); once more where the maximum lies too far above the reference, as in a unit's first block.
+        f32x2 acc[4];
+        const f32x2 c2 = pack2(sc, sc);
+#pragma unroll 1
+        while (true) {
+          const float ref = (m == -INFINITY ? 0.f : m) - PA_BIAS;
+          const f32x2 r2 = pack2(-ref, -ref);
+          float top[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) top[q] = __uint_as_float(u[q]);
+          for (int q = 0; q < 4; ++q) {
+            acc[q] = 0ull;
+            top[q] = -INFINITY;
+          }
 #pragma unroll
-        for (int q = 4; q < 124; q += 2) top[(q >> 1) & 3] = max3(top[(q >> 1) & 3], __uint_as_float(u[q]), __uint_as_float(u[q + 1]));
-        const float last = max3(__uint_as_float(u[124]), __uint_as_float(u[125]), fmaxf(__uint_as_float(u[126]), __uint_as_float(u[127])));
-        const float mx = max3(max3(top[0], top[1], top[2]), top[3], last) * sc;
-        const bool move = mx > m + MOVE_AT || (m == -INFINITY && mx > m);
-        if (__any_sync(0xffffffffu, move)) {
+          for (int q0 = 0; q0 < 64; q0 += 16) {
+            uint32_t pp[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float x = __uint_as_float(u[2 * (q0 + q)]), y = __uint_as_float(u[2 * (q0 + q) + 1]);
+              top[q & 3] = max3(top[q & 3], x, y);
+              const float2 e = unpack2(fma2_to(pack2(x, y), c2, r2));
+              const float p0 = ex2(e.x), p1 = ex2(e.y);
+              acc[q & 3] = add2(acc[q & 3], pack2(p0, p1));
+              pp[q] = Pair<T>::pack(p0, p1);
+            }
+            tmem_st16(s_at + q0, pp);
+          }
+          const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc;
+          const bool move = mx > m + MOVE_AT || (m == -INFINITY && mx > m);
+          if (!__any_sync(0xffffffffu, move)) break;
           const float f = move ? ex2(m - mx) : 1.f;  // (0 where m is -inf)
           if (i > 0) {
 #pragma unroll 1
@@ -282,21 +311,6 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
           }
           __syncwarp();
         }
-        const float ref = (m == -INFINITY ? 0.f : m) - PA_BIAS;
-        const f32x2 c2 = pack2(sc, sc), r2 = pack2(-ref, -ref);
-        f32x2 acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int q0 = 0; q0 < 64; q0 += 16) {
-          uint32_t pp[16];
-#pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const float2 e = unpack2(fma2_to(pack2(__uint_as_float(u[2 * (q0 + q)]), __uint_as_float(u[2 * (q0 + q) + 1])), c2, r2));
-            const float p0 = ex2(e.x), p1 = ex2(e.y);
-            acc[q & 3] = add2(acc[q & 3], pack2(p0, p1));
-            pp[q] = Pair<T>::pack(p0, p1);
-          }
-          tmem_st16(s_at + q0, pp);
-        }
         const float2 s0 = unpack2(add2(acc[0], acc[1])), s1 = unpack2(add2(acc[2], acc[3]));
         l += (s0.x + s0.y) + (s1.x + s1.y);
         tc::tmem_wait_st();
@@ -312,8 +326,6 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
       if (lane == 0) mbar_arrive(idle);
       block0 += nb;
       ++units;
-      const int i = two ? c * 128 + row : row;  // of the tile
-      const Row mine = row_of(a, p, kv, tile * MT + i);
       const bool whole = nb == p.nb;
       float* dst = mine.in ? state_of<MT, HD>(a, r, p, whole, mine, c * 128 + row, !two && c) : nullptr;
       const int width = whole ? a.p.hd : HD;

@@ -177,33 +177,35 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
     };
     do {
       const int kv = p.u / p.nt, tile = p.u - kv * p.nt, nb = blocks_of(p, r.end);
-      {  // the unit's queries, 16 rows a warp; zeros for rows that take no part
+      const Row mine = row_of(a, p, kv, tile * MT + row);
+      {  // the unit's queries, 16 of the quarter's rows a warp, a row at a time; zeros for rows that take no part
         constexpr int DL = HD / 32;  // dimensions of a lane
         const int d0 = lane * DL;
         const uint32_t at = base + (d0 >> 6) * (MT * 128) + (d0 & 7) * 2;
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-          const int rr = (warp - 4) * 16 + i;
-          const Row row_i = row_of(a, p, kv, tile * MT + rr);
-          float x[DL];
+        const long long q_row = mine.in ? mine.b * a.p.q_stride + mine.h * a.p.hd : -1;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 16; i0 += 4) {
+          float x[4][DL];
 #pragma unroll
-          for (int d = 0; d < DL; ++d) x[d] = 0.f;
-          if (row_i.in && d0 < a.p.hd) {
-            const float* q = (const float*)a.p.q + row_i.b * a.p.q_stride + row_i.h * a.p.hd + d0;
+          for (int i = 0; i < 4; ++i) {
+            const long long off = __shfl_sync(0xffffffffu, q_row, half * 16 + i0 + i);
+            const float* q = (const float*)a.p.q + off + d0;
 #pragma unroll
             for (int d = 0; d < DL; d += 2) {
-              const float2 two = paged::load2(q + d);
-              x[d] = two.x * sign;
-              x[d + 1] = two.y * sign;
+              const float2 two = off >= 0 && d0 < a.p.hd ? *reinterpret_cast<const float2*>(q + d) : make_float2(0.f, 0.f);
+              x[i][d] = two.x * sign;
+              x[i][d + 1] = two.y * sign;
             }
           }
-          float up = 1.f, down = 1.f;
-          {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = quarter * 32 + half * 16 + i0 + i;
+            float up = 1.f, down = 1.f;
             // a power of two that keeps the pieces normal: fp16 pieces with the row's largest at 2^10, whatever its size; bf16
             // pieces, whose range is fp32's own, with only small ones raised to 2^-50. The scores undo it.
             float top = 0.f;
 #pragma unroll
-            for (int d = 0; d < DL; ++d) top = fmaxf(top, fabsf(x[d]));
+            for (int d = 0; d < DL; ++d) top = fmaxf(top, fabsf(x[i][d]));
             top = warp_max(top);
             const int ex = (int)(__float_as_uint(top) >> 23) - 127;
             if (ex < 128) {  // (a row with an infinity passes as it is)
@@ -211,18 +213,18 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
               up = __uint_as_float((uint32_t)(127 + shift) << 23);
               down = __uint_as_float((uint32_t)(127 - shift) << 23);
             }
-          }
-          if (lane == 0) undo[rr] = down;
-          const uint32_t dst = at + rr * 128 + ((((d0 >> 3) & 7) ^ (rr & 7)) << 4);
-          uint32_t w[DL / 2][NQ];
+            if (lane == 0) undo[rr] = down;
+            const uint32_t dst = at + rr * 128 + ((((d0 >> 3) & 7) ^ (rr & 7)) << 4);
+            uint32_t w[DL / 2][NQ];
 #pragma unroll
-          for (int d = 0; d < DL; d += 2) split<T, NQ>(x[d] * up, x[d + 1] * up, w[d / 2]);
+            for (int d = 0; d < DL; d += 2) split<T, NQ>(x[i][d] * up, x[i][d + 1] * up, w[d / 2]);
 #pragma unroll
-          for (int i2 = 0; i2 < NQ; ++i2) {
-            if constexpr (DL == 4)
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + i2 * MT * HD * 2), "r"(w[0][i2]), "r"(w[1][i2]) : "memory");
-            else
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + i2 * MT * HD * 2), "r"(w[0][i2]) : "memory");
+            for (int k = 0; k < NQ; ++k) {
+              if constexpr (DL == 4)
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + k * MT * HD * 2), "r"(w[0][k]), "r"(w[1][k]) : "memory");
+              else
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + k * MT * HD * 2), "r"(w[0][k]) : "memory");
+            }
           }
         }
         fence_proxy_async();
@@ -280,9 +282,9 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
         for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(u[i]);
 #pragma unroll
         for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(u[i]));
-        const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), other = trade(mine);
+        const float own = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), other = trade(own);
         if (C::three && j > 0) fold(block - 1);  // (one O buffer: it is read before P is handed over)
-        const float mn = fmaxf(m, fmaxf(mine, other) * c), f = mn > m ? ex2(m - mn) : 1.f;
+        const float mn = fmaxf(m, fmaxf(own, other) * c), f = mn > m ? ex2(m - mn) : 1.f;
         l *= f;
         m = mn;
         const float ref = (mn == -INFINITY ? 0.f : mn) - PA_BIAS;
@@ -317,7 +319,6 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
       fold(block - 1);
       l += trade(l);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      const Row mine = row_of(a, p, kv, tile * MT + row);
       if (mine.in) {
         const bool whole = nb == p.nb;
         float* dst = state_of<MT, HD>(a, r, p, whole, mine, row);
