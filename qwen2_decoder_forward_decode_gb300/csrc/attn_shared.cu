@@ -5,8 +5,8 @@
 // o = sum 2^(s - m) V. States of disjoint sets merge as M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i. So
 // the shared positions are read once for all rows (sequence, head) of a group and KV head, and each sequence's own
 // positions by themselves:
-//   1. the own positions: the kernels of attn_paged.cu with each sequence's first positions left out and their states
-//      kept in fp32;
+//   1. the own positions: a list of short tiles, a range a warp (attn_shared_own.cu; fp32 caches and longer heads by the
+//      kernels of attn_paged_simt.cu with each sequence's first positions left out), their states kept in fp32;
 //   2. the shared ones: matrix products of up to 256 rows with blocks of keys and values on the tensor cores
 //      (attn_shared_pair.cu, for fp32 callers attn_shared_tc.cu; fp32 caches and longer heads on the CUDA cores,
 //      attn_shared_simt.cu). All blocks of all groups form one list that is cut into
@@ -27,6 +27,7 @@ constexpr int JN_THREADS = 256, JN_WARPS = JN_THREADS / 32;
 struct JoinArgs {
   SharedArgs s;
   Geometry geo;
+  int own_hb, own_hd;  // of attn_shared_own.cu's parts; own_hb 0: it has not run
 };
 
 // The sum of states, NV groups of 4 dimensions a lane.
@@ -71,7 +72,28 @@ __device__ __forceinline__ bool join_row(const JoinArgs& ja, int row, int part, 
   };
   const SharedHead head = *a.head;
   if (head.bad) return false;
-  if (part == 0) take(p.state + (size_t)row * comb_stride(p.hd), p.hd);
+  if (ja.own_hb == 0) {  // (the CUDA cores' kernels join their parts themselves)
+    if (part == 0) take(p.state + (size_t)row * comb_stride(p.hd), p.hd);
+  } else {
+    int from;
+    const int len = paged::seq_len(p, b, from), rw = own_rows(ja.own_hd), nt = (len + rw - 1) / rw;
+    if (nt) {
+      const SharedHead own = *a.own_head;
+      const int grp = p.nq / p.nkv, g = h / grp, hg = h - g * grp, hb = hg / ja.own_hb, n_hb = (grp + ja.own_hb - 1) / ja.own_hb;
+      const int v = a.own_at[b] + (g * n_hb + hb) * (OWN_WEIGHT + nt);
+      const Range r{own.each, own.rest, 0, 0};
+      const int c0 = cta_of(r, v + OWN_WEIGHT), c1 = nt <= OWN_WHOLE ? c0 : cta_of(r, v + OWN_WEIGHT + nt - 1);
+      if (c0 == c1) {
+        if (part == 0) take(p.state + (size_t)row * comb_stride(p.hd), p.hd);
+      } else {
+#pragma unroll 4
+        for (int c = c0 + part; c <= c1; c += WPR) {
+          const int slot = 2 * c + (c == c0 && cut(r, c) < v ? 1 : 0);
+          take(p.part + ((size_t)slot * ja.own_hb + (hg - hb * ja.own_hb)) * comb_stride(ja.own_hd), ja.own_hd);
+        }
+      }
+    }
+  }
   int lo = 0, hi = a.n_groups;  // the last group that begins at or before b
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -175,14 +197,17 @@ cudaError_t launch_join(const JoinArgs& ja, int nsm, cudaStream_t s) {
 
 // The workspace: the counters and parts of attn_paged.cu, the head and the groups' places, states, parts.
 struct Layout {
-  size_t head, at, own, whole, parts, bytes;
+  size_t head, at, own_at, own, whole, parts, bytes;
 };
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 Layout layout(int n_seqs, int n_heads, int n_kv_heads, int head_dim) {
   Layout y;
-  y.head = up256(OP_COUNTER_BYTES + 2 * paged::PA_MAX_CTAS * paged::part_floats(n_heads, n_kv_heads, head_dim) * sizeof(float));
+  // (parts of the paged kernels' CTAs, or of attn_shared_own.cu's warps)
+  static_assert(paged::PA_MAX_CTAS <= SH_MAX_CTAS * OWN_WARPS, "parts");
+  y.head = up256(OP_COUNTER_BYTES + 2 * SH_MAX_CTAS * OWN_WARPS * paged::part_floats(n_heads, n_kv_heads, head_dim) * sizeof(float));
   y.at = y.head + 256;
-  y.own = y.at + up256((size_t)n_seqs * sizeof(int));
+  y.own_at = y.at + up256((size_t)n_seqs * sizeof(int));
+  y.own = y.own_at + up256((size_t)n_seqs * sizeof(int));
   const size_t states = up256((size_t)n_seqs * n_heads * comb_stride(head_dim) * sizeof(float));
   y.whole = y.own + states;
   y.parts = y.whole + 2 * states;
@@ -223,6 +248,8 @@ qw_status qw_op_shared_attention(const qw_paged_kv* cache, int32_t n_seqs, int32
   if (n_groups == 0) return op_fail(QW_ERR_INVALID_ARG, "sequences without a group");
   const Geometry least = geometry(c.dtype, io_dtype, c.head_dim, 1);
   const int64_t tiles = ((int64_t)n_seqs * (n_heads / c.n_kv_heads) + least.mt - 1) / least.mt + n_groups;
+  const int64_t own = (int64_t)max_blocks * c.page_size / own_rows(c.head_dim) + 1 + OWN_WEIGHT;
+  if ((int64_t)n_seqs * n_heads * own > 0x7fffffffll) return op_fail(QW_ERR_UNSUPPORTED, "n_seqs * n_heads * max_blocks * page_size too large");
   if (tiles * c.n_kv_heads * (2 * ((int64_t)max_blocks * c.page_size / least.bk + 1) + SH_WEIGHT) > 0x7fffffffll)
     return op_fail(QW_ERR_UNSUPPORTED, "n_seqs * n_heads * max_blocks * page_size too large");
   if (!block_table || !lens || !cu_seqs || !shared_lens || !workspace || !err_dev) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
@@ -247,14 +274,20 @@ qw_status qw_op_shared_attention(const qw_paged_kv* cache, int32_t n_seqs, int32
   ja.s.cu = cu_seqs;
   ja.s.head = (SharedHead*)(ws + y.head);
   ja.s.at = (int*)(ws + y.at);
+  ja.s.own_head = ja.s.head + 1;
+  ja.s.own_at = (int*)(ws + y.own_at);
   ja.s.whole = (float*)(ws + y.whole);
   ja.s.parts = (float*)(ws + y.parts);
   ja.geo = geometry(c.dtype, io_dtype, c.head_dim, nsm);
   cudaStream_t s = (cudaStream_t)cuda_stream;
-  if ((e = paged::launch_paged(c.dtype, io_dtype, nsm, ja.s.p, s))) return op_cuda_fail(e, "shared attention launch");
-  e = c.dtype == QW_F32 || c.head_dim > 128 ? launch_shared_simt(c.dtype, io_dtype, ja.geo.ctas, ja.s, s)
-      : io_dtype == QW_F32                  ? launch_shared_tc(c, ja.geo.ctas, ja.s, s)
-                                            : launch_shared_pair(c, ja.geo.ctas, ja.s, s);
+  const bool tc = c.dtype != QW_F32 && c.head_dim <= 128;
+  ja.own_hb = !tc ? 0 : n_heads / c.n_kv_heads <= 8 ? 8 : 16;
+  ja.own_hd = c.head_dim <= 32 && ja.own_hb == 8 ? 32 : c.head_dim <= 64 ? 64 : 128;
+  e = tc ? launch_own(c.dtype, io_dtype, ja.geo.ctas, ja.s, s) : paged::launch_paged(c.dtype, io_dtype, nsm, ja.s.p, s);
+  if (e) return op_cuda_fail(e, "shared attention launch");
+  e = !tc ? launch_shared_simt(c.dtype, io_dtype, ja.geo.ctas, ja.s, s)
+      : io_dtype == QW_F32 ? launch_shared_tc(c, ja.geo.ctas, ja.s, s)
+                           : launch_shared_pair(c, ja.geo.ctas, ja.s, s);
   if (e) return op_cuda_fail(e, "shared attention launch");
   e = io_dtype == QW_F32 ? launch_join<float>(ja, nsm, s) : io_dtype == QW_F16 ? launch_join<f16>(ja, nsm, s) : launch_join<bf16>(ja, nsm, s);
   if (e) return op_cuda_fail(e, "shared attention launch");

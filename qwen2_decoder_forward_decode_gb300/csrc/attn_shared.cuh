@@ -17,6 +17,11 @@ using paged::Range;
 constexpr int SH_MAX_CTAS = 160;  // of the tensor-core kernel, one an SM; the CUDA cores' kernel takes two
 constexpr int SH_WEIGHT = 2;      // of a unit's ends in the list, in blocks
 
+// The own positions of 16-bit caches, see attn_shared_own.cu: positions of a tile, a unit's weight in tiles, units of so many
+// tiles are not split, head dimensions and heads of a part.
+constexpr int OWN_WEIGHT = 2, OWN_WHOLE = 2, OWN_WARPS = 8;
+__host__ __device__ constexpr int own_rows(int hd) { return hd <= 64 ? 32 : 16; }
+
 struct SharedHead {  // of the workspace
   int bad, each, rest, total;
 };
@@ -26,6 +31,8 @@ struct SharedArgs {
   const int* cu;
   SharedHead* head;
   int* at;       // [n_groups] where the list has the group
+  SharedHead* own_head;  // the same for the list of own positions (16-bit caches)
+  int* own_at;           // [n_seqs]
   float* whole;  // [2][n_seqs][nq][comb_stride(hd)] states of units that one CTA covers, see state_of
   float* parts;  // [2 * CTAs][rows of a tile][comb_stride(HD)] of the others
 };
@@ -216,6 +223,7 @@ inline Geometry geometry(int cache_dtype, int io_dtype, int hd, int nsm) {
 // attn_shared_simt.cu: the others
 cudaError_t launch_shared_tc(const qw_paged_kv& cache, int ctas, const SharedArgs& a, cudaStream_t s);
 cudaError_t launch_shared_pair(const qw_paged_kv& cache, int ctas, const SharedArgs& a, cudaStream_t s);
+cudaError_t launch_own(int cache_dtype, int io_dtype, int ctas, const SharedArgs& a, cudaStream_t s);
 cudaError_t launch_shared_simt(int cache_dtype, int io_dtype, int ctas, const SharedArgs& a, cudaStream_t s);
 
 }  // namespace shared_attn

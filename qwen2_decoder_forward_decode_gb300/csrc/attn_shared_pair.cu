@@ -209,30 +209,33 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
         const int d0 = lane * DL;
         const uint32_t at = base + c * (128 * HD * 2) + (d0 >> 6) * (128 * 128) + ((warp & 3) * 32) * 128 + (d0 & 7) * 2;
         const long long q_row = mine.in ? mine.b * a.p.q_stride + mine.h * a.p.hd : -1;
-#pragma unroll 1
-        for (int i0 = 0; i0 < 32; i0 += 8) {
-          uint32_t w[8][DL / 2];
+        uint32_t w[32][DL / 2];  // (all in flight at once)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const long long off = __shfl_sync(0xffffffffu, q_row, i0 + i);
-            const T* q = (const T*)a.p.q + off + d0;
-#pragma unroll
-            for (int d = 0; d < DL / 2; ++d) w[i][d] = off >= 0 && d0 < a.p.hd ? *reinterpret_cast<const uint32_t*>(q + 2 * d) : 0u;
+        for (int i = 0; i < 32; ++i) {
+          const long long off = __shfl_sync(0xffffffffu, q_row, i);
+          const bool there = off >= 0 && d0 < a.p.hd;
+          const T* q = (const T*)a.p.q + (there ? off + d0 : 0);
+          if constexpr (DL == 4) {
+            uint2 x = make_uint2(0u, 0u);
+            if (there) x = *reinterpret_cast<const uint2*>(q);
+            w[i][0] = x.x;
+            w[i][1] = x.y;
+          } else {
+            w[i][0] = there ? *reinterpret_cast<const uint32_t*>(q) : 0u;
           }
+        }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = i0 + i;
-            const uint32_t dst = at + rr * 128 + ((((d0 >> 3) & 7) ^ (rr & 7)) << 4);
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t dst = at + i * 128 + ((((d0 >> 3) & 7) ^ (i & 7)) << 4);
 #pragma unroll
-            for (int d = 0; d < DL / 2; ++d) {
-              const float2 x = Pair<T>::unpack(w[i][d]);
-              w[i][d] = Pair<T>::pack(x.x * sign, x.y * sign);
-            }
-            if constexpr (DL == 4)
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[i][0]), "r"(w[i][1]) : "memory");
-            else
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w[i][0]) : "memory");
+          for (int d = 0; d < DL / 2; ++d) {
+            const float2 x = Pair<T>::unpack(w[i][d]);
+            w[i][d] = Pair<T>::pack(x.x * sign, x.y * sign);
           }
+          if constexpr (DL == 4)
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[i][0]), "r"(w[i][1]) : "memory");
+          else
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w[i][0]) : "memory");
         }
         fence_proxy_async();
       }
