@@ -56,52 +56,71 @@ struct Sum {
   }
 };
 
-template <int NV, int WPR>  // WPR: warps of a row
+// Adds the states at s0, s0 + step, ..., n of them, 4 fetched at a time.
+template <int NV>
+__device__ __forceinline__ void add_states(Sum<NV>& sum, const float* s0, long long step, int n, int state_hd, int hd) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += 4) {
+    float2 ml[4];
+    float4 x[4][NV];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float* s = s0 + (i0 + i) * step;
+      ml[i] = i0 + i < n ? *reinterpret_cast<const float2*>(s + state_hd) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        x[i][v] = i0 + i < n && 4 * lane + 128 * v < hd ? *reinterpret_cast<const float4*>(s + 4 * lane + 128 * v) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum.add(ml[i].x, ml[i].y, x[i]);
+  }
+}
+
+// The sum of a row's states (the part `part` of WPR). What places them is loaded in three rounds: a warp waits for memory three
+// or four times, not once for each of a dozen numbers. false: the call's groups are bad.
+template <int NV, int WPR>
 __device__ __forceinline__ bool join_row(const JoinArgs& ja, int row, int part, Sum<NV>& sum) {
   const SharedArgs& a = ja.s;
   const PagedAttnArgs& p = a.p;
-  const int lane = threadIdx.x & 31, b = row / p.nq, h = row - b * p.nq;
+  const int lane = threadIdx.x & 31, b = row / p.nq, h = row - b * p.nq, grp = p.nq / p.nkv, kv = h / grp, hg = h - kv * grp;
   sum.clear();
-  auto take = [&](const float* s, int hd) {
-    const float2 ml = *reinterpret_cast<const float2*>(s + hd);
-    float4 x[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      x[i] = 4 * lane + 128 * i < p.hd ? *reinterpret_cast<const float4*>(s + 4 * lane + 128 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    sum.add(ml.x, ml.y, x);
-  };
-  const SharedHead head = *a.head;
+  const SharedHead head = *a.head, own = ja.own_hb ? *a.own_head : SharedHead{0, 0, 0, 0};
+  const int mine = __ldg(p.skip + b), len = __ldg(p.lens + b), own_at = ja.own_hb ? a.own_at[b] : 0;
+  // the last group that begins at or before b: 32 of them at a time
+  int lo = 0, hi = a.n_groups;
+#pragma unroll 1
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const unsigned before = __ballot_sync(0xffffffffu, at < hi && __ldg(a.cu + min(at, hi - 1)) <= b);
+    const int last = before ? 31 - __clz(before) : 0;
+    lo += last * step;
+    hi = min(hi, lo + step);
+  }
+  const int first = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1), at = a.at[lo];
+  const int pre = __ldg(p.skip + first);
   if (head.bad) return false;
   if (ja.own_hb == 0) {  // (the CUDA cores' kernels join their parts themselves)
-    if (part == 0) take(p.state + (size_t)row * comb_stride(p.hd), p.hd);
+    add_states<NV>(sum, p.state + (size_t)row * comb_stride(p.hd), 0, part == 0, p.hd, p.hd);
   } else {
     int from;
-    const int len = paged::seq_len(p, b, from), rw = own_rows(ja.own_hd), nt = (len + rw - 1) / rw;
+    const int left = paged::seq_len(p, b, from), rw = own_rows(ja.own_hd), nt = (left + rw - 1) / rw;
     if (nt) {
-      const SharedHead own = *a.own_head;
-      const int grp = p.nq / p.nkv, g = h / grp, hg = h - g * grp, hb = hg / ja.own_hb, n_hb = (grp + ja.own_hb - 1) / ja.own_hb;
-      const int v = a.own_at[b] + (g * n_hb + hb) * (OWN_WEIGHT + nt);
+      const int hb = hg / ja.own_hb, n_hb = (grp + ja.own_hb - 1) / ja.own_hb;
+      const int v = own_at + (kv * n_hb + hb) * (OWN_WEIGHT + nt);
       const Range r{own.each, own.rest, 0, 0};
       const int c0 = cta_of(r, v + OWN_WEIGHT), c1 = nt <= OWN_WHOLE ? c0 : cta_of(r, v + OWN_WEIGHT + nt - 1);
       if (c0 == c1) {
-        if (part == 0) take(p.state + (size_t)row * comb_stride(p.hd), p.hd);
-      } else {
-#pragma unroll 4
-        for (int c = c0 + part; c <= c1; c += WPR) {
-          const int slot = 2 * c + (c == c0 && cut(r, c) < v ? 1 : 0);
-          take(p.part + ((size_t)slot * ja.own_hb + (hg - hb * ja.own_hb)) * comb_stride(ja.own_hd), ja.own_hd);
-        }
+        add_states<NV>(sum, p.state + (size_t)row * comb_stride(p.hd), 0, part == 0, p.hd, p.hd);
+      } else {  // (only the first part may have a slot of odd number)
+        const long long size = (long long)ja.own_hb * comb_stride(ja.own_hd);
+        const float* s = p.part + (hg - hb * ja.own_hb) * comb_stride(ja.own_hd);
+        if (part == 0) add_states<NV>(sum, s + (2 * c0 + (cut(r, c0) < v ? 1 : 0)) * size, 0, 1, ja.own_hd, p.hd);
+        const int c = c0 + 1 + part;
+        add_states<NV>(sum, s + 2 * c * size, 2 * WPR * size, c <= c1 ? (c1 - c) / WPR + 1 : 0, ja.own_hd, p.hd);
       }
     }
   }
-  int lo = 0, hi = a.n_groups;  // the last group that begins at or before b
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.cu + mid) <= b) lo = mid;
-    else hi = mid;
-  }
-  const int first = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1), grp = p.nq / p.nkv;
-  const int pre = __ldg(p.skip + first), mine = __ldg(p.skip + b), len = __ldg(p.lens + b);
   const long long room = (long long)p.max_blocks * p.page;
   if (pre <= 0 || pre > room || mine != pre || len < pre) {
     // the sequence has no shared part, or one that its group's first sequence does not have: then positions are missing
@@ -109,28 +128,24 @@ __device__ __forceinline__ bool join_row(const JoinArgs& ja, int row, int part, 
     return true;
   }
   const int rows = (end - first) * grp, mt = ja.geo.mt, nt = (rows + mt - 1) / mt, nb = (pre + ja.geo.bk - 1) / ja.geo.bk;
-  const int kv = h / grp, i = (b - first) * grp + (h - kv * grp), tile = i / mt;
+  const int i = (b - first) * grp + hg, tile = i / mt;
   const bool pair = mt == 256;
   const int big = pair ? 2 : 1, cost = pair ? block_cost<256>(rows, tile) : 1;  // numbers of a block, in full tiles and in this one
-  const bool halves = cost < big;                                               // even and odd blocks have states of their own
+  const int states = cost < big ? 2 : 1;                                        // even and odd blocks have states of their own
   const int numbers = pair ? head_numbers<256>(rows, nt, nb) : head_numbers<128>(rows, nt, nb);
-  const int v = a.at[lo] + kv * numbers + tile * (SH_WEIGHT + big * nb);
+  const int v = at + kv * numbers + tile * (SH_WEIGHT + big * nb);
   const Range r{head.each, head.rest, 0, 0};
   const int c0 = cta_of(r, v + SH_WEIGHT), c1 = cta_of(r, v + SH_WEIGHT + cost * (nb - 1));
   if (c0 == c1) {
-    if (part == 0) {
-      take(a.whole + (size_t)row * comb_stride(p.hd), p.hd);
-      if (halves) take(a.whole + ((size_t)p.n_seqs * p.nq + row) * comb_stride(p.hd), p.hd);
-    }
+    add_states<NV>(sum, a.whole + (size_t)row * comb_stride(p.hd), (long long)p.n_seqs * p.nq * comb_stride(p.hd), part == 0 ? states : 0, p.hd, p.hd);
     return true;
   }
-#pragma unroll 4
-  for (int c = c0 + part; c <= c1; c += WPR) {
-    const int slot = 2 * c + (c == c0 && cut(r, c) < v ? 1 : 0);
-    const float* s = a.parts + ((size_t)slot * mt + (i - tile * mt)) * comb_stride(ja.geo.hd);
-    take(s, ja.geo.hd);
-    if (halves) take(s + (size_t)(mt / 2) * comb_stride(ja.geo.hd), ja.geo.hd);
-  }
+  const long long size = (long long)mt * comb_stride(ja.geo.hd), second = size / 2;
+  const float* s = a.parts + (i - tile * mt) * comb_stride(ja.geo.hd);
+  if (part == 0) add_states<NV>(sum, s + (2 * c0 + (cut(r, c0) < v ? 1 : 0)) * size, second, states, ja.geo.hd, p.hd);
+  const int c = c0 + 1 + part, n = c <= c1 ? (c1 - c) / WPR + 1 : 0;
+#pragma unroll 1
+  for (int k = 0; k < states; ++k) add_states<NV>(sum, s + k * second + 2 * c * size, 2 * WPR * size, n, ja.geo.hd, p.hd);
   return true;
 }
 
