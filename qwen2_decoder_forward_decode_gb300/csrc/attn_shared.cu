@@ -100,52 +100,77 @@ __device__ __forceinline__ bool join_row(const JoinArgs& ja, int row, int part, 
   const int first = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1), at = a.at[lo];
   const int pre = __ldg(p.skip + first);
   if (head.bad) return false;
-  if (ja.own_hb == 0) {  // (the CUDA cores' kernels join their parts themselves)
-    add_states<NV>(sum, p.state + (size_t)row * comb_stride(p.hd), 0, part == 0, p.hd, p.hd);
-  } else {
-    int from;
-    const int left = paged::seq_len(p, b, from), rw = own_rows(ja.own_hd), nt = (left + rw - 1) / rw;
-    if (nt) {
-      const int hb = hg / ja.own_hb, n_hb = (grp + ja.own_hb - 1) / ja.own_hb;
-      const int v = own_at + (kv * n_hb + hb) * (OWN_WEIGHT + nt);
-      const Range r{own.each, own.rest, 0, 0};
-      const int c0 = cta_of(r, v + OWN_WEIGHT), c1 = nt <= OWN_WHOLE ? c0 : cta_of(r, v + OWN_WEIGHT + nt - 1);
-      if (c0 == c1) {
-        add_states<NV>(sum, p.state + (size_t)row * comb_stride(p.hd), 0, part == 0, p.hd, p.hd);
-      } else {  // (only the first part may have a slot of odd number)
-        const long long size = (long long)ja.own_hb * comb_stride(ja.own_hd);
-        const float* s = p.part + (hg - hb * ja.own_hb) * comb_stride(ja.own_hd);
-        if (part == 0) add_states<NV>(sum, s + (2 * c0 + (cut(r, c0) < v ? 1 : 0)) * size, 0, 1, ja.own_hd, p.hd);
-        const int c = c0 + 1 + part;
-        add_states<NV>(sum, s + 2 * c * size, 2 * WPR * size, c <= c1 ? (c1 - c) / WPR + 1 : 0, ja.own_hd, p.hd);
-      }
+  // up to five runs of states: own positions (first part, others), shared positions (first part, others of the even and of the
+  // odd blocks); one place in the code adds them
+  struct Run {
+    const float* s;
+    long long step;
+    int n, hd;
+  };
+  int from;
+  const int left = paged::seq_len(p, b, from), rw = own_rows(ja.own_hd), nt_own = (left + rw - 1) / rw;
+  const bool split_own = ja.own_hb && nt_own;
+  int c0_own = 0, c1_own = 0;
+  const float *s_own = p.state + (size_t)row * comb_stride(p.hd), *s_own_even = nullptr;
+  long long size_own = 0;
+  if (split_own) {
+    const int hb = hg / ja.own_hb, n_hb = (grp + ja.own_hb - 1) / ja.own_hb;
+    const int v = own_at + (kv * n_hb + hb) * (OWN_WEIGHT + nt_own);
+    const Range r{own.each, own.rest, 0, 0};
+    c0_own = cta_of(r, v + OWN_WEIGHT);
+    c1_own = nt_own <= OWN_WHOLE ? c0_own : cta_of(r, v + OWN_WEIGHT + nt_own - 1);
+    if (c0_own != c1_own) {  // (only the first part may have a slot of odd number)
+      size_own = (long long)ja.own_hb * comb_stride(ja.own_hd);
+      s_own_even = p.part + (hg - hb * ja.own_hb) * comb_stride(ja.own_hd);
+      s_own = s_own_even + (2 * c0_own + (cut(r, c0_own) < v ? 1 : 0)) * size_own;
     }
   }
   const long long room = (long long)p.max_blocks * p.page;
-  if (pre <= 0 || pre > room || mine != pre || len < pre) {
-    // the sequence has no shared part, or one that its group's first sequence does not have: then positions are missing
-    if (part == 0 && lane == 0 && h == 0 && mine != pre && mine > 0 && mine <= len) atomicOr(p.err, ERR_PAGE);
-    return true;
+  const bool in = pre > 0 && pre <= room && mine == pre && len >= pre;
+  // a sequence that claims a shared part which its group's first sequence does not have misses positions
+  if (!in && part == 0 && lane == 0 && h == 0 && mine != pre && mine > 0 && mine <= len) atomicOr(p.err, ERR_PAGE);
+  int c0 = 0, c1 = 0, states = 0;
+  const float *s = nullptr, *s_even = nullptr;
+  long long size = 0, second = 0;
+  if (in) {
+    const int rows = (end - first) * grp, mt = ja.geo.mt, nt = (rows + mt - 1) / mt, nb = (pre + ja.geo.bk - 1) / ja.geo.bk;
+    const int i = (b - first) * grp + hg, tile = i / mt;
+    const bool pair = mt == 256;
+    const int big = pair ? 2 : 1, cost = pair ? block_cost<256>(rows, tile) : 1;  // numbers of a block, in full tiles and in this one
+    const int numbers = pair ? head_numbers<256>(rows, nt, nb) : head_numbers<128>(rows, nt, nb);
+    const int v = at + kv * numbers + tile * (SH_WEIGHT + big * nb);
+    const Range r{head.each, head.rest, 0, 0};
+    c0 = cta_of(r, v + SH_WEIGHT);
+    c1 = cta_of(r, v + SH_WEIGHT + cost * (nb - 1));
+    states = cost < big ? 2 : 1;  // even and odd blocks have states of their own
+    if (c0 == c1) {
+      s = a.whole + (size_t)row * comb_stride(p.hd);
+      second = (long long)p.n_seqs * p.nq * comb_stride(p.hd);
+    } else {
+      size = (long long)mt * comb_stride(ja.geo.hd);
+      second = size / 2;
+      s_even = a.parts + (i - tile * mt) * comb_stride(ja.geo.hd);
+      s = s_even + (2 * c0 + (cut(r, c0) < v ? 1 : 0)) * size;
+    }
   }
-  const int rows = (end - first) * grp, mt = ja.geo.mt, nt = (rows + mt - 1) / mt, nb = (pre + ja.geo.bk - 1) / ja.geo.bk;
-  const int i = (b - first) * grp + hg, tile = i / mt;
-  const bool pair = mt == 256;
-  const int big = pair ? 2 : 1, cost = pair ? block_cost<256>(rows, tile) : 1;  // numbers of a block, in full tiles and in this one
-  const int states = cost < big ? 2 : 1;                                        // even and odd blocks have states of their own
-  const int numbers = pair ? head_numbers<256>(rows, nt, nb) : head_numbers<128>(rows, nt, nb);
-  const int v = at + kv * numbers + tile * (SH_WEIGHT + big * nb);
-  const Range r{head.each, head.rest, 0, 0};
-  const int c0 = cta_of(r, v + SH_WEIGHT), c1 = cta_of(r, v + SH_WEIGHT + cost * (nb - 1));
-  if (c0 == c1) {
-    add_states<NV>(sum, a.whole + (size_t)row * comb_stride(p.hd), (long long)p.n_seqs * p.nq * comb_stride(p.hd), part == 0 ? states : 0, p.hd, p.hd);
-    return true;
-  }
-  const long long size = (long long)mt * comb_stride(ja.geo.hd), second = size / 2;
-  const float* s = a.parts + (i - tile * mt) * comb_stride(ja.geo.hd);
-  if (part == 0) add_states<NV>(sum, s + (2 * c0 + (cut(r, c0) < v ? 1 : 0)) * size, second, states, ja.geo.hd, p.hd);
-  const int c = c0 + 1 + part, n = c <= c1 ? (c1 - c) / WPR + 1 : 0;
 #pragma unroll 1
-  for (int k = 0; k < states; ++k) add_states<NV>(sum, s + k * second + 2 * c * size, 2 * WPR * size, n, ja.geo.hd, p.hd);
+  for (int k = 0; k < 5; ++k) {
+    Run x;
+    if (k < 2) {
+      const int c = c0_own + 1 + part;
+      x.hd = size_own ? ja.own_hd : p.hd;
+      x.s = k == 0 ? s_own : s_own_even + 2 * c * size_own;
+      x.step = 2 * WPR * size_own;
+      x.n = k == 0 ? part == 0 && (nt_own || !ja.own_hb) : c <= c1_own ? (c1_own - c) / WPR + 1 : 0;
+    } else {
+      const int c = c0 + 1 + part;
+      x.hd = size ? ja.geo.hd : p.hd;
+      x.s = k == 2 ? s : s_even + (k - 3) * second + 2 * c * size;
+      x.step = k == 2 ? second : 2 * WPR * size;
+      x.n = k == 2 ? (part == 0 ? states : 0) : k - 3 < states && c <= c1 ? (c1 - c) / WPR + 1 : 0;
+    }
+    if (x.n) add_states<NV>(sum, x.s, x.step, x.n, x.hd, p.hd);
+  }
   return true;
 }
 

@@ -132,17 +132,26 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
       do {
         const int nb = blocks_of(p, r.end);
         const bool two = p.c == 2;  // both halves have rows
-        if (!(ok = tc::mbar_wait(q_full, units & 1, err))) break;
+        if (!(ok = wait_for(q_full, units & 1, err))) break;
         ++units;
-        auto landed = [&](int i, uint32_t& addr) {  // tile i of the unit
+        // Tile i of the unit. A wait names a phase by its parity only, so that a chain sees every tile of a slot land, and no slot is
+        // filled again before both have: a tile of the other chain is waited for in its turn, too, and given back at once.
+        auto landed = [&](int i, uint32_t& addr) {
           const uint32_t n = tile0 + i, s = n % NS;
           addr = base + C::OFF_RING + s * C::TILE;
-          return tc::mbar_wait(full0 + 8 * s, n / NS & 1, err);
+          return wait_for(full0 + 8 * s, n / NS & 1, err);
         };
-        auto release = [&](int i) {  // (a tile expects both chains)
-          const uint32_t bar = empty0 + 8 * ((uint32_t)(tile0 + i) % NS);
-          if (!two) mbar_arrive(bar);
-          tc::mma_commit(bar);
+        auto release = [&](int i) { tc::mma_commit(empty0 + 8 * ((uint32_t)(tile0 + i) % NS)); };
+        int seen = 0;  // where the halves take even and odd blocks: tiles before it are used or passed by
+        auto pass_to = [&](int i) {
+          if (two) return true;
+          for (; seen < i; ++seen) {
+            uint32_t addr;
+            if (!landed(seen, addr)) return false;
+            mbar_arrive(empty0 + 8 * ((uint32_t)(tile0 + seen) % NS));
+          }
+          ++seen;
+          return true;
         };
         const uint32_t ql = desc_lo(base) + (two ? c * (128 * HD * 2 >> 4) : 0);
         auto products_s = [&](uint32_t k) {
@@ -158,7 +167,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
         int j = two ? 0 : c;
         bool first = true;
         uint32_t k, v;
-        if (j < nb && (ok = landed(k_tile(j), k))) {
+        if (j < nb && (ok = pass_to(k_tile(j)) && landed(k_tile(j), k))) {
           tc::tc_fence_after();
           if ((ok = turn())) {
             products_s(k);
@@ -169,7 +178,8 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
         for (; j < nb && ok; j += step) {
           const bool more = j + step < nb;
           // (the tiles landed long ago, mostly: their waits pass while the softmax is at work)
-          ok = !*s_abort && landed(v_tile(j, nb), v) && (!more || landed(k_tile(j + step), k)) && tc::mbar_wait(p_full, steps & 1, err) && turn();
+          ok = !*s_abort && pass_to(v_tile(j, nb)) && landed(v_tile(j, nb), v) && (!more || (pass_to(k_tile(j + step)) && landed(k_tile(j + step), k))) &&
+               wait_for(p_full, steps & 1, err) && turn();
           if (!ok) break;
           ++steps;
           tc::tc_fence_after();
@@ -183,59 +193,60 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
           release(v_tile(j, nb));
           if (more) release(k_tile(j + step));
         }
+        if (ok) ok = pass_to(2 * nb);
         mbar_arrive(idle);  // (so that no issuer is a unit behind)
         tile0 += 2 * nb;
       } while (ok && next_unit<MT, BK>(a, r.end, p));
       if (!ok) *s_abort = 1;
       tc::mma_commit(done + 8 * c);  // arrives once all products issued above are done
-      tc::mbar_wait(done + 8 * c, 0, err);
+      wait_for(done + 8 * c, 0, err);
     }
   } else {
     setmaxnreg_inc<192>();
     // ---- softmax: chain c, row `row` of its 128
     const int c = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), s_at = lanes + c * 128, o_at = lanes + C::O_COL + c * 128;
-    const float sc = fmaxf(fabsf(a.p.scale) * paged::LOG2E, 1e-38f);  // (not 0: masked scores stay -inf)
-    const float sign = a.p.scale > 0.f ? 1.f : a.p.scale < 0.f ? -1.f : 0.f;
+    // (the scale's sign goes to the queries; 0 becomes the least positive number, with which masked scores stay -inf and no
+    // finite score is above 1e-6)
+    const float sc = fmaxf(fabsf(a.p.scale) * paged::LOG2E, __uint_as_float(1u));
+    const uint32_t sign = a.p.scale < 0.f ? 0x80008000u : 0u;
     int block0 = 0, units = 0, steps = 0, segments = 0;
     bool ok = true;
     do {
       const int kv = p.u / p.nt, tile = p.u - kv * p.nt, nb = blocks_of(p, r.end);
       const bool two = p.c == 2;
-      if (units > 0 && !tc::mbar_wait(idle, (units - 1) & 1, err)) ok = false;  // (all products of the last unit are done)
+      if (units > 0 && !wait_for(idle, (units - 1) & 1, err)) ok = false;  // (all products of the last unit are done)
       const Row mine = row_of(a, p, kv, tile * MT + (two ? c * 128 : 0) + row);
       if (two || c == 0) {  // the queries of the warp's rows, a row at a time; zeros for rows that take no part
         constexpr int DL = HD / 32;  // dimensions of a lane
         const int d0 = lane * DL;
         const uint32_t at = base + c * (128 * HD * 2) + (d0 >> 6) * (128 * 128) + ((warp & 3) * 32) * 128 + (d0 & 7) * 2;
         const long long q_row = mine.in ? mine.b * a.p.q_stride + mine.h * a.p.hd : -1;
-        uint32_t w[32][DL / 2];  // (all in flight at once)
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += 8) {
+          uint32_t w[8][DL / 2];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const long long off = __shfl_sync(0xffffffffu, q_row, i);
-          const bool there = off >= 0 && d0 < a.p.hd;
-          const T* q = (const T*)a.p.q + (there ? off + d0 : 0);
-          if constexpr (DL == 4) {
-            uint2 x = make_uint2(0u, 0u);
-            if (there) x = *reinterpret_cast<const uint2*>(q);
-            w[i][0] = x.x;
-            w[i][1] = x.y;
-          } else {
-            w[i][0] = there ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+          for (int i = 0; i < 8; ++i) {
+            const long long off = __shfl_sync(0xffffffffu, q_row, i0 + i);
+            const bool there = off >= 0 && d0 < a.p.hd;
+            const T* q = (const T*)a.p.q + (there ? off + d0 : 0);
+            if constexpr (DL == 4) {
+              uint2 x = make_uint2(0u, 0u);
+              if (there) x = *reinterpret_cast<const uint2*>(q);
+              w[i][0] = x.x;
+              w[i][1] = x.y;
+            } else {
+              w[i][0] = there ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+            }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint32_t dst = at + i * 128 + ((((d0 >> 3) & 7) ^ (i & 7)) << 4);
-#pragma unroll
-          for (int d = 0; d < DL / 2; ++d) {
-            const float2 x = Pair<T>::unpack(w[i][d]);
-            w[i][d] = Pair<T>::pack(x.x * sign, x.y * sign);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t dst = at + (i0 + i) * 128 + ((((d0 >> 3) & 7) ^ i) << 4);
+            if constexpr (DL == 4)
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[i][0] ^ sign), "r"(w[i][1] ^ sign) : "memory");
+            else
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w[i][0] ^ sign) : "memory");
           }
-          if constexpr (DL == 4)
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[i][0]), "r"(w[i][1]) : "memory");
-          else
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w[i][0]) : "memory");
         }
         fence_proxy_async();
       }
@@ -246,56 +257,39 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
       const int n = two ? nb : c == 0 ? (nb + 1) / 2 : nb / 2;
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
-        if (*s_abort || !tc::mbar_wait(s_full0 + 8 * c, steps & 1, err)) ok = false;
+        if (*s_abort || !wait_for(s_full0 + 8 * c, steps & 1, err)) ok = false;
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         ++steps;
         tc::tc_fence_after();
-        uint32_t u[128];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tc::tmem_ld32_nowait(s_at + 32 * q, u + 32 * q);
-        tc::tmem_wait_ld();
-        const uint4 mask = *reinterpret_cast<const uint4*>(masks + ((block0 + (two ? i : 2 * i + c)) % TC_MASKS) * 4);
-        any |= (mask.x | mask.y | mask.z | mask.w) != 0u;
-        if ((mask.x & mask.y & mask.z & mask.w) != 0xffffffffu) {
-#pragma unroll
-          for (int q = 0; q < 32; ++q) {
-            if (!(mask.x >> q & 1)) u[q] = 0xff800000u;
-            if (!(mask.y >> q & 1)) u[32 + q] = 0xff800000u;
-            if (!(mask.z >> q & 1)) u[64 + q] = 0xff800000u;
-            if (!(mask.w >> q & 1)) u[96 + q] = 0xff800000u;
-          }
-        }
-        // Probabilities over the reference so far, and the block's maximum beside them (its comparisons run beside the
-        // exponentials); once more where the maximum lies too far above the reference, as in a unit's first block.
-        f32x2 acc[4];
-        const f32x2 c2 = pack2(sc, sc);
+        const uint32_t* mask = masks + ((block0 + (two ? i : 2 * i + c)) % TC_MASKS) * 4;
+        // the block's maximum, 64 positions at a time; scores of positions that are not there become -inf in TMEM
+        float mx = -INFINITY;
 #pragma unroll 1
-        while (true) {
-          const float ref = (m == -INFINITY ? 0.f : m) - PA_BIAS;
-          const f32x2 r2 = pack2(-ref, -ref);
-          float top[4];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t u[64];
+          tc::tmem_ld32_nowait(s_at + 64 * h, u);
+          tc::tmem_ld32_nowait(s_at + 64 * h + 32, u + 32);
+          tc::tmem_wait_ld();
+          const uint2 there = *reinterpret_cast<const uint2*>(mask + 2 * h);
+          any |= (there.x | there.y) != 0u;
+          if ((there.x & there.y) != 0xffffffffu) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            acc[q] = 0ull;
-            top[q] = -INFINITY;
-          }
-#pragma unroll
-          for (int q0 = 0; q0 < 64; q0 += 16) {
-            uint32_t pp[16];
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              const float x = __uint_as_float(u[2 * (q0 + q)]), y = __uint_as_float(u[2 * (q0 + q) + 1]);
-              top[q & 3] = max3(top[q & 3], x, y);
-              const float2 e = unpack2(fma2_to(pack2(x, y), c2, r2));
-              const float p0 = ex2(e.x), p1 = ex2(e.y);
-              acc[q & 3] = add2(acc[q & 3], pack2(p0, p1));
-              pp[q] = Pair<T>::pack(p0, p1);
+            for (int q = 0; q < 32; ++q) {
+              if (!(there.x >> q & 1)) u[q] = 0xff800000u;
+              if (!(there.y >> q & 1)) u[32 + q] = 0xff800000u;
             }
-            tmem_st16(s_at + q0, pp);
+            tc::tmem_st32(s_at + 64 * h, u);
+            tc::tmem_st32(s_at + 64 * h + 32, u + 32);
+            tc::tmem_wait_st();
           }
-          const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc;
-          const bool move = mx > m + MOVE_AT || (m == -INFINITY && mx > m);
-          if (!__any_sync(0xffffffffu, move)) break;
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int q = 0; q < 32; ++q) top[q & 3] = max3(top[q & 3], __uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]));
+          mx = fmaxf(mx, fmaxf(max3(top[0], top[1], top[2]), top[3]));
+        }
+        mx *= sc;
+        const bool move = mx > m + MOVE_AT || (m == -INFINITY && mx > m);
+        if (__any_sync(0xffffffffu, move)) {
           const float f = move ? ex2(m - mx) : 1.f;  // (0 where m is -inf)
           if (i > 0) {
 #pragma unroll 1
@@ -314,6 +308,24 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
           }
           __syncwarp();
         }
+        const float ref = (m == -INFINITY ? 0.f : m) - PA_BIAS;
+        const f32x2 c2 = pack2(sc, sc), r2 = pack2(-ref, -ref);
+        f32x2 acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {  // (the probabilities of a half go over scores that are used up)
+          uint32_t u[64];
+          tc::tmem_ld32_nowait(s_at + 64 * h, u);
+          tc::tmem_ld32_nowait(s_at + 64 * h + 32, u + 32);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            const float2 e = unpack2(fma2_to(pack2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1])), c2, r2));
+            const float p0 = ex2(e.x), p1 = ex2(e.y);
+            acc[q & 3] = add2(acc[q & 3], pack2(p0, p1));
+            u[q] = Pair<T>::pack(p0, p1);
+          }
+          tc::tmem_st32(s_at + 32 * h, u);
+        }
         const float2 s0 = unpack2(add2(acc[0], acc[1])), s1 = unpack2(add2(acc[2], acc[3]));
         l += (s0.x + s0.y) + (s1.x + s1.y);
         tc::tmem_wait_st();
@@ -321,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full0 + 8 * c);
       }
-      if (ok && n > 0 && !tc::mbar_wait(o_full0 + 8 * c, segments & 1, err)) ok = false;
+      if (ok && n > 0 && !wait_for(o_full0 + 8 * c, segments & 1, err)) ok = false;
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       if (n > 0) ++segments;
       tc::tc_fence_after();

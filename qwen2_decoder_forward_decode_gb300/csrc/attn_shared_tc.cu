@@ -108,11 +108,11 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
       bool ok = true;
       do {
         const int nb = blocks_of(p, r.end);
-        if (!(ok = tc::mbar_wait(q_full, units & 1, err))) break;
+        if (!(ok = wait_for(q_full, units & 1, err))) break;
         ++units;
         auto tile = [&](uint32_t& addr) {
           const int s = n % NS;
-          if (!tc::mbar_wait(full0 + 8 * s, n / NS & 1, err)) return false;
+          if (!wait_for(full0 + 8 * s, n / NS & 1, err)) return false;
           tc::tc_fence_after();
           addr = base + C::OFF_RING + s * C::TILE;
           return true;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
           if (*s_abort) ok = false;
           // S of the next block goes where P of the last one was, whose product was issued before
           if (ok && j + 1 < nb) ok = issue_s(block + 1);
-          if (!ok || !(ok = tc::mbar_wait(p_full0 + 8 * (block & 1), block >> 1 & 1, err))) break;
+          if (!ok || !(ok = wait_for(p_full0 + 8 * (block & 1), block >> 1 & 1, err))) break;
           uint32_t v;
           if (!(ok = tile(v))) break;
           const uint32_t vl = desc_lo(v, BK * 128), o = tmem + C::O_COL + (block & 1) * (C::NO - 1) * 128;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
       } while (ok && next_unit<MT, BK>(a, r.end, p));
       if (!ok) *s_abort = 1;
       tc::mma_commit(done);  // arrives once all products issued above are done
-      tc::mbar_wait(done, 0, err);
+      wait_for(done, 0, err);
     }
   } else {
     setmaxnreg_inc<192>();
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
       xch[(2 * (trades & 1) + half) * MT + row] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(pair);
-      if (!tc::mbar_wait(pair, trades & 1, err)) ok = false;
+      if (!wait_for(pair, trades & 1, err)) ok = false;
       __syncwarp();  // (TMEM is read and written by whole warps)
       const float other = xch[(2 * (trades & 1) + (half ^ 1)) * MT + row];
       ++trades;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
       float m = -INFINITY, l = 0.f, f_last = 1.f, c = 0.f;
       bool any = false;
       auto fold = [&](int j) {  // O of block j, whose probabilities moved the reference by f_last
-        if (!tc::mbar_wait(o_full0 + 8 * (j & 1), j >> 1 & 1, err)) {
+        if (!wait_for(o_full0 + 8 * (j & 1), j >> 1 & 1, err)) {
           ok = false;
           return;
         }
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
 #pragma unroll 1
       for (int j = 0; j < nb; ++j, ++block) {
         const int b = block & 1;
-        if (*s_abort || !tc::mbar_wait(s_full0 + 8 * b, block >> 1 & 1, err)) ok = false;
+        if (*s_abort || !wait_for(s_full0 + 8 * b, block >> 1 & 1, err)) ok = false;
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc::tc_fence_after();
         if (j == 0) c = fmaxf(sc * undo[row], 1e-38f);  // (not 0: masked scores stay -inf)

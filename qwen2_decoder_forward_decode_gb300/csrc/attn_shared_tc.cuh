@@ -9,6 +9,13 @@ namespace shared_attn {
 
 constexpr int TC_BK = 128, TC_PRODUCERS = 4, TC_MASKS = 16;
 
+// Every launch meets these kernels' code cold, and fetching it costs about a cycle a byte: what does not run in the main loop is
+// kept short (loops, one place for a piece of code, functions of their own).
+
+// Bounded wait, as tc::mbar_wait, with the waiting out of line.
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, int* err) { return tc::mbar_wait(bar, parity, err); }
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int* err) { return mbar_test(bar, parity) || wait_long(bar, parity, err); }
+
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -119,17 +126,19 @@ __device__ __forceinline__ void produce(const SharedArgs& a, const PageMaps& map
     }
     return x;
   };
-  auto request = [&](const void* cache, const CUtensorMap* map, int kv, const Rows& x) {
+  auto request = [&](bool values, int kv, const Rows& x) {
+    const void* cache = values ? a.p.v : a.p.k;
+    const CUtensorMap* map = values ? &maps.v : &maps.k;
     const int s = n % NS;
     const uint32_t full = full0 + 8 * s;
     if (n >= NS) {
       const uint32_t par = (n / NS & 1) ^ 1;
-      if (!mbar_test(empty0 + 8 * s, par)) {
+      if (!__all_sync(0xffffffffu, mbar_test(empty0 + 8 * s, par))) {  // (one answer for the warp: it announces together)
         if (told < n) {
           paged::cp_wait<0>();
           announce(n);
         }
-        if (!tc::mbar_wait(empty0 + 8 * s, par, a.p.err)) *s_abort = 1;
+        if (!wait_long(empty0 + 8 * s, par, a.p.err)) *s_abort = 1;
       }
     }
     if (*s_abort) ok = false;
@@ -151,7 +160,7 @@ __device__ __forceinline__ void produce(const SharedArgs& a, const PageMaps& map
       return;
     }
     const char* src = (const char*)cache + ch * 16;
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < 32 / RP; ++i) {
       const int row = i * RP + r0;
       const long long o = __shfl_sync(0xffffffffu, x.off, row);
@@ -166,19 +175,21 @@ __device__ __forceinline__ void produce(const SharedArgs& a, const PageMaps& map
   };
   do {
     const int kv = p.u / p.nt, t1 = p.t + blocks_of(p, r.end);
-    int id = entry(p.t);
-    Rows last{};
+    int id = entry(p.t), t = p.t;
+    Rows now{}, last{};
 #pragma unroll 1
-    for (int t = p.t; t < t1 && ok; ++t) {
-      const Rows now = find(kv, t, id);
-      if (t + 1 < t1) id = entry(t + 1);
-      if (lane == 0) masks[(block % TC_MASKS) * 4 + warp] = now.mask;
-      ++block;
-      request(a.p.k, &maps.k, kv, now);
-      if (t > p.t && ok) request(a.p.v, &maps.v, kv, last);
-      last = now;
+    for (int i = 0, end = 2 * (t1 - p.t); i < end && ok; ++i) {  // K_0, K_1, V_0, ..., V_{n-1}
+      const bool values = i > 0 && (i % 2 == 0 || i + 1 == end);
+      if (!values) {
+        last = now;
+        now = find(kv, t, id);
+        if (t + 1 < t1) id = entry(t + 1);
+        ++t;
+        if (lane == 0) masks[(block % TC_MASKS) * 4 + warp] = now.mask;
+        ++block;
+      }
+      request(values, kv, values && i + 1 < end ? last : now);
     }
-    if (ok) request(a.p.v, &maps.v, kv, last);
   } while (ok && next_unit<MT, TC_BK>(a, r.end, p));
   paged::cp_wait<0>();
   if (told < n) announce(n);

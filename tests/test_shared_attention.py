@@ -327,6 +327,22 @@ def test_calls_repeat_bit_by_bit_captured_and_on_other_streams(io, cache, hd):
     c.check(err=32, only=[0, 1, 3, 22, 23])  # (sequence 2 is now too short to share, and its own table has no such pages)
 
 
+@pytest.mark.parametrize("io,cache,hd,page", [("bf16", "bf16", 128, 64), ("f16", "f16", 64, 16), ("f32", "f16", 128, 64), ("bf16", "bf16", 128, 5)])
+def test_many_calls_of_many_units_agree(io, cache, hd, page):
+    """Short and long groups of few rows in turn, hundreds of times: a wait that is answered for another tile, or a tile that
+    is given back twice, shows as other bits or as a wait that runs out."""
+    rng = np.random.default_rng(hd)
+    groups = [(int(p), [int(p) + int(rng.integers(0, 40))] * int(rng.integers(1, 3))) for p in rng.integers(1, 1500, 200)]
+    c = Call(groups, 28, 4, hd, page, io, cache)
+    c.run()
+    c.check()
+    out, lse = c.out.clone(), c.lse.clone()
+    for _ in range(400):
+        c.run()
+    torch.cuda.synchronize()
+    assert int(c.err) == 0 and torch.equal(c.out.view(torch.uint8), out.view(torch.uint8)) and torch.equal(c.lse, lse)
+
+
 def test_two_streams_with_their_own_workspaces():
     calls = [Call([(900, [920, 910]), (200, [222] * 9)], 12, 2, 128, 16, "bf16", "bf16", seed=i) for i in range(2)]
     streams = [torch.cuda.Stream() for _ in calls]
