@@ -207,9 +207,8 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
     const int c = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), s_at = lanes + c * 128, o_at = lanes + C::O_COL + c * 128;
     // (the scale's sign goes to the queries; 0 becomes the least positive number, with which masked scores stay -inf and no
-    // finite score is above 1e-6)
+    // finite score lies further than 1e-6 from 0)
     const float sc = fmaxf(fabsf(a.p.scale) * paged::LOG2E, __uint_as_float(1u));
-    const uint32_t sign = a.p.scale < 0.f ? 0x80008000u : 0u;
     int block0 = 0, units = 0, steps = 0, segments = 0;
     bool ok = true;
     do {
@@ -217,35 +216,28 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
       const bool two = p.c == 2;
       if (units > 0 && !wait_for(idle, (units - 1) & 1, err)) ok = false;  // (all products of the last unit are done)
       const Row mine = row_of(a, p, kv, tile * MT + (two ? c * 128 : 0) + row);
-      if (two || c == 0) {  // the queries of the warp's rows, a row at a time; zeros for rows that take no part
-        constexpr int DL = HD / 32;  // dimensions of a lane
-        const int d0 = lane * DL;
-        const uint32_t at = base + c * (128 * HD * 2) + (d0 >> 6) * (128 * 128) + ((warp & 3) * 32) * 128 + (d0 & 7) * 2;
+      if (two || c == 0) {  // the queries of the warp's rows, all requested at once; zeros for rows that take no part
+        constexpr int CH = HD / 8, RP = 32 / CH;  // chunks of a row, rows a step
+        const int ch = lane % CH, w0 = (warp & 3) * 32;
+        const uint32_t at = base + c * (128 * HD * 2) + (ch >> 3) * (128 * 128);
         const long long q_row = mine.in ? mine.b * a.p.q_stride + mine.h * a.p.hd : -1;
+#pragma unroll 4
+        for (int i = 0; i < 32; i += RP) {
+          const int rr = i + lane / CH;
+          const long long off = __shfl_sync(0xffffffffu, q_row, rr);
+          const bool there = off >= 0 && ch * 8 < a.p.hd;
+          paged::cp_async16_or_zero(at + (w0 + rr) * 128 + (((ch & 7) ^ (rr & 7)) << 4), (const T*)a.p.q + (there ? off + ch * 8 : 0), there);
+        }
+        paged::cp_commit();
+        paged::cp_wait<0>();
+        if (a.p.scale < 0.f) {  // (the scale's sign goes to the queries: each lane's own chunks)
 #pragma unroll 1
-        for (int i0 = 0; i0 < 32; i0 += 8) {
-          uint32_t w[8][DL / 2];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const long long off = __shfl_sync(0xffffffffu, q_row, i0 + i);
-            const bool there = off >= 0 && d0 < a.p.hd;
-            const T* q = (const T*)a.p.q + (there ? off + d0 : 0);
-            if constexpr (DL == 4) {
-              uint2 x = make_uint2(0u, 0u);
-              if (there) x = *reinterpret_cast<const uint2*>(q);
-              w[i][0] = x.x;
-              w[i][1] = x.y;
-            } else {
-              w[i][0] = there ? *reinterpret_cast<const uint32_t*>(q) : 0u;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t dst = at + (i0 + i) * 128 + ((((d0 >> 3) & 7) ^ i) << 4);
-            if constexpr (DL == 4)
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[i][0] ^ sign), "r"(w[i][1] ^ sign) : "memory");
-            else
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w[i][0] ^ sign) : "memory");
+          for (int i = 0; i < 32; i += RP) {
+            const int rr = i + lane / CH;
+            uint4* x = reinterpret_cast<uint4*>(sh_smem + (at - base) + (w0 + rr) * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+            uint4 v = *x;
+            v.x ^= 0x80008000u; v.y ^= 0x80008000u; v.z ^= 0x80008000u; v.w ^= 0x80008000u;
+            *x = v;
           }
         }
         fence_proxy_async();

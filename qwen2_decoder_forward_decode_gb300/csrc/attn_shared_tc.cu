@@ -183,20 +183,29 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
         const int d0 = lane * DL;
         const uint32_t at = base + (d0 >> 6) * (MT * 128) + (d0 & 7) * 2;
         const long long q_row = mine.in ? mine.b * a.p.q_stride + mine.h * a.p.hd : -1;
-#pragma unroll 1
-        for (int i0 = 0; i0 < 16; i0 += 4) {
-          float x[4][DL];
+        float x[4][DL], next[4][DL];
+        auto fetch = [&](int i0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const long long off = __shfl_sync(0xffffffffu, q_row, half * 16 + i0 + i);
-            const float* q = (const float*)a.p.q + off + d0;
+            const bool there = off >= 0 && d0 < a.p.hd;
+            const float* q = (const float*)a.p.q + (there ? off + d0 : 0);
 #pragma unroll
             for (int d = 0; d < DL; d += 2) {
-              const float2 two = off >= 0 && d0 < a.p.hd ? *reinterpret_cast<const float2*>(q + d) : make_float2(0.f, 0.f);
-              x[i][d] = two.x * sign;
-              x[i][d + 1] = two.y * sign;
+              const float2 two = there ? *reinterpret_cast<const float2*>(q + d) : make_float2(0.f, 0.f);
+              next[i][d] = two.x;
+              next[i][d + 1] = two.y;
             }
           }
+        };
+        fetch(0);
+#pragma unroll 1
+        for (int i0 = 0; i0 < 16; i0 += 4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int d = 0; d < DL; ++d) x[i][d] = next[i][d] * sign;
+          if (i0 < 12) fetch(i0 + 4);  // (the next rows come while these are taken apart)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int rr = quarter * 32 + half * 16 + i0 + i;
