@@ -56,36 +56,16 @@ struct Sum {
   }
 };
 
-// Adds the states at s0, s0 + step, ..., n of them, 4 fetched at a time.
-template <int NV>
-__device__ __forceinline__ void add_states(Sum<NV>& sum, const float* s0, long long step, int n, int state_hd, int hd) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += 4) {
-    float2 ml[4];
-    float4 x[4][NV];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float* s = s0 + (i0 + i) * step;
-      ml[i] = i0 + i < n ? *reinterpret_cast<const float2*>(s + state_hd) : make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        x[i][v] = i0 + i < n && 4 * lane + 128 * v < hd ? *reinterpret_cast<const float4*>(s + 4 * lane + 128 * v) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum.add(ml[i].x, ml[i].y, x[i]);
-  }
-}
-
-// The sum of a row's states (the part `part` of WPR). What places them is loaded in three rounds: a warp waits for memory three
-// or four times, not once for each of a dozen numbers. false: the call's groups are bad.
-template <int NV, int WPR>
-__device__ __forceinline__ bool join_row(const JoinArgs& ja, int row, int part, Sum<NV>& sum) {
+// The sum of the states of head h of sequence b (of WPR warps, the part `part`). What places them is loaded in three rounds, and
+// the code is short: cold, it costs a cycle a byte. false: the call's groups are bad.
+template <int NV, int WPR, int MT>
+__device__ __forceinline__ bool join_row(const JoinArgs& ja, int b, int h, int part, Sum<NV>& sum) {
   const SharedArgs& a = ja.s;
   const PagedAttnArgs& p = a.p;
-  const int lane = threadIdx.x & 31, b = row / p.nq, h = row - b * p.nq, grp = p.nq / p.nkv, kv = h / grp, hg = h - kv * grp;
+  const int lane = threadIdx.x & 31, grp = p.nq / p.nkv, kv = h / grp, hg = h - kv * grp;
+  constexpr int BK = MT == 64 ? 64 : 128;
   sum.clear();
-  const SharedHead head = *a.head, own = ja.own_hb ? *a.own_head : SharedHead{0, 0, 0, 0};
+  const SharedHead head = *a.head, own = ja.own_hb ? *a.own_head : SharedHead{0, 1, 0, 0};
   const int mine = __ldg(p.skip + b), len = __ldg(p.lens + b), own_at = ja.own_hb ? a.own_at[b] : 0;
   // the last group that begins at or before b: 32 of them at a time
   int lo = 0, hi = a.n_groups;
@@ -97,86 +77,60 @@ __device__ __forceinline__ bool join_row(const JoinArgs& ja, int row, int part, 
     lo += last * step;
     hi = min(hi, lo + step);
   }
-  const int first = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1), at = a.at[lo];
-  const int pre = __ldg(p.skip + first);
+  const int first = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1), at = a.at[lo], pre = __ldg(p.skip + first);
   if (head.bad) return false;
-  // up to five runs of states: own positions (first part, others), shared positions (first part, others of the even and of the
-  // odd blocks); one place in the code adds them
-  struct Run {
-    const float* s;
-    long long step;
-    int n, hd;
-  };
   int from;
-  const int left = paged::seq_len(p, b, from), rw = own_rows(ja.own_hd), nt_own = (left + rw - 1) / rw;
-  const bool split_own = ja.own_hb && nt_own;
-  int c0_own = 0, c1_own = 0;
-  const float *s_own = p.state + (size_t)row * comb_stride(p.hd), *s_own_even = nullptr;
-  long long size_own = 0;
-  if (split_own) {
-    const int hb = hg / ja.own_hb, n_hb = (grp + ja.own_hb - 1) / ja.own_hb;
-    const int v = own_at + (kv * n_hb + hb) * (OWN_WEIGHT + nt_own);
-    const Range r{own.each, own.rest, 0, 0};
-    c0_own = cta_of(r, v + OWN_WEIGHT);
-    c1_own = nt_own <= OWN_WHOLE ? c0_own : cta_of(r, v + OWN_WEIGHT + nt_own - 1);
-    if (c0_own != c1_own) {  // (only the first part may have a slot of odd number)
-      size_own = (long long)ja.own_hb * comb_stride(ja.own_hd);
-      s_own_even = p.part + (hg - hb * ja.own_hb) * comb_stride(ja.own_hd);
-      s_own = s_own_even + (2 * c0_own + (cut(r, c0_own) < v ? 1 : 0)) * size_own;
-    }
-  }
+  const int left = paged::seq_len(p, b, from), rw = ja.own_hb ? own_rows(ja.own_hd) : 1, nt_own = (left + rw - 1) / rw;
+  const int hb_own = ja.own_hb == 16 ? hg >> 4 : hg >> 3, n_hb = ja.own_hb == 16 ? (grp + 15) >> 4 : (grp + 7) >> 3;
+  const int v_own = own_at + (kv * n_hb + hb_own) * (OWN_WEIGHT + nt_own);
   const long long room = (long long)p.max_blocks * p.page;
   const bool in = pre > 0 && pre <= room && mine == pre && len >= pre;
   // a sequence that claims a shared part which its group's first sequence does not have misses positions
   if (!in && part == 0 && lane == 0 && h == 0 && mine != pre && mine > 0 && mine <= len) atomicOr(p.err, ERR_PAGE);
-  int c0 = 0, c1 = 0, states = 0;
-  const float *s = nullptr, *s_even = nullptr;
-  long long size = 0, second = 0;
-  if (in) {
-    const int rows = (end - first) * grp, mt = ja.geo.mt, nt = (rows + mt - 1) / mt, nb = (pre + ja.geo.bk - 1) / ja.geo.bk;
-    const int i = (b - first) * grp + hg, tile = i / mt;
-    const bool pair = mt == 256;
-    const int big = pair ? 2 : 1, cost = pair ? block_cost<256>(rows, tile) : 1;  // numbers of a block, in full tiles and in this one
-    const int numbers = pair ? head_numbers<256>(rows, nt, nb) : head_numbers<128>(rows, nt, nb);
-    const int v = at + kv * numbers + tile * (SH_WEIGHT + big * nb);
-    const Range r{head.each, head.rest, 0, 0};
-    c0 = cta_of(r, v + SH_WEIGHT);
-    c1 = cta_of(r, v + SH_WEIGHT + cost * (nb - 1));
-    states = cost < big ? 2 : 1;  // even and odd blocks have states of their own
-    if (c0 == c1) {
-      s = a.whole + (size_t)row * comb_stride(p.hd);
-      second = (long long)p.n_seqs * p.nq * comb_stride(p.hd);
-    } else {
-      size = (long long)mt * comb_stride(ja.geo.hd);
-      second = size / 2;
-      s_even = a.parts + (i - tile * mt) * comb_stride(ja.geo.hd);
-      s = s_even + (2 * c0 + (cut(r, c0) < v ? 1 : 0)) * size;
-    }
-  }
+  const int rows = (end - first) * grp, nt = (rows + MT - 1) / MT, nb = (pre + BK - 1) / BK, i = (b - first) * grp + hg, tile = i / MT;
+  const int cost = block_cost<MT>(rows, tile);
+  const bool halves = MT == 256 && cost == 1;  // even and odd blocks have states of their own
+  const int v = at + kv * head_numbers<MT>(rows, nt, nb) + tile * (SH_WEIGHT + block_cost<MT>(MT, 0) * nb);
+  // the first and the last range of each list that has a part: lanes 0, 1 own positions, 2, 3 shared ones
+  const Range r = lane < 2 ? Range{max(own.each, 1), own.rest, 0, 0} : Range{max(head.each, 1), head.rest, 0, 0};
+  const int x = lane == 0 ? v_own + OWN_WEIGHT : lane == 1 ? v_own + OWN_WEIGHT + nt_own - 1 : lane == 2 ? v + SH_WEIGHT : v + SH_WEIGHT + cost * (nb - 1);
+  const int c = cta_of(r, x);
+  const int odd = cut(r, c) < (lane < 2 ? v_own : v);  // the slot's number, in the first range
+  const int c0_own = __shfl_sync(0xffffffffu, c, 0), c1_own = __shfl_sync(0xffffffffu, c, 1), odd_own = __shfl_sync(0xffffffffu, odd, 0);
+  const int c0 = __shfl_sync(0xffffffffu, c, 2), c1 = __shfl_sync(0xffffffffu, c, 3), odd_sh = __shfl_sync(0xffffffffu, odd, 2);
+  const size_t row = (size_t)b * p.nq + h;
+  const bool split_own = ja.own_hb && nt_own > OWN_WHOLE && c0_own != c1_own, split = in && c0 != c1;
+  const int n_own = ja.own_hb && !nt_own ? 0 : split_own ? c1_own - c0_own + 1 : 1;
+  const int n = n_own + (!in ? 0 : (c1 - c0 + 1) << halves);
+  const int hd_own = split_own ? ja.own_hd : p.hd, hd_sh = split ? ja.geo.hd : p.hd;
+  const float* s_own = split_own ? p.part + (hg - hb_own * ja.own_hb) * comb_stride(ja.own_hd) : p.state + row * comb_stride(p.hd);
+  const float* s_sh = split ? a.parts + (i - tile * MT) * comb_stride(ja.geo.hd) : a.whole + row * comb_stride(p.hd);
+  const long long slot_own = split_own ? ja.own_hb * comb_stride(ja.own_hd) : 0, slot_sh = split ? MT * comb_stride(ja.geo.hd) : 0;
+  const long long second = split ? MT / 2 * comb_stride(ja.geo.hd) : (long long)p.n_seqs * p.nq * comb_stride(p.hd);
 #pragma unroll 1
-  for (int k = 0; k < 5; ++k) {
-    Run x;
-    if (k < 2) {
-      const int c = c0_own + 1 + part;
-      x.hd = size_own ? ja.own_hd : p.hd;
-      x.s = k == 0 ? s_own : s_own_even + 2 * c * size_own;
-      x.step = 2 * WPR * size_own;
-      x.n = k == 0 ? part == 0 && (nt_own || !ja.own_hb) : c <= c1_own ? (c1_own - c) / WPR + 1 : 0;
-    } else {
-      const int c = c0 + 1 + part;
-      x.hd = size ? ja.geo.hd : p.hd;
-      x.s = k == 2 ? s : s_even + (k - 3) * second + 2 * c * size;
-      x.step = k == 2 ? second : 2 * WPR * size;
-      x.n = k == 2 ? (part == 0 ? states : 0) : k - 3 < states && c <= c1 ? (c1 - c) / WPR + 1 : 0;
+  for (int j0 = part; j0 < n; j0 += 4 * WPR) {
+    float2 ml[4];
+    float4 o[4][NV];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int j = j0 + q * WPR, js = j - n_own, k = j < n_own ? j : js >> halves;
+      const bool is_own = j < n_own;
+      const int slot = 2 * ((is_own ? c0_own : c0) + k) + (k == 0 ? (is_own ? odd_own : odd_sh) : 0), hd = is_own ? hd_own : hd_sh;
+      const float* s = is_own ? s_own + slot * slot_own : s_sh + slot * slot_sh + (halves && (js & 1) ? second : 0);
+      ml[q] = j < n ? *reinterpret_cast<const float2*>(s + hd) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int w = 0; w < NV; ++w)
+        o[q][w] = j < n && 4 * lane + 128 * w < p.hd ? *reinterpret_cast<const float4*>(s + 4 * lane + 128 * w) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if (x.n) add_states<NV>(sum, x.s, x.step, x.n, x.hd, p.hd);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum.add(ml[q].x, ml[q].y, o[q]);
   }
   return true;
 }
 
 template <int NV, typename IO>
-__device__ __forceinline__ void write_row(const PagedAttnArgs& p, int row, const Sum<NV>& s) {
-  const int lane = threadIdx.x & 31, b = row / p.nq, h = row - b * p.nq;
+__device__ __forceinline__ void write_row(const PagedAttnArgs& p, int b, int h, const Sum<NV>& s) {
+  const int lane = threadIdx.x & 31;
   // l = 0: no position was left, and out is 0; or every score was -inf, and 0 / 0 is the formula's NaN
   const float inv = s.l == 0.f && s.m == -INFINITY ? 1.f : 1.f / s.l;
 #pragma unroll
@@ -186,27 +140,26 @@ __device__ __forceinline__ void write_row(const PagedAttnArgs& p, int row, const
       paged::store4((IO*)p.out + b * p.out_stride + h * p.hd + d,
                     make_float4(s.o[i].x * inv, s.o[i].y * inv, s.o[i].z * inv, s.o[i].w * inv));
   }
-  if (lane == 0 && p.lse) p.lse[row] = (s.m - PA_BIAS + log2f(s.l)) * paged::LN2;
+  if (lane == 0 && p.lse) p.lse[(size_t)b * p.nq + h] = (s.m - PA_BIAS + log2f(s.l)) * paged::LN2;
 }
 
-template <int NV, int WPR, typename IO>
-__global__ void __launch_bounds__(JN_THREADS) join_kernel(const JoinArgs ja) {
+// A row a warp, or a CTA where rows are few and their parts may be many; blockIdx.y is the sequence.
+template <int NV, int WPR, int MT, typename IO>
+__global__ void __launch_bounds__(JN_THREADS) join_kernel(const __grid_constant__ JoinArgs ja) {
   const PagedAttnArgs& p = ja.s.p;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = p.n_seqs * p.nq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
   pdl_wait();
   Sum<NV> sum;
   if constexpr (WPR == 1) {
-#pragma unroll 1
-    for (int row = blockIdx.x * JN_WARPS + warp; row < rows; row += gridDim.x * JN_WARPS) {
-      join_row<NV, 1>(ja, row, 0, sum);
-      write_row<NV, IO>(p, row, sum);
-    }
+    const int h = blockIdx.x * JN_WARPS + warp;
+    if (h >= p.nq) return;
+    join_row<NV, 1, MT>(ja, b, h, 0, sum);
+    write_row<NV, IO>(p, b, h, sum);
   } else {
     static_assert(WPR == JN_WARPS, "a CTA a row");
     __shared__ float2 s_ml[JN_WARPS];
     __shared__ float4 s_o[JN_WARPS][NV * 32];
-    const int row = blockIdx.x;
-    join_row<NV, WPR>(ja, row, warp, sum);
+    join_row<NV, WPR, MT>(ja, b, blockIdx.x, warp, sum);
     if (lane == 0) s_ml[warp] = make_float2(sum.m, sum.l);
 #pragma unroll
     for (int i = 0; i < NV; ++i) s_o[warp][32 * i + lane] = sum.o[i];
@@ -219,20 +172,21 @@ __global__ void __launch_bounds__(JN_THREADS) join_kernel(const JoinArgs ja) {
       for (int i = 0; i < NV; ++i) x[i] = s_o[w][32 * i + lane];
       sum.add(s_ml[w].x, s_ml[w].y, x);
     }
-    write_row<NV, IO>(p, row, sum);
+    write_row<NV, IO>(p, b, blockIdx.x, sum);
   }
 }
 
-template <int NV, typename IO>
+template <int NV, int MT, typename IO>
 cudaError_t launch_join(const JoinArgs& ja, int nsm, cudaStream_t s) {
-  const int rows = ja.s.p.n_seqs * ja.s.p.nq;
-  if (rows <= 8 * nsm) return launch_k(join_kernel<NV, JN_WARPS, IO>, dim3(rows), dim3(JN_THREADS), 0, s, true, ja);
-  const int ctas = std::min((rows + JN_WARPS - 1) / JN_WARPS, 16 * nsm);
-  return launch_k(join_kernel<NV, 1, IO>, dim3(ctas), dim3(JN_THREADS), 0, s, true, ja);
+  const int nq = ja.s.p.nq, n = ja.s.p.n_seqs;
+  if (n * nq <= 8 * nsm) return launch_k(join_kernel<NV, JN_WARPS, MT, IO>, dim3(nq, n), dim3(JN_THREADS), 0, s, true, ja);
+  return launch_k(join_kernel<NV, 1, MT, IO>, dim3((nq + JN_WARPS - 1) / JN_WARPS, n), dim3(JN_THREADS), 0, s, true, ja);
 }
 template <typename IO>
 cudaError_t launch_join(const JoinArgs& ja, int nsm, cudaStream_t s) {
-  return ja.s.p.hd <= 128 ? launch_join<1, IO>(ja, nsm, s) : launch_join<2, IO>(ja, nsm, s);
+  if (ja.s.p.hd > 128) return launch_join<2, 64, IO>(ja, nsm, s);
+  if (ja.geo.mt == 64) return launch_join<1, 64, IO>(ja, nsm, s);
+  return launch_join<1, std::is_same<IO, float>::value ? 128 : 256, IO>(ja, nsm, s);
 }
 
 // The workspace: the counters and parts of attn_paged.cu, the head and the groups' places, states, parts.
