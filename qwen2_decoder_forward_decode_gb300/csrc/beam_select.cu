@@ -36,10 +36,16 @@ constexpr float BS_LOG2E_HI = 1.44269502162933349609375f, BS_LOG2E_LO = 1.925963
 constexpr double BS_LN2 = 0.693147180559945309417232121458;
 constexpr float BS_FAR = 1048576.f;  // maxima beyond it take the slow sum
 
+// The sum of a piece: of 2^(z log2(e) - ref) in units of 2^-38, which add and shift without rounding and fast (64-bit floating
+// point costs 30 to 40 cycles an operation here), or, where the largest logit lies far out, of exp(z - ref), a double.
+constexpr int BS_UNIT = 38;
 struct PieceState {
-  double sum;  // of 2^(z log2(e) - ref), or of exp(z - ref)
+  union {
+    u64 units;
+    double sum;
+  };
   float ref;
-  int slow;    // which of the two
+  int slow;  // which of the two
 };
 struct BeamArgs {
   const void* logits;
@@ -54,13 +60,16 @@ struct BeamArgs {
   int* err;
 };
 
-// (logit, lower id first) as an integer; -0 counts as 0; NaN above everything
+// (logit, lower id first) as an integer; -0 counts as 0; a NaN's is any
 __device__ __forceinline__ uint32_t value_key(float z) {
   const uint32_t u = __float_as_uint(z + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
 constexpr uint32_t BS_NONE = 0x007fffffu;  // the key of -inf: every candidate's is above
+
+// units / 2^d for a whole number d >= 0 (or infinite)
+__device__ __forceinline__ u64 shifted(u64 units, float d) { return d < 64.f ? units >> (int)d : 0ull; }
 
 // 2^d of a whole number d <= 0, exactly; 0 below the normal numbers
 __device__ __forceinline__ float power2(float d) { return d < -126.f ? 0.f : __uint_as_float((uint32_t)(127 + (int)d) << 23); }
@@ -145,6 +154,7 @@ struct BeamShared {
   uint32_t sub[64 * 32];             // of their lanes, where the candidates are many
   u64 key[BS_CAP + BS_MAX_OUT];
   int work[2 * BS_MAX_OUT + 2], equals[2 * BS_MAX_OUT + 2];
+  u64 units[BS_NW];
   double sum[BS_NW];
   float ref[BS_NW];
   uint32_t most[BS_NW];
@@ -152,18 +162,19 @@ struct BeamShared {
   uint32_t bound;
 };
 
-// The largest key that `k` of the n keys reach, or one between it and the next larger; `least` if fewer than k are above
-// it. A warp; keys may be of any number.
-__device__ __forceinline__ uint32_t key_bound(const uint32_t* keys, int n, int k, uint32_t least, int lane) {
+// The largest key that `k` of a warp's keys (NR a lane, of any number) reach, or one between it and the next larger; `least` if
+// fewer than k are above it.
+template <int NR>
+__device__ __forceinline__ uint32_t key_bound(const uint32_t* keys, int k, uint32_t least) {
   uint32_t most = least, low = 0xffffffffu;
-#pragma unroll 1
-  for (int i = lane; i < n; i += 32) {
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
     most = max(most, keys[i]);
     low = min(low, keys[i]);
   }
   most = __reduce_max_sync(0xffffffffu, most);
   low = max(least, __reduce_min_sync(0xffffffffu, low));
-  if (n < k || most <= low) return n < k ? least : low;
+  if (most <= low) return low;
   // common leading bits are the bound's, the others are tried from the top
   int bit = 31 - __clz(most ^ low);
   uint32_t v = bit == 31 ? 0u : most >> (bit + 1) << (bit + 1);
@@ -171,13 +182,57 @@ __device__ __forceinline__ uint32_t key_bound(const uint32_t* keys, int n, int k
   for (; bit >= 0; --bit) {
     const uint32_t t = v | 1u << bit;
     int c = 0;
-#pragma unroll 4
-    for (int i = lane; i < n; i += 32) c += keys[i] >= t;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) c += keys[i] >= t;
     c = __reduce_add_sync(0xffffffffu, c);
     if (c >= k) v = t;
     if (c == k) break;
   }
   return max(v, least);
+}
+
+// The piece's bound and the chunks that reach it, in order: all above it, of those that equal it the first k. A warp.
+template <int NR>
+__device__ __noinline__ void choose_chunks(BeamShared& sh, int n, int k, int lane) {
+  uint32_t keys[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) keys[i] = 32 * i + lane < n ? sh.top[32 * i + lane] : 0u;
+  const uint32_t b = key_bound<NR>(keys, k, BS_NONE);
+  int n_work = 0, same = 0;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    if (32 * i >= n) break;
+    const uint32_t top = keys[i];
+    const unsigned eq = __ballot_sync(0xffffffffu, top == b && b > BS_NONE);
+    const bool take = top > b || (top == b && b > BS_NONE && same + __popc(eq & ((1u << lane) - 1u)) < k);
+    const unsigned mask = __ballot_sync(0xffffffffu, take);
+    if (take) sh.work[n_work + __popc(mask & ((1u << lane) - 1u))] = 32 * i + lane;
+    n_work += __popc(mask);
+    same += __popc(eq);
+  }
+  if (lane == 0) {
+    sh.bound = b;
+    sh.n_work = n_work;
+    sh.n = 0;
+  }
+}
+// A closer bound, of the lanes' maxima of those chunks (rare; more than a lane's registers should hold).
+__device__ __noinline__ void closer_bound(BeamShared& sh, int n_work, int k, int lane) {
+  uint32_t v = 0;
+#pragma unroll 1
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t t = v | 1u << bit;
+    int c = 0;
+#pragma unroll 4
+    for (int i = 0; i < n_work; ++i) c += sh.sub[i * 32 + lane] >= t;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (c >= k) v = t;
+    if (c == k) break;
+  }
+  if (lane == 0) {
+    sh.bound = max(v, sh.bound);
+    sh.n = 0;
+  }
 }
 
 template <typename T, bool WIDE>
@@ -220,7 +275,8 @@ __global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
     for (int q = 0; q < U; ++q) {
       const int c = c0 + q * BS_NW;
       if (c >= n) break;
-      const uint32_t top = __reduce_max_sync(0xffffffffu, value_key(now[q].top()));
+      const float lane_top = now[q].top();
+      const uint32_t top = __reduce_max_sync(0xffffffffu, lane_top == lane_top ? value_key(lane_top) : 0xffffffffu);  // (NaN above everything)
       if (lane == 0) sh.top[c] = top;
       most = max(most, top);
       if (top > far_low && top < far_high) {  // else nothing next to the others, or the piece takes the slow sum
@@ -245,12 +301,12 @@ __global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
     }
   }
   {
+    // (a lane's sum is below 2^11: halves of 25 bits, whose sums over the lanes fit 32)
     const float2 s0 = unpack2(acc[0]), s1 = unpack2(acc[1]);
-    double s = ((double)s0.x + (double)s0.y) + ((double)s1.x + (double)s1.y);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const u64 mine = any ? (u64)__float2ull_rn(s0.x * 0x1p38f) + __float2ull_rn(s0.y * 0x1p38f) + __float2ull_rn(s1.x * 0x1p38f) + __float2ull_rn(s1.y * 0x1p38f) : 0ull;
+    const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)mine & 0x1ffffffu), hi = __reduce_add_sync(0xffffffffu, (uint32_t)(mine >> 25));
     if (lane == 0) {
-      sh.sum[warp] = any ? s : 0.;
+      sh.units[warp] = ((u64)hi << 25) + lo;
       sh.ref[warp] = any ? ref : -INFINITY;
       sh.most[warp] = most;
     }
@@ -276,38 +332,30 @@ __global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
       double t = 0.;
 #pragma unroll
       for (int w = 0; w < BS_NW; ++w) t += sh.sum[w];
-      *state = PieceState{t, peak > BS_NONE ? m : -INFINITY, 1};
+      PieceState st;
+      st.sum = t;
+      st.ref = peak > BS_NONE ? m : -INFINITY;
+      st.slow = 1;
+      *state = st;
     }
   } else if (tid == 0) {
     float r = -INFINITY;
 #pragma unroll
     for (int w = 0; w < BS_NW; ++w) r = fmaxf(r, sh.ref[w]);
-    double t = 0.;
+    u64 t = 0;
 #pragma unroll
-    for (int w = 0; w < BS_NW; ++w)
-      if (sh.ref[w] > -INFINITY) t += sh.sum[w] * (double)power2(sh.ref[w] - r);
-    *state = PieceState{t, r, 0};
+    for (int w = 0; w < BS_NW; ++w) t += shifted(sh.units[w], r - sh.ref[w]);
+    PieceState st;
+    st.units = t;
+    st.ref = r;
+    st.slow = 0;
+    *state = st;
   }
 
   // ---- the piece's candidates
   if (warp == 0) {
-    const uint32_t b = key_bound(sh.top, n, k, BS_NONE, lane);
-    int n_work = 0, same = 0;
-#pragma unroll 1
-    for (int c0 = 0; c0 < n; c0 += 32) {
-      const uint32_t top = c0 + lane < n ? sh.top[c0 + lane] : 0u;
-      const unsigned eq = __ballot_sync(0xffffffffu, top == b && b > BS_NONE);
-      const bool take = top > b || (top == b && b > BS_NONE && same + __popc(eq & ((1u << lane) - 1u)) < k);
-      const unsigned mask = __ballot_sync(0xffffffffu, take);
-      if (take) sh.work[n_work + __popc(mask & ((1u << lane) - 1u))] = c0 + lane;
-      n_work += __popc(mask);
-      same += __popc(eq);
-    }
-    if (lane == 0) {
-      sh.bound = b;
-      sh.n_work = n_work;
-      sh.n = 0;
-    }
+    if (n <= 256) choose_chunks<8>(sh, n, k, lane);
+    else choose_chunks<BS_MAX_CHUNKS / 32>(sh, n, k, lane);
   }
   __syncthreads();
   const int n_work = sh.n_work;  // at most 2 k
@@ -337,13 +385,7 @@ __global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
     __syncthreads();
     if (sh.n <= BS_CAP) break;  // (the second bound: fewer than k lanes of 8 logits lie above it)
     __syncthreads();
-    if (warp == 0) {
-      const uint32_t b = key_bound(sh.sub, n_work * 32, k, bound, lane);
-      if (lane == 0) {
-        sh.bound = b;
-        sh.n = 0;
-      }
-    }
+    if (warp == 0) closer_bound(sh, n_work, k, lane);
     __syncthreads();
     bound = sh.bound;
   }
@@ -412,14 +454,34 @@ struct Best {
 // equal scores: the lower beam, then the larger logit, then the lower id
 __device__ __forceinline__ bool wins(int row, u64 key, int row2, u64 key2) { return row != row2 ? row < row2 : key > key2; }
 
+// ln(units 2^(ref - 38)), to 1e-12: units = 2^e x with x in [0.70, 1.42), and ln x = 2 atanh(t) = 2 (t + t^3 / 3 + ...) with
+// t = (x - 1) / (x + 1), |t| < 0.172, from an fp32 reciprocal and a Newton step. About 15 operations of 64 bits.
+__device__ __forceinline__ double ln_units(u64 units, float ref) {
+  if (units == 0) return -INFINITY;
+  int e = 63 - __clzll((long long)units);
+  u64 bits = units << (63 - e);  // the leading bit at the top
+  if (bits > 0xb504f333f9de6484ull) ++e;  // above sqrt(2)
+  const double x = (double)units * __longlong_as_double((long long)(1023 - e) << 52), y = x + 1.;
+  double r = (double)__frcp_rn((float)y);
+  r = r * (2. - y * r);
+  const double t = (x - 1.) * r, q = t * t;
+  double p = 1. / 13.;
+  p = p * q + 1. / 11.;
+  p = p * q + 1. / 9.;
+  p = p * q + 1. / 7.;
+  p = p * q + 1. / 5.;
+  p = p * q + 1. / 3.;
+  return 2. * (t + t * q * p) + ((double)ref + (double)(e - BS_UNIT)) * BS_LN2;
+}
+
 // ln of a row's sum of exponentials, with pieces that were summed from the definition; NaN if there is one. A warp.
 __device__ __noinline__ double far_norm(const PieceState* st, int n, int lane) {
   double m = -INFINITY, s = 0.;
   bool nan = false;
 #pragma unroll 1
   for (int p = lane; p < n; p += 32) {
-    if (st[p].ref == -INFINITY && st[p].sum == 0.) continue;  // nothing but -inf
-    const double x = (st[p].slow ? (double)st[p].ref : (double)st[p].ref * BS_LN2) + log(st[p].sum);
+    if (st[p].ref == -INFINITY) continue;  // nothing but -inf
+    const double x = st[p].slow ? (double)st[p].ref + log(st[p].sum) : (double)st[p].ref * BS_LN2 + log((double)st[p].units * 0x1p-38);
     if (x != x) {
       nan = true;
       continue;
@@ -428,7 +490,7 @@ __device__ __noinline__ double far_norm(const PieceState* st, int n, int lane) {
     s = s * exp(m - hi) + exp(x - hi);
     m = hi;
   }
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o; o >>= 1) {
     const double m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
     const double hi = fmax(m, m2);
@@ -441,8 +503,11 @@ __device__ __noinline__ double far_norm(const PieceState* st, int n, int lane) {
 __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
   __shared__ double s_norm[BS_MAX_BEAMS], s_score[BS_MAX_BEAMS], s_weight[BS_MAX_BEAMS];
   __shared__ float s_ref[BS_MAX_BEAMS];
+  __shared__ u64 s_units[BS_MAX_BEAMS];
   __shared__ int s_kind[BS_MAX_BEAMS];  // 0: no candidates, 1: the row's logits, 2: ended
   __shared__ Best s_head[BS_MAX_LISTS], s_run[32][BS_MAX_OUT];
+  __shared__ alignas(16) uint32_t s_high[BS_MAX_LISTS];  // upper halves of the heads' scores
+  __shared__ int s_pick[BS_MAX_OUT];
   __shared__ int s_surv[32], s_row[BS_MAX_OUT], s_token[BS_MAX_OUT], s_len[BS_MAX_OUT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.x, k = a.n_out, P = a.pieces;
   pdl_wait();
@@ -453,8 +518,9 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
     const bool ended = a.ended && a.ended[row];
     const bool bad = c != c || c == INFINITY || !(weight > 0.f && weight < INFINITY);
     const int kind = bad || c == -INFINITY ? 0 : ended ? 2 : 1;
-    double s = 0.;
-    float ref = NAN;  // NaN: s is the normaliser already
+    double far_s = 0.;
+    u64 s = 0;
+    float ref = NAN;  // NaN: far_s is the normaliser already
     if (kind == 1) {
       const PieceState* st = a.state + (size_t)row * P;
       bool far = false;
@@ -465,19 +531,21 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
         ref = fmaxf(ref, st[p].ref);
       }
       if (__any_sync(0xffffffffu, far)) {
-        s = far_norm(st, P, lane);
+        far_s = far_norm(st, P, lane);
         ref = NAN;
       } else {
         ref = warp_max(ref);
 #pragma unroll 1
-        for (int p = lane; p < P; p += 32) s += st[p].sum * (double)power2(st[p].ref - ref);
+        for (int p = lane; p < P; p += 32) s += shifted(st[p].units, ref - st[p].ref);
+#pragma unroll 1
         for (int o = P > 16 ? 16 : P > 8 ? 8 : P > 4 ? 4 : P > 2 ? 2 : P > 1 ? 1 : 0; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       }
     }
     if (lane == 0) {
       if (bad) atomicOr(a.err, ERR_NONFINITE);
       s_kind[w] = kind;
-      s_norm[w] = s;
+      s_norm[w] = far_s;
+      s_units[w] = s;
       s_ref[w] = ref;
       s_score[w] = c;
       s_weight[w] = weight;
@@ -485,9 +553,9 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
   }
   if (tid < 32) s_surv[tid] = -1;
   __syncthreads();
-  if (tid < a.beams && s_kind[tid] == 1) {  // one logarithm for all rows: 64-bit arithmetic is slow here
+  if (tid < a.beams && s_kind[tid] == 1) {  // one logarithm for all rows
     const float ref = s_ref[tid];
-    const double norm = ref == ref ? (double)ref * BS_LN2 + log(s_norm[tid]) : s_norm[tid];
+    const double norm = ref == ref ? ln_units(s_units[tid], ref) : s_norm[tid];
     s_norm[tid] = norm;
     if (!(fabs(norm) < INFINITY)) {
       s_kind[tid] = 0;
@@ -513,27 +581,42 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
   if (lists <= 32) {
     if (tid < lists) s_surv[tid] = tid;
   } else {  // the lists with the n_out best heads
-    for (int l = tid; l < lists; l += BS_NT) s_head[l] = best_of(l, 0);
+    if (tid < BS_MAX_LISTS) {
+      s_head[tid] = tid < lists ? best_of(tid, 0) : Best{0, 0};
+      s_high[tid] = (uint32_t)(s_head[tid].score >> 32);
+    }
     __syncthreads();
-    for (int l = tid; l < lists; l += BS_NT) {
-      const Best b = s_head[l];
-      if (!b.key) continue;
-      int rank = 0;
-#pragma unroll 4
-      for (int j = 0; j < lists; ++j) {
-        const u64 other = s_head[j].score;
-        rank += other > b.score || (other == b.score && s_head[j].key && wins(j / P, s_head[j].key, l / P, b.key));
+    static_assert(BS_MAX_LISTS <= BS_NT, "a list a thread");
+    const int l = tid;
+    const Best b = s_head[l];
+    if (b.key) {
+      const uint32_t mine = s_high[l];
+      int rank = 0, same = 0;
+#pragma unroll 2
+      for (int j = 0; j < lists; j += 4) {  // (behind the last list are zeros)
+        const uint4 h = *reinterpret_cast<const uint4*>(s_high + j);
+        rank += (h.x > mine) + (h.y > mine) + (h.z > mine) + (h.w > mine);
+        same += (h.x == mine) + (h.y == mine) + (h.z == mine) + (h.w == mine);
+      }
+      if (same > 1) {  // before it: better, or equal and of a lower beam, or of this one with a better key
+        const int l0 = l / P * P;
+#pragma unroll 1
+        for (int j = 0; j < lists; ++j) {
+          const Best o = s_head[j];
+          rank += s_high[j] == mine && (o.score > b.score || (o.score == b.score && o.key && (j < l0 || (j < l0 + P && o.key > b.key))));
+        }
       }
       if (rank < k) s_surv[rank] = l;
     }
   }
   __syncthreads();
+#pragma unroll 1
   for (int x = tid; x < 32 * k; x += BS_NT) {
     const int i = x / k, r = x - i * k, list = s_surv[i];
     // a list behind i better heads has k - i candidates
     s_run[i][r] = list >= 0 && (lists <= 32 || i + r < k) ? best_of(list, r) : Best{0, 0};
   }
-  if (tid < k) s_row[tid] = -1;
+  if (tid < k) s_pick[tid] = -1;
   __syncthreads();
   if (warp == 0) {  // a list a lane, the best head taken n_out times
     const int list = s_surv[lane], w = list >= 0 ? list / P : 0;
@@ -554,44 +637,62 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
           best = other;
       }
       if (lane == best) {
-        const int row = g * a.beams + w, o = g * k + i;
-        const bool old = s_kind[w] == 2;
-        const int token = old ? a.end_id : (int)(0xffffffffu - (uint32_t)b.key);
-        a.parents[o] = row;
-        a.tokens[o] = token;
-        a.scores_out[o] = (float)score_of(w, b.key);
-        if (a.ended_out) a.ended_out[o] = old || token == a.end_id;
-        s_row[i] = row;
-        s_token[i] = old ? -1 : token;
+        s_pick[i] = lane * BS_MAX_OUT + at;
         b = ++at < k ? s_run[lane][at] : Best{0, 0};
       }
     }
   }
   __syncthreads();
-  for (int i = tid; i < k; i += BS_NT) {
-    const int o = g * k + i;
-    if (s_row[i] >= 0) continue;  // fewer candidates than places
-    a.parents[o] = a.tokens[o] = -1;
-    a.scores_out[o] = -INFINITY;
-    if (a.ended_out) a.ended_out[o] = 1;
-    if (a.history) a.lens_out[o] = 0;
+  if (tid < k) {  // a candidate a thread
+    const int pick = s_pick[tid], o = g * k + tid;
+    int row = -1, token = -1;
+    if (pick >= 0) {
+      const int i = pick / BS_MAX_OUT, w = s_surv[i] / P;
+      const u64 key = s_run[i][pick % BS_MAX_OUT].key;
+      const bool old = s_kind[w] == 2;
+      row = g * a.beams + w;
+      token = old ? a.end_id : (int)(0xffffffffu - (uint32_t)key);
+      a.scores_out[o] = (float)score_of(w, key);
+      if (a.ended_out) a.ended_out[o] = old || token == a.end_id;
+      s_token[tid] = old ? -1 : token;
+    } else {  // fewer candidates than places
+      a.scores_out[o] = -INFINITY;
+      if (a.ended_out) a.ended_out[o] = 1;
+    }
+    a.parents[o] = row;
+    a.tokens[o] = token;
+    s_row[tid] = row;
   }
   if (!a.history) return;
+  __syncthreads();
+#pragma unroll 1
   for (int i = tid; i < k; i += BS_NT) {
     const int row = s_row[i], held = row >= 0 ? a.lens[row] : 0, len = max(0, min(held, a.width));
     s_len[i] = len;
-    if (row < 0) continue;
+    if (row < 0) {
+      a.lens_out[g * k + i] = 0;
+      continue;
+    }
     const bool grows = s_token[i] >= 0, fits = len < a.width;
     if (grows && fits) a.history_out[(size_t)(g * k + i) * a.width + len] = s_token[i];
     a.lens_out[g * k + i] = len + (grows && fits);
     if (held != len || (grows && !fits)) atomicOr(a.err, ERR_CAPACITY);
   }
   __syncthreads();
-  const int step = (a.width + 31) / 32 * 32;  // (a warp stays within a history)
-#pragma unroll 4
-  for (long long x = tid; x < (long long)k * step; x += BS_NT) {
-    const int i = (int)(x / step), j = (int)(x - (long long)i * step);
-    if (j < s_len[i]) a.history_out[(size_t)(g * k + i) * a.width + j] = a.history[(size_t)s_row[i] * a.width + j];
+#pragma unroll 1
+  for (int i = warp; i < k; i += BS_NW) {  // a history a warp, 512 tokens in flight
+    const int n = s_len[i];
+    const int* src = a.history + (size_t)max(s_row[i], 0) * a.width;
+    int* dst = a.history_out + (size_t)(g * k + i) * a.width;
+#pragma unroll 1
+    for (int j0 = lane; j0 < n; j0 += 512) {
+      int x[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) x[q] = j0 + 32 * q < n ? src[j0 + 32 * q] : 0;
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (j0 + 32 * q < n) dst[j0 + 32 * q] = x[q];
+    }
   }
 }
 
