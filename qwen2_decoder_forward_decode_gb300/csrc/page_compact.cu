@@ -16,6 +16,7 @@
 namespace qw {
 namespace {
 
+constexpr int CP_MARK_THREADS = 1024;  // few CTAs: each adds its counts to every range's
 constexpr int CP_RANGES = 1024, CP_RANGE_MIN = 2048, CP_THREADS = 256, CP_SEG = 128;
 constexpr int CP_PAD = 8;  // a range's counter has a sector of its own
 constexpr size_t CP_HEAD = 64 + CP_RANGES * CP_PAD * 4;
@@ -39,26 +40,34 @@ struct CompactArgs {
   int* err;
 };
 
-__global__ void __launch_bounds__(CP_THREADS) compact_marks_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(CP_MARK_THREADS) compact_marks_kernel(const CompactArgs a) {
   __shared__ int s_free[CP_RANGES];  // the CTA's pages by range: a million would meet at few counters
   pdl_trigger();
-  for (int i = threadIdx.x; i < a.ranges; i += CP_THREADS) s_free[i] = 0;
+  for (int i = threadIdx.x; i < a.ranges; i += CP_MARK_THREADS) s_free[i] = 0;
   __syncthreads();
-  const int n_free = *a.n_free, first = blockIdx.x * CP_THREADS + threadIdx.x, step = gridDim.x * CP_THREADS;
+  const int n_free = *a.n_free, first = blockIdx.x * CP_MARK_THREADS + threadIdx.x, step = gridDim.x * CP_MARK_THREADS;
   const long long room = min((long long)a.max_blocks * a.page, 0x7fffffffll);
   int bad = 0;
   if (n_free < 0 || n_free > a.n_pages) {
     bad = ERR_CAPACITY;
   } else {
-#pragma unroll 4
-    for (int i = first; i < n_free; i += step) {
-      const int id = a.free_pages[i];
-      if (id < 0 || id >= a.n_pages) {
-        bad |= ERR_PAGE;
-        continue;
+#pragma unroll 1
+    for (long long i0 = first; i0 < n_free; i0 += 4ll * step) {
+      int id[4];
+      uint32_t was[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) id[q] = i0 + (long long)q * step < n_free ? a.free_pages[i0 + (long long)q * step] : -2;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        was[q] = 0;
+        if (id[q] >= 0 && id[q] < a.n_pages) {
+          was[q] = atomicOr(a.bits + (id[q] >> 5), 1u << (id[q] & 31)) >> (id[q] & 31) & 1;
+          atomicAdd(s_free + id[q] / a.range, 1);
+        } else if (i0 + (long long)q * step < n_free) {
+          bad |= ERR_PAGE;
+        }
       }
-      if (atomicOr(a.bits + (id >> 5), 1u << (id & 31)) >> (id & 31) & 1) bad |= ERR_PAGE;  // twice on the list
-      atomicAdd(s_free + id / a.range, 1);
+      if (was[0] | was[1] | was[2] | was[3]) bad |= ERR_PAGE;  // twice on the list
     }
   }
 #pragma unroll 1
@@ -71,7 +80,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_marks_kernel(const Compact
     atomicOr(a.err, bad);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.ranges; i += CP_THREADS)
+  for (int i = threadIdx.x; i < a.ranges; i += CP_MARK_THREADS)
     if (s_free[i]) atomicAdd(&a.head->free_in[i * CP_PAD], s_free[i]);
 }
 
@@ -189,18 +198,22 @@ __global__ void __launch_bounds__(CP_THREADS) compact_tables_kernel(const Compac
       const int b = t / a.segs, j0 = (t - b * a.segs) * CP_SEG;
       const int have = bad ? 0 : pages_of(a.lens[b], a.page), end = min(apart ? a.max_blocks : have, j0 + CP_SEG);
       const size_t row = (size_t)b * a.max_blocks;
-#pragma unroll 4
-      for (int j = j0 + lane; j < end; j += 32) {
-        int id = a.table[row + j];
-        if (j < have) {
-          if (id < 0 || id >= n) atomicOr(a.err, ERR_PAGE);
-          else if (id >= live) {
-            const int k = a.number[id];
-            if (k >= 0) id = a.dst[k];
-          }
-        }
-        a.table_out[row + j] = id;
+      static_assert(CP_SEG == 128, "four entries a lane");
+      int id[4], k[4];  // (the three loads of an entry wait for each other, those of four entries do not)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int j = j0 + lane + 32 * q;
+        id[q] = j < end ? a.table[row + j] : 0;
+        if (j < min(have, end) && (id[q] < 0 || id[q] >= n)) atomicOr(a.err, ERR_PAGE);
       }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) k[q] = j0 + lane + 32 * q < min(have, end) && id[q] >= live && id[q] < n ? a.number[id[q]] : -1;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (k[q] >= 0) id[q] = a.dst[k[q]];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (j0 + lane + 32 * q < end) a.table_out[row + j0 + lane + 32 * q] = id[q];
     }
   }
   __syncthreads();
@@ -263,8 +276,8 @@ qw_status qw_op_page_compact(int32_t n_seqs, int32_t page_size, int32_t n_pages,
     const int64_t want = (threads + CP_THREADS - 1) / CP_THREADS;
     return dim3((unsigned)(want < 1 ? 1 : want < 4 * nsm ? want : 4 * nsm));
   };
-  const int64_t most = n_pages > n_seqs ? n_pages : n_seqs, rows = (int64_t)n_seqs * segs * 32;
-  if ((e = launch_k(compact_marks_kernel, grid(most / 8 + 1), dim3(CP_THREADS), 0, s, false, a)) ||
+  const int64_t most = n_pages > n_seqs ? n_pages : n_seqs, marks = (most + 2 * CP_MARK_THREADS - 1) / (2 * CP_MARK_THREADS), rows = (int64_t)n_seqs * segs * 32;
+  if ((e = launch_k(compact_marks_kernel, dim3((unsigned)(marks < nsm ? marks : nsm)), dim3(CP_MARK_THREADS), 0, s, false, a)) ||
       (e = launch_k(compact_moves_kernel, dim3(ranges), dim3(CP_THREADS), 0, s, true, a)) ||
       (e = launch_k(compact_tables_kernel, grid(rows > n_pages / 32 ? rows : n_pages / 32), dim3(CP_THREADS), 0, s, true, a)))
     return op_cuda_fail(e, "page compaction launch");
