@@ -19,8 +19,9 @@ template <int HD>
 struct Cfg {
   static constexpr int LD = HD + 4;   // floats of a row: 8 rows' same 16 bytes lie in distinct banks
   static constexpr int PS = BK + 4;
-  static constexpr int SMEM = (MT + 2 * BK) * LD * 4 + MT * PS * 4;
-  static_assert(SMEM <= 226 * 1024, "shared memory");
+  static constexpr int SMEM = (MT + 2 * BK) * LD * 4;
+  static_assert(SMEM <= 226 * 1024 && (HD > 128 || SMEM <= 112 * 1024), "shared memory: two CTAs an SM up to 128 dimensions");
+  static_assert(MT * PS <= BK * LD, "probabilities take the keys' place");
 };
 
 // 4 elements at p as floats
@@ -38,7 +39,7 @@ __global__ void __launch_bounds__(THREADS, HD <= 128 ? 2 : 1) shared_simt_kernel
   constexpr int LD = C::LD, PS = C::PS, G4 = HD / 4, NC = HD / 64;  // groups of 4 dimensions; those of a thread
   extern __shared__ __align__(16) float sh_f[];
   __shared__ long long s_off[BK];
-  float *qs = sh_f, *ks = qs + MT * LD, *vs = ks + BK * LD, *ps = vs + BK * LD;
+  float *qs = sh_f, *ks = qs + MT * LD, *vs = ks + BK * LD, *ps = ks;  // (probabilities take the place of used keys)
   const int tid = threadIdx.x, x = tid & 15, y = tid >> 4;
   pdl_trigger();
   Unit p;
