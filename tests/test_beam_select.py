@@ -297,3 +297,30 @@ def test_many_groups():
     c = Call(rand_logits(3000, 300, "f16"), 2, 4, -3 * rng.random(3000), ended=rng.random(3000) < 0.1, end_id=0)
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("gap", [0, 1])
+@pytest.mark.parametrize("vocab", [100, 2000, 33000])
+def test_a_nan_anywhere_leaves_a_row_without_candidates(dtype, gap, vocab):
+    z = rand_logits(6, vocab, dtype, 3)
+    for row, at in enumerate((0, vocab - 1, vocab // 2, vocab // 3, 7)):
+        z[row, at] = float("nan")
+    z[1, vocab - 1] = -float("nan")
+    c = Call(z, 3, 4, [-1.0] * 6, gap=gap)
+    c.run()
+    c.check()
+    assert int(c.err) == 2 and c.parents[4:8].tolist() == [5] * 4
+
+
+def test_two_streams_with_their_own_workspaces():
+    calls = [Call(rand_logits(16, 40000, "bf16", i), 4, 8, -np.random.default_rng(i).random(16), width=30, seed=i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for s, c in zip(streams, calls):
+            with torch.cuda.stream(s):
+                c.run()
+    torch.cuda.synchronize()
+    for c in calls:
+        c.check()
