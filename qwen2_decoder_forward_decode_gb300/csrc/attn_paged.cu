@@ -76,7 +76,6 @@ __global__ void __launch_bounds__(MmaCfg<T, HD, HB, IO>::NT, 1) paged_mma_kernel
   const int group = a.nq / a.nkv, n_hb = (group + HB - 1) / HB, n_units = a.nkv * n_hb;
   float* comb = reinterpret_cast<float*>(pa_smem + NS * NW * Ld::STAGE);
   const uint32_t ring = smem_addr(pa_smem) + warp * NS * Ld::STAGE;
-  if (a.state) pdl_trigger();  // (the shared beginning's attention goes on beside this one)
   Place ld;
   const Range r = find_range<IO, TILE, V, C::NT>(a, n_units, ld);
   if (r.begin >= r.end) return;
@@ -343,14 +342,6 @@ size_t part_floats(int n_heads, int n_kv_heads, int head_dim) {
 }
 static_assert(PA_LEVELS * 2 * PA_MAX_CTAS * sizeof(unsigned int) <= OP_COUNTER_BYTES, "counters");
 
-cudaError_t launch_paged(int cache_dtype, int io_dtype, int nsm, const PagedAttnArgs& a, cudaStream_t s) {
-  const int ctas = nsm < PA_MAX_CTAS / 2 ? nsm : PA_MAX_CTAS / 2;
-  if (cache_dtype == QW_F32 || a.hd > 128) return launch_simt(cache_dtype, io_dtype, 2 * ctas, a, s);
-  if (cache_dtype == QW_F16)
-    return io_dtype == QW_F32 ? launch_16bit<f16, float>(ctas, a, s) : launch_16bit<f16, f16>(ctas, a, s);
-  return io_dtype == QW_F32 ? launch_16bit<bf16, float>(ctas, a, s) : launch_16bit<bf16, bf16>(ctas, a, s);
-}
-
 qw_status check_attention(const qw_paged_kv* cache, qw_paged_kv* norm, int32_t n_seqs, int32_t n_heads, int32_t max_blocks,
                           int32_t io_dtype, float scale) {
   qw_paged_kv c;
@@ -410,7 +401,13 @@ qw_status qw_op_paged_attention(const qw_paged_kv* cache, int32_t n_seqs, int32_
   PagedAttnArgs a{c.k, c.v, c.page_stride, c.head_stride, c.pos_stride, n_seqs, n_heads, c.n_kv_heads, c.head_dim,
                   c.page_size, c.n_pages, max_blocks, block_table, lens, q, out, q_stride, out_stride, scale, lse,
                   (unsigned int*)workspace, (float*)((char*)workspace + OP_COUNTER_BYTES), err_dev, nullptr, nullptr};
-  e = launch_paged(c.dtype, io_dtype, nsm, a, (cudaStream_t)cuda_stream);
+  cudaStream_t s = (cudaStream_t)cuda_stream;
+  const int ctas = nsm < PA_MAX_CTAS / 2 ? nsm : PA_MAX_CTAS / 2;
+  if (c.dtype == QW_F32 || c.head_dim > 128) e = launch_simt(c.dtype, io_dtype, 2 * ctas, a, s);
+  else if (c.dtype == QW_F16)
+    e = io_dtype == QW_F32 ? launch_16bit<f16, float>(ctas, a, s) : launch_16bit<f16, f16>(ctas, a, s);
+  else
+    e = io_dtype == QW_F32 ? launch_16bit<bf16, float>(ctas, a, s) : launch_16bit<bf16, bf16>(ctas, a, s);
   if (e) return op_cuda_fail(e, "paged attention launch");
   return QW_OK;
 }

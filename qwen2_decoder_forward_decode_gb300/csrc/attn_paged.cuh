@@ -132,8 +132,8 @@ __device__ __forceinline__ int seq_len(const PagedAttnArgs& a, int b) {
 }
 
 // The list weighs a unit's end (the merge of the warps, the next queries) like V tiles, in front of its own.
-// A place is tile t of nt of unit u of sequence b, whose len positions begin at `from`; v: where the list has the unit. All numbers of the
-// list fit 31 bits (the host refuses shapes that could hold more).
+// A place is tile t of nt of unit u of sequence b, whose len positions begin at `from`; v: where the list has the unit. All
+// numbers of the list fit 31 bits (the host refuses shapes that could hold more).
 struct Place {
   int b, u, t, nt, len, v, from;
 };
@@ -452,8 +452,7 @@ struct Finish {
 
 // attn_paged_simt.cu: fp32 caches, and heads of more than 128 dimensions
 cudaError_t launch_simt(int cache_dtype, int io_dtype, int ctas, const PagedAttnArgs& a, cudaStream_t s);
-// attn_paged.cu: the kernel that the shape takes, and the floats of its parts in the workspace
-cudaError_t launch_paged(int cache_dtype, int io_dtype, int nsm, const PagedAttnArgs& a, cudaStream_t s);
+// attn_paged.cu: the floats of a part in the workspace
 size_t part_floats(int n_heads, int n_kv_heads, int head_dim);
 // Shapes and pointers of attention over a paged cache, as both entry points check them; *norm is the cache with the strides
 // along extents of 1 set to 0.

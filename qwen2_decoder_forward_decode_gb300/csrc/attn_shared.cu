@@ -77,7 +77,7 @@ __device__ __forceinline__ bool join_row(const JoinArgs& ja, int b, int h, int p
     lo += last * step;
     hi = min(hi, lo + step);
   }
-  const int first = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1), at = a.at[lo], pre = __ldg(p.skip + first);
+  const int first = min(max(__ldg(a.cu + lo), 0), b), end = __ldg(a.cu + lo + 1), at = a.at[lo], pre = __ldg(p.skip + first);  // (bad ones stay inside)
   if (head.bad) return false;
   int from;
   const int left = paged::seq_len(p, b, from), rw = ja.own_hb ? own_rows(ja.own_hd) : 1, nt_own = (left + rw - 1) / rw;
@@ -277,7 +277,8 @@ qw_status qw_op_shared_attention(const qw_paged_kv* cache, int32_t n_seqs, int32
   const bool tc = c.dtype != QW_F32 && c.head_dim <= 128;
   ja.own_hb = !tc ? 0 : n_heads / c.n_kv_heads <= 8 ? 8 : 16;
   ja.own_hd = c.head_dim <= 32 && ja.own_hb == 8 ? 32 : c.head_dim <= 64 ? 64 : 128;
-  e = tc ? launch_own(c.dtype, io_dtype, ja.geo.ctas, ja.s, s) : paged::launch_paged(c.dtype, io_dtype, nsm, ja.s.p, s);
+  e = tc ? launch_own(c.dtype, io_dtype, ja.geo.ctas, ja.s, s)
+         : paged::launch_simt(c.dtype, io_dtype, 2 * std::min(nsm, paged::PA_MAX_CTAS / 2), ja.s.p, s);
   if (e) return op_cuda_fail(e, "shared attention launch");
   e = !tc ? launch_shared_simt(c.dtype, io_dtype, ja.geo.ctas, ja.s, s)
       : io_dtype == QW_F32 ? launch_shared_tc(c, ja.geo.ctas, ja.s, s)

@@ -41,12 +41,16 @@ struct ForkArgs {
   int* err;
 };
 
+// (a negative count is taken as 0: so a page's crossings of the line sum to what its end says, and every place in the list is
+// inside it)
+__device__ __forceinline__ int shares_of(const ForkArgs& a, int id) { return max(a.shares[id], 0); }
+
 __device__ __forceinline__ void hold(const ForkArgs& a, int* gone, int id, int d) {
   if (id < 0 || id >= a.n_pages) {
     atomicOr(a.err, ERR_PAGE);
     return;
   }
-  const int was = a.shares[id] + atomicAdd(a.delta + id, d), is = was + d;
+  const int was = shares_of(a, id) + atomicAdd(a.delta + id, d), is = was + d;
   if ((was < 0) != (is < 0)) atomicAdd(gone + id / a.range, is < 0 ? 1 : -1);
 }
 
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(FORK_POOL_THREADS) fork_pool_kernel(const Fork
       const long long id = base + s * FORK_POOL_THREADS + tid;
       bool g = false;
       if (id < end) {
-        const int d = a.delta[id], now = a.shares[id] + d;
+        const int d = a.delta[id], now = shares_of(a, (int)id) + d;
         g = d != 0 && now < 0;
         if (d) a.delta[id] = 0;
         if (d || a.shares_out != a.shares) a.shares_out[id] = g ? 0 : now;

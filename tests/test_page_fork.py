@@ -207,6 +207,17 @@ def test_bad_parents_and_pages_are_reported():
     assert taken(f.table, 8).reshape(2, 4)[0, 1] == pool.n_pages  # as it was
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_negative_counts_are_zeros(in_place):
+    pool = Pool([[60, 50], [33], [20, 20]], 4, 16)
+    f = Fork(pool, [0, 0, 0, 2, 2, 2, 2, 1, 3], in_place=in_place)
+    f.tshares[:pool.n_pages] = torch.where(f.tshares[:pool.n_pages] == 0, torch.full_like(f.tshares[:pool.n_pages], -3), f.tshares[:pool.n_pages])
+    f.run()
+    if in_place:  # (counts that nobody touched stay as they were)
+        f.shares[:pool.n_pages].clamp_(min=0)
+    f.check()
+
+
 def test_a_captured_fork_follows_the_device():
     """Two forks one after the other as a graph, there and back, with other parents at each replay."""
     from qwen2_decoder_forward_decode_gb300 import binding

@@ -244,6 +244,20 @@ def test_bad_groups_give_nothing(io, cache, hd, cu):
     c.check()
 
 
+@pytest.mark.parametrize("io,cache,hd", [("f32", "f16", 64), ("f32", "f32", 32), ("bf16", "bf16", 128), ("f32", "f16", 256)])
+@pytest.mark.parametrize("cu", [[-(1 << 30), 2, 4], [1 << 30, 2, 4], [0, 1 << 30, 4], [0, -(1 << 30), 4], [0, 2, 1 << 30], [-1, -1, -1]])
+def test_bounds_far_out_give_nothing(io, cache, hd, cu):
+    c = Call([(100, [110, 105]), (40, [40, 50])], 4, 2, hd, 16, io, cache)
+    c.tcu.copy_(torch.tensor(cu, dtype=torch.int32))
+    c.run()
+    got, lse = c.got()
+    assert int(c.err) & 32 and (got == 0).all() and np.isneginf(lse).all()
+    c.err.zero_()
+    c.tcu.copy_(torch.from_numpy(c.cu))
+    c.run()
+    c.check()
+
+
 @pytest.mark.parametrize("io,cache,hd", [("f32", "f16", 64), ("f32", "f32", 32)])
 def test_bad_shared_lengths_are_reported(io, cache, hd):
     c = Call([(100, [110, 105, 103]), (40, [40, 50])], 4, 2, hd, 16, io, cache)
