@@ -44,7 +44,7 @@ namespace {
 // What is rounded to fewer bits than fp32: an fp32 caller's queries and probabilities over fp16 caches to two pieces (22
 // bits of the row's largest element, the smallest step 2^-34 of it), the probabilities of 16-bit callers to two
 // pieces too (22 bits; bf16 16, for outputs of 8); exponentials are ex2's, good to 2^-22. The fp32 caller of a bf16
-// cache with groups of more than 8 heads of 128 keeps three pieces of 16 rows: 210 bytes a thread spill (with at most 8
+// cache with groups of more than 8 heads of 128 keeps three pieces of 16 rows: 234 bytes a thread spill (with at most 8
 // heads 20 bytes).
 template <typename T, int HD, int HB, typename IO>
 struct MmaCfg {
@@ -400,7 +400,7 @@ qw_status qw_op_paged_attention(const qw_paged_kv* cache, int32_t n_seqs, int32_
     return op_cuda_fail(e, "device query");
   PagedAttnArgs a{c.k, c.v, c.page_stride, c.head_stride, c.pos_stride, n_seqs, n_heads, c.n_kv_heads, c.head_dim,
                   c.page_size, c.n_pages, max_blocks, block_table, lens, q, out, q_stride, out_stride, scale, lse,
-                  (unsigned int*)workspace, (float*)((char*)workspace + OP_COUNTER_BYTES), err_dev, nullptr, nullptr};
+                  (unsigned int*)workspace, (float*)((char*)workspace + OP_COUNTER_BYTES), err_dev};
   cudaStream_t s = (cudaStream_t)cuda_stream;
   const int ctas = nsm < PA_MAX_CTAS / 2 ? nsm : PA_MAX_CTAS / 2;
   if (c.dtype == QW_F32 || c.head_dim > 128) e = launch_simt(c.dtype, io_dtype, 2 * ctas, a, s);

@@ -40,10 +40,15 @@ struct PagedAttnArgs {
   unsigned int* counters;  // [PA_LEVELS][2 * PA_MAX_CTAS], zero between calls
   float* part;             // [2 * PA_MAX_CTAS][HB][comb_stride(HD)]
   int* err;
-  // for attention that computes a shared beginning elsewhere, else null: the first positions of a sequence that are left
-  // out (none of them where the sequence is shorter), and the states [n_seqs][nq][comb_stride(hd)] that replace out and lse
+  static constexpr bool OWN = false;
+};
+// The same for attention that computes a shared beginning elsewhere: the first positions of a sequence that are left out (none
+// of them where the sequence is shorter), and the states [n_seqs][nq][comb_stride(hd)] that replace out and lse. The kernels
+// are templates of the two, so that calls without such a beginning pay nothing for it (0.2 us of 7 where they looked).
+struct OwnAttnArgs : PagedAttnArgs {
   const int* skip;
   float* state;
+  static constexpr bool OWN = true;
 };
 
 __host__ __device__ constexpr int comb_stride(int hd) { return hd + 4; }  // o, then m and l
@@ -109,24 +114,27 @@ __device__ __forceinline__ void split(float a, float b, uint32_t* piece) {
 // ---- the list of tiles ---------------------------------------------------------------------------------
 
 // the positions of a sequence that are attended to, and in `from` the first of them
-__device__ __forceinline__ int seq_len(const PagedAttnArgs& a, int b, int& from, bool& bad) {
+template <typename A>
+__device__ __forceinline__ int seq_len(const A& a, int b, int& from, bool& bad) {
   const long long room = (long long)a.max_blocks * a.page;
   int len = __ldg(a.lens + b);
   bad = len < 0 || len > room;
   len = len < 0 ? 0 : len > room ? (int)room : len;
   from = 0;
-  if (a.skip) {
+  if constexpr (A::OWN) {
     const int skip = __ldg(a.skip + b);
     bad |= skip < 0 || skip > room;
     if (skip > 0 && skip <= len) from = skip;
   }
   return len - from;
 }
-__device__ __forceinline__ int seq_len(const PagedAttnArgs& a, int b, int& from) {
+template <typename A>
+__device__ __forceinline__ int seq_len(const A& a, int b, int& from) {
   bool bad;
   return seq_len(a, b, from, bad);
 }
-__device__ __forceinline__ int seq_len(const PagedAttnArgs& a, int b) {
+template <typename A>
+__device__ __forceinline__ int seq_len(const A& a, int b) {
   int from;
   return seq_len(a, b, from);
 }
@@ -139,8 +147,8 @@ struct Place {
 };
 
 // The next tile; false behind the list's end `end` (as a number of the list).
-template <int TILE, int V>
-__device__ __forceinline__ bool advance(const PagedAttnArgs& a, int n_units, int end, Place& p) {
+template <int TILE, int V, typename A>
+__device__ __forceinline__ bool advance(const A& a, int n_units, int end, Place& p) {
   if (++p.t < p.nt) return p.v + V + p.t < end;
   p.t = 0;
   p.v += V + p.nt;
@@ -169,8 +177,8 @@ __device__ __forceinline__ int cta_of(const Range& r, int x) {
 }
 
 // The CTA's range and its first place. Every CTA sums the sequences' tiles itself (L2 serves the lengths).
-template <typename IO, int TILE, int V, int NT>
-__device__ __forceinline__ Range find_range(const PagedAttnArgs& a, int n_units, Place& first) {
+template <typename IO, int TILE, int V, int NT, typename A>
+__device__ __forceinline__ Range find_range(const A& a, int n_units, Place& first) {
   __shared__ int w_sum[NT / 32];
   __shared__ Place s_at[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -198,7 +206,7 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs& a, int n_units,
 #pragma unroll 1
     for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
       if (seq_len(a, b) > 0) continue;
-      if (a.state) {
+      if constexpr (A::OWN) {
 #pragma unroll 1
         for (int h = tid; h < a.nq; h += NT)
           *reinterpret_cast<float2*>(a.state + ((size_t)b * a.nq + h) * comb_stride(a.hd) + a.hd) = make_float2(-INFINITY, 0.f);
@@ -266,10 +274,11 @@ struct Loader {
   static __device__ __forceinline__ uint32_t at(int row, int chunk) { return (uint32_t)(row * CH + (chunk ^ (row & 7 & (CH - 1)))) * 16; }
   static_assert((CH & (CH - 1)) == 0, "chunks are permuted by exclusive or");
   // byte offset of the lane's row (lanes 0 .. RW - 1) in the caches, or -1: no such row
-  static __device__ __forceinline__ long long row(const PagedAttnArgs& a, const Place& p, int n_hb, int warp, int lane) {
+  template <typename A>
+  static __device__ __forceinline__ long long row(const A& a, const Place& p, int n_hb, int warp, int lane) {
     int j = p.t * TILE + warp * RW + lane;
     if (lane >= RW || j >= p.len) return -1;
-    j += p.from;
+    if constexpr (A::OWN) j += p.from;
     const int blk = j / a.page, id = __ldg(a.table + (size_t)p.b * a.max_blocks + blk);
     if (id < 0 || id >= a.n_pages) {
       if (p.u == 0) atomicOr(a.err, ERR_PAGE);
@@ -344,11 +353,12 @@ struct Finish {
     *reinterpret_cast<float4*>(row + d) = s.o;
     if (d == 0) *reinterpret_cast<float2*>(row + hd) = make_float2(s.m, s.l);
   }
-  static __device__ __forceinline__ void write_out(const PagedAttnArgs& a, const Place& p, int n_hb, int h, int d, const Acc& s) {
+  template <typename A>
+  static __device__ __forceinline__ void write_out(const A& a, const Place& p, int n_hb, int h, int d, const Acc& s) {
     const int group = a.nq / a.nkv, g = p.u / n_hb, hg = (p.u - g * n_hb) * HB + h;
     if (hg >= group || d >= a.hd) return;
     const int head = g * group + hg;
-    if (a.state) {
+    if constexpr (A::OWN) {
       put(a.state + ((size_t)p.b * a.nq + head) * comb_stride(a.hd), a.hd, d, s);
       return;
     }
@@ -366,8 +376,8 @@ struct Finish {
   // The CTA's state of the unit at p (comb: [NW][HB][CS] in shared memory, one per warp), covering tiles
   // [t0, t1) of it. All threads call it; comb may be written again afterwards. True if the unit is split:
   // its part then lies in the workspace, for join().
-  template <int NW>
-  static __device__ __forceinline__ bool unit(const PagedAttnArgs& a, const Range& r, const Place& p, int n_hb, const float* comb,
+  template <int NW, typename A>
+  static __device__ __forceinline__ bool unit(const A& a, const Range& r, const Place& p, int n_hb, const float* comb,
                                               int t0, int t1) {
     __syncthreads();
     const bool whole = t0 == 0 && t1 == p.nt;
@@ -388,8 +398,8 @@ struct Finish {
   // announces its part and merges the group if it is the last to; the group's first slot takes the sum. The
   // parts are fetched into shared memory (buf, all of the kernel's) together. Done once at the CTA's
   // end: an announcement takes a memory fence and an atomic's round trip, about 1 us, a level 2 us.
-  template <int V>
-  static __device__ __forceinline__ void join(const PagedAttnArgs& a, const Range& r, const Place* pend, int n, int n_hb, float* buf) {
+  template <int V, typename A>
+  static __device__ __forceinline__ void join(const A& a, const Range& r, const Place* pend, int n, int n_hb, float* buf) {
     constexpr int S4 = HB * CS / 4;
     // what is merged next: states of CTAs from, from + step, ...; the unit's first slot and its CTAs
     __shared__ int s_from[2], s_count[2], s_first[2], s_c0[2], s_c1[2], s_last[2];
@@ -452,6 +462,7 @@ struct Finish {
 
 // attn_paged_simt.cu: fp32 caches, and heads of more than 128 dimensions
 cudaError_t launch_simt(int cache_dtype, int io_dtype, int ctas, const PagedAttnArgs& a, cudaStream_t s);
+cudaError_t launch_simt(int cache_dtype, int io_dtype, int ctas, const OwnAttnArgs& a, cudaStream_t s);
 // attn_paged.cu: the floats of a part in the workspace
 size_t part_floats(int n_heads, int n_kv_heads, int head_dim);
 // Shapes and pointers of attention over a paged cache, as both entry points check them; *norm is the cache with the strides
@@ -459,8 +470,8 @@ size_t part_floats(int n_heads, int n_kv_heads, int head_dim);
 qw_status check_attention(const qw_paged_kv* cache, qw_paged_kv* norm, int32_t n_seqs, int32_t n_heads, int32_t max_blocks,
                           int32_t io_dtype, float scale);
 
-template <typename K>
-cudaError_t launch(K kernel, int threads, int smem, int ctas, const PagedAttnArgs& a, cudaStream_t s) {
+template <typename K, typename A>
+cudaError_t launch(K kernel, int threads, int smem, int ctas, const A& a, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   return e ? e : launch_k(kernel, dim3(ctas), dim3(threads), smem, s, false, a);
 }

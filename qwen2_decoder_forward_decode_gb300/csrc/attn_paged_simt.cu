@@ -38,8 +38,8 @@ __device__ __forceinline__ ulonglong2 lds4(const unsigned char* p, bf16) {
   return make_ulonglong2(pack2(bf_lo(u.x), bf_hi(u.x)), pack2(bf_lo(u.y), bf_hi(u.y)));
 }
 
-template <typename T, int HD, int HB, typename IO>
-__global__ void __launch_bounds__(SimtCfg<T, HD, HB>::NT, 2) paged_simt_kernel(const PagedAttnArgs a) {
+template <typename T, int HD, int HB, typename IO, typename A>
+__global__ void __launch_bounds__(SimtCfg<T, HD, HB>::NT, 2) paged_simt_kernel(const A a) {
   using C = SimtCfg<T, HD, HB>;
   using Ld = typename C::Ld;
   using Fin = Finish<IO, HB, HD, C::NT, C::SMEM>;
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(SimtCfg<T, HD, HB>::NT, 2) paged_simt_kernel(c
   float* ps = qs + HB * HD + warp * (RW + 1) * HB;  // [RW][HB] probabilities, then [HB] factors
   unsigned char* ring_p = pa_smem + warp * NS * Ld::STAGE;
   const uint32_t ring = smem_addr(ring_p);
-  if (a.state) pdl_trigger();  // (the shared beginning's attention goes on beside this one)
+  if constexpr (A::OWN) pdl_trigger();  // (the shared beginning's attention goes on beside this one)
   Place ld;
   const Range r = find_range<IO, TILE, V, C::NT>(a, n_units, ld);
   if (r.begin >= r.end) return;
@@ -258,20 +258,19 @@ __global__ void __launch_bounds__(SimtCfg<T, HD, HB>::NT, 2) paged_simt_kernel(c
   if (n_pend) Fin::template join<V>(a, r, pend, n_pend, n_hb, reinterpret_cast<float*>(pa_smem));
 }
 
-template <typename T, int HD, int HB, typename IO>
-cudaError_t run(int ctas, const PagedAttnArgs& a, cudaStream_t s) {
+template <typename T, int HD, int HB, typename IO, typename A>
+cudaError_t run(int ctas, const A& a, cudaStream_t s) {
   using C = SimtCfg<T, HD, HB>;
-  return launch(paged_simt_kernel<T, HD, HB, IO>, C::NT, C::SMEM, ctas, a, s);
+  return launch(paged_simt_kernel<T, HD, HB, IO, A>, C::NT, C::SMEM, ctas, a, s);
 }
 // groups of at most 4 heads take half the arithmetic
-template <typename T, int HD, typename IO>
-cudaError_t run(int ctas, const PagedAttnArgs& a, cudaStream_t s) {
+template <typename T, int HD, typename IO, typename A>
+cudaError_t run(int ctas, const A& a, cudaStream_t s) {
   return a.nq / a.nkv <= 4 ? run<T, HD, 4, IO>(ctas, a, s) : run<T, HD, 8, IO>(ctas, a, s);
 }
 
-}  // namespace
-
-cudaError_t launch_simt(int cache_dtype, int io_dtype, int ctas, const PagedAttnArgs& a, cudaStream_t s) {
+template <typename A>
+cudaError_t run(int cache_dtype, int io_dtype, int ctas, const A& a, cudaStream_t s) {
   if (cache_dtype == QW_F16)
     return io_dtype == QW_F32 ? run<f16, 256, float>(ctas, a, s) : run<f16, 256, f16>(ctas, a, s);
   if (cache_dtype == QW_BF16)
@@ -279,6 +278,15 @@ cudaError_t launch_simt(int cache_dtype, int io_dtype, int ctas, const PagedAttn
   return a.hd <= 32    ? run<float, 32, float>(ctas, a, s)
          : a.hd <= 64  ? run<float, 64, float>(ctas, a, s)
          : a.hd <= 128 ? run<float, 128, float>(ctas, a, s) : run<float, 256, float>(ctas, a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_simt(int cache_dtype, int io_dtype, int ctas, const PagedAttnArgs& a, cudaStream_t s) {
+  return run(cache_dtype, io_dtype, ctas, a, s);
+}
+cudaError_t launch_simt(int cache_dtype, int io_dtype, int ctas, const OwnAttnArgs& a, cudaStream_t s) {
+  return run(cache_dtype, io_dtype, ctas, a, s);
 }
 
 }  // namespace paged

@@ -61,7 +61,7 @@ struct Sum {
 template <int NV, int WPR, int MT>
 __device__ __forceinline__ bool join_row(const JoinArgs& ja, int b, int h, int part, Sum<NV>& sum) {
   const SharedArgs& a = ja.s;
-  const PagedAttnArgs& p = a.p;
+  const OwnAttnArgs& p = a.p;
   const int lane = threadIdx.x & 31, grp = p.nq / p.nkv, kv = h / grp, hg = h - kv * grp;
   constexpr int BK = MT == 64 ? 64 : 128;
   sum.clear();
@@ -129,7 +129,7 @@ __device__ __forceinline__ bool join_row(const JoinArgs& ja, int b, int h, int p
 }
 
 template <int NV, typename IO>
-__device__ __forceinline__ void write_row(const PagedAttnArgs& p, int b, int h, const Sum<NV>& s) {
+__device__ __forceinline__ void write_row(const OwnAttnArgs& p, int b, int h, const Sum<NV>& s) {
   const int lane = threadIdx.x & 31;
   // l = 0: no position was left, and out is 0; or every score was -inf, and 0 / 0 is the formula's NaN
   const float inv = s.l == 0.f && s.m == -INFINITY ? 1.f : 1.f / s.l;
@@ -146,7 +146,7 @@ __device__ __forceinline__ void write_row(const PagedAttnArgs& p, int b, int h, 
 // A row a warp, or a CTA where rows are few and their parts may be many; blockIdx.y is the sequence.
 template <int NV, int WPR, int MT, typename IO>
 __global__ void __launch_bounds__(JN_THREADS) join_kernel(const __grid_constant__ JoinArgs ja) {
-  const PagedAttnArgs& p = ja.s.p;
+  const OwnAttnArgs& p = ja.s.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
   pdl_wait();
   Sum<NV> sum;
@@ -261,9 +261,9 @@ qw_status qw_op_shared_attention(const qw_paged_kv* cache, int32_t n_seqs, int32
     return op_cuda_fail(e, "device query");
   char* ws = (char*)workspace;
   JoinArgs ja;
-  ja.s.p = PagedAttnArgs{c.k, c.v, c.page_stride, c.head_stride, c.pos_stride, n_seqs, n_heads, c.n_kv_heads, c.head_dim,
+  ja.s.p = OwnAttnArgs{{c.k, c.v, c.page_stride, c.head_stride, c.pos_stride, n_seqs, n_heads, c.n_kv_heads, c.head_dim,
                          c.page_size, c.n_pages, max_blocks, block_table, lens, q, out, q_stride, out_stride, scale, lse,
-                         (unsigned int*)ws, (float*)(ws + OP_COUNTER_BYTES), err_dev, shared_lens, (float*)(ws + y.own)};
+                         (unsigned int*)ws, (float*)(ws + OP_COUNTER_BYTES), err_dev}, shared_lens, (float*)(ws + y.own)};
   ja.s.n_groups = n_groups;
   ja.s.cu = cu_seqs;
   ja.s.head = (SharedHead*)(ws + y.head);

@@ -11,7 +11,7 @@ using paged::comb_stride;
 using paged::cta_of;
 using paged::cut;
 using paged::PA_BIAS;
-using paged::PagedAttnArgs;
+using paged::OwnAttnArgs;
 using paged::Range;
 
 constexpr int SH_MAX_CTAS = 160;  // of the tensor-core kernel, one an SM; the CUDA cores' kernel takes two
@@ -26,7 +26,7 @@ struct SharedHead {  // of the workspace
   int bad, each, rest, total;
 };
 struct SharedArgs {
-  PagedAttnArgs p;  // skip: the shared positions of each sequence; state: of the positions behind them
+  OwnAttnArgs p;  // skip: the shared positions of each sequence; state: of the positions behind them
   int n_groups;
   const int* cu;
   SharedHead* head;

@@ -35,7 +35,7 @@ template <int RW, int HB>
 __device__ __forceinline__ Range find_own(const SharedArgs& a, int n_units, Place& first) {
   __shared__ int w_sum[OWN_WARPS];
   __shared__ Place s_at[OWN_WARPS + 1];
-  const PagedAttnArgs& p = a.p;
+  const OwnAttnArgs& p = a.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.n_seqs + OWN_NT - 1) / OWN_NT, b0 = min(p.n_seqs, tid * per), b1 = min(p.n_seqs, b0 + per);
   int mine = 0;
@@ -101,7 +101,7 @@ template <typename T, int HD, int HB, typename IO>
 __global__ void __launch_bounds__(OWN_NT, 1) own_kernel(const SharedArgs sa) {
   using C = OwnCfg<T, HD, HB, IO>;
   using Ld = typename C::Ld;
-  const PagedAttnArgs& a = sa.p;
+  const OwnAttnArgs& a = sa.p;
   constexpr int NS = C::NS, R = C::R, NQ = C::NQ, NP = C::NP, CS = comb_stride(HD), TILE = Ld::TILE, V = OWN_WEIGHT;
   using Raw = typename std::conditional<C::F32IO, float2, uint32_t>::type;  // two query elements
   constexpr int NKK = HD / 16, NA = HB == 8 ? (NQ + 1) / 2 : NQ, NPA = HB == 8 ? (NP + 1) / 2 : NP;  // products per step
