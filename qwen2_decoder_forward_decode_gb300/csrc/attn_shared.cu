@@ -65,8 +65,7 @@ __device__ __forceinline__ bool join_row(const JoinArgs& ja, int b, int h, int p
   const int lane = threadIdx.x & 31, grp = p.nq / p.nkv, kv = h / grp, hg = h - kv * grp;
   constexpr int BK = MT == 64 ? 64 : 128;
   sum.clear();
-  const SharedHead head = *a.head, own = ja.own_hb ? *a.own_head : SharedHead{0, 1, 0, 0};
-  const int mine = __ldg(p.skip + b), len = __ldg(p.lens + b), own_at = ja.own_hb ? a.own_at[b] : 0;
+  const int mine = __ldg(p.skip + b), len = __ldg(p.lens + b);
   // the last group that begins at or before b: 32 of them at a time
   int lo = 0, hi = a.n_groups;
 #pragma unroll 1
@@ -77,7 +76,10 @@ __device__ __forceinline__ bool join_row(const JoinArgs& ja, int b, int h, int p
     lo += last * step;
     hi = min(hi, lo + step);
   }
-  const int first = min(max(__ldg(a.cu + lo), 0), b), end = __ldg(a.cu + lo + 1), at = a.at[lo], pre = __ldg(p.skip + first);  // (bad ones stay inside)
+  const int first = min(max(__ldg(a.cu + lo), 0), b), end = __ldg(a.cu + lo + 1), pre = __ldg(p.skip + first);  // (bad ones stay inside)
+  pdl_wait();  // (what stands above are the call's inputs, that no kernel of it writes)
+  const SharedHead head = *a.head, own = ja.own_hb ? *a.own_head : SharedHead{0, 1, 0, 0};
+  const int own_at = ja.own_hb ? a.own_at[b] : 0, at = a.at[lo];
   if (head.bad) return false;
   int from;
   const int left = paged::seq_len(p, b, from), rw = ja.own_hb ? own_rows(ja.own_hd) : 1, nt_own = (left + rw - 1) / rw;
@@ -90,10 +92,10 @@ __device__ __forceinline__ bool join_row(const JoinArgs& ja, int b, int h, int p
   const int rows = (end - first) * grp, nt = (rows + MT - 1) / MT, nb = (pre + BK - 1) / BK, i = (b - first) * grp + hg, tile = i / MT;
   const int cost = block_cost<MT>(rows, tile);
   const bool halves = MT == 256 && cost == 1;  // even and odd blocks have states of their own
-  const int v = at + kv * head_numbers<MT>(rows, nt, nb) + tile * (SH_WEIGHT + block_cost<MT>(MT, 0) * nb);
+  const int v = at + kv * head_numbers<MT>(rows, nt, nb) + tile * (unit_weight<MT>(block_cost<MT>(MT, 0)) + block_cost<MT>(MT, 0) * nb);
   // the first and the last range of each list that has a part: lanes 0, 1 own positions, 2, 3 shared ones
   const Range r = lane < 2 ? Range{max(own.each, 1), own.rest, 0, 0} : Range{max(head.each, 1), head.rest, 0, 0};
-  const int x = lane == 0 ? v_own + OWN_WEIGHT : lane == 1 ? v_own + OWN_WEIGHT + nt_own - 1 : lane == 2 ? v + SH_WEIGHT : v + SH_WEIGHT + cost * (nb - 1);
+  const int x = lane == 0 ? v_own + OWN_WEIGHT : lane == 1 ? v_own + OWN_WEIGHT + nt_own - 1 : v + unit_weight<MT>(cost) + (lane == 2 ? 0 : cost * (nb - 1));
   const int c = cta_of(r, x);
   const int odd = cut(r, c) < (lane < 2 ? v_own : v);  // the slot's number, in the first range
   const int c0_own = __shfl_sync(0xffffffffu, c, 0), c1_own = __shfl_sync(0xffffffffu, c, 1), odd_own = __shfl_sync(0xffffffffu, odd, 0);
@@ -143,23 +145,21 @@ __device__ __forceinline__ void write_row(const OwnAttnArgs& p, int b, int h, co
   if (lane == 0 && p.lse) p.lse[(size_t)b * p.nq + h] = (s.m - PA_BIAS + log2f(s.l)) * paged::LN2;
 }
 
-// A row a warp, or a CTA where rows are few and their parts may be many; blockIdx.y is the sequence.
+// A row a warp, or a CTA where rows are few and their parts may be many.
 template <int NV, int WPR, int MT, typename IO>
-__global__ void __launch_bounds__(JN_THREADS) join_kernel(const __grid_constant__ JoinArgs ja) {
+__global__ void __launch_bounds__(JN_THREADS, 4) join_kernel(const __grid_constant__ JoinArgs ja) {
   const OwnAttnArgs& p = ja.s.p;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
-  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = WPR == 1 ? blockIdx.x * JN_WARPS + warp : blockIdx.x, b = x / p.nq, h = x - b * p.nq;
   Sum<NV> sum;
   if constexpr (WPR == 1) {
-    const int h = blockIdx.x * JN_WARPS + warp;
-    if (h >= p.nq) return;
+    if (b >= p.n_seqs) return;
     join_row<NV, 1, MT>(ja, b, h, 0, sum);
     write_row<NV, IO>(p, b, h, sum);
   } else {
     static_assert(WPR == JN_WARPS, "a CTA a row");
     __shared__ float2 s_ml[JN_WARPS];
     __shared__ float4 s_o[JN_WARPS][NV * 32];
-    join_row<NV, WPR, MT>(ja, b, blockIdx.x, warp, sum);
+    join_row<NV, WPR, MT>(ja, b, h, warp, sum);
     if (lane == 0) s_ml[warp] = make_float2(sum.m, sum.l);
 #pragma unroll
     for (int i = 0; i < NV; ++i) s_o[warp][32 * i + lane] = sum.o[i];
@@ -172,15 +172,15 @@ __global__ void __launch_bounds__(JN_THREADS) join_kernel(const __grid_constant_
       for (int i = 0; i < NV; ++i) x[i] = s_o[w][32 * i + lane];
       sum.add(s_ml[w].x, s_ml[w].y, x);
     }
-    write_row<NV, IO>(p, b, blockIdx.x, sum);
+    write_row<NV, IO>(p, b, h, sum);
   }
 }
 
 template <int NV, int MT, typename IO>
 cudaError_t launch_join(const JoinArgs& ja, int nsm, cudaStream_t s) {
   const int nq = ja.s.p.nq, n = ja.s.p.n_seqs;
-  if (n * nq <= 8 * nsm) return launch_k(join_kernel<NV, JN_WARPS, MT, IO>, dim3(nq, n), dim3(JN_THREADS), 0, s, true, ja);
-  return launch_k(join_kernel<NV, 1, MT, IO>, dim3((nq + JN_WARPS - 1) / JN_WARPS, n), dim3(JN_THREADS), 0, s, true, ja);
+  if (n * nq <= 8 * nsm) return launch_k(join_kernel<NV, JN_WARPS, MT, IO>, dim3(nq * n), dim3(JN_THREADS), 0, s, true, ja);
+  return launch_k(join_kernel<NV, 1, MT, IO>, dim3((nq * n + JN_WARPS - 1) / JN_WARPS), dim3(JN_THREADS), 0, s, true, ja);
 }
 template <typename IO>
 cudaError_t launch_join(const JoinArgs& ja, int nsm, cudaStream_t s) {
@@ -244,7 +244,7 @@ qw_status qw_op_shared_attention(const qw_paged_kv* cache, int32_t n_seqs, int32
   const int64_t tiles = ((int64_t)n_seqs * (n_heads / c.n_kv_heads) + least.mt - 1) / least.mt + n_groups;
   const int64_t own = (int64_t)max_blocks * c.page_size / own_rows(c.head_dim) + 1 + OWN_WEIGHT;
   if ((int64_t)n_seqs * n_heads * own > 0x7fffffffll) return op_fail(QW_ERR_UNSUPPORTED, "n_seqs * n_heads * max_blocks * page_size too large");
-  if (tiles * c.n_kv_heads * (2 * ((int64_t)max_blocks * c.page_size / least.bk + 1) + SH_WEIGHT) > 0x7fffffffll)
+  if (tiles * c.n_kv_heads * (2 * ((int64_t)max_blocks * c.page_size / least.bk + 1) + unit_weight<256>(2)) > 0x7fffffffll)
     return op_fail(QW_ERR_UNSUPPORTED, "n_seqs * n_heads * max_blocks * page_size too large");
   if (!block_table || !lens || !cu_seqs || !shared_lens || !workspace || !err_dev) return op_fail(QW_ERR_INVALID_ARG, "null pointer");
   const int64_t width = (int64_t)n_heads * c.head_dim;

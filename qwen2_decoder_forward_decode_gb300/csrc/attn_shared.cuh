@@ -15,7 +15,6 @@ using paged::OwnAttnArgs;
 using paged::Range;
 
 constexpr int SH_MAX_CTAS = 160;  // of the tensor-core kernel, one an SM; the CUDA cores' kernel takes two
-constexpr int SH_WEIGHT = 2;      // of a unit's ends in the list, in blocks
 
 // The own positions of 16-bit caches, see attn_shared_own.cu: positions of a tile, a unit's weight in tiles, units of so many
 // tiles are not split, head dimensions and heads of a part.
@@ -46,10 +45,16 @@ struct Unit {
 };
 template <int MT>
 __host__ __device__ __forceinline__ int block_cost(int rows, int tile) { return MT == 256 && rows - tile * MT > MT / 2 ? 2 : 1; }
+// A unit's ends (queries, first products, states) count like 4 blocks before it, 2 where a block is long (the CUDA cores). Measured
+// with 2, 4 and 8: 256 sequences of 16383 shared positions 94, 92, 89 us (bf16, blocks of cost 2), 136, 134, 136 (fp32 callers);
+// 256 prompts of one sequence 231, 226, 235 (cost 1); an fp32 cache 32.6, 32.9, 34.7.
+template <int MT>
+__host__ __device__ constexpr int unit_weight(int cost) { return MT == 64 ? 2 : 4 * cost; }
 // numbers of one KV head's units
 template <int MT>
 __host__ __device__ __forceinline__ int head_numbers(int rows, int nt, int nb) {
-  return nt * SH_WEIGHT + ((nt - 1) * block_cost<MT>(MT, 0) + block_cost<MT>(rows, nt - 1)) * nb;
+  const int full = block_cost<MT>(MT, 0), last = block_cost<MT>(rows, nt - 1);
+  return (nt - 1) * (unit_weight<MT>(full) + full * nb) + unit_weight<MT>(last) + last * nb;
 }
 
 // The group g; its numbers in the list, 0 if it has nothing to do. bad: its bounds or its length are out of range.
@@ -75,7 +80,7 @@ __device__ __forceinline__ int load_group(const SharedArgs& a, int g, Unit& p, b
 template <int MT, int BK>
 __device__ __forceinline__ bool next_unit(const SharedArgs& a, int end, Unit& p) {
   p.t = 0;
-  p.v += SH_WEIGHT + p.c * p.nb;
+  p.v += unit_weight<MT>(p.c) + p.c * p.nb;
   if (p.v >= end) return false;
   if (++p.u < a.p.nkv * p.nt) {
     p.c = block_cost<MT>(p.rows, p.u % p.nt);
@@ -89,7 +94,8 @@ __device__ __forceinline__ bool next_unit(const SharedArgs& a, int end, Unit& p)
 }
 
 // the unit's blocks from p.t on that lie before the list's end `end`
-__device__ __forceinline__ int blocks_of(const Unit& p, int end) { return min(p.nb, (end - p.v - SH_WEIGHT + p.c - 1) / p.c) - p.t; }
+template <int MT>
+__device__ __forceinline__ int blocks_of(const Unit& p, int end) { return min(p.nb, (end - p.v - unit_weight<MT>(p.c) + p.c - 1) / p.c) - p.t; }
 
 // The CTA's range of the list and its first unit; CTA 0 leaves the cuts and the groups' places for the join. A cut that
 // falls on a unit's weight moves to the unit's beginning, one inside a block to the next block. scratch: shared memory, free
@@ -148,12 +154,12 @@ __device__ __forceinline__ Range find_groups(const SharedArgs& a, Unit& first, v
         for (int k = 0; k < 2; ++k) {
           const int x = cut(r, c + k);
           if (x < at || x >= at + n) continue;
-          const int per_head = n / a.p.nkv, kv = (x - at) / per_head, big = SH_WEIGHT + block_cost<MT>(MT, 0) * p.nb;
+          const int per_head = n / a.p.nkv, kv = (x - at) / per_head, big = unit_weight<MT>(block_cost<MT>(MT, 0)) + block_cost<MT>(MT, 0) * p.nb;
           const int in = x - at - kv * per_head, tile = min(in / big, p.nt - 1);
           p.u = kv * p.nt + tile;
           p.v = at + kv * per_head + tile * big;
           p.c = block_cost<MT>(p.rows, tile);
-          p.t = (max(0, x - p.v - SH_WEIGHT) + p.c - 1) / p.c;
+          p.t = (max(0, x - p.v - unit_weight<MT>(p.c)) + p.c - 1) / p.c;
           s_at[k] = p;
         }
       at += n;
@@ -162,7 +168,7 @@ __device__ __forceinline__ Range find_groups(const SharedArgs& a, Unit& first, v
   __syncthreads();
   if (c < ctas) {
     first = s_at[0];
-    auto place = [](const Unit& x) { return x.v + (x.t ? SH_WEIGHT + x.c * x.t : 0); };
+    auto place = [](const Unit& x) { return x.v + (x.t ? unit_weight<MT>(x.c) + x.c * x.t : 0); };
     r.begin = place(first);
     r.end = c + 1 == ctas ? total : place(s_at[1]);
     if (first.t == first.nb) next_unit<MT, BK>(a, r.end, first);

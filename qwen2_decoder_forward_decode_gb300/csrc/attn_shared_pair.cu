@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
         return true;
       };
       do {
-        const int nb = blocks_of(p, r.end);
+        const int nb = blocks_of<MT>(p, r.end);
         const bool two = p.c == 2;  // both halves have rows
         if (!(ok = wait_for(q_full, units & 1, err))) break;
         ++units;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
     int block0 = 0, units = 0, steps = 0, segments = 0;
     bool ok = true;
     do {
-      const int kv = p.u / p.nt, tile = p.u - kv * p.nt, nb = blocks_of(p, r.end);
+      const int kv = p.u / p.nt, tile = p.u - kv * p.nt, nb = blocks_of<MT>(p, r.end);
       const bool two = p.c == 2;
       if (units > 0 && !wait_for(idle, (units - 1) & 1, err)) ok = false;  // (all products of the last unit are done)
       const Row mine = row_of(a, p, kv, tile * MT + (two ? c * 128 : 0) + row);

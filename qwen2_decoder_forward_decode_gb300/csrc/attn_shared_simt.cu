@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(THREADS, HD <= 128 ? 2 : 1) shared_simt_kernel
   }
   const float sc = a.p.scale * paged::LOG2E;
   do {
-    const int kv = p.u / p.nt, tile = p.u - kv * p.nt, t1 = p.t + blocks_of(p, r.end);
+    const int kv = p.u / p.nt, tile = p.u - kv * p.nt, t1 = p.t + blocks_of<MT>(p, r.end);
     __syncthreads();
 #pragma unroll 1
     for (int i = tid; i < MT * G4; i += THREADS) {

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
       int n = 0, block = 0, units = 0;  // tiles, blocks and units so far
       bool ok = true;
       do {
-        const int nb = blocks_of(p, r.end);
+        const int nb = blocks_of<MT>(p, r.end);
         if (!(ok = wait_for(q_full, units & 1, err))) break;
         ++units;
         auto tile = [&](uint32_t& addr) {
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_tc_kernel(const __grid_cons
       return other;
     };
     do {
-      const int kv = p.u / p.nt, tile = p.u - kv * p.nt, nb = blocks_of(p, r.end);
+      const int kv = p.u / p.nt, tile = p.u - kv * p.nt, nb = blocks_of<MT>(p, r.end);
       const Row mine = row_of(a, p, kv, tile * MT + row);
       {  // the unit's queries, 16 of the quarter's rows a warp, a row at a time; zeros for rows that take no part
         constexpr int DL = HD / 32;  // dimensions of a lane

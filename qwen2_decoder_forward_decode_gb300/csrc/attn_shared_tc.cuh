@@ -174,7 +174,7 @@ __device__ __forceinline__ void produce(const SharedArgs& a, const PageMaps& map
     }
   };
   do {
-    const int kv = p.u / p.nt, t1 = p.t + blocks_of(p, r.end);
+    const int kv = p.u / p.nt, t1 = p.t + blocks_of<MT>(p, r.end);
     int id = entry(p.t), t = p.t;
     Rows now{}, last{};
 #pragma unroll 1
