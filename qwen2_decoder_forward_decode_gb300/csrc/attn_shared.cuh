@@ -17,8 +17,9 @@ using paged::Range;
 constexpr int SH_MAX_CTAS = 160;  // of the tensor-core kernel, one an SM; the CUDA cores' kernel takes two
 
 // The own positions of 16-bit caches, see attn_shared_own.cu: positions of a tile, a unit's weight in tiles, units of so many
-// tiles are not split, head dimensions and heads of a part.
-constexpr int OWN_WEIGHT = 2, OWN_WHOLE = 2, OWN_WARPS = 8;
+// tiles are not split, head dimensions and heads of a part. (Weights of 1 to 6 are within 1%; units of up to 4 or 8 tiles kept whole
+// cost 48 sequences of 1 to 200 own positions 2 and 20%.)
+constexpr int OWN_WEIGHT = 4, OWN_WHOLE = 2, OWN_WARPS = 8;
 __host__ __device__ constexpr int own_rows(int hd) { return hd <= 64 ? 32 : 16; }
 
 struct SharedHead {  // of the workspace

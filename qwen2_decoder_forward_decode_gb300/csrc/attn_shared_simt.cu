@@ -6,7 +6,8 @@
 // outputs of the same rows at dimensions 4 x + 64 c; rows' statistics go across the 16 threads x, probabilities through
 // shared memory within the warp. Products are packed pairs (f32x2).
 // What bounds it: shared-memory loads, 16 bytes for every 4 packed products; two CTAs an SM up to 128 dimensions, so that
-// one computes while the other waits for its block.
+// one computes while the other waits for its block. 256 rows of 28 and 4 heads of 128 behind 8000 positions: 739 us
+// (40 TFLOP/s; one CTA an SM 848), of 8 and 2 heads 225.
 #include "attn_shared.cuh"
 
 namespace qw {

@@ -13,6 +13,9 @@
 // Precision: queries and probabilities are sums of pieces of the cache's type, two of fp16 (22 bits of the row's largest
 // element), three of bf16, whose products are added up lowest piece first. Exponentials are ex2's, good to 2^-22.
 //
+// What bounds it: the softmax and the fold of O, 128 rows by 8 warps, and of bf16 caches the products of three pieces. 256 sequences,
+// 28 and 4 heads of 128 behind 16383 positions: 134 us with the fp16 cache, 172 with bf16; behind 8000 89.
+//
 // Every wait is bounded: on expiry ERR_TIMEOUT is set, the CTA stops issuing work, waits (bounded) for what it issued, and
 // releases its TMEM.
 #include <math.h>

@@ -83,7 +83,7 @@ inline void make_page_maps(const qw_paged_kv& c, PageMaps& m) {
 //   - Else, and where a block is cut by the shared part's end or has a bad page, cp.async does, 16 bytes a lane, with zeros for
 //     positions that are not there. It moves about 26 bytes a cycle and SM where TMA keeps up with L2 (16383 positions, 256
 //     sequences: 4200 cycles a block of 128 rows and positions against 1300 of products).
-// full[NS] expects TC_PRODUCERS arrivals, empty[NS] one. masks [TC_MASKS][4]: the positions of a block that exist.
+// full[NS] expects TC_PRODUCERS arrivals, empty[NS] what the caller set. masks [TC_MASKS][4]: the positions of a block that exist.
 template <typename T, int MT, int HD, int NS>
 __device__ __forceinline__ void produce(const SharedArgs& a, const PageMaps& maps, const Range& r, Unit p, uint32_t ring, uint32_t full0,
                                         uint32_t empty0, uint32_t* masks, volatile int* s_abort) {

@@ -22,8 +22,8 @@ inline size_t dtype_size(int32_t t) { return t == QW_F32 ? 4 : 2; }
 inline bool dtype_known(int32_t t) { return t == QW_F32 || t == QW_F16 || t == QW_BF16; }
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-// Both operators with a workspace keep their counters (zero between calls) in its first bytes, so that one workspace
-// can serve them in turn.
+// The attentions and the log probabilities keep their counters (zero between calls) in their workspace's first bytes, so that
+// one workspace can serve them in turn.
 constexpr size_t OP_COUNTER_BYTES = 16384;
 
 // Every pointer must be memory of the current device: a host pointer or another device's would
