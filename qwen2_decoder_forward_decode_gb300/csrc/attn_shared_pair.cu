@@ -11,9 +11,8 @@
 //                    products at the same time and then for the softmax (4000 cycles a block of 256 rows). (One warp for both
 //                    chains is in their way, too: a step's waits and commits take it as long as the products themselves,
 //                    4200 cycles.)
-//   warps 4 .. 7     softmax of chain A, 8 .. 11 of chain B: one row a lane, 64 of its 128 scores in registers at a time (once for
-//                    the maximum, once for the probabilities; all 128 at once spill, and maxima taken with the
-//                    probabilities of a block before changed nothing)
+//   warps 4 .. 7     softmax of chain A, 8 .. 11 of chain B: one row a lane, 64 of its 128 scores in registers at a time, once for the
+//                    maximum, once for the probabilities (one pass, with the maximum of the block before, was within 2%)
 // O stays in TMEM. Its reference m moves only when a row's maximum exceeds it by more than 2^5; then the warp rescales its
 // rows of O, which is safe: S of a block is issued after the chain's last P V, so that is done when S arrives. P is at most
 // 2^15 then, in fp16's range, and keeps its digits down to 2^-24 of the row's largest (PA_BIAS).

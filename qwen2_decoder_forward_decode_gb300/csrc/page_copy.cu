@@ -1,9 +1,10 @@
 // Copies of pages inside the caches of all layers: the partly filled last pages of forked sequences, and the pages that a
 // compaction moves.
 //
-// What bounds it: HBM, every byte once in and once out. A unit is a page of one layer's keys or values; CTAs of 256
-// threads take units in turn, each thread four vectors of 16 bytes at a time. 256 pages of 12 layers, 64 positions of 4 heads of
-// 128, bf16: 130 us (5.8 TB/s of the copy's 6.8); 16 last pages of 28 layers 3.4 us.
+// What bounds it: HBM, every byte once in and once out. A unit is a page of one layer's keys or values, and a CTA's; there are CTAs
+// enough that the last ones even out (64 an SM; 8 an SM, of which 5 fit at a time, took units in turn in 123 us where this takes
+// 119). 128 threads, each eight vectors of 16 bytes at a time; 512 threads 127. 256 pages of 12 layers, 64 positions of 4 heads of 128,
+// bf16: 119 us (6.4 TB/s of the copy's 6.8); 16 last pages of 28 layers 3.2 us.
 #include "common.cuh"
 #include "op_util.h"
 
@@ -12,7 +13,7 @@
 namespace qw {
 namespace {
 
-constexpr int COPY_MAX_CACHES = 128, COPY_THREADS = 256, COPY_VECS = 4;
+constexpr int COPY_MAX_CACHES = 128, COPY_THREADS = 128, COPY_VECS = 8;
 
 struct CopyArgs {
   int n, n_caches, n_pages, page, nkv, row;  // row: vectors of a head's dimensions
@@ -113,7 +114,7 @@ extern "C" qw_status qw_op_page_copy(const qw_paged_kv* caches, int32_t n_caches
   if ((e = cudaGetDevice(&dev)) || (e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)))
     return op_cuda_fail(e, "device query");
   const int64_t units = (int64_t)n * 2 * n_caches;
-  const int ctas = (int)(units < 8 * nsm ? units : 8 * nsm);
+  const int ctas = (int)(units < 64 * nsm ? units : 64 * nsm);
   if ((e = launch_k(page_copy_kernel, dim3(ctas), dim3(COPY_THREADS), 0, (cudaStream_t)cuda_stream, false, a)))
     return op_cuda_fail(e, "page copy launch");
   return QW_OK;
