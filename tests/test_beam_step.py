@@ -224,3 +224,54 @@ def test_a_beam_search_over_pages(io, cache, nq, nkv, hd, page):
             y = ref.rope(x[:, nq:nq + nkv] * (1 + layer), np.arange(len(held)), s.freqs, False, s.mscale, hd)
             half = ref.EPS_HALF[cache] * 2 + 8 * ref.U
             np.testing.assert_allclose(k, y, rtol=0, atol=half * np.abs(y).max() + ref.TINY[cache])
+
+
+@pytest.mark.parametrize("io,cache,nq,nkv,hd,page", [("bf16", "bf16", 14, 2, 128, 16), ("f32", "f16", 4, 2, 64, 5)])
+def test_two_steps_as_a_graph(io, cache, nq, nkv, hd, page):
+    """Twelve steps, called one by one and as replays of two captured ones: the same bits, whatever the beams do."""
+    G, W, vocab, prompts = 2, 5, 97, [70, 41]
+
+    def begin():
+        s = Search(G, W, nq, nkv, hd, page, 200, 40, vocab, io, cache, 40)
+        s.new.zero_()
+        s.new[::W] = torch.tensor(prompts, dtype=torch.int32, device="cuda")
+        s.append(torch.from_numpy(np.random.default_rng(1).integers(0, vocab, sum(prompts))).cuda(), sum(prompts))
+        s.shared.copy_(torch.tensor(np.repeat(prompts, W), dtype=torch.int32))
+        first_q = s.q[torch.cumsum(torch.tensor(prompts), 0).cuda() - 1].clone()
+        s.q[:s.n].zero_()
+        s.q[0:s.n:W] = first_q
+        s.scores[::W] = 0.0
+        s.new.fill_(1)
+        return s
+
+    def step(s):
+        s.attend()
+        s.select(-1)
+        s.fork()
+        s.append(s.tokens, s.n)
+
+    a, b = begin(), begin()
+    for _ in range(12):
+        step(a)
+    step(b)
+    step(b)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(b)
+        step(b)
+    for _ in range(5):
+        g.replay()
+    a.check_pool()
+    b.check_pool()
+    assert a.hlens.tolist() == b.hlens.tolist() == [12] * a.n
+    for name in ("history", "scores", "lens", "n_free", "shares", "parents"):
+        x, y = getattr(a, name), getattr(b, name)
+        if name == "history":
+            x, y = x[:, :12], y[:, :12]
+        assert torch.equal(x, y), name
+    assert torch.equal(a.free[:int(a.n_free)], b.free[:int(b.n_free)])
+    for w in range(a.n):
+        for layer in range(2):
+            for x, y in zip(a.rows(w, layer), b.rows(w, layer)):
+                np.testing.assert_array_equal(x, y)
