@@ -133,7 +133,9 @@ __device__ __forceinline__ Range find_groups(const SharedArgs& a, Unit& first, v
     if (w < warp) base += w_sum[w];
     total += w_sum[w];
   }
-  const int ctas = min((int)gridDim.x, total), c = blockIdx.x;
+  // Every range has a number of each half of a block: a range of the second half alone would be empty, and the join adds the
+  // parts of all ranges between a unit's first block and its last.
+  const int ctas = min((int)gridDim.x, MT == 256 ? total / 2 : total), c = blockIdx.x;  // (a list that is not empty has 5 numbers)
   Range r{0, 0, 0, 0};
   if (ctas) {
     r.each = total / ctas;
