@@ -36,7 +36,8 @@ constexpr int BS_MAX_VOCAB = 1 << 21;
 constexpr int BS_CAP = 512;                          // candidates of a piece before they are ranked
 constexpr float BS_LOG2E_HI = 1.44269502162933349609375f, BS_LOG2E_LO = 1.92596303e-8f;  // their sum is log2(e) to 2^-50
 constexpr double BS_LN2 = 0.693147180559945309417232121458;
-constexpr float BS_FAR = 1048576.f;  // maxima beyond it take the slow sum
+constexpr float BS_FAR = 1048576.f;  // maxima beyond it take the slow sum,
+constexpr float BS_NEAR = BS_FAR - 128.f;  // and those below -BS_NEAR: chunks below -BS_FAR are left out of the other one
 
 // The sum of a piece: of 2^(z log2(e) - ref) in units of 2^-38, which add and shift without rounding and fast (64-bit floating
 // point costs 30 to 40 cycles an operation here), or, where the largest logit lies far out, of exp(z - ref), a double.
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
       const uint32_t top = __reduce_max_sync(0xffffffffu, lane_top == lane_top ? value_key(lane_top) : 0xffffffffu);  // (NaN above everything)
       if (lane == 0) sh.top[c] = top;
       most = max(most, top);
-      if (top > far_low && top < far_high) {  // else nothing next to the others, or the piece takes the slow sum
+      if (top > far_low && top < far_high) {  // else e^-128 of the piece's largest and less, or the piece takes the slow sum
         const float need = ceilf(key_value(top) * BS_LOG2E_HI);
         if (!any || need > ref) {
           const float f = any ? power2(ref - need) : 0.f;
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
 #pragma unroll
   for (int w = 0; w < BS_NW; ++w) peak = max(peak, sh.most[w]);
   PieceState* state = a.state + (size_t)row * a.pieces + piece;
-  if (peak <= far_low || peak >= far_high) {
+  if (peak <= value_key(-BS_NEAR) || peak >= far_high) {
     // the largest logit is far out, or there is a NaN: the definition, on a few threads' patience
     const float m = peak >= 0xff800000u ? INFINITY : key_value(max(peak, BS_NONE));  // (+inf or NaN: the sum becomes NaN)
     double s = 0.;
