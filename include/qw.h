@@ -400,7 +400,8 @@ qw_status qw_op_page_fork(int32_t n_seqs, int32_t n_out, int32_t page_size, int3
  *       Their number stays n_free[0]
  * Other tables of the same pool can be rewritten from the moves. If a page is on the list twice or outside
  * [0, n_pages) (QW_DEV_PAGE), or n_free or a length is out of range (QW_DEV_CAPACITY), nothing moves and the outputs are
- * the inputs. A table entry outside [0, n_pages) stays and sets QW_DEV_PAGE. n_pages and max_moves <= 2^30.
+ * the inputs. Else a table entry outside [0, n_pages) stays and sets QW_DEV_PAGE, whether pages move or not. n_pages and
+ * max_moves <= 2^30.
  * workspace: at least qw_op_page_compact_workspace() bytes, with the rules of qw_op_page_fork's. */
 size_t qw_op_page_compact_workspace(int32_t n_pages);
 qw_status qw_op_page_compact(int32_t n_seqs, int32_t page_size, int32_t n_pages, int32_t max_blocks, int32_t max_moves,

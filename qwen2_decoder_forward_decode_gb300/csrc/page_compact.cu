@@ -191,31 +191,29 @@ __global__ void __launch_bounds__(CP_THREADS) compact_tables_kernel(const Compac
       a.shares_out[a.dst[i]] = a.shares[from];
       if (a.shares_out == a.shares) a.shares_out[from] = 0;
     }
-  const bool apart = a.table_out != a.table;
-  if (moves || apart) {
-    const int n_tasks = a.n * a.segs;  // (the host bounds it)
+  const bool apart = a.table_out != a.table;  // (in place, entries are checked even where nothing moves)
+  const int n_tasks = a.n * a.segs;  // (the host bounds it)
 #pragma unroll 1
-    for (int t = blockIdx.x * (CP_THREADS / 32) + warp; t < n_tasks; t += gridDim.x * (CP_THREADS / 32)) {
-      const int b = t / a.segs, j0 = (t - b * a.segs) * CP_SEG;
-      const int have = bad ? 0 : pages_of(a.lens[b], a.page), end = min(apart ? a.max_blocks : have, j0 + CP_SEG);
-      const size_t row = (size_t)b * a.max_blocks;
-      static_assert(CP_SEG == 128, "four entries a lane");
-      int id[4], k[4];  // (the three loads of an entry wait for each other, those of four entries do not)
+  for (int t = blockIdx.x * (CP_THREADS / 32) + warp; t < n_tasks; t += gridDim.x * (CP_THREADS / 32)) {
+    const int b = t / a.segs, j0 = (t - b * a.segs) * CP_SEG;
+    const int have = bad ? 0 : pages_of(a.lens[b], a.page), end = min(apart ? a.max_blocks : have, j0 + CP_SEG);
+    const size_t row = (size_t)b * a.max_blocks;
+    static_assert(CP_SEG == 128, "four entries a lane");
+    int id[4], k[4];  // (the three loads of an entry wait for each other, those of four entries do not)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int j = j0 + lane + 32 * q;
-        id[q] = j < end ? a.table[row + j] : 0;
-        if (j < min(have, end) && (id[q] < 0 || id[q] >= n)) atomicOr(a.err, ERR_PAGE);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) k[q] = j0 + lane + 32 * q < min(have, end) && id[q] >= live && id[q] < n ? a.number[id[q]] : -1;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (k[q] >= 0) id[q] = a.dst[k[q]];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (j0 + lane + 32 * q < end) a.table_out[row + j0 + lane + 32 * q] = id[q];
+    for (int q = 0; q < 4; ++q) {
+      const int j = j0 + lane + 32 * q;
+      id[q] = j < end ? a.table[row + j] : 0;
+      if (j < min(have, end) && (id[q] < 0 || id[q] >= n)) atomicOr(a.err, ERR_PAGE);
     }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) k[q] = j0 + lane + 32 * q < min(have, end) && id[q] >= live && id[q] < n ? a.number[id[q]] : -1;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (k[q] >= 0) id[q] = a.dst[k[q]];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if ((apart && j0 + lane + 32 * q < end) || k[q] >= 0) a.table_out[row + j0 + lane + 32 * q] = id[q];
   }
   __syncthreads();
   if (s_last) {
