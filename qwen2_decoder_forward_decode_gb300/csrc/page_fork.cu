@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(FORK_POOL_THREADS) fork_pool_kernel(const Fork
   if (tid == 0) {
     if (c == 0) {
       *a.n_free_out = bad ? n_free : min(keep + total, a.n_pages);
-      if (!bad && keep + total > a.n_pages) atomicOr(a.err, ERR_CAPACITY);  // pages that were held and on the list
+      if (!bad && keep + total > a.n_pages) atomicOr(a.err, ERR_PAGE);  // pages that were held and on the list
     }
     s_last = atomicAdd(&a.head->ticket, 1u) == gridDim.x - 1;  // (every CTA has read the counts by then)
   }
