@@ -502,8 +502,9 @@ qw_status qw_op_paged_attention(const qw_paged_kv *cache, int32_t n_seqs, int32_
  *   cu_seqs [n_groups + 1], 1 <= n_groups <= n_seqs; shared_lens [n_seqs]
  *   workspace at least qw_op_shared_attention_workspace() bytes, with the rules of qw_op_paged_attention's, which it
  *       serves too
- * Probabilities of 16-bit callers are rounded to the cache's type over the shared positions (not in lse); an fp32 caller's
- * keep 22 bits and more, as there. Equal inputs give equal bits on equal devices. */
+ * Probabilities keep two pieces of the cache's type (22 bits, bf16 16) for 16-bit callers and 22 bits and more for fp32 ones, as
+ * there. A 16-bit caller's values whose sum over the shared positions passes 2^113 overflow. Equal inputs give equal bits on equal
+ * devices. */
 size_t qw_op_shared_attention_workspace(int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
 qw_status qw_op_shared_attention(const qw_paged_kv *cache, int32_t n_seqs, int32_t n_heads, const int32_t *block_table,
                                  int32_t max_blocks, const int32_t *lens, int32_t n_groups, const int32_t *cu_seqs,

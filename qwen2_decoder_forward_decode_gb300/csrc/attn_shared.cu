@@ -15,8 +15,8 @@
 // The second launch goes on beside the first (programmatic dependent launch: it waits for it at its end only), the third
 // is in place when the second ends.
 // Measured in a CUDA graph: 4 samples of a prompt of 178 (12 and 2 heads of 128, fp16 cache, fp32 queries) 15.4 us, three launches'
-// chains of loads; 256 sequences of 1 to 256 own positions behind 16383 (28 and 4 heads, bf16) 89 us: own positions 20, shared
-// ones 58, join 11 (7168 rows of 8 states each, 30 MB that L2 holds). The same without sharing reads 8.7 GB, 1.3 ms at the copy rate.
+// chains of loads; 256 sequences of 1 to 256 own positions behind 16383 (28 and 4 heads, bf16) 102 us: own positions 20, shared
+// ones 71, join 11 (7168 rows of 8 states each, 30 MB that L2 holds). The same without sharing reads 8.7 GB, 1.3 ms at the copy rate.
 #include "attn_shared.cuh"
 
 #include <algorithm>

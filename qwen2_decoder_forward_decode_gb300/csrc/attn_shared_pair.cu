@@ -2,7 +2,7 @@
 // most 128 dimensions.
 //
 // Two chains of products run side by side, so that one's products fill the time of the other's softmax: S = Q K^T (128 rows x
-// 128 positions), P = 2^(S - m) written over it, O += P V, all in TMEM. A unit of more than 128 rows has its first 128 in
+// 128 positions), P = 2^(S - m) in two pieces written over it, O += P V, all in TMEM. A unit of more than 128 rows has its first 128 in
 // chain A and the others in chain B, over the same blocks of keys and values; one of fewer rows has its even blocks in A and
 // its odd ones in B, with a state each.
 //   warps 0 .. 3     producers (attn_shared_tc.cuh)
@@ -17,12 +17,14 @@
 // rows of O, which is safe: S of a block is issued after the chain's last P V, so that is done when S arrives. P is at most
 // 2^15 then, in fp16's range, and keeps its digits down to 2^-24 of the row's largest (PA_BIAS).
 //
-// Precision: probabilities are rounded once to the cache's type, whose bits the output has too; their sum l takes them before
-// that. The tensor cores' additions cut: over 1000 products of 16 positions about 1e-5 of the norm, next to the output's
-// 2^-9 or 2^-12.
-// What bounds it: of many rows the chain of one block, S, softmax, P V: 3500 cycles for both chains' blocks, of which the products
-// are 2050 (the tensor cores are busy 44% of the kernel; the exponentials' pipe 1000). 256 sequences, 28 and 4 heads of 128
-// behind 16383 positions: 60 us, 1010 TFLOP/s. Of few rows HBM and L2: 16 groups of 8 behind 512 to 4096 positions 29 us, 86 MB.
+// Precision: probabilities are sums of two pieces of the cache's type, as over own positions and in attn_paged.cu (22 bits, bf16
+// 16, so that the output's own rounding is what remains); their sum l takes them before that. One piece would save 8 of a step's
+// 24 products, 13 us of 256 sequences behind 16383 positions, and raises bf16's error against 64 bits by a third. The tensor
+// cores' additions cut: over 1000 products of 16 positions about 1e-5 of the norm, next to the output's 2^-9 or 2^-12.
+// What bounds it: of many rows the chain of one block, S, softmax, P V: 4400 cycles for both chains' blocks, of which the products
+// are 3070. 256 sequences, 28 and 4 heads of 128 behind 16383 positions: 73 us, 1240 TFLOP/s of products (830 of the formula's). Of few
+// rows HBM and L2: 16 groups of 8 behind 512 to 4096 positions 30 us, 86 MB. The shares of 72 and 56 registers spill in the
+// producers and issuers: 324 to 336 bytes of stores a thread.
 //
 // Every wait is bounded: on expiry ERR_TIMEOUT is set, the CTA stops issuing work, waits (bounded) for what it issued, and
 // releases its TMEM.
@@ -34,7 +36,7 @@ namespace qw {
 namespace shared_attn {
 namespace {
 
-using paged::Pair;
+using paged::split;
 
 constexpr int MT = 256, BK = TC_BK, THREADS = 512, MMA_WARP = 12, TMEM_WARP = 15;  // (a warp whose lanes never part allocates and frees TMEM)
 constexpr float MOVE_AT = 5.f;  // base-2 growth of a row's maximum that moves its reference
@@ -188,7 +190,10 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
           tc::tc_fence_after();
           const uint32_t vl = desc_lo(v, BK * 128);
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) mma_ts(o_col, s_col + kk * 8, vl + kk * (2048 >> 4), idO, !first || kk > 0);
+          for (int piece = 1; piece >= 0; --piece)  // the lower one first
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk)
+              mma_ts(o_col, s_col + (kk >> 2) * 64 + piece * 32 + (kk & 3) * 8, vl + kk * (2048 >> 4), idO, !first || piece == 0 || kk > 0);
           first = false;
           if (more) products_s(k);
           else tc::mma_commit(o_full0 + 8 * c);
@@ -307,8 +312,8 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
         const f32x2 c2 = pack2(sc, sc), r2 = pack2(-ref, -ref);
         f32x2 acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {  // (the probabilities of a half go over scores that are used up)
-          uint32_t u[64];
+        for (int h = 0; h < 2; ++h) {  // (both pieces of a half's probabilities go over its scores)
+          uint32_t u[64], w[2][32];
           tc::tmem_ld32_nowait(s_at + 64 * h, u);
           tc::tmem_ld32_nowait(s_at + 64 * h + 32, u + 32);
           tc::tmem_wait_ld();
@@ -317,9 +322,13 @@ __global__ void __launch_bounds__(THREADS, 1) shared_pair_kernel(const __grid_co
             const float2 e = unpack2(fma2_to(pack2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1])), c2, r2));
             const float p0 = ex2(e.x), p1 = ex2(e.y);
             acc[q & 3] = add2(acc[q & 3], pack2(p0, p1));
-            u[q] = Pair<T>::pack(p0, p1);
+            uint32_t pieces[2];
+            split<T, 2>(p0, p1, pieces);
+            w[0][q] = pieces[0];
+            w[1][q] = pieces[1];
           }
-          tc::tmem_st32(s_at + 32 * h, u);
+          tc::tmem_st32(s_at + 64 * h, w[0]);
+          tc::tmem_st32(s_at + 64 * h + 32, w[1]);
         }
         const float2 s0 = unpack2(add2(acc[0], acc[1])), s1 = unpack2(add2(acc[2], acc[3]));
         l += (s0.x + s0.y) + (s1.x + s1.y);
