@@ -538,7 +538,9 @@ qw_status qw_op_token_logprobs(int32_t logits_dtype, int32_t n_rows, int32_t voc
  * beam i of group g, scores[w] the sum of its tokens' log probabilities. The beam can go on with any token t of a logit
  * above -inf, and its score becomes scores[w] + z_t - ln sum_j exp(z_j); an ended beam (ended[w] != 0) stays as it is, a
  * single candidate with its own score and the token end_id. The n_out best of a group, by weights[w] * score, in order; equal
- * ones by the lower beam, then the larger logit, then the lower id. The order is that of the scores in 64 bits.
+ * ones by the lower beam, then the larger logit, then the lower id. The order is that of the scores in 64 bits, whose
+ * normaliser is exact to 1e-10 where tokens above 2^-10 carry a row (a beam with one token left keeps its score as it is),
+ * to 2e-8 of wide rows, and to 2e-7 at worst (thousands of equal logits that carry a row together, logits beyond 2^20).
  *   logits [n_groups * n_beams][row_stride >= vocab] of logits_dtype, aligned to its own size
  *   scores [rows]; -inf: a beam that is not there. weights [rows], positive, such as a power of 1 / length; NULL: 1
  *   ended [rows] or NULL: none. end_id: the token that ends a beam, or -1

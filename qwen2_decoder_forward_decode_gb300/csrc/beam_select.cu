@@ -10,13 +10,18 @@
 //   - Candidates of different beams may lie closer than fp32 tells, and their order decides what the beams become. So the
 //     order is that of scores in 64 bits, and the normaliser is summed for it: exponents are taken over an integer
 //     power of two, 2^(z log2(e) - k), with log2(e) in two parts (one rounding of a small number each), so moving k is
-//     exact; a lane's sums are fp32 over at most some hundred logits, all sums of sums 64-bit. Against 64 bits
-//     the normaliser is off by 1e-8 where fp32 sums of fp32 exponents give 1e-7.
+//     exact; a lane's sum carries its rounding errors along in a second number, all sums of sums are whole numbers or 64-bit.
+//   - ex2 is good to 2^-22 only. So a piece's logits above 2^-10 of its sum (at most 1024) are taken again in 64 bits, relative to
+//     the piece's largest, in the place of what they were in the sum: a lane's share of a chunk is taken out as it went in, and
+//     its other logits are put back. What remains are the smaller ones, whose errors mostly cancel once their mean is added back.
+//     Against 64 bits the normaliser is off by 1e-10 where few tokens carry a row (by nothing where it is one), by 1e-9 to 2e-8
+//     of wide rows, by 2e-7 at worst (thousands of equal logits that carry a row together).
 //   - A second launch joins a group: pieces' sums, then the lists, of which only those with the n_out best heads count. A warp
 //     holds a list a lane and takes the best head n_out times.
-// What bounds it: the instructions of a logit (unpacking, two exponent products and a sum in pairs, an exponential, a maximum), at
-// 57% of the issue slots, then the groups' latency. 64 x 4 beams of 152064 logits, bf16: 27 us (2.9 TB/s; rows 20, groups 7);
-// 4 beams 13.5, all latency; 8 x 32 beams, 32 candidates, fp32: 65 (2.4 TB/s).
+// What takes its time (no single resource is used up): the instructions of a logit (unpacking, two exponent products, a sum and
+// its rounding in pairs, an exponential, a maximum), the second look and its 64-bit operations, then the groups' latency.
+// 64 x 4 beams of 152064 logits, bf16: 33 us (2.4 TB/s); 4 beams 18, all latency; 8 x 32 beams, 32 candidates, fp32: 73 (2.1 TB/s).
+// The sums' rounding costs 2.4 us of the 33, the logits that are taken again 3 to 4.
 #include "common.cuh"
 #include "op_util.h"
 
@@ -39,16 +44,15 @@ constexpr double BS_LN2 = 0.693147180559945309417232121458;
 constexpr float BS_FAR = 1048576.f;  // maxima beyond it take the slow sum,
 constexpr float BS_NEAR = BS_FAR - 128.f;  // and those below -BS_NEAR: chunks below -BS_FAR are left out of the other one
 
-// The sum of a piece: of 2^(z log2(e) - ref) in units of 2^-38, which add and shift without rounding and fast (64-bit floating
-// point costs 30 to 40 cycles an operation here), or, where the largest logit lies far out, of exp(z - ref), a double.
-constexpr int BS_UNIT = 38;
+// Sums of 2^(z log2(e) - ref) are kept in units of 2^-38, which add and shift without rounding and fast (64-bit floating
+// point costs 30 to 40 cycles an operation here).
+constexpr double BS_REST = 0x1p-38 * (1. + 5.17e-8);  // ex2's results are 5.17e-8 too small on average over a factor of 2, 1.42e-7 at most (measured)
+constexpr int BS_HOT = 1152;  // logits of a piece that are taken again: 1024 by the rule, whose bound is off by e^0.11 at most
+// A piece's sum of exponentials: e^top exact + 2^ref rest, top its largest logit (-inf: none).
 struct PieceState {
-  union {
-    u64 units;
-    double sum;
-  };
-  float ref;
-  int slow;  // which of the two
+  double exact;
+  long long rest;  // in units
+  float top, ref;
 };
 struct BeamArgs {
   const void* logits;
@@ -70,6 +74,12 @@ __device__ __forceinline__ uint32_t value_key(float z) {
 }
 __device__ __forceinline__ float key_value(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
 constexpr uint32_t BS_NONE = 0x007fffffu;  // the key of -inf: every candidate's is above
+
+// x, |x| < 2^11, in units of 2^-38, rounded: its 2^-13ths first, what they leave is below 2^-14 (a conversion to 64 bits costs 200 cycles)
+__device__ __forceinline__ long long to_units(float x) {
+  const float t = fmaf(x, 8192.f, 12582912.f), left = fmaf(t - 12582912.f, -1.f / 8192.f, x);
+  return ((long long)(__float_as_int(t) - 0x4b400000) << 25) + __float2int_rn(left * 0x1p38f);
+}
 
 // units / 2^d for a whole number d >= 0 (or infinite)
 __device__ __forceinline__ u64 shifted(u64 units, float d) { return d < 64.f ? units >> (int)d : 0ull; }
@@ -163,6 +173,11 @@ struct BeamShared {
   uint32_t most[BS_NW];
   int n, n_work;
   uint32_t bound;
+  float chunk_ref[BS_MAX_CHUNKS];  // what a chunk was summed with
+  uint16_t hot[BS_HOT];            // chunk * 32 + lane of logits that are taken again
+  int n_hot;
+  long long moved[BS_NW];  // what that changes in the sum, in units
+  long long exact[BS_NW];  // their own sum in units of 2^-52
 };
 
 // The largest key that `k` of a warp's keys (NR a lane, of any number) reach, or one between it and the next larger; `least` if
@@ -238,8 +253,72 @@ __device__ __noinline__ void closer_bound(BeamShared& sh, int n_work, int k, int
   }
 }
 
+__device__ __forceinline__ long long warp_add(long long v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The terms of a chunk over 2^ref, and their sums by halves of a pair
+template <typename C>
+__device__ __forceinline__ f32x2 chunk_terms(const C& x, float ref, f32x2* e) {
+  const f32x2 hi2 = pack2(BS_LOG2E_HI, BS_LOG2E_HI), lo2 = pack2(BS_LOG2E_LO, BS_LOG2E_LO), r2 = pack2(-ref, -ref);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 z = x.two(i);
+    const f32x2 z2 = pack2(z.x, z.y);
+    const float2 y = unpack2(fma2_to(z2, lo2, fma2_to(z2, hi2, r2)));
+    e[i] = pack2(ex2(y.x), ex2(y.y));
+  }
+  return add2(add2(e[0], e[1]), add2(e[2], e[3]));
+}
+
+// e^d of -700 < d <= 0 to 1e-10 of it, 1 of 0: d = n ln 2 + r, the series of e^r, from r^4 on in fp32 (at most 6e-4 of it). 64-bit
+// operations are what bounds where it is used: 8 here, 17 in exp(); 256 x 4 beams of 4000 logits 31 -> 28 us.
+__device__ __forceinline__ double exp_down(double d) {
+  const float n = rintf((float)d * BS_LOG2E_HI);
+  const double r = fma((double)n, -BS_LN2, d);
+  const float f = (float)r;
+  float q = fmaf(f, 1.f / 362880, 1.f / 40320);
+  q = fmaf(f, q, 1.f / 5040);
+  q = fmaf(f, q, 1.f / 720);
+  q = fmaf(f, q, 1.f / 120);
+  q = fmaf(f, q, 1.f / 24);
+  double p = fma((double)q, r, 1. / 6.);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.);
+  p = fma(p, r, 1.);
+  return __hiloint2double(__double2hiint(p) + ((int)n << 20), __double2loint(p));
+}
+
+// The logits from the key `least` on of a lane's share of a chunk, taken out of the sum over 2^ref (what that changes in it, in
+// units) and summed by themselves relative to `top` (in 2^-52).
+template <typename C>
+__device__ __forceinline__ void take_out(const C& x, float chunk_ref, uint32_t least, float ref, float top, long long& moved, long long& exact) {
+  f32x2 e[4];
+  const float2 sum = unpack2(chunk_terms(x, chunk_ref, e));
+  const float unit = power2(chunk_ref - ref);
+  float stays = 0.f;
+  unsigned mask = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 two = unpack2(e[i >> 1]);
+    if (value_key(x.at(i)) >= least) mask |= 1u << i;
+    else stays += i & 1 ? two.y : two.x;
+  }
+  moved += to_units(stays * unit) - to_units(sum.x * unit) - to_units(sum.y * unit);
+#pragma unroll 1
+  for (; mask; mask &= mask - 1) {
+    const int at = __ffs(mask) - 1;
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v = at == i ? x.at(i) : v;
+    exact += __double_as_longlong(1. + exp_down((double)v - (double)top)) - 0x3ff0000000000000ll;  // (in [1, 2] a number's bits count steps of 2^-52)
+  }
+}
+
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(BS_NT, WIDE && sizeof(T) == 2 ? 4 : 1) beam_rows_kernel(const BeamArgs a) {
   using C = Chunk<T, WIDE>;
   __shared__ BeamShared sh;
   pdl_trigger();
@@ -252,13 +331,14 @@ __global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
   const T* z = (const T*)a.logits + row * a.row_stride + from;
   const int left = a.vocab - from;
   const uint32_t far_low = value_key(-BS_FAR), far_high = value_key(BS_FAR);
+  if (tid == 0) sh.n_hot = 0;
 
   float ref = 0.f;  // an integer; meaningful once `any`
   bool any = false;
-  f32x2 acc[2] = {0ull, 0ull};
+  f32x2 acc = 0ull, rest = 0ull;  // a sum, and what its additions rounded off
   uint32_t most = 0;  // of the warp's chunks
   constexpr int U = 4;  // chunks requested at a time
-  const f32x2 hi2 = pack2(BS_LOG2E_HI, BS_LOG2E_HI), lo2 = pack2(BS_LOG2E_LO, BS_LOG2E_LO);
+  const f32x2 minus = pack2(-1.f, -1.f);
   C next[U];
 #pragma unroll
   for (int q = 0; q < U; ++q) {
@@ -287,26 +367,23 @@ __global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
         if (!any || need > ref) {
           const float f = any ? power2(ref - need) : 0.f;
           const f32x2 f2 = pack2(f, f);
-          mul2(acc[0], f2);
-          mul2(acc[1], f2);
+          mul2(acc, f2);
+          mul2(rest, f2);
           ref = need;
           any = true;
         }
-        const f32x2 r2 = pack2(-ref, -ref);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = now[q].two(i);
-          const f32x2 x2 = pack2(x.x, x.y);
-          const float2 e = unpack2(fma2_to(x2, lo2, fma2_to(x2, hi2, r2)));
-          acc[i & 1] = add2(acc[i & 1], pack2(ex2(e.x), ex2(e.y)));
-        }
+        if (lane == 0) sh.chunk_ref[c] = ref;
+        f32x2 e[4];
+        const f32x2 x = chunk_terms(now[q], ref, e), sum = add2(acc, x), part = fma2_to(acc, minus, sum);  // (a - b as -1 * b + a)
+        rest = add2(rest, add2(fma2_to(fma2_to(part, minus, sum), minus, acc), fma2_to(part, minus, x)));
+        acc = sum;
       }
     }
   }
   {
     // (a lane's sum is below 2^11: halves of 25 bits, whose sums over the lanes fit 32)
-    const float2 s0 = unpack2(acc[0]), s1 = unpack2(acc[1]);
-    const u64 mine = any ? (u64)__float2ull_rn(s0.x * 0x1p38f) + __float2ull_rn(s0.y * 0x1p38f) + __float2ull_rn(s1.x * 0x1p38f) + __float2ull_rn(s1.y * 0x1p38f) : 0ull;
+    const float2 s0 = unpack2(acc), s1 = unpack2(rest);
+    const u64 mine = any ? (u64)(to_units(s0.x) + to_units(s0.y) + to_units(s1.x) + to_units(s1.y)) : 0ull;
     const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)mine & 0x1ffffffu), hi = __reduce_add_sync(0xffffffffu, (uint32_t)(mine >> 25));
     if (lane == 0) {
       sh.units[warp] = ((u64)hi << 25) + lo;
@@ -318,10 +395,11 @@ __global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
   uint32_t peak = 0;
 #pragma unroll
   for (int w = 0; w < BS_NW; ++w) peak = max(peak, sh.most[w]);
-  PieceState* state = a.state + (size_t)row * a.pieces + piece;
-  if (peak <= value_key(-BS_NEAR) || peak >= far_high) {
+  const bool far = peak <= value_key(-BS_NEAR) || peak >= far_high;
+  const float m = peak >= 0xff800000u ? INFINITY : key_value(max(peak, BS_NONE));  // (+inf or NaN: the sum becomes NaN)
+  u64 units = 0;  // the sum over 2^ref
+  if (far) {
     // the largest logit is far out, or there is a NaN: the definition, on a few threads' patience
-    const float m = peak >= 0xff800000u ? INFINITY : key_value(max(peak, BS_NONE));  // (+inf or NaN: the sum becomes NaN)
     double s = 0.;
     if (peak > BS_NONE)
 #pragma unroll 1
@@ -330,37 +408,68 @@ __global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     __syncthreads();
     if (lane == 0) sh.sum[warp] = s;
-    __syncthreads();
-    if (tid == 0) {
-      double t = 0.;
+  } else {
+    ref = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < BS_NW; ++w) t += sh.sum[w];
-      PieceState st;
-      st.sum = t;
-      st.ref = peak > BS_NONE ? m : -INFINITY;
-      st.slow = 1;
-      *state = st;
-    }
-  } else if (tid == 0) {
-    float r = -INFINITY;
+    for (int w = 0; w < BS_NW; ++w) ref = fmaxf(ref, sh.ref[w]);
 #pragma unroll
-    for (int w = 0; w < BS_NW; ++w) r = fmaxf(r, sh.ref[w]);
-    u64 t = 0;
-#pragma unroll
-    for (int w = 0; w < BS_NW; ++w) t += shifted(sh.units[w], r - sh.ref[w]);
-    PieceState st;
-    st.units = t;
-    st.ref = r;
-    st.slow = 0;
-    *state = st;
+    for (int w = 0; w < BS_NW; ++w) units += shifted(sh.units[w], ref - sh.ref[w]);
   }
 
-  // ---- the piece's candidates
+  uint32_t least = 0xffffffffu;  // of the logits above 2^-10 of the sum
+  if (!far) {
+    const float y = fmaf(m, BS_LOG2E_LO, fmaf(m, BS_LOG2E_HI, -ref));  // the largest term's exponent
+    least = value_key(m + (log2f((float)units) - (38.f + 10.f) - y) * (float)BS_LN2);
+  }
+
+  // ---- the piece's candidates; meanwhile the other warps look for those logits
   if (warp == 0) {
     if (n <= 256) choose_chunks<8>(sh, n, k, lane);
     else choose_chunks<BS_MAX_CHUNKS / 32>(sh, n, k, lane);
+  } else if (!far) {
+#pragma unroll 1
+    for (int c0 = warp - 1; c0 < n; c0 += 32 * (BS_NW - 1)) {  // a chunk a lane; those found 8 at a time
+      const int mine = c0 + lane * (BS_NW - 1);
+      unsigned hot = __ballot_sync(0xffffffffu, mine < n && sh.top[mine] >= least);
+#pragma unroll 1
+      while (hot) {
+        C x[8];
+        int at[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          at[q] = hot ? c0 + (__ffs(hot) - 1) * (BS_NW - 1) : -1;
+          hot &= hot - 1;
+          if (at[q] >= 0) x[q].load(z + at[q] * BS_CHUNK, left - at[q] * BS_CHUNK, lane);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (at[q] >= 0 && value_key(x[q].top()) >= least) {
+            const int i = atomicAdd(&sh.n_hot, 1);
+            if (i < BS_HOT) sh.hot[i] = (uint16_t)(at[q] * 32 + lane);
+          }
+      }
+    }
   }
   __syncthreads();
+  {  // a share a thread, from the last thread on: the first ones have more to do
+    const int n_hot = min(sh.n_hot, BS_HOT);
+    long long moved = 0, exact = 0;
+#pragma unroll 1
+    for (int i = BS_NT - 1 - tid; i < n_hot; i += BS_NT) {
+      const int c = sh.hot[i] >> 5;
+      C x;
+      x.load(z + c * BS_CHUNK, left - c * BS_CHUNK, sh.hot[i] & 31);
+      take_out(x, sh.chunk_ref[c], least, ref, m, moved, exact);
+    }
+    if (__any_sync(0xffffffffu, exact != 0)) {
+      moved = warp_add(moved);
+      exact = warp_add(exact);
+    }
+    if (lane == 0) {
+      sh.moved[warp] = moved;
+      sh.exact[warp] = exact;
+    }
+  }
   const int n_work = sh.n_work;  // at most 2 k
   uint32_t bound = sh.bound;
   // keys above the bound into the list, the equals counted; again with a closer bound if they are too many
@@ -391,6 +500,19 @@ __global__ void __launch_bounds__(BS_NT) beam_rows_kernel(const BeamArgs a) {
     if (warp == 0) closer_bound(sh, n_work, k, lane);
     __syncthreads();
     bound = sh.bound;
+  }
+  if (tid == BS_NT - 1) {
+    PieceState st{0., (long long)units, m, far ? -INFINITY : ref};
+    long long exact = 0;
+#pragma unroll
+    for (int w = 0; w < BS_NW; ++w) {
+      if (far) st.exact += sh.sum[w];
+      st.rest += sh.moved[w];
+      exact += sh.exact[w];
+    }
+    if (!far) st.exact = (double)exact * 0x1p-52;
+    st.rest = max(st.rest, 0ll);  // (negative by its rounding only)
+    a.state[(size_t)row * a.pieces + piece] = st;
   }
   int n_key = sh.n;
   const int want = bound > BS_NONE ? k - n_key : 0;  // equals that may still count, those with the lowest ids
@@ -457,56 +579,29 @@ struct Best {
 // equal scores: the lower beam, then the larger logit, then the lower id
 __device__ __forceinline__ bool wins(int row, u64 key, int row2, u64 key2) { return row != row2 ? row < row2 : key > key2; }
 
-// ln(units 2^(ref - 38)), to 1e-12: units = 2^e x with x in [0.70, 1.42), and ln x = 2 atanh(t) = 2 (t + t^3 / 3 + ...) with
-// t = (x - 1) / (x + 1), |t| < 0.172, from an fp32 reciprocal and a Newton step. About 15 operations of 64 bits.
-__device__ __forceinline__ double ln_units(u64 units, float ref) {
-  if (units == 0) return -INFINITY;
-  int e = 63 - __clzll((long long)units);
-  u64 bits = units << (63 - e);  // the leading bit at the top
-  if (bits > 0xb504f333f9de6484ull) ++e;  // above sqrt(2)
-  const double x = (double)units * __longlong_as_double((long long)(1023 - e) << 52), y = x + 1.;
-  double r = (double)__frcp_rn((float)y);
-  r = r * (2. - y * r);
-  const double t = (x - 1.) * r, q = t * t;
+// ln x of x >= 1, to 1e-12, 0 of 1: x = 2^e y with y in [0.70, 1.42), and ln y = 2 atanh(t) = 2 (t + t^3 / 3 + ...) with
+// t = (y - 1) / (y + 1), |t| < 0.172, from an fp32 reciprocal and a Newton step. About 15 operations of 64 bits.
+__device__ __forceinline__ double ln_sum(double x) {
+  const long long bits = __double_as_longlong(x), digits = bits & 0xfffffffffffffll;
+  int e = (int)(bits >> 52) - 1023;
+  const bool high = digits > 0x6a09e667f3bccll;  // above sqrt(2)
+  e += high;
+  const double y = __longlong_as_double(digits | (long long)(high ? 1022 : 1023) << 52), d = y + 1.;
+  double r = (double)__frcp_rn((float)d);
+  r = r * (2. - d * r);
+  const double t = (y - 1.) * r, q = t * t;
   double p = 1. / 13.;
   p = p * q + 1. / 11.;
   p = p * q + 1. / 9.;
   p = p * q + 1. / 7.;
   p = p * q + 1. / 5.;
   p = p * q + 1. / 3.;
-  return 2. * (t + t * q * p) + ((double)ref + (double)(e - BS_UNIT)) * BS_LN2;
-}
-
-// ln of a row's sum of exponentials, with pieces that were summed from the definition; NaN if there is one. A warp.
-__device__ __noinline__ double far_norm(const PieceState* st, int n, int lane) {
-  double m = -INFINITY, s = 0.;
-  bool nan = false;
-#pragma unroll 1
-  for (int p = lane; p < n; p += 32) {
-    if (st[p].ref == -INFINITY) continue;  // nothing but -inf
-    const double x = st[p].slow ? (double)st[p].ref + log(st[p].sum) : (double)st[p].ref * BS_LN2 + log((double)st[p].units * 0x1p-38);
-    if (x != x) {
-      nan = true;
-      continue;
-    }
-    const double hi = fmax(m, x);
-    s = s * exp(m - hi) + exp(x - hi);
-    m = hi;
-  }
-#pragma unroll 1
-  for (int o = 16; o; o >>= 1) {
-    const double m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    const double hi = fmax(m, m2);
-    s = (m > -INFINITY ? s * exp(m - hi) : 0.) + (m2 > -INFINITY ? s2 * exp(m2 - hi) : 0.);
-    m = hi;
-  }
-  return __any_sync(0xffffffffu, nan) ? (double)NAN : m + log(s);
+  return 2. * (t + t * q * p) + (double)e * BS_LN2;
 }
 
 __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
-  __shared__ double s_norm[BS_MAX_BEAMS], s_score[BS_MAX_BEAMS], s_weight[BS_MAX_BEAMS];
-  __shared__ float s_ref[BS_MAX_BEAMS];
-  __shared__ u64 s_units[BS_MAX_BEAMS];
+  __shared__ double s_norm[BS_MAX_BEAMS], s_score[BS_MAX_BEAMS], s_weight[BS_MAX_BEAMS];  // norm: ln of the sum of exp(z - top)
+  __shared__ float s_top[BS_MAX_BEAMS];
   __shared__ int s_kind[BS_MAX_BEAMS];  // 0: no candidates, 1: the row's logits, 2: ended
   __shared__ Best s_head[BS_MAX_LISTS], s_run[32][BS_MAX_OUT];
   __shared__ alignas(16) uint32_t s_high[BS_MAX_LISTS];  // upper halves of the heads' scores
@@ -514,42 +609,47 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
   __shared__ int s_surv[32], s_row[BS_MAX_OUT], s_token[BS_MAX_OUT], s_len[BS_MAX_OUT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.x, k = a.n_out, P = a.pieces;
   pdl_wait();
+  // Every row's sum of exp(z - top), a few lanes a row: one for each of its pieces and one for what they leave
+  const int L = P >= 16 ? 32 : P >= 8 ? 16 : P >= 4 ? 8 : P >= 2 ? 4 : 2, sub = lane & (L - 1);
 #pragma unroll 1
-  for (int w = warp; w < a.beams; w += BS_NW) {
-    const int row = g * a.beams + w;
+  for (int w0 = warp * (32 / L); w0 < a.beams; w0 += BS_NW * (32 / L)) {
+    const int w = w0 + lane / L, row = g * a.beams + min(w, a.beams - 1);
     const float c = a.scores[row], weight = a.weights ? a.weights[row] : 1.f;
     const bool ended = a.ended && a.ended[row];
+    const PieceState* st = a.state + (size_t)row * P;
+    const PieceState first = sub < P ? st[sub] : PieceState{0., 0, -INFINITY, -INFINITY};  // (nothing that is used where the row has no candidates)
     const bool bad = c != c || c == INFINITY || !(weight > 0.f && weight < INFINITY);
     const int kind = bad || c == -INFINITY ? 0 : ended ? 2 : 1;
-    double far_s = 0.;
-    u64 s = 0;
-    float ref = NAN;  // NaN: far_s is the normaliser already
-    if (kind == 1) {
-      const PieceState* st = a.state + (size_t)row * P;
-      bool far = false;
-      ref = -INFINITY;
+    float top = first.top, ref = first.ref;
 #pragma unroll 1
-      for (int p = lane; p < P; p += 32) {
-        far |= st[p].slow;
-        ref = fmaxf(ref, st[p].ref);
-      }
-      if (__any_sync(0xffffffffu, far)) {
-        far_s = far_norm(st, P, lane);
-        ref = NAN;
-      } else {
-        ref = warp_max(ref);
-#pragma unroll 1
-        for (int p = lane; p < P; p += 32) s += shifted(st[p].units, ref - st[p].ref);
-#pragma unroll 1
-        for (int o = P > 16 ? 16 : P > 8 ? 8 : P > 4 ? 4 : P > 2 ? 2 : P > 1 ? 1 : 0; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      }
+    for (int p = sub + L; p < P; p += L) {
+      top = fmaxf(top, st[p].top);
+      ref = fmaxf(ref, st[p].ref);
     }
-    if (lane == 0) {
+#pragma unroll 1
+    for (int o = L / 2; o; o >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+    }
+    u64 rest = shifted((u64)first.rest, ref - first.ref);
+#pragma unroll 1
+    for (int p = sub + L; p < P; p += L) rest += shifted((u64)st[p].rest, ref - st[p].ref);
+#pragma unroll 1
+    for (int o = L / 2; o; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+    double s = 0.;
+#pragma unroll 1
+    for (int p = sub; p <= P; p += L) {
+      const double x = p == P ? (double)rest * BS_REST : p == sub ? first.exact : st[p].exact;
+      const double of = p == P ? (double)ref * BS_LN2 : (double)(p == sub ? first.top : st[p].top);
+      if (x != 0.) s += x * exp(of == (double)top ? 0. : of - (double)top);
+    }
+#pragma unroll 1
+    for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (sub == 0 && w < a.beams) {
       if (bad) atomicOr(a.err, ERR_NONFINITE);
       s_kind[w] = kind;
-      s_norm[w] = far_s;
-      s_units[w] = s;
-      s_ref[w] = ref;
+      s_norm[w] = s;
+      s_top[w] = top;
       s_score[w] = c;
       s_weight[w] = weight;
     }
@@ -557,17 +657,21 @@ __global__ void __launch_bounds__(BS_NT) beam_groups_kernel(const BeamArgs a) {
   if (tid < 32) s_surv[tid] = -1;
   __syncthreads();
   if (tid < a.beams && s_kind[tid] == 1) {  // one logarithm for all rows
-    const float ref = s_ref[tid];
-    const double norm = ref == ref ? ln_units(s_units[tid], ref) : s_norm[tid];
-    s_norm[tid] = norm;
-    if (!(fabs(norm) < INFINITY)) {
+    const double sum = s_norm[tid];
+    if (sum > 0. && sum < INFINITY) {
+      s_norm[tid] = ln_sum(sum);
+      if (fabsf(s_top[tid]) >= BS_FAR) {  // far out the normaliser is one number of 64 bits, whose step may exceed ln of the sum
+        s_norm[tid] += (double)s_top[tid];
+        s_top[tid] = 0.f;
+      }
+    } else {  // nothing but -inf, or a NaN
       s_kind[tid] = 0;
       atomicOr(a.err, ERR_NONFINITE);
     }
   }
   __syncthreads();
   auto score_of = [&](int w, u64 key) {  // in 64 bits
-    return s_kind[w] == 2 ? s_score[w] : s_score[w] + ((double)key_value((uint32_t)(key >> 32)) - s_norm[w]);
+    return s_kind[w] == 2 ? s_score[w] : s_score[w] + (((double)key_value((uint32_t)(key >> 32)) - (double)s_top[w]) - s_norm[w]);
   };
   auto best_of = [&](int list, int r) {
     const int w = list / P, p = list - w * P;
