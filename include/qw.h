@@ -504,7 +504,10 @@ qw_status qw_op_paged_attention(const qw_paged_kv *cache, int32_t n_seqs, int32_
  *       serves too
  * Probabilities keep two pieces of the cache's type (22 bits, bf16 16) for 16-bit callers and 22 bits and more for fp32 ones, as
  * there. A 16-bit caller's values whose sum over the shared positions passes 2^113 overflow. Equal inputs give equal bits on equal
- * devices. */
+ * devices.
+ * It pays where it saves much: it takes three launches and sums partial results up, 7 to 30 us that qw_op_paged_attention does
+ * not take. Where the groups' later sequences would read less than about 100 MB of shared keys and values in all, that call is faster,
+ * over tables that hold the shared pages (as forks leave them). */
 size_t qw_op_shared_attention_workspace(int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
 qw_status qw_op_shared_attention(const qw_paged_kv *cache, int32_t n_seqs, int32_t n_heads, const int32_t *block_table,
                                  int32_t max_blocks, const int32_t *lens, int32_t n_groups, const int32_t *cu_seqs,

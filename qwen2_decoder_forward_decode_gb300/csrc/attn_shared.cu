@@ -15,8 +15,13 @@
 // The second launch goes on beside the first (programmatic dependent launch: it waits for it at its end only), the third
 // is in place when the second ends.
 // Measured in a CUDA graph: 4 samples of a prompt of 178 (12 and 2 heads of 128, fp16 cache, fp32 queries) 15.4 us, three launches'
-// chains of loads; 256 sequences of 1 to 256 own positions behind 16383 (28 and 4 heads, bf16) 102 us: own positions 20, shared
-// ones 71, join 11 (7168 rows of 8 states each, 30 MB that L2 holds). The same without sharing reads 8.7 GB, 1.3 ms at the copy rate.
+// chains of loads; 256 sequences of 1 to 256 own positions behind 16383 (28 and 4 heads, bf16) 101 us: own positions 20, shared
+// ones 70, join 11 (7168 rows of 8 states each, 30 MB that L2 holds). The same without sharing reads 8.7 GB, 1.3 ms at the copy rate.
+// When it pays, next to attn_paged.cu over tables that hold all pages (us, paged / shared; 28 and 4 heads, bf16, own positions 64):
+// one prompt of 2048, 4 rows 11 / 16, 32 rows 27 / 26; of 8192, 4 rows 19 / 20, 8 rows 25 / 24; 64 prompts of 512, 2 rows 32 / 39,
+// 4 rows 56 / 47; 8 prompts of 2048, 4 rows 27.0 / 27.5, 8 rows 44 / 30; 64 prompts of 2048 of one row 57 / 75. 12 and 2 heads,
+// fp32 over fp16: 64 prompts of 512, 4 rows 34 / 33; of 2048, 2 rows 49 / 55. So from 100 to 150 MB on that need not be read again; which call
+// to make is the caller's choice, who knows the lengths.
 #include "attn_shared.cuh"
 
 #include <algorithm>

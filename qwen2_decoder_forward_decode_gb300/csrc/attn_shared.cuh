@@ -47,8 +47,9 @@ struct Unit {
 template <int MT>
 __host__ __device__ __forceinline__ int block_cost(int rows, int tile) { return MT == 256 && rows - tile * MT > MT / 2 ? 2 : 1; }
 // A unit's ends (queries, first products, states) count like 4 blocks before it, 2 where a block is long (the CUDA cores). Measured
-// with 2, 4 and 8: 256 sequences of 16383 shared positions 94, 92, 89 us (bf16, blocks of cost 2; when probabilities were one piece, 102 with 8 now), 136, 134, 136 (fp32 callers);
-// 256 prompts of one sequence 231, 226, 235 (cost 1); an fp32 cache 32.6, 32.9, 34.7.
+// with 2, 4 and 8: 256 sequences of 16383 shared positions 94, 92, 89 us (bf16, blocks of cost 2), 136, 134, 136 (fp32 callers);
+// 256 prompts of one sequence 231, 226, 235 (cost 1); an fp32 cache 32.6, 32.9, 34.7. (bf16 with probabilities of one piece; with
+// two, at these weights, 101 and 248.)
 template <int MT>
 __host__ __device__ constexpr int unit_weight(int cost) { return MT == 64 ? 2 : 4 * cost; }
 // numbers of one KV head's units

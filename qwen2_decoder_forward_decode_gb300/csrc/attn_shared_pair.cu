@@ -21,10 +21,10 @@
 // 16, so that the output's own rounding is what remains); their sum l takes them before that. One piece would save 8 of a step's
 // 24 products, 13 us of 256 sequences behind 16383 positions, and raises bf16's error against 64 bits by a third. The tensor
 // cores' additions cut: over 1000 products of 16 positions about 1e-5 of the norm, next to the output's 2^-9 or 2^-12.
-// What bounds it: of many rows the chain of one block, S, softmax, P V: 4400 cycles for both chains' blocks, of which the products
-// are 3070. 256 sequences, 28 and 4 heads of 128 behind 16383 positions: 73 us, 1240 TFLOP/s of products (830 of the formula's). Of few
+// What bounds it: of many rows the chain of one block, S, softmax, P V, that the two chains fill to 53% of the tensor cores' time.
+// 256 sequences, 28 and 4 heads of 128 behind 16383 positions: 72 us, 1260 TFLOP/s of products (840 of the formula's). Of few
 // rows HBM and L2: 16 groups of 8 behind 512 to 4096 positions 30 us, 86 MB. The shares of 72 and 56 registers spill in the
-// producers and issuers: 324 to 336 bytes of stores a thread.
+// producers and issuers, 324 to 336 bytes of stores a thread.
 //
 // Every wait is bounded: on expiry ERR_TIMEOUT is set, the CTA stops issuing work, waits (bounded) for what it issued, and
 // releases its TMEM.

@@ -14,7 +14,8 @@
 // element), three of bf16, whose products are added up lowest piece first. Exponentials are ex2's, good to 2^-22.
 //
 // What bounds it: the softmax and the fold of O, 128 rows by 8 warps, and of bf16 caches the products of three pieces. 256 sequences,
-// 28 and 4 heads of 128 behind 16383 positions: 134 us with the fp16 cache, 172 with bf16; behind 8000 89.
+// 28 and 4 heads of 128 behind 16383 positions: 132 us with the fp16 cache, 173 with bf16; behind 8000 88. The registers' shares spill:
+// 236 to 376 bytes of stores a thread.
 //
 // Every wait is bounded: on expiry ERR_TIMEOUT is set, the CTA stops issuing work, waits (bounded) for what it issued, and
 // releases its TMEM.
