@@ -377,8 +377,9 @@ qw_status qw_op_page_release(int32_t n_seqs, int32_t page_size, int32_t n_pages,
  * If there are too few free pages, a length is negative or beyond max_blocks pages, or n_free is outside [0, n_pages],
  * QW_DEV_CAPACITY is set and nothing is forked, ended or taken: lens_out 0, nothing to copy, shares, list and count as they
  * were. A parent outside [-1, n_seqs) counts as -1, a page id outside [0, n_pages) is copied and not counted, and a list that would
- * have more than n_pages pages (some were held and on it) ends there; all three set QW_DEV_PAGE. A negative count is taken as 0. A partly filled last page has no other holder than its row (every fork leaves it
- * so): the child that keeps it appends to it. n_seqs and n_out <= 16384, n_pages <= 2^30.
+ * have more than n_pages pages (some were held and on it) ends there; all three set QW_DEV_PAGE. A negative count is taken as 0.
+ * A partly filled last page has no other holder than its row (every fork leaves it so): the child that keeps it appends to it.
+ * n_seqs and n_out <= 16384, n_pages <= 2^30.
  * workspace: at least qw_op_page_fork_workspace() bytes, 16-byte aligned, zeroed once before its first use; it serves this
  * call alone, and every call leaves it ready for the next with the same n_pages. Calls that may run at the same time need
  * workspaces of their own. */
